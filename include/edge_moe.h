@@ -237,9 +237,11 @@ int edge_moe_prefetch(const edge_moe_dims* dims, const edge_moe_weights* weights
  *
  * Layouts: each matrix is stored N x K like the int4 one; codes [N][K/2] bytes,
  * two E2M1 codes per byte (element 2i in the low nibble: sign bit 3, exponent
- * bits 2..1 with bias 1, mantissa bit 0); scales [N][K/32] bytes, one E8M0
- * power of two 2^(X - 127) per 32 consecutive elements along K (X = 255 is
- * NaN: not allowed).  The weight is code value * 2^(X - 127) exactly.  LoRA
+ * bits 2..1 with bias 1, mantissa bit 0); one E8M0 scale byte per 32
+ * consecutive elements along K, the power of two 2^(X - 127) (X = 255 is NaN:
+ * not allowed), stored K-step-major: [K/128][N][4], for each 128-element step
+ * of K the four block scales of every row in turn.  The weight is code value *
+ * 2^(X - 127) exactly.  edge_moe_mx_quantize writes both.  LoRA
  * factors are bf16 as in edge_moe_weights.  16-byte aligned device pointers.
  *
  * Arithmetic: the int4 layer's, except that the inputs of the four large
@@ -260,12 +262,12 @@ int edge_moe_prefetch(const edge_moe_dims* dims, const edge_moe_weights* weights
  * multiple of 8 from 8 to 32; any T.  quant_group is not used.  Other shapes:
  * EDGE_MOE_EUNSUPPORTED.  Every batch size runs the tiled large-batch kernels. */
 typedef struct edge_moe_weights_mx {
-    const uint8_t*  s_up_q;  const uint8_t* s_up_e;   /* [G][h][d/2], [G][h][d/32] */
-    const uint8_t*  s_dn_q;  const uint8_t* s_dn_e;   /* [G][d][h/2], [G][d][h/32] */
-    const uint8_t*  a_up_q;  const uint8_t* a_up_e;   /* [E][r][d/2], [E][r][d/32] */
-    const uint8_t*  b_up_q;  const uint8_t* b_up_e;   /* [E][h][r/2], [E][h][r/32] */
-    const uint8_t*  a_dn_q;  const uint8_t* a_dn_e;   /* [E][r][h/2], [E][r][h/32] */
-    const uint8_t*  b_dn_q;  const uint8_t* b_dn_e;   /* [E][d][r/2], [E][d][r/32] */
+    const uint8_t*  s_up_q;  const uint8_t* s_up_e;   /* [G][h][d/2], [G][d/128][h][4] */
+    const uint8_t*  s_dn_q;  const uint8_t* s_dn_e;   /* [G][d][h/2], [G][h/128][d][4] */
+    const uint8_t*  a_up_q;  const uint8_t* a_up_e;   /* [E][r][d/2], [E][d/128][r][4] */
+    const uint8_t*  b_up_q;  const uint8_t* b_up_e;   /* [E][h][r/2], [E][r/128][h][4] */
+    const uint8_t*  a_dn_q;  const uint8_t* a_dn_e;   /* [E][r][h/2], [E][h/128][r][4] */
+    const uint8_t*  b_dn_q;  const uint8_t* b_dn_e;   /* [E][d][r/2], [E][r/128][d][4] */
     const uint16_t* lora_up_u; const uint16_t* lora_up_v;
     const uint16_t* lora_dn_u; const uint16_t* lora_dn_v;
 } edge_moe_weights_mx;
@@ -279,6 +281,37 @@ size_t edge_moe_workspace_bytes_mx(const edge_moe_dims* dims);
 int edge_moe_forward_mx(const edge_moe_dims* dims, const uint16_t* x, const int32_t* topk_idx,
                         const float* topk_w, const edge_moe_weights_mx* weights, float* y, void* ws,
                         size_t ws_bytes, void* stream, const edge_moe_trace* trace);
+
+/* ------------------------------------------------------- MX matrix operators --
+ * Element formats and dense element types of the calls below. */
+#define EDGE_MOE_MX_FP4 0   /* E2M1, two codes per byte, block exponent emax = 2 */
+#define EDGE_MOE_MX_FP8 1   /* E4M3, one code per byte, emax = 8                 */
+#define EDGE_MOE_BF16   0   /* bf16 (uint16 bit patterns) */
+#define EDGE_MOE_FLOAT  1   /* float32 */
+
+/* Quantise M dense matrices of N rows x K to a microscaling format, in the
+ * layouts of edge_moe_weights_mx: codes [M][N][K/2] (FP4) or [M][N][K] (FP8)
+ * bytes, scales [M][K/128][N][4].  Per block of 32 along K: X = floor(log2 max|v|)
+ * - emax + 127 limited to 0..254 (0 for an all-zero block), each code the
+ * format's value nearest to v / 2^(X - 127), ties to the even code, saturated
+ * at 6 (FP4) or 448 (FP8), the sign kept (also a zero's).  A block that holds a
+ * NaN or an infinity gets X = 255 and zero codes: it reads back as NaN.
+ *   src         rows of K elements of src_type, src_stride elements apart
+ *               (row n of matrix m is row m N + n; src_stride >= K)
+ * K a multiple of 128 up to 32768, M N up to 2^30 rows (EDGE_MOE_EUNSUPPORTED
+ * otherwise); src and its row stride in bytes, and codes, 16-byte aligned,
+ * scales 4-byte aligned.  Makes the matrices of edge_moe_forward_mx and
+ * edge_moe_mx_product from dense weights; results are those of the layer's own
+ * MXFP8 rounding of its inputs. */
+int edge_moe_mx_quantize(int32_t M, int32_t N, int32_t K, int32_t format, int32_t src_type, const void* src,
+                         int64_t src_stride, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* The way back: dst[row][i] = code value * 2^(X - 127), rounded once to dst_type
+ * (exact in float32, and in bf16 down to its smallest subnormal; past the type's
+ * range an infinity); X = 255 gives NaN.  Only the K elements of each dst row are
+ * written.  Arguments as edge_moe_mx_quantize's. */
+int edge_moe_mx_dequantize(int32_t M, int32_t N, int32_t K, int32_t format, int32_t dst_type, const uint8_t* codes,
+                           const uint8_t* scales, void* dst, int64_t dst_stride, void* stream);
 
 /* ------------------------------------------------ expert streaming from host --
  * The pages keep the expert library in host memory and bring the experts a

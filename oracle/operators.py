@@ -1,0 +1,62 @@
+"""The MX-matrix and router-training operators in plain float64 (oracle; test
+infrastructure only, no code shared with the library).
+
+Formats, block scales and layouts are the MX mode's (oracle/mx.py); here also
+the E2M1 encoder, non-finite blocks, the product of quantised rows with MXFP4
+matrices, the router's load and losses, and their gradients.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+from . import mx
+
+FP4, FP8 = 0, 1
+
+
+def e2m1_encode(v: np.ndarray) -> np.ndarray:
+    """float64 values -> E2M1 codes: nearest magnitude of 0, 0.5, 1, 1.5, 2, 3, 4,
+    6, ties to the even code, past 6 saturated; the sign bit is v's."""
+    a = np.abs(np.asarray(v, dtype=np.float64))
+    grid = mx.e2m1_to_f64(np.arange(8))
+    mids = (grid[1:] + grid[:-1]) / 2
+    low = np.searchsorted(mids, a, side="left")        # at a midpoint: the lower code
+    up = low + ((low % 2 == 1) & (a == mids[np.minimum(low, 6)]))
+    return (up | np.where(np.signbit(v), 8, 0)).astype(np.uint8)
+
+
+def quantize(v: np.ndarray, fmt: int):
+    """Rows [..., K] -> (codes [..., K] one per element, E8M0 bytes [..., K/32])."""
+    v = np.asarray(v, dtype=np.float64)
+    b = v.reshape(v.shape[:-1] + (v.shape[-1] // 32, 32))
+    bad = ~np.isfinite(b).all(-1)
+    b = np.where(bad[..., None], 0.0, b)
+    amax = np.abs(b).max(-1)
+    e = np.frexp(amax)[1] - 1                            # floor(log2), exact
+    x = np.where(amax > 0, np.clip(e - (2 if fmt == FP4 else 8) + 127, 0, 254), 0)
+    a = b / np.exp2(x - 127.0)[..., None]
+    codes = e2m1_encode(a) if fmt == FP4 else mx.e4m3_encode(a)
+    codes = np.where(bad[..., None], 0, codes).astype(np.uint8)
+    return codes.reshape(v.shape), np.where(bad, 255, x).astype(np.uint8)
+
+
+def values(codes: np.ndarray, x: np.ndarray, fmt: int) -> np.ndarray:
+    """The values of codes [..., K] with E8M0 bytes [..., K/32]."""
+    c = mx.e2m1_to_f64(codes) if fmt == FP4 else mx.e4m3_to_f64(codes)
+    return c * np.repeat(mx.e8m0_to_f64(x), 32, axis=-1)
+
+
+def rounded(v: np.ndarray, fmt: int) -> np.ndarray:
+    """The values v's rows take in the format."""
+    return values(*quantize(v, fmt), fmt)
+
+
+def pack(codes: np.ndarray, fmt: int) -> np.ndarray:
+    """Stored bytes of codes [..., K]: E2M1 two a byte, element 2i in the low nibble."""
+    return codes[..., 0::2] | (codes[..., 1::2] << 4) if fmt == FP4 else codes
+
+
+def by_step(x: np.ndarray) -> np.ndarray:
+    """E8M0 bytes [M, N, K/32] -> the stored [M, K/128, N, 4]."""
+    M, N, nb = x.shape
+    return np.ascontiguousarray(x.reshape(M, N, nb // 4, 4).transpose(0, 2, 1, 3))

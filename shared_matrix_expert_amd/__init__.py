@@ -32,7 +32,12 @@ EXPORTED = ("edge_moe_workspace_bytes", "edge_moe_route", "edge_moe_forward",
             "edge_moe_forward_noalloc", "edge_moe_forward_persistent", "edge_moe_mfma_peak",
             "edge_moe_workspace_bytes_mx", "edge_moe_forward_mx", "edge_moe_prefetch_ws_bytes",
             "edge_moe_prefetch", "edge_moe_cache_create", "edge_moe_cache_destroy", "edge_moe_cache_map",
-            "edge_moe_cache_prefetch", "edge_moe_cache_totals", "edge_moe_cache_slot_of")
+            "edge_moe_cache_prefetch", "edge_moe_cache_totals", "edge_moe_cache_slot_of",
+            "edge_moe_mx_quantize", "edge_moe_mx_dequantize")
+
+# element formats and dense types of the MX matrix operators
+MX_FP4, MX_FP8 = 0, 1
+_BF16, _FLOAT = 0, 1
 
 
 class CDims(ctypes.Structure):
@@ -150,6 +155,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.edge_moe_cache_totals.restype = i32
     lib.edge_moe_cache_slot_of.argtypes = [vp, i32]
     lib.edge_moe_cache_slot_of.restype = i32
+    i64 = ctypes.c_int64
+    lib.edge_moe_mx_quantize.argtypes = [i32, i32, i32, i32, i32, vp, i64, vp, vp, vp]
+    lib.edge_moe_mx_quantize.restype = i32
+    lib.edge_moe_mx_dequantize.argtypes = [i32, i32, i32, i32, i32, vp, vp, vp, i64, vp]
+    lib.edge_moe_mx_dequantize.restype = i32
     lib.edge_moe_residual.argtypes = [ctypes.c_int32, ctypes.c_int32, vp, vp, vp, vp]
     lib.edge_moe_residual.restype = i32
     lib.edge_moe_copy.argtypes = [vp, vp, sz, vp]
@@ -327,6 +337,107 @@ def edge_moe_forward_noalloc(dims, x, topk_idx, topk_w, weights, y, stream=None)
                                          ctypes.byref(cweights(weights)), _ptr(y), _stream(stream))
     if st != EDGE_MOE_OK:
         raise EdgeMoeError("edge_moe_forward_noalloc", st)
+
+
+# ------------------------------------------------------------------ MX matrices --
+# The calls below check types, shapes and devices of what they are given (their
+# kernels trust the sizes in the arguments), beyond what the library checks.
+
+def _same_device(*tensors) -> None:
+    """Every tensor on the current GPU: the library launches there."""
+    import torch
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != cur):
+            raise ValueError(f"tensors must be on the current GPU (cuda:{cur}), got one on {t.device}")
+
+
+def _dense_type(t) -> int:
+    """bf16 (bfloat16, or int16 / uint16 bit patterns) or float32."""
+    name = str(t.dtype)
+    if name in ("torch.bfloat16", "torch.int16", "torch.uint16"):
+        return _BF16
+    if name == "torch.float32":
+        return _FLOAT
+    raise ValueError(f"expected bfloat16 (or its int16 bits) or float32, got {name}")
+
+
+def _row_stride(t) -> int:
+    """Elements between the rows of t [..., N, K]: one stride for all rows."""
+    if t.dim() < 2:
+        raise ValueError("expected rows: a tensor of at least two dimensions")
+    K = t.shape[-1]
+    if K != 1 and t.stride(-1) != 1:
+        raise ValueError("the elements of a row must be contiguous")
+    stride, span = None, 1
+    for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n != 1:
+            if stride is None:
+                stride = s
+                if span != 1:
+                    raise ValueError("the rows must lie at one stride")
+            elif s != stride * span:
+                raise ValueError("the rows must lie at one stride")
+        span *= n
+    return max(K, 8) if stride is None else stride
+
+
+def _mx_shape(fmt, dense, codes, scales):
+    """(M, N, K) of a dense tensor and its MX codes and scales, checked against each other."""
+    if fmt not in (MX_FP4, MX_FP8):
+        raise ValueError("format must be MX_FP4 or MX_FP8")
+    if dense.dim() < 2:
+        raise ValueError("expected rows: a tensor of at least two dimensions")
+    N, K = dense.shape[-2], dense.shape[-1]
+    M = dense.numel() // max(1, N * K)
+    _uint8(codes, M * N * (K // 2 if fmt == MX_FP4 else K), "codes")
+    _uint8(scales, M * N * (K // 32), "scales")
+    return M, N, K
+
+
+def _uint8(t, count: int, what: str) -> None:
+    if str(t.dtype) != "torch.uint8" or t.numel() != count:
+        raise ValueError(f"{what}: expected {count} uint8 values, got {t.numel()} of {t.dtype}")
+
+
+def edge_moe_mx_quantize(fmt, src, codes, scales, stream=None) -> None:
+    """Dense matrices src [..., N, K] (bf16 or float32, rows at one stride) to
+    MX codes [..., N, K/2] (MX_FP4) or [..., N, K] (MX_FP8) and E8M0 scales
+    [..., K/128, N, 4], both uint8."""
+    M, N, K = _mx_shape(fmt, src, codes, scales)
+    _same_device(src, codes, scales)
+    st = load().edge_moe_mx_quantize(M, N, K, fmt, _dense_type(src), src.data_ptr(), _row_stride(src), _ptr(codes),
+                                     _ptr(scales), _stream(stream))
+    if st != EDGE_MOE_OK:
+        raise EdgeMoeError("edge_moe_mx_quantize", st)
+
+
+def edge_moe_mx_dequantize(fmt, codes, scales, dst, stream=None) -> None:
+    """MX codes and scales back to dense dst [..., N, K] (bf16 or float32)."""
+    M, N, K = _mx_shape(fmt, dst, codes, scales)
+    _same_device(dst, codes, scales)
+    st = load().edge_moe_mx_dequantize(M, N, K, fmt, _dense_type(dst), _ptr(codes), _ptr(scales), dst.data_ptr(),
+                                       _row_stride(dst), _stream(stream))
+    if st != EDGE_MOE_OK:
+        raise EdgeMoeError("edge_moe_mx_dequantize", st)
+
+
+def mx_weights(dense: dict, stream=None) -> dict:
+    """The MX weight dict of edge_moe_forward_mx from dense matrices: "s_up"
+    [G][h][d], "s_dn" [G][d][h], "a_up" [E][r][d], "b_up" [E][h][r], "a_dn"
+    [E][r][h], "b_dn" [E][d][r] (bf16 or float32) are quantised to MXFP4; the
+    LoRA factors, bf16, are taken as they are."""
+    import torch
+    out = {}
+    for key in _WEIGHT_KEYS[:12:2]:
+        src = dense[key]
+        M, N, K = src.shape
+        out[key] = torch.empty(M, N, K // 2, dtype=torch.uint8, device=src.device)
+        out[key + "_scale"] = torch.empty(M, K // 128, N, 4, dtype=torch.uint8, device=src.device)
+        edge_moe_mx_quantize(MX_FP4, src, out[key], out[key + "_scale"], stream)
+    for key in _WEIGHT_KEYS[12:16]:
+        out[key] = dense[key]
+    return out
 
 
 def edge_moe_residual(x, y, x_out, stream=None) -> None:

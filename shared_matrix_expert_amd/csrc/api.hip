@@ -240,6 +240,8 @@ void* scratch_ptr() {
 namespace em {
 // The layer's shape checks, for the host-side expert cache (cache.hip).
 int layer_dims_status(const edge_moe_dims* d) { return check_dims(d); }
+// The device check, for the other entry points' sources (operators.hip).
+int device_status() { return check_device(); }
 
 void prof_begin(hipStream_t s) {
     ProfState& p = prof();

@@ -1,0 +1,192 @@
+// MX quantiser: dense rows (bf16 or float32) to microscaling codes and E8M0
+// scales, and back.  Layouts are the MX layer's: codes row-major (E2M1 two per
+// byte, element 2i in the low nibble; E4M3 one per byte), scales K-step-major
+// [K/128][N][4] for each matrix of N rows.
+//
+// Both directions read each input once and write each output once with a
+// handful of conversions per element, so they are bound by HBM.  Sixteen lanes
+// take one 128-element step of a row (8 elements each): a scale block is four
+// neighbouring lanes, its maximum two quad permutes, and a wave's accesses are
+// whole 256-byte (bf16) or 512-byte (float32) row segments.  A workgroup takes
+// 16 rows x 4 steps: the four steps' loads are in flight together, and the
+// scale words of its 16 rows fall in one 64-byte run per step.
+#include "mx_format.h"
+#include "operators.h"
+
+namespace em {
+
+namespace {
+
+constexpr int QR = 16;    // rows per workgroup
+constexpr int QS = 4;     // K steps per workgroup
+
+// Value of the lane's quad neighbours under an xor of 1 (0xB1) or 2 (0x4E).
+template <int CTRL>
+EM_DEV uint32_t quad(uint32_t v) { return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, false); }
+
+EM_DEV uint32_t quad_max(uint32_t v) {
+    v = max(v, quad<0xB1>(v));
+    return max(v, quad<0x4E>(v));
+}
+
+}  // namespace
+
+template <int FMT, bool F32>
+__global__ void __launch_bounds__(256)
+mxq_quantize(const void* __restrict__ src, int64_t stride, int64_t rows, int N, int K, uint8_t* __restrict__ codes,
+             uint8_t* __restrict__ scales) {
+    const int l16 = threadIdx.x & 15;
+    const int64_t row = (int64_t)blockIdx.x * QR + (threadIdx.x >> 4);
+    if (row >= rows) return;
+    const int steps = K / kMxStep, s0 = blockIdx.y * QS;
+    const int64_t m = row / N, n = row - m * N;
+    uint8_t* srow = scales + (m * steps * N + n) * 4;          // + step * N * 4 + block
+    uint4 v[QS][F32 ? 2 : 1];
+#pragma unroll
+    for (int i = 0; i < QS; ++i) {
+        const int64_t k = (int64_t)min(s0 + i, steps - 1) * kMxStep + 8 * l16;
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(src) + (row * stride + k) * (F32 ? 4 : 2));
+        v[i][0] = p[0];
+        if constexpr (F32) v[i][1] = p[1];
+    }
+#pragma unroll
+    for (int i = 0; i < QS; ++i) {
+        if (s0 + i >= steps) break;
+        uint32_t hi;                                            // upper 16 bits of the block's largest magnitude
+        float f[8];
+        if constexpr (F32) {
+            const uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+            uint32_t a = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                a = max(a, w[j] & 0x7FFFFFFFu);
+                f[j] = __uint_as_float(w[j]);
+            }
+            hi = quad_max(a) >> 16;
+        } else {
+            hi = quad_max(amax8_bf16(v[i][0]));
+        }
+        const int X = e8m0_of<FMT>(hi);
+        const bool bad = X == 255;
+        const float sc = e8m0_f32(bad ? 127 : X);
+        const int64_t at = row * K + (int64_t)(s0 + i) * kMxStep + 8 * l16;
+        if constexpr (FMT == kMxFp4) {
+            const uint32_t c = F32 ? fp4x8_f32(f, sc) : fp4x8_bf16(v[i][0], sc);
+            *reinterpret_cast<uint32_t*>(codes + (at >> 1)) = bad ? 0u : c;
+        } else {
+            uint32_t c0, c1;
+            if constexpr (F32) {
+                c0 = fp8x4_f32(f, sc);
+                c1 = fp8x4_f32(f + 4, sc);
+            } else {
+                const uint32_t lim = e4m3_limit(bad ? 127 : X);
+                c0 = fp8x4_bf16(v[i][0].x, v[i][0].y, sc, lim);
+                c1 = fp8x4_bf16(v[i][0].z, v[i][0].w, sc, lim);
+            }
+            *reinterpret_cast<uint2*>(codes + at) = bad ? make_uint2(0u, 0u) : make_uint2(c0, c1);
+        }
+        if ((l16 & 3) == 0) srow[(int64_t)(s0 + i) * N * 4 + (l16 >> 2)] = (uint8_t)X;
+    }
+}
+
+// Back: value(code) * 2^(X - 127), exact in float32, then rounded once to the
+// dense type (a code has at most four significant bits, so bf16 rounds only
+// below its smallest subnormal; past the type's range an infinity).  X = 255
+// and the E4M3 NaN code give NaN.
+template <int FMT, bool F32>
+__global__ void __launch_bounds__(256)
+mxq_dequantize(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t stride, int64_t rows, int N,
+               int K, void* __restrict__ dst) {
+    const int l16 = threadIdx.x & 15;
+    const int64_t row = (int64_t)blockIdx.x * QR + (threadIdx.x >> 4);
+    if (row >= rows) return;
+    const int steps = K / kMxStep, s0 = blockIdx.y * QS;
+    const int64_t m = row / N, n = row - m * N;
+    const uint8_t* srow = scales + (m * steps * N + n) * 4 + (l16 >> 2);
+    uint32_t q[QS][FMT == kMxFp4 ? 1 : 2];
+    int X[QS];
+#pragma unroll
+    for (int i = 0; i < QS; ++i) {
+        const int st = min(s0 + i, steps - 1);
+        const int64_t at = row * K + (int64_t)st * kMxStep + 8 * l16;
+        if constexpr (FMT == kMxFp4) {
+            q[i][0] = *reinterpret_cast<const uint32_t*>(codes + (at >> 1));
+        } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(codes + at);
+            q[i][0] = w.x;
+            q[i][1] = w.y;
+        }
+        X[i] = srow[(int64_t)st * N * 4];
+    }
+#pragma unroll
+    for (int i = 0; i < QS; ++i) {
+        if (s0 + i >= steps) break;
+        const float sc = X[i] == 255 ? __uint_as_float(0x7FC00000u) : e8m0_f32(X[i]);
+        float f[8];
+        if constexpr (FMT == kMxFp4) {
+            const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i][0], 1.0f, 0);
+            const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i][0], 1.0f, 1);
+            const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i][0], 1.0f, 2);
+            const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i][0], 1.0f, 3);
+            f[0] = a.x * sc; f[1] = a.y * sc; f[2] = b.x * sc; f[3] = b.y * sc;
+            f[4] = c.x * sc; f[5] = c.y * sc; f[6] = d.x * sc; f[7] = d.y * sc;
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q[i][h], 1.0f, false);
+                const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q[i][h], 1.0f, true);
+                f[4 * h] = a.x * sc; f[4 * h + 1] = a.y * sc; f[4 * h + 2] = b.x * sc; f[4 * h + 3] = b.y * sc;
+            }
+        }
+        const int64_t at = row * stride + (int64_t)(s0 + i) * kMxStep + 8 * l16;
+        if constexpr (F32) {
+            float4* o = reinterpret_cast<float4*>(static_cast<float*>(dst) + at);
+            o[0] = make_float4(f[0], f[1], f[2], f[3]);
+            o[1] = make_float4(f[4], f[5], f[6], f[7]);
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const f32x2 v = {f[2 * j], f[2 * j + 1]};
+                w[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+            }
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+namespace {
+dim3 quant_grid(const MxRows& r) {
+    return dim3((unsigned)((r.rows + QR - 1) / QR), (unsigned)((r.K / kMxStep + QS - 1) / QS));
+}
+}  // namespace
+
+hipError_t launch_mx_quantize(const MxRows& r, const void* src, uint8_t* codes, uint8_t* scales, hipStream_t s) {
+    const dim3 g = quant_grid(r);
+    prof_begin(s);
+    if (r.fmt == kMxFp4) {
+        if (r.f32) mxq_quantize<kMxFp4, true><<<g, 256, 0, s>>>(src, r.stride, r.rows, r.N, r.K, codes, scales);
+        else mxq_quantize<kMxFp4, false><<<g, 256, 0, s>>>(src, r.stride, r.rows, r.N, r.K, codes, scales);
+    } else {
+        if (r.f32) mxq_quantize<kMxFp8, true><<<g, 256, 0, s>>>(src, r.stride, r.rows, r.N, r.K, codes, scales);
+        else mxq_quantize<kMxFp8, false><<<g, 256, 0, s>>>(src, r.stride, r.rows, r.N, r.K, codes, scales);
+    }
+    prof_end(s, "mxq_quantize");
+    return hipGetLastError();
+}
+
+hipError_t launch_mx_dequantize(const MxRows& r, const uint8_t* codes, const uint8_t* scales, void* dst, hipStream_t s) {
+    const dim3 g = quant_grid(r);
+    prof_begin(s);
+    if (r.fmt == kMxFp4) {
+        if (r.f32) mxq_dequantize<kMxFp4, true><<<g, 256, 0, s>>>(codes, scales, r.stride, r.rows, r.N, r.K, dst);
+        else mxq_dequantize<kMxFp4, false><<<g, 256, 0, s>>>(codes, scales, r.stride, r.rows, r.N, r.K, dst);
+    } else {
+        if (r.f32) mxq_dequantize<kMxFp8, true><<<g, 256, 0, s>>>(codes, scales, r.stride, r.rows, r.N, r.K, dst);
+        else mxq_dequantize<kMxFp8, false><<<g, 256, 0, s>>>(codes, scales, r.stride, r.rows, r.N, r.K, dst);
+    }
+    prof_end(s, "mxq_dequantize");
+    return hipGetLastError();
+}
+
+}  // namespace em
