@@ -313,6 +313,48 @@ int edge_moe_mx_quantize(int32_t M, int32_t N, int32_t K, int32_t format, int32_
 int edge_moe_mx_dequantize(int32_t M, int32_t N, int32_t K, int32_t format, int32_t dst_type, const uint8_t* codes,
                            const uint8_t* scales, void* dst, int64_t dst_stride, void* stream);
 
+/* Product of bf16 rows with MXFP4 matrices, dense or grouped over a routed
+ * batch's experts:
+ *   y[r] = bf16( sum_k Q(x[src(r)])[k] * W_m[k] ),   r = 0..R-1
+ * Q rounds an x row to MXFP8 or MXFP4 along K (x_format; the rule of
+ * edge_moe_mx_quantize), W_m is matrix m's stored value, exactly, and m the
+ * matrix whose rows offsets[m] .. offsets[m + 1] - 1 hold r. */
+typedef struct edge_moe_mx_dims {
+    int32_t T;          /* rows of x, 1..2^20                            */
+    int32_t R;          /* rows of y, 0..2^25                            */
+    int32_t M;          /* matrices, 1..1024                             */
+    int32_t N;          /* rows of a matrix = columns of y, 1..32768     */
+    int32_t K;          /* a multiple of 128, up to 32768                */
+    int32_t x_format;   /* EDGE_MOE_MX_FP8 or EDGE_MOE_MX_FP4            */
+} edge_moe_mx_dims;
+
+/* Workspace bytes of edge_moe_mx_product (0 for dims it does not take). */
+size_t edge_moe_mx_product_ws_bytes(const edge_moe_mx_dims* dims);
+
+/*   x        T rows of K bf16, x_stride elements apart (x_stride >= K, a
+ *            multiple of 8; 16-byte aligned)
+ *   row_src  int32[R]: the x row of each y row (any number of y rows may share
+ *            one), or NULL: y row r reads x row r (R <= T).  An entry outside
+ *            0..T-1 gives a row of zeros.
+ *   offsets  int32[M + 1], ascending: rows of matrix m (empty ones allowed), e.g.
+ *            the expert_offsets of edge_moe_trace, with its row_token as
+ *            row_src; NULL with M = 1: all R rows.  y rows before offsets[0] and
+ *            from offsets[M] on are left as they were.  Values are clamped to
+ *            0..R; descending ones leave rows unwritten or take them twice, but
+ *            never write outside y.
+ *   codes, scales  the matrices as edge_moe_mx_quantize writes them (FP4);
+ *            16- and 4-byte aligned
+ *   y        R rows of N bf16, y_stride elements apart (y_stride >= N); only N
+ *            elements of a row are written
+ *   ws       256-byte aligned, at least edge_moe_mx_product_ws_bytes(dims)
+ * The matrix cores sum the 128 products of one instruction to about 2^-13.5 of
+ * their magnitude sum and the instructions' sums in float32; y is rounded once to
+ * bf16.  A NaN or infinity in an x block, and X = 255 in W, give NaN in the sums
+ * they enter.  Runs of one call on the same inputs are bitwise equal. */
+int edge_moe_mx_product(const edge_moe_mx_dims* dims, const uint16_t* x, int64_t x_stride, const int32_t* row_src,
+                        const int32_t* offsets, const uint8_t* codes, const uint8_t* scales, uint16_t* y,
+                        int64_t y_stride, void* ws, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------ expert streaming from host --
  * The pages keep the expert library in host memory and bring the experts a
  * batch routes to into a small GPU memory, evicting the least recently used,

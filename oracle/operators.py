@@ -60,3 +60,22 @@ def by_step(x: np.ndarray) -> np.ndarray:
     """E8M0 bytes [M, N, K/32] -> the stored [M, K/128, N, 4]."""
     M, N, nb = x.shape
     return np.ascontiguousarray(x.reshape(M, N, nb // 4, 4).transpose(0, 2, 1, 3))
+
+
+def product(x: np.ndarray, fmt: int, W: np.ndarray, offsets=None, row_src=None, R=None):
+    """Rows of x [T][K] rounded to fmt, times the matrices W [M][N][K] (float64
+    values).  Returns (y [R][N], the magnitude sums of its products [R][N]);
+    rows of no matrix are NaN."""
+    q = rounded(x, fmt)
+    R = (len(x) if row_src is None else len(row_src)) if R is None else R
+    src = np.arange(R) if row_src is None else np.asarray(row_src)
+    rows = np.where(((src >= 0) & (src < len(x)))[:, None], q[np.clip(src, 0, len(x) - 1)], 0.0)
+    off = np.array([0, R]) if offsets is None else np.asarray(offsets)
+    y = np.full((R, W.shape[1]), np.nan)
+    mag = np.full((R, W.shape[1]), np.nan)
+    for m in range(len(off) - 1):
+        s = slice(off[m], off[m + 1])
+        if off[m + 1] > off[m]:
+            y[s] = rows[s] @ W[m].T
+            mag[s] = np.abs(rows[s]) @ np.abs(W[m]).T
+    return y, mag

@@ -33,7 +33,7 @@ EXPORTED = ("edge_moe_workspace_bytes", "edge_moe_route", "edge_moe_forward",
             "edge_moe_workspace_bytes_mx", "edge_moe_forward_mx", "edge_moe_prefetch_ws_bytes",
             "edge_moe_prefetch", "edge_moe_cache_create", "edge_moe_cache_destroy", "edge_moe_cache_map",
             "edge_moe_cache_prefetch", "edge_moe_cache_totals", "edge_moe_cache_slot_of",
-            "edge_moe_mx_quantize", "edge_moe_mx_dequantize")
+            "edge_moe_mx_quantize", "edge_moe_mx_dequantize", "edge_moe_mx_product_ws_bytes", "edge_moe_mx_product")
 
 # element formats and dense types of the MX matrix operators
 MX_FP4, MX_FP8 = 0, 1
@@ -91,6 +91,10 @@ class CCacheStats(ctypes.Structure):
 class CTrace(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("expert_offsets", "row_token", "row_slot", "act", "expert_out")]
+
+
+class CMxDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "R", "M", "N", "K", "x_format")]
 
 
 class EdgeMoeError(RuntimeError):
@@ -160,6 +164,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.edge_moe_mx_quantize.restype = i32
     lib.edge_moe_mx_dequantize.argtypes = [i32, i32, i32, i32, i32, vp, vp, vp, i64, vp]
     lib.edge_moe_mx_dequantize.restype = i32
+    lib.edge_moe_mx_product_ws_bytes.argtypes = [ctypes.POINTER(CMxDims)]
+    lib.edge_moe_mx_product_ws_bytes.restype = sz
+    lib.edge_moe_mx_product.argtypes = [ctypes.POINTER(CMxDims), vp, i64, vp, vp, vp, vp, vp, i64, vp, sz, vp]
+    lib.edge_moe_mx_product.restype = i32
     lib.edge_moe_residual.argtypes = [ctypes.c_int32, ctypes.c_int32, vp, vp, vp, vp]
     lib.edge_moe_residual.restype = i32
     lib.edge_moe_copy.argtypes = [vp, vp, sz, vp]
@@ -420,6 +428,32 @@ def edge_moe_mx_dequantize(fmt, codes, scales, dst, stream=None) -> None:
                                        _row_stride(dst), _stream(stream))
     if st != EDGE_MOE_OK:
         raise EdgeMoeError("edge_moe_mx_dequantize", st)
+
+
+def edge_moe_mx_product_ws_bytes(T, R, M, N, K, x_format) -> int:
+    return int(load().edge_moe_mx_product_ws_bytes(ctypes.byref(CMxDims(T, R, M, N, K, x_format))))
+
+
+def edge_moe_mx_product(x_format, x, codes, scales, y, ws, offsets=None, row_src=None, stream=None) -> None:
+    """y [R][N] (bf16) = the rows of x [T][K] (bf16), rounded to x_format, times
+    MXFP4 matrices codes [M][N][K/2], scales [M][K/128][N][4] (or one matrix
+    without the leading dimension).  offsets int32 [M + 1]: the y rows of each
+    matrix; row_src int32 [R]: the x row of each y row."""
+    if x.dim() != 2 or y.dim() != 2 or _dense_type(x) != _BF16 or _dense_type(y) != _BF16:
+        raise ValueError("x and y must be bfloat16 (or int16 bits) [rows][columns]")
+    (T, K), (R, N) = x.shape, y.shape
+    M = 1 if codes.dim() == 2 else codes.shape[0]
+    _uint8(codes, M * N * (K // 2), "codes")
+    _uint8(scales, M * N * (K // 32), "scales")
+    for t, n, what in ((offsets, M + 1, "offsets"), (row_src, R, "row_src")):
+        if t is not None and (str(t.dtype) != "torch.int32" or t.numel() != n):
+            raise ValueError(f"{what}: expected {n} int32 values, got {t.numel()} of {t.dtype}")
+    _same_device(x, codes, scales, y, ws, offsets, row_src)
+    st = load().edge_moe_mx_product(ctypes.byref(CMxDims(T, R, M, N, K, x_format)), x.data_ptr(), _row_stride(x),
+                                    _ptr(row_src), _ptr(offsets), _ptr(codes), _ptr(scales), y.data_ptr(),
+                                    max(_row_stride(y), N), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
+    if st != EDGE_MOE_OK:
+        raise EdgeMoeError("edge_moe_mx_product", st)
 
 
 def mx_weights(dense: dict, stream=None) -> dict:

@@ -25,4 +25,23 @@ struct MxRows {
 hipError_t launch_mx_quantize(const MxRows& r, const void* src, uint8_t* codes, uint8_t* scales, hipStream_t s);
 hipError_t launch_mx_dequantize(const MxRows& r, const uint8_t* codes, const uint8_t* scales, void* dst, hipStream_t s);
 
+
+// ---- MX product (mx_product.hip)
+struct MxProduct {
+    int T, R, M, N, K, fmt;
+    const uint16_t* x;          // [T] rows of K bf16, x_stride elements apart
+    int64_t x_stride;
+    const int32_t* row_src;     // [R] x row of each y row, or null (row r reads x row r)
+    const int32_t* offsets;     // [M + 1] first y row of each matrix, or null (M = 1)
+    const uint8_t* codes;       // [M][N][K/2] E2M1
+    const uint8_t* scales;      // [M][K/128][N][4] E8M0
+    uint16_t* y;                // [R] rows of N bf16, y_stride elements apart
+    int64_t y_stride;
+    int vec;                    // y rows take 8-byte stores at every fourth column
+    uint8_t* xq;                // workspace: x's codes [T][K] or [T][K/2] ...
+    uint8_t* xs;                // ... and scales [K/128][T][4]
+};
+size_t mx_product_ws_bytes(const MxProduct& a);
+hipError_t launch_mx_product(MxProduct a, void* ws, hipStream_t s);
+
 }  // namespace em

@@ -177,3 +177,171 @@ def test_weights_of_the_layer():
         em.edge_moe_forward_mx(D, x, idx, w, weights, y, ws)
         ys.append(y)
     assert torch.equal(*ys)
+
+
+# ------------------------------------------------------------------ the product ---
+
+def matrices(M, N, K, seed):
+    """Random MXFP4 matrices, weights near N(0, 0.02^2): device codes and scales, float64 values."""
+    rng = np.random.default_rng(seed)
+    codes = rng.integers(0, 16, (M, N, K), dtype=np.uint8)
+    x = rng.integers(118, 122, (M, N, K // 32), dtype=np.uint8)
+    return (torch.from_numpy(ops.pack(codes, ops.FP4)).to(DEV), torch.from_numpy(ops.by_step(x)).to(DEV),
+            ops.values(codes, x, ops.FP4))
+
+
+def rows_of(T, K, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(T, K, generator=g).to(torch.bfloat16)
+
+
+def within(y, ref, mag, K):
+    """|dy| <= 2^-8 |y| (one rounding to bf16) + 2^-13 times the products'
+    magnitude sum (an instruction's sum of 128 products is good to about 2^-13.5
+    of theirs) + K / 128 float32 additions of partial sums no larger than it."""
+    got = y.float().cpu().numpy().astype(np.float64)
+    tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -13 + K / 128 * 2.0 ** -24) * (1 + 2.0 ** -8) * mag + 2.0 ** -133
+    live = np.isfinite(ref)
+    worst = float(np.max(np.abs(got - ref)[live] / tol[live], initial=0.0))
+    say(f"  worst |dy| / tolerance = {worst:.3g}")
+    assert np.isfinite(got[live]).all() and worst <= 1.0
+
+
+def product(fmt, x, codes, scales, y, offsets=None, row_src=None, stream=None):
+    (T, K), (R, N) = x.shape, y.shape
+    ws = torch.empty(em.edge_moe_mx_product_ws_bytes(T, R, codes.shape[0], N, K, fmt), dtype=torch.uint8, device=DEV)
+    em.edge_moe_mx_product(fmt, x, codes, scales, y, ws, offsets=offsets, row_src=row_src, stream=stream)
+    return ws
+
+
+def i32(v):
+    return torch.tensor(np.asarray(v), dtype=torch.int32, device=DEV)
+
+
+@fmt_of
+@pytest.mark.parametrize("T,N,K", [(1, 16, 128), (1, 2048, 4096), (2, 1, 256), (3, 37, 384), (16, 64, 640),
+                                   (17, 100, 512), (33, 50, 1024), (64, 96, 128), (65, 257, 256), (127, 33, 384),
+                                   (191, 512, 512), (192, 256, 128), (257, 300, 1152), (700, 1030, 256)])
+def test_product_dense(fmt, T, N, K):
+    say(f"case: product {T} x {N} x {K}")
+    q, e, W = matrices(1, N, K, T + N)
+    x = rows_of(T, K, T)
+    y = torch.full((T, N), float("nan"), dtype=torch.bfloat16, device=DEV)
+    product(fmt, x.to(DEV), q, e, y)
+    within(y, *ops.product(x.double().numpy(), fmt, W), K)
+
+
+@fmt_of
+@pytest.mark.parametrize("sizes,T", [([5], 5), ([0, 7, 0, 0, 20, 1, 0], 28), ([0, 0, 0], 4), ([90, 0, 300, 10, 0], 400),
+                                     ([500, 3, 0, 260], 763), ("many", 130), ("many routed", 40)])
+def test_product_grouped(fmt, sizes, T):
+    """Ragged groups, empty ones among them, up to hundreds of matrices; rows
+    before the first and behind the last group keep what they held."""
+    rng = np.random.default_rng(9)
+    N, K = 72, 256
+    src = None
+    if sizes == "many":
+        sizes = np.bincount(rng.integers(0, 200, 130), minlength=200)
+    elif sizes == "many routed":
+        sizes = np.bincount(rng.choice(512, 400), minlength=512)
+        src = rng.integers(0, T, 400)
+    n = int(np.sum(sizes))
+    head, tail = (0, 0) if src is not None else (2, 3)
+    R = head + n + tail
+    off = head + np.concatenate([[0], np.cumsum(sizes)])
+    q, e, W = matrices(len(sizes), N, K, 4)
+    x = rows_of(max(T, R) if src is None else T, K, 6)
+    y = torch.full((R, N), 3.25, dtype=torch.bfloat16, device=DEV)
+    say(f"case: {len(sizes)} groups, {R} rows")
+    product(fmt, x.to(DEV), q, e, y, offsets=i32(off), row_src=None if src is None else i32(src))
+    ref, mag = ops.product(x.double().numpy(), fmt, W, off, src, R)
+    within(y, ref, mag, K)
+    assert bool((y[:head] == 3.25).all()) and bool((y[head + n:] == 3.25).all())
+
+
+@fmt_of
+@pytest.mark.parametrize("R,T", [(40, 7), (500, 60)])
+def test_product_gathered_rows(fmt, R, T):
+    """Shared x rows, and entries that name no row: zeros."""
+    rng = np.random.default_rng(2)
+    src = rng.integers(0, T, R)
+    src[[0, 5, R - 1]] = [-1, T, 2 ** 31 - 1]
+    q, e, W = matrices(2, 48, 384, 1)
+    off = [0, R // 3, R]
+    x = rows_of(T, 384, 3)
+    y = torch.full((R, 48), float("nan"), dtype=torch.bfloat16, device=DEV)
+    product(fmt, x.to(DEV), q, e, y, offsets=i32(off), row_src=i32(src))
+    within(y, *ops.product(x.double().numpy(), fmt, W, off, src), 384)
+    assert bool((y[[0, 5, R - 1]] == 0).all())
+
+
+@fmt_of
+@pytest.mark.parametrize("T", [5, 90, 230])
+def test_product_strided_rows(fmt, T):
+    q, e, W = matrices(1, 44, 256, 8)
+    x = rows_of(T, 512, 1)
+    y = torch.full((T, 100), 2.5, dtype=torch.bfloat16, device=DEV)
+    for shift in (8, 5):                          # aligned and odd columns of a wider buffer
+        out = y[:, shift:shift + 44]
+        product(fmt, x.to(DEV)[:, 128:384], q, e, out)
+        within(out, *ops.product(x[:, 128:384].double().numpy(), fmt, W), 256)
+        assert bool((y[:, :shift] == 2.5).all()) and bool((y[:, shift + 44:] == 2.5).all())
+        y.fill_(2.5)
+
+
+@fmt_of
+@pytest.mark.parametrize("T", [4, 100, 300])
+def test_product_non_finite(fmt, T):
+    """NaN and infinities of x and NaN scales of W stay in the rows and columns they enter."""
+    q, e, W = matrices(1, 40, 256, 2)
+    e[0, 1, 7, 2] = 255                           # row 7 of W, block 6
+    x = rows_of(T, 256, 4)
+    x[1, 200] = float("nan")
+    x[3, 0] = float("-inf")
+    y = torch.zeros(T, 40, dtype=torch.bfloat16, device=DEV)
+    product(fmt, x.to(DEV), q, e, y)
+    bad = torch.zeros(T, 40, dtype=torch.bool)
+    bad[[1, 3]] = True
+    bad[:, 7] = True
+    assert torch.equal(torch.isnan(y).cpu(), bad)
+    ref, mag = ops.product(np.nan_to_num(x.double().numpy(), nan=0.0, posinf=0.0, neginf=0.0), fmt, W)
+    ref[bad.numpy()] = np.nan
+    within(y, ref, mag, 256)
+
+
+@fmt_of
+@pytest.mark.parametrize("off", [[0, 30, 10, 40], [-5, 20, 90, 40], [40, 0, 0, 40], [7, 7, 7, 7]])
+@pytest.mark.parametrize("R", [40, 500])
+def test_product_bad_offsets_stay_inside(fmt, off, R):
+    """Descending or out-of-range offsets: nothing outside y's rows is written."""
+    q, e, _ = matrices(3, 32, 128, 2)
+    off = [o * R // 40 for o in off]
+    buf = torch.full((R + 64, 32), 1.5, dtype=torch.bfloat16, device=DEV)
+    product(fmt, rows_of(R, 128, 4).to(DEV), q, e, buf[32:32 + R], offsets=i32(off))
+    assert bool((buf[:32] == 1.5).all()) and bool((buf[32 + R:] == 1.5).all())
+
+
+@pytest.mark.parametrize("T", [3, 70, 260])
+def test_product_repeats_streams_and_graphs(T):
+    """Bitwise the same again, on another stream, and in every replay of a
+    captured graph with eager work on the workspace's memory between replays."""
+    q, e, W = matrices(1, 300, 512, 5)
+    x = rows_of(T, 512, 7).to(DEV)
+    y0, y1 = (torch.zeros(T, 300, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    product(em.MX_FP8, x, q, e, y0)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    ws = product(em.MX_FP8, x, q, e, y1, stream=s)
+    s.synchronize()
+    assert torch.equal(y0, y1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        em.edge_moe_mx_product(em.MX_FP8, x, q, e, y1, ws)
+    for i in range(4):
+        x.copy_(rows_of(T, 512, 20 + i))
+        y1.fill_(9)
+        ws.fill_(i)
+        graph.replay()
+        torch.cuda.synchronize()
+        product(em.MX_FP8, x, q, e, y0)
+        assert torch.equal(y0, y1), f"replay {i}"

@@ -91,3 +91,40 @@ def test_binding_checks_shapes_types_and_devices():
             em._row_stride(t)
     with pytest.raises(ValueError):
         em._dense_type(src.half())
+
+
+def test_product_validation_before_any_device_call():
+    lib = em.load()
+    ok = dict(T=8, R=8, M=1, N=64, K=256, fmt=em.MX_FP8, x=BASE, xs=256, src=None, off=None, q=BASE, e=BASE, y=BASE,
+              ys=64, ws=BASE, nb=1 << 30)
+
+    def call(**kw):
+        a = {**ok, **kw}
+        d = em.CMxDims(a["T"], a["R"], a["M"], a["N"], a["K"], a["fmt"])
+        return lib.edge_moe_mx_product(ctypes.byref(d), a["x"], a["xs"], a["src"], a["off"], a["q"], a["e"], a["y"],
+                                       a["ys"], a["ws"], a["nb"], None)
+    for bad in (dict(T=0), dict(R=-1), dict(M=0), dict(N=0), dict(K=0), dict(fmt=2), dict(x=None), dict(x=BASE + 8),
+                dict(xs=248), dict(xs=260), dict(src=BASE + 2), dict(off=BASE + 1), dict(q=None), dict(q=BASE + 8),
+                dict(e=BASE + 2), dict(y=None), dict(y=BASE + 1), dict(ys=63), dict(M=2), dict(R=9), dict(ws=BASE + 16)):
+        assert call(**bad) == em.EDGE_MOE_EINVAL, bad
+    for bad in (dict(K=192, xs=192), dict(T=(1 << 20) + 1), dict(R=(1 << 25) + 1, src=BASE), dict(M=1025, off=BASE),
+                dict(N=32769, ys=32769), dict(K=32896, xs=32896)):
+        assert call(**bad) == em.EDGE_MOE_EUNSUPPORTED, bad
+    assert call(ws=None) == em.EDGE_MOE_EWORKSPACE
+    need = em.edge_moe_mx_product_ws_bytes(8, 8, 1, 64, 256, em.MX_FP8)
+    assert need >= 8 * (256 + 8) and call(nb=need - 1) == em.EDGE_MOE_EWORKSPACE
+    assert lib.edge_moe_mx_product(None, BASE, 256, None, None, BASE, BASE, BASE, 64, BASE, 1 << 30, None) == em.EDGE_MOE_EINVAL
+    assert em.edge_moe_mx_product_ws_bytes(8, 8, 1, 64, 200, em.MX_FP8) == 0
+
+
+def test_product_binding_checks():
+    x, y = torch.zeros(4, 256, dtype=torch.bfloat16), torch.zeros(4, 64, dtype=torch.bfloat16)
+    q, e = torch.zeros(1, 64, 128, dtype=torch.uint8), torch.zeros(1, 2, 64, 4, dtype=torch.uint8)
+    ws = torch.zeros(4096, dtype=torch.uint8)
+    ok = dict(x=x, codes=q, scales=e, y=y)
+    for bad in (dict(x=x.float()), dict(x=x[0]), dict(codes=q[..., :64]), dict(scales=e[..., :2]), dict(y=y.float()),
+                dict(y=y[:, :32]), dict(offsets=torch.zeros(3, dtype=torch.int32)), dict(offsets=torch.zeros(2)),
+                dict(row_src=torch.zeros(5, dtype=torch.int32)), dict(row_src=torch.zeros(4, dtype=torch.int64)), {}):
+        a = {**ok, **bad}
+        with pytest.raises((ValueError, RuntimeError, AssertionError)):     # the last: host tensors
+            em.edge_moe_mx_product(em.MX_FP8, a.pop("x"), a.pop("codes"), a.pop("scales"), a.pop("y"), ws, **a)
