@@ -282,6 +282,67 @@ int edge_moe_forward_mx(const edge_moe_dims* dims, const uint16_t* x, const int3
                         const float* topk_w, const edge_moe_weights_mx* weights, float* y, void* ws,
                         size_t ws_bytes, void* stream, const edge_moe_trace* trace);
 
+/* ---------------------------------------------------- training the router ----
+ * Load of the router over a batch, its balance and z losses, and the router's
+ * backward pass.  p_t = softmax of token t's logits over all E experts, lse_t =
+ * log sum exp of them.  The tokens form n_seq sequences: sequence s holds tokens
+ * seq_offsets[s] .. seq_offsets[s + 1] - 1 (device int32[n_seq + 1], ascending;
+ * NULL with n_seq = 1: all T tokens); tokens before the first and from
+ * seq_offsets[n_seq] on (padding) enter nothing.  Values are clamped to 0..T;
+ * descending ones give unspecified results inside the outputs.  n_seq up to 4095.
+ *
+ *   counts  [n_seq][E] int32 out: c_se, the picks (t, j) in sequence s with
+ *           topk_idx = e; entries outside 0..E-1 (dropped slots) are not counted
+ *   probs   [n_seq][E] float32 out: P_se, the mean of p_te over the sequence
+ *   loss    [2] float32 out: the balance loss, the mean over the sequences that
+ *           have tokens of sum_e f_se P_se with f_se = E c_se / (k n_s) (1 for an
+ *           even load), and the z loss, the mean of lse_t^2 over their tokens
+ * An empty sequence has zero counts and probabilities; no token at all: losses 0.
+ * A logit of -infinity is an expert of probability 0; a token whose logits are all
+ * -infinity has no distribution and adds zeros.  NaN and +infinity give NaN.
+ * logits: [T][E] as edge_moe_route writes logits_out.  Of dims, T, n_experts and
+ * top_k are used (all must pass the layer's checks).  Sums over tokens are kept in
+ * float64 past 32 tokens; results are bitwise reproducible. */
+size_t edge_moe_balance_ws_bytes(const edge_moe_dims* dims, int32_t n_seq);
+int edge_moe_balance(const edge_moe_dims* dims, const float* logits, const int32_t* topk_idx,
+                     const int32_t* seq_offsets, int32_t n_seq, int32_t* counts, float* probs, float* loss, void* ws,
+                     size_t ws_bytes, void* stream);
+
+/* Backward pass of edge_moe_route and edge_moe_balance:
+ *   dz_te =  sum_{j: topk_idx_tj = e} w_tj (dw_tj - sum_i w_ti dw_ti)
+ *          + d_loss[0] / (S' n_s) p_te (f_se - sum_i p_ti f_si)
+ *          + d_loss[1] 2 / n lse_t p_te
+ * (S' sequences with tokens, n tokens in them; the counts are constants, as the
+ * selection is), and from it
+ *   dx = dz W_r,   dW_r = dz^T x,   dbias = sum_t dz_t
+ * A host struct of device pointers; each output may be NULL and is then not
+ * computed.  d_topk_w or d_loss (or both) must be given. */
+typedef struct edge_moe_route_grad {
+    const float*    logits;       /* [T][E] (with the bias, as routed)                     */
+    const int32_t*  topk_idx;     /* [T][k], with d_topk_w; entries outside 0..E-1 skipped */
+    const float*    topk_w;       /* [T][k], with d_topk_w                                 */
+    const float*    d_topk_w;     /* [T][k] gradient at the selection weights, or NULL     */
+    const float*    d_loss;       /* [2] gradient at the losses, or NULL                   */
+    const int32_t*  counts;       /* [n_seq][E] from edge_moe_balance, with d_loss         */
+    const int32_t*  seq_offsets;  /* as given to edge_moe_balance, with d_loss             */
+    int32_t         n_seq;
+    const uint16_t* x;            /* [T][d] bf16, 16-byte aligned, with dw_router          */
+    const uint16_t* w_router;     /* [E][d] bf16, 16-byte aligned, with dx                 */
+    float*          dlogits;      /* [T][E] float32 out or NULL                            */
+    float*          dx;           /* [T][d] float32 out or NULL, 16-byte aligned           */
+    float*          dw_router;    /* [E][d] float32 out or NULL, 16-byte aligned           */
+    float*          dbias;        /* [E] float32 out or NULL                               */
+} edge_moe_route_grad;
+
+/* Workspace bytes of edge_moe_route_backward (0 for invalid dims). */
+size_t edge_moe_route_backward_ws_bytes(const edge_moe_dims* dims);
+
+/* dz is kept to all 24 bits of its float32 (the sum of three bf16 terms), x and
+ * W_r enter exactly and the sums are float32; bitwise reproducible.  An infinite
+ * or NaN dz, x or W_r gives unspecified values in the sums it enters. */
+int edge_moe_route_backward(const edge_moe_dims* dims, const edge_moe_route_grad* grad, void* ws, size_t ws_bytes,
+                            void* stream);
+
 /* ------------------------------------------------------- MX matrix operators --
  * Element formats and dense element types of the calls below. */
 #define EDGE_MOE_MX_FP4 0   /* E2M1, two codes per byte, block exponent emax = 2 */

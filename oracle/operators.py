@@ -79,3 +79,71 @@ def product(x: np.ndarray, fmt: int, W: np.ndarray, offsets=None, row_src=None, 
             y[s] = rows[s] @ W[m].T
             mag[s] = np.abs(rows[s]) @ np.abs(W[m]).T
     return y, mag
+
+
+# ------------------------------------------------------------------ the router ----
+
+def _softmax(z):
+    """Rows of logits -> (probabilities, log sum exp); a row of -inf alone: zeros."""
+    m = z.max(1, keepdims=True)
+    b = np.where(np.isneginf(m), 0.0, m)
+    e = np.exp(z - b)
+    n = e.sum(1, keepdims=True)
+    none = n == 0
+    return np.where(none, 0.0, e / np.where(none, 1, n)), np.where(none, 0.0, b + np.log(np.where(none, 1, n)))[:, 0]
+
+
+def _seqs(T, offsets):
+    off = [0, T] if offsets is None else [int(v) for v in offsets]
+    return list(zip(off[:-1], off[1:]))
+
+
+def balance(logits, topk_idx, offsets=None):
+    """(counts [S][E], mean probabilities [S][E], [balance loss, z loss])."""
+    z = np.asarray(logits, dtype=np.float64)
+    (T, E), k = z.shape, topk_idx.shape[1]
+    p, lse = _softmax(z)
+    seqs = _seqs(T, offsets)
+    counts = np.zeros((len(seqs), E), dtype=np.int64)
+    probs = np.zeros((len(seqs), E))
+    per_seq, z2 = [], []
+    for s, (lo, hi) in enumerate(seqs):
+        if hi <= lo:
+            continue
+        ids = topk_idx[lo:hi].reshape(-1)
+        counts[s] = np.bincount(ids[(ids >= 0) & (ids < E)], minlength=E)
+        probs[s] = p[lo:hi].mean(0)
+        per_seq.append(float(E / (k * (hi - lo)) * counts[s] @ probs[s]))
+        z2.extend(lse[lo:hi] ** 2)
+    return counts, probs, np.array([np.mean(per_seq) if per_seq else 0.0, np.mean(z2) if z2 else 0.0])
+
+
+def route_backward(logits, topk_idx, topk_w=None, d_topk_w=None, d_loss=None, counts=None, offsets=None):
+    """(dz [T][E], the magnitudes of the terms it is summed from [T][E])."""
+    z = np.asarray(logits, dtype=np.float64)
+    T, E = z.shape
+    k = topk_idx.shape[1]
+    dz, mag = np.zeros((T, E)), np.zeros((T, E))
+    if d_topk_w is not None:
+        w, dw = np.asarray(topk_w, np.float64), np.asarray(d_topk_w, np.float64)
+        v = w * (dw - (w * dw).sum(1, keepdims=True))
+        a = np.abs(w) * (np.abs(dw) + np.abs(w * dw).sum(1, keepdims=True))
+        for j in range(k):
+            t = np.nonzero((topk_idx[:, j] >= 0) & (topk_idx[:, j] < E))[0]
+            np.add.at(dz, (t, topk_idx[t, j]), v[t, j])
+            np.add.at(mag, (t, topk_idx[t, j]), a[t, j])
+    if d_loss is not None:
+        p, lse = _softmax(z)
+        seqs = _seqs(T, offsets)
+        live = sum(hi > lo for lo, hi in seqs)
+        n = sum(max(hi - lo, 0) for lo, hi in seqs)
+        gb, gz = (float(v) for v in d_loss)
+        for s, (lo, hi) in enumerate(seqs):
+            if hi <= lo:
+                continue
+            f = np.asarray(counts[s], np.float64) * E / (k * (hi - lo))
+            q = p[lo:hi]
+            mean = (q @ f)[:, None]
+            dz[lo:hi] += gb / live / (hi - lo) * q * (f - mean) + 2 * gz / n * lse[lo:hi, None] * q
+            mag[lo:hi] += abs(gb) / live / (hi - lo) * q * (f + mean) + 2 * abs(gz) / n * np.abs(lse[lo:hi, None]) * q
+    return dz, mag

@@ -33,7 +33,9 @@ EXPORTED = ("edge_moe_workspace_bytes", "edge_moe_route", "edge_moe_forward",
             "edge_moe_workspace_bytes_mx", "edge_moe_forward_mx", "edge_moe_prefetch_ws_bytes",
             "edge_moe_prefetch", "edge_moe_cache_create", "edge_moe_cache_destroy", "edge_moe_cache_map",
             "edge_moe_cache_prefetch", "edge_moe_cache_totals", "edge_moe_cache_slot_of",
-            "edge_moe_mx_quantize", "edge_moe_mx_dequantize", "edge_moe_mx_product_ws_bytes", "edge_moe_mx_product")
+            "edge_moe_mx_quantize", "edge_moe_mx_dequantize", "edge_moe_mx_product_ws_bytes", "edge_moe_mx_product",
+            "edge_moe_balance_ws_bytes", "edge_moe_balance", "edge_moe_route_backward_ws_bytes",
+            "edge_moe_route_backward")
 
 # element formats and dense types of the MX matrix operators
 MX_FP4, MX_FP8 = 0, 1
@@ -95,6 +97,13 @@ class CTrace(ctypes.Structure):
 
 class CMxDims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "R", "M", "N", "K", "x_format")]
+
+
+class CRouteGrad(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("logits", "topk_idx", "topk_w", "d_topk_w", "d_loss", "counts",
+                                                "seq_offsets")]
+                + [("n_seq", ctypes.c_int32)]
+                + [(n, ctypes.c_void_p) for n in ("x", "w_router", "dlogits", "dx", "dw_router", "dbias")])
 
 
 class EdgeMoeError(RuntimeError):
@@ -168,6 +177,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.edge_moe_mx_product_ws_bytes.restype = sz
     lib.edge_moe_mx_product.argtypes = [ctypes.POINTER(CMxDims), vp, i64, vp, vp, vp, vp, vp, i64, vp, sz, vp]
     lib.edge_moe_mx_product.restype = i32
+    lib.edge_moe_balance_ws_bytes.argtypes = [ctypes.POINTER(CDims), i32]
+    lib.edge_moe_balance_ws_bytes.restype = sz
+    lib.edge_moe_balance.argtypes = [ctypes.POINTER(CDims), vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]
+    lib.edge_moe_balance.restype = i32
+    lib.edge_moe_route_backward_ws_bytes.argtypes = [ctypes.POINTER(CDims)]
+    lib.edge_moe_route_backward_ws_bytes.restype = sz
+    lib.edge_moe_route_backward.argtypes = [ctypes.POINTER(CDims), ctypes.POINTER(CRouteGrad), vp, sz, vp]
+    lib.edge_moe_route_backward.restype = i32
     lib.edge_moe_residual.argtypes = [ctypes.c_int32, ctypes.c_int32, vp, vp, vp, vp]
     lib.edge_moe_residual.restype = i32
     lib.edge_moe_copy.argtypes = [vp, vp, sz, vp]
@@ -347,9 +364,72 @@ def edge_moe_forward_noalloc(dims, x, topk_idx, topk_w, weights, y, stream=None)
         raise EdgeMoeError("edge_moe_forward_noalloc", st)
 
 
-# ------------------------------------------------------------------ MX matrices --
+# ---------------------------------------------- MX matrices, router training ----
 # The calls below check types, shapes and devices of what they are given (their
 # kernels trust the sizes in the arguments), beyond what the library checks.
+
+def _sized(t, dtype: str, count: int, what: str) -> Optional[int]:
+    """Address of a contiguous tensor of `count` values of dtype (None passes)."""
+    if t is None:
+        return None
+    if str(t.dtype) != dtype or t.numel() != count:
+        raise ValueError(f"{what}: expected {count} values of {dtype}, got {t.numel()} of {t.dtype}")
+    return _ptr(t)
+
+
+def _bf16_sized(t, count: int, what: str) -> Optional[int]:
+    if t is not None and (_dense_type(t) != _BF16 or t.numel() != count):
+        raise ValueError(f"{what}: expected {count} bfloat16 values (or int16 bits), got {t.numel()} of {t.dtype}")
+    return _ptr(t)
+
+
+def edge_moe_balance_ws_bytes(dims, n_seq=1) -> int:
+    return int(load().edge_moe_balance_ws_bytes(ctypes.byref(cdims(dims)), int(n_seq)))
+
+
+def edge_moe_balance(dims, logits, topk_idx, counts, probs, loss, ws, seq_offsets=None, stream=None) -> None:
+    """The router's load: counts [S][E] int32, mean probabilities probs [S][E]
+    and loss [2] (balance, z), float32, from logits [T][E] and topk_idx [T][k].
+    seq_offsets int32 [S + 1]: the sequences' tokens (None: one sequence)."""
+    T, E, k = dims.T, dims.n_experts, dims.top_k
+    S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+    f, i = "torch.float32", "torch.int32"
+    _same_device(logits, topk_idx, counts, probs, loss, ws, seq_offsets)
+    st = load().edge_moe_balance(ctypes.byref(cdims(dims)), _sized(logits, f, T * E, "logits"),
+                                 _sized(topk_idx, i, T * k, "topk_idx"), _sized(seq_offsets, i, S + 1, "seq_offsets"),
+                                 S, _sized(counts, i, S * E, "counts"), _sized(probs, f, S * E, "probs"),
+                                 _sized(loss, f, 2, "loss"), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
+    if st != EDGE_MOE_OK:
+        raise EdgeMoeError("edge_moe_balance", st)
+
+
+def edge_moe_route_backward_ws_bytes(dims) -> int:
+    return int(load().edge_moe_route_backward_ws_bytes(ctypes.byref(cdims(dims))))
+
+
+def edge_moe_route_backward(dims, logits, topk_idx, ws, topk_w=None, d_topk_w=None, d_loss=None, counts=None,
+                            seq_offsets=None, x=None, w_router=None, dlogits=None, dx=None, dw_router=None, dbias=None,
+                            stream=None) -> None:
+    """The router's backward pass: from d_topk_w [T][k] and / or d_loss [2] (with
+    edge_moe_balance's counts and seq_offsets) to those of dlogits [T][E], dx
+    [T][d], dw_router [E][d], dbias [E] (float32) that are given.  dx needs
+    w_router, dw_router needs x (bf16)."""
+    T, E, k, d = dims.T, dims.n_experts, dims.top_k, dims.d
+    S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+    f, i = "torch.float32", "torch.int32"
+    _same_device(logits, topk_idx, ws, topk_w, d_topk_w, d_loss, counts, seq_offsets, x, w_router, dlogits, dx,
+                 dw_router, dbias)
+    g = CRouteGrad(_sized(logits, f, T * E, "logits"), _sized(topk_idx, i, T * k, "topk_idx"),
+                   _sized(topk_w, f, T * k, "topk_w"), _sized(d_topk_w, f, T * k, "d_topk_w"),
+                   _sized(d_loss, f, 2, "d_loss"), _sized(counts, i, S * E, "counts"),
+                   _sized(seq_offsets, i, S + 1, "seq_offsets"), S, _bf16_sized(x, T * d, "x"),
+                   _bf16_sized(w_router, E * d, "w_router"), _sized(dlogits, f, T * E, "dlogits"),
+                   _sized(dx, f, T * d, "dx"), _sized(dw_router, f, E * d, "dw_router"), _sized(dbias, f, E, "dbias"))
+    st = load().edge_moe_route_backward(ctypes.byref(cdims(dims)), ctypes.byref(g), _ptr(ws),
+                                        ws.numel() * ws.element_size(), _stream(stream))
+    if st != EDGE_MOE_OK:
+        raise EdgeMoeError("edge_moe_route_backward", st)
+
 
 def _same_device(*tensors) -> None:
     """Every tensor on the current GPU: the library launches there."""

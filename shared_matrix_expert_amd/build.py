@@ -21,7 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libedge_moe.so")
 SOURCES = ["api.hip", "router.hip", "dispatch.hip", "gemm.hip", "decode.hip", "layer.hip",
            "prefill.hip", "calib.hip", "mx.hip", "prefetch.hip", "cache.hip", "mx_quant.hip",
-           "mx_product.hip", "operators.hip"]
+           "mx_product.hip", "router_train.hip", "operators.hip"]
 ARCH = "gfx950"
 
 
@@ -31,7 +31,8 @@ ARCH = "gfx950"
 KERNEL_SOURCES = (("dec_layer", "layer.hip"), ("pl_", "layer.hip"), ("dec_", "decode.hip"),
                   ("router_", "router.hip"), ("perm_", "dispatch.hip"), ("pf_", "prefill.hip"),
                   ("mfma_peak", "calib.hip"), ("mx_", "mx.hip"), ("prefetch_", "prefetch.hip"), ("cache_", "cache.hip"),
-                  ("mxq_", "mx_quant.hip"), ("mxp_", "mx_product.hip"), ("copy_bytes", "gemm.hip"))
+                  ("mxq_", "mx_quant.hip"), ("mxp_", "mx_product.hip"), ("rt_", "router_train.hip"),
+                  ("copy_bytes", "gemm.hip"))
 
 
 def include_closure(src: str, root_csrc: str = CSRC, root_inc: str = os.path.join(ROOT, "include"),

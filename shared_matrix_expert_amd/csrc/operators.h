@@ -44,4 +44,41 @@ struct MxProduct {
 size_t mx_product_ws_bytes(const MxProduct& a);
 hipError_t launch_mx_product(MxProduct a, void* ws, hipStream_t s);
 
+// ---- router load and losses (router_train.hip)
+struct RouterLoad {
+    int T, E, k, S, vec;            // vec: logit rows take 16-byte accesses
+    const float* logits;            // [T][E]
+    const int32_t* topk_idx;        // [T][k]
+    const int32_t* seq_offsets;     // [S + 1] or null (S = 1: every token)
+    int32_t* counts;                // [S][E]
+    float* probs;                   // [S][E]
+    float* loss;                    // [2]
+    // workspace
+    float* part_p; int32_t* part_c; // [chunks + S][E]
+    double* part_z;                 // [chunks + S]
+    double* dots;                   // [S * E / 64][2]
+    uint32_t* done;
+};
+size_t router_load_ws_bytes(const RouterLoad& a);
+hipError_t launch_router_load(RouterLoad a, void* ws, hipStream_t s);
+
+// ---- router backward (router_train.hip)
+struct RouterGrad {
+    int T, E, k, S, d, vec;
+    int Tp, Ep;                     // T and E up to multiples of 32
+    int slices;                     // token slices of dW_r
+    const float* logits; const int32_t* topk_idx; const float* topk_w;
+    const float* d_topk_w;          // [T][k] or null
+    const float* d_loss;            // [2] or null
+    const int32_t* counts; const int32_t* seq_offsets;
+    const uint16_t* x; const uint16_t* w_router;
+    float* dlogits; float* dx; float* dw_router; float* dbias;   // each may be null
+    // workspace
+    uint16_t* planes;               // [3][Tp][Ep] bf16: dz = their sum
+    float* part_w;                  // [slices][E][d]
+    float* part_b;                  // [Tp / 16][E]
+};
+size_t router_grad_ws_bytes(RouterGrad a);
+hipError_t launch_router_grad(RouterGrad a, void* ws, hipStream_t s);
+
 }  // namespace em

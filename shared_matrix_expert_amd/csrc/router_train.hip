@@ -1,0 +1,753 @@
+// Training side of the router: its load and losses (edge_moe_balance) and its
+// backward pass (edge_moe_route_backward).
+//
+// With z the logits of a token, p = softmax(z) over all E experts, lse = log sum
+// exp z, and for each sequence s of n_s tokens c_se = picks of expert e,
+// f_se = E / (k n_s) c_se, P_se = mean of p_te over the sequence:
+//   balance loss  L_b = 1/S' sum over the S' sequences with tokens of sum_e f_se P_se
+//   z loss        L_z = 1/n sum over their n tokens of lse_t^2
+// The counts are constants to the gradient, so with g_b, g_z the losses'
+// gradients and w = softmax over the selected logits:
+//   dz_te =  g_b / (S' n_s) p_te (f_se - sum_i p_ti f_si)  +  2 g_z / n lse_t p_te
+//          + sum_{j: idx_tj = e} w_tj (dw_tj - sum_i w_ti dw_ti)
+//   dx = dz W_r,   dW_r = dz^T x,   dbias = sum_t dz
+//
+// Kernels:
+//   rt_load         softmax rows of a chunk of tokens, column sums and counts
+//   rt_load_reduce  chunks added in order (float64) per sequence; the losses
+//   rt_dlogits      dz by rows, float32 and / or as three bf16 planes
+//   rt_gemm         dx and dW_r on the bf16 matrix cores: dz is the exact sum of
+//                   its planes (hi + mid + lo: 24 bits), x and W_r are bf16, every
+//                   product is exact in float32 and the sums are float32
+//   rt_finish       the token slices of dW_r and the chunks of dbias, in order
+#include "common.h"
+#include "operators.h"
+
+namespace em {
+
+namespace {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int LCH = 32;        // tokens per workgroup of rt_load
+constexpr int DCH = 16;        // tokens per workgroup of rt_dlogits
+
+// ---- wave sums -----------------------------------------------------------------
+EM_DEV float wave_max(float v) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+    return v;
+}
+EM_DEV float wave_sum(float v) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+    return v;
+}
+
+// ---- sequences -----------------------------------------------------------------
+// Tokens [lo(s), hi(s)) of sequence s; offsets outside 0..T or descending are
+// clamped, so that no token outside 0..T-1 is named.
+struct Seqs {
+    const int32_t* off;
+    int S, T;
+    EM_DEV int lo(int s) const { return off ? min(max(off[s], 0), T) : 0; }
+    EM_DEV int hi(int s) const { return off ? min(max(off[s + 1], lo(s)), T) : T; }
+};
+
+// First sequence that can hold token t: the last one that starts at or before
+// it (0 if none does).  64 offsets a step: two rounds of loads up to S = 4095.
+EM_DEV int find_seq(const Seqs& q, int t) {
+    if (!q.off) return 0;
+    const int lane = lane_id();
+    int base = 0;
+    if (q.S >= 64) {
+        const int n = __popcll(__ballot(64 * lane <= q.S && q.off[min(64 * lane, q.S)] <= t));
+        base = 64 * max(n - 1, 0);
+    }
+    const int n = __popcll(__ballot(base + lane <= q.S && q.off[min(base + lane, q.S)] <= t));
+    return min(max(base + n - 1, 0), q.S - 1);
+}
+
+// Sequences with tokens, and their tokens.
+EM_DEV void live_seqs(const Seqs& q, int& live, int& tokens) {
+    if (!q.off) {
+        live = 1;
+        tokens = q.T;
+        return;
+    }
+    int l = 0, n = 0;
+    for (int s = lane_id(); s < q.S; s += 64) {
+        const int c = q.hi(s) - q.lo(s);
+        l += c > 0;
+        n += c;
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) {
+        l += __shfl_xor(l, o, 64);
+        n += __shfl_xor(n, o, 64);
+    }
+    live = l;
+    tokens = n;
+}
+
+// ---- logit rows ----------------------------------------------------------------
+// A wave holds a row: lane l has experts 256 i + 4 l + c (c < 4).  Experts past
+// E read as -infinity (probability 0).
+template <int NV>
+EM_DEV void load_row(float (&v)[NV][4], const float* __restrict__ row, int E, bool vec) {
+    const int lane = lane_id();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = 256 * i + 4 * lane;
+        if (vec) {
+            const float4 f = e < E ? *reinterpret_cast<const float4*>(row + e)
+                                   : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            v[i][0] = f.x; v[i][1] = f.y; v[i][2] = f.z; v[i][3] = f.w;
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[i][c] = e + c < E ? row[e + c] : -INFINITY;
+        }
+    }
+}
+
+// v becomes softmax(v); the row's log sum exp is returned.  A row of -infinity
+// alone (every expert masked) has no distribution: probabilities and lse 0.
+template <int NV>
+EM_DEV float softmax_row(float (&v)[NV][4]) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) m = fmaxf(m, v[i][c]);
+    m = wave_max(m);
+    const bool none = m == -INFINITY;
+    const float b = none ? 0.f : m;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            v[i][c] = expf(v[i][c] - b);
+            s += v[i][c];
+        }
+    s = wave_sum(s);
+    const float inv = none ? 0.f : 1.f / s;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[i][c] *= inv;
+    return none ? 0.f : m + logf(s);
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------ the load -----
+// Chunk c of LCH tokens; its part of sequence s goes to slot c + s of the
+// partial sums (both grow along the tokens, so a slot has one owner).  Bound by
+// reading the logits once.
+template <int NV>
+__global__ void __launch_bounds__(256)
+rt_load(RouterLoad a) {
+    __shared__ __attribute__((aligned(16))) float red[4][NV * 256];
+    __shared__ int hist[NV * 256];
+    __shared__ double zred[4];
+    const Seqs q{a.seq_offsets, a.S, a.T};
+    const int tid = threadIdx.x, lane = lane_id(), wv = wave_id();
+    const int t0 = blockIdx.x * LCH, t1 = min(a.T, t0 + LCH);
+    if (blockIdx.x == 0 && tid == 0) *a.done = 0;
+    for (int s = find_seq(q, t0); s < a.S; ++s) {
+        if (q.lo(s) >= t1) break;
+        const int lo = max(q.lo(s), t0), hi = min(q.hi(s), t1);
+        if (lo >= hi) continue;
+        for (int e = tid; e < NV * 256; e += 256) hist[e] = 0;
+        __syncthreads();
+        for (int i = tid; i < (hi - lo) * a.k; i += 256) {
+            const int e = a.topk_idx[(int64_t)lo * a.k + i];
+            if ((unsigned)e < (unsigned)a.E) atomicAdd(&hist[e], 1);
+        }
+        float acc[NV][4], cur[NV][4], nxt[NV][4];
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[i][c] = 0.f;
+        double z2 = 0.0;
+        if (lo + wv < hi) load_row<NV>(cur, a.logits + (int64_t)(lo + wv) * a.E, a.E, a.vec);
+        for (int t = lo + wv; t < hi; t += 4) {
+            if (t + 4 < hi) load_row<NV>(nxt, a.logits + (int64_t)(t + 4) * a.E, a.E, a.vec);
+            const float lse = softmax_row<NV>(cur);
+            z2 += (double)lse * (double)lse;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    acc[i][c] += cur[i][c];
+                    cur[i][c] = nxt[i][c];
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            *reinterpret_cast<float4*>(&red[wv][256 * i + 4 * lane]) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        if (lane == 0) zred[wv] = z2;
+        __syncthreads();
+        const int64_t slot = blockIdx.x + s;
+        for (int e = tid; e < a.E; e += 256) {
+            a.part_p[slot * a.E + e] = (red[0][e] + red[1][e]) + (red[2][e] + red[3][e]);
+            a.part_c[slot * a.E + e] = hist[e];
+        }
+        if (tid == 0) a.part_z[slot] = (zred[0] + zred[1]) + (zred[2] + zred[3]);
+        __syncthreads();
+    }
+}
+
+// 64 experts of one sequence: 16 lanes rows of threads add interleaved chunks in
+// float64, the rows are added in order.  The last workgroup to arrive forms the
+// losses from every workgroup's dot product.  Those are passed with
+// device-coherent accesses and a counted wait, not fences (a fence writes back
+// the XCD's whole L2).
+__global__ void __launch_bounds__(1024)
+rt_load_reduce(RouterLoad a) {
+    __shared__ double sp[16][64];
+    __shared__ int sc[16][64];
+    __shared__ int last;
+    const Seqs q{a.seq_offsets, a.S, a.T};
+    const int col = threadIdx.x & 63, row = threadIdx.x >> 6;
+    const int s = blockIdx.y, e = blockIdx.x * 64 + col;
+    const int lo = q.lo(s), hi = q.hi(s), n = hi - lo;
+    const int c0 = lo / LCH, c1 = n > 0 ? (hi - 1) / LCH + 1 : c0;
+    double p = 0.0;
+    int cnt = 0;
+    if (e < a.E) {
+#pragma unroll 4
+        for (int c = c0 + row; c < c1; c += 16) {
+            p += (double)a.part_p[(int64_t)(c + s) * a.E + e];
+            cnt += a.part_c[(int64_t)(c + s) * a.E + e];
+        }
+    }
+    sp[row][col] = p;
+    sc[row][col] = cnt;
+    __syncthreads();
+    const int nblk = gridDim.x * gridDim.y;
+    if (row == 0) {
+        for (int r = 1; r < 16; ++r) {
+            p += sp[r][col];
+            cnt += sc[r][col];
+        }
+        const double mean = n > 0 ? p / n : 0.0;
+        double dot = 0.0;
+        if (e < a.E) {
+            a.counts[(int64_t)s * a.E + e] = cnt;
+            a.probs[(int64_t)s * a.E + e] = (float)mean;
+            dot = n > 0 ? (double)cnt * mean * (double)a.E / ((double)a.k * n) : 0.0;
+        }
+        double z = 0.0;                                   // the sequence's z sum, by its first workgroup
+        if (blockIdx.x == 0)
+            for (int c = c0 + col; c < c1; c += 64) z += a.part_z[c + s];
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) {
+            dot += __shfl_xor(dot, o, 64);
+            z += __shfl_xor(z, o, 64);
+        }
+        if (col == 0) {
+            const int id = blockIdx.y * gridDim.x + blockIdx.x;
+            __hip_atomic_store(&a.dots[2 * id], dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_store(&a.dots[2 * id + 1], z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            last = __hip_atomic_fetch_add(a.done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (unsigned)nblk - 1;
+        }
+    }
+    __syncthreads();
+    if (!last || row != 0) return;
+    double b = 0.0, z = 0.0;
+    for (int i = col; i < nblk; i += 64) {
+        b += __hip_atomic_load(&a.dots[2 * i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        z += __hip_atomic_load(&a.dots[2 * i + 1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) {
+        b += __shfl_xor(b, o, 64);
+        z += __shfl_xor(z, o, 64);
+    }
+    int live, tokens;
+    live_seqs(q, live, tokens);
+    if (col == 0) {
+        a.loss[0] = live ? (float)(b / live) : 0.f;
+        a.loss[1] = tokens ? (float)(z / tokens) : 0.f;
+    }
+}
+
+// ------------------------------------------------------------------ dz -----------
+// One wave a token, DCH tokens a workgroup (each wave a run of neighbours, so
+// that the sequence's f stays in registers).  Rows T .. Tp - 1 and columns
+// E .. Ep - 1 of the planes are zeros.
+template <int NV>
+__global__ void __launch_bounds__(256)
+rt_dlogits(RouterGrad a) {
+    __shared__ __attribute__((aligned(16))) float red[4][NV * 256];
+    const Seqs q{a.seq_offsets, a.S, a.T};
+    const int tid = threadIdx.x, lane = lane_id(), wv = wave_id();
+    constexpr int PER = DCH / 4;
+    const int t0 = blockIdx.x * DCH + wv * PER;
+    float gb = 0.f, gz = 0.f;
+    if (a.d_loss) {
+        int live, tokens;
+        live_seqs(q, live, tokens);
+        gb = live ? a.d_loss[0] / (float)live : 0.f;
+        gz = tokens ? 2.f * a.d_loss[1] / (float)tokens : 0.f;
+    }
+    int s = a.d_loss ? find_seq(q, t0) : 0, have = -1;
+    int slo = a.d_loss ? q.lo(s) : 0, shi = a.d_loss ? q.hi(s) : 0;
+    float f[NV][4], acc[NV][4], nxt[NV][4];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) f[i][c] = acc[i][c] = 0.f;
+    if (t0 < a.T) load_row<NV>(nxt, a.logits + (int64_t)t0 * a.E, a.E, a.vec);
+    for (int j = 0; j < PER; ++j) {
+        const int t = t0 + j;
+        if (t >= a.Tp) break;
+        float d[NV][4];
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) d[i][c] = t < a.T ? nxt[i][c] : 0.f;
+        if (t < a.T) {
+            if (j + 1 < PER && t + 1 < a.T) load_row<NV>(nxt, a.logits + (int64_t)(t + 1) * a.E, a.E, a.vec);
+            // the selection weights' gradient: lane j has the token's pick j
+            int pick = -1;
+            float pv = 0.f;
+            if (a.d_topk_w) {
+                float w = 0.f, dw = 0.f;
+                if (lane < a.k) {
+                    pick = a.topk_idx[(int64_t)t * a.k + lane];
+                    w = a.topk_w[(int64_t)t * a.k + lane];
+                    dw = a.d_topk_w[(int64_t)t * a.k + lane];
+                }
+                const float mean = wave_sum(w * dw);
+                pv = w * (dw - mean);
+            }
+            while (t >= shi && s + 1 < a.S) {           // the token's sequence (none: neither loss has it)
+                ++s;
+                slo = q.lo(s);
+                shi = q.hi(s);
+            }
+            const bool in = a.d_loss && t >= slo && t < shi;
+            if (in) {
+                const float lse = softmax_row<NV>(d);
+                const int n = shi - slo;
+                if (have != s) {
+                    have = s;
+                    const float r = (float)a.E / ((float)a.k * (float)n);
+#pragma unroll
+                    for (int i = 0; i < NV; ++i)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int e = 256 * i + 4 * lane + c;
+                            f[i][c] = e < a.E ? (float)a.counts[(int64_t)s * a.E + e] * r : 0.f;
+                        }
+                }
+                float mean = 0.f;
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) mean = fmaf(d[i][c], f[i][c], mean);
+                mean = wave_sum(mean);
+                const float b = gb / (float)n, z = gz * lse;
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) d[i][c] *= fmaf(b, f[i][c] - mean, z);
+            } else {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) d[i][c] = 0.f;
+            }
+            // picks in slot order: a fixed order also where one expert is named twice
+            if (a.d_topk_w)
+                for (int p = 0; p < a.k; ++p) {
+                    const int e = __builtin_amdgcn_readlane(pick, p);
+                    const float v = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(pv), p));
+#pragma unroll
+                    for (int i = 0; i < NV; ++i)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) d[i][c] += 256 * i + 4 * lane + c == e ? v : 0.f;
+                }
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[i][c] += d[i][c];
+            if (a.dlogits) {
+                float* row = a.dlogits + (int64_t)t * a.E;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int e = 256 * i + 4 * lane;
+                    if (a.vec) {
+                        if (e < a.E) *reinterpret_cast<float4*>(row + e) = make_float4(d[i][0], d[i][1], d[i][2], d[i][3]);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            if (e + c < a.E) row[e + c] = d[i][c];
+                    }
+                }
+            }
+        }
+        if (a.planes) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int e = 256 * i + 4 * lane;
+                if (e >= a.Ep) continue;
+                // experts past E are zero: their logits read as -infinity
+                float r[4] = {d[i][0], d[i][1], d[i][2], d[i][3]};
+#pragma unroll
+                for (int p = 0; p < 3; ++p) {
+                    const f32x2 u = {r[0], r[1]}, v = {r[2], r[3]};
+                    const uint32_t a0 = __builtin_bit_cast(uint32_t, __builtin_convertvector(u, bf16x2));
+                    const uint32_t a1 = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+                    *reinterpret_cast<uint2*>(a.planes + ((int64_t)p * a.Tp + t) * a.Ep + e) = make_uint2(a0, a1);
+                    r[0] -= bf16_to_f32(a0 & 0xFFFFu);
+                    r[1] -= bf16_to_f32(a0 >> 16);
+                    r[2] -= bf16_to_f32(a1 & 0xFFFFu);
+                    r[3] -= bf16_to_f32(a1 >> 16);
+                }
+            }
+        }
+    }
+    if (!a.part_b) return;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        *reinterpret_cast<float4*>(&red[wv][256 * i + 4 * lane]) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+    __syncthreads();
+    for (int e = tid; e < a.E; e += 256)
+        a.part_b[(int64_t)blockIdx.x * a.E + e] = (red[0][e] + red[1][e]) + (red[2][e] + red[3][e]);
+}
+
+// ------------------------------------------------------------------ dx, dW_r ------
+// out[i][n] = sum_k A[i][k] B[k][n], A the three planes of dz and B bf16 rows:
+//   DX  A = dz [t][e] (K contiguous), B = W_r;   DW  A = dz^T (K by rows), B = x
+// A workgroup takes BI x 256 of out; K steps of 32 arrive by direct global -> LDS
+// loads, one step ahead in two stages.  An operand whose K runs down the rows is
+// transposed in registers: a lane reads a short run of columns of its eight K
+// rows, and byte permutes pair the rows; operand c of lane m is then column
+// C m + c of the run of 16 C, so that a lane ends with C neighbouring columns of
+// out.  Bound by the matrix cores (three products an element).
+namespace {
+
+enum RtMode { RT_DX = 0, RT_DW = 1 };
+
+template <int BI_>
+struct RtCfg {
+    static constexpr int BI = BI_, BN = 256, BK = 32;
+    static constexpr int WI = BI / 64, WN = BI == 256 ? 2 : 4;      // waves: 64 rows x (256 / WN) columns each
+    static constexpr int WAVES = WI * WN, TH = 64 * WAVES;
+    static constexpr int NC = BN / WN / 16;                          // columns a lane ends with
+    static constexpr int P_B = BI * BK * 2, B_B = BK * BN * 2;       // one plane's tile, B's tile
+    static constexpr int STAGE = 3 * P_B + B_B;
+    static constexpr int A_INSTR = 3 * P_B / 1024 / WAVES, B_INSTR = B_B / 1024 / WAVES;
+};
+
+EM_DEV void rt_dma16(const void* src, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(src), "s"(dst) : "memory", "m0");
+}
+
+// Eight K rows of C bf16 columns (C = 4: two words a row, C = 8: four) to C
+// operands of eight K elements.
+template <int C>
+EM_DEV void transpose8(const uint32_t (&r)[8][C / 2], uint4 (&o)[C]) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const uint32_t sel = c & 1 ? 0x07060302u : 0x05040100u;
+        o[c].x = __builtin_amdgcn_perm(r[1][c / 2], r[0][c / 2], sel);
+        o[c].y = __builtin_amdgcn_perm(r[3][c / 2], r[2][c / 2], sel);
+        o[c].z = __builtin_amdgcn_perm(r[5][c / 2], r[4][c / 2], sel);
+        o[c].w = __builtin_amdgcn_perm(r[7][c / 2], r[6][c / 2], sel);
+    }
+}
+
+template <int C>
+EM_DEV void read_rows(uint32_t (&r)[8][C / 2], const uint8_t* p, int row_bytes) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if constexpr (C == 8) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p + i * row_bytes);
+            r[i][0] = v.x; r[i][1] = v.y; r[i][2] = v.z; r[i][3] = v.w;
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(p + i * row_bytes);
+            r[i][0] = v.x; r[i][1] = v.y;
+        }
+    }
+}
+
+}  // namespace
+
+template <int MODE, int BI>
+__global__ void __launch_bounds__(RtCfg<BI>::TH)
+rt_gemm(RouterGrad a) {
+    using C = RtCfg<BI>;
+    constexpr int NC = C::NC;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * C::STAGE];
+    const int lane = lane_id(), wv = wave_id(), g = lane >> 4, m = lane & 15;
+    const int wi = wv / C::WN, wn = wv % C::WN;
+    const int I = MODE == RT_DX ? a.T : a.E;                 // rows of out
+    const int rows_b = MODE == RT_DX ? a.E : a.T;            // rows of B
+    const uint16_t* B = MODE == RT_DX ? a.w_router : a.x;
+    // XCD x = blockIdx % 8 takes neighbouring tiles
+    const int nn = (a.d + C::BN - 1) / C::BN, ni = (I + BI - 1) / BI;
+    const int total = nn * ni * (MODE == RT_DX ? 1 : a.slices);
+    const int per = (total + 7) >> 3, at = blockIdx.x >> 3;
+    const int b = (blockIdx.x & 7) * per + at;
+    if (at >= per || b >= total) return;
+    // DX: rows slowest; DW: token slices slowest (a slice's x and dz are shared by its tiles)
+    const int z = MODE == RT_DX ? 0 : b / (nn * ni);
+    const int i0 = (MODE == RT_DX ? b / nn : (b % (nn * ni)) % ni) * BI;
+    const int n0 = (MODE == RT_DX ? b % nn : (b % (nn * ni)) / ni) * C::BN;
+    const int K = MODE == RT_DX ? a.Ep : a.Tp;
+    const int steps = K / C::BK;
+    const int s0 = MODE == RT_DX ? 0 : (int)((int64_t)steps * z / a.slices);
+    const int s1 = MODE == RT_DX ? steps : (int)((int64_t)steps * (z + 1) / a.slices);
+
+    // ---- load sources: 1 KB pieces of the planes' tiles, then of B's
+    const uint8_t* asrc[C::A_INSTR];
+    int64_t astep;
+#pragma unroll
+    for (int p = 0; p < C::A_INSTR; ++p) {
+        const int piece = C::A_INSTR * wv + p, plane = piece / (C::P_B / 1024), in = piece % (C::P_B / 1024);
+        const uint16_t* base = a.planes + (int64_t)plane * a.Tp * a.Ep;
+        if constexpr (MODE == RT_DX) {                       // [BI][32 e]: 64-byte rows, segments swizzled
+            const int r = 16 * in + (lane >> 2);
+            asrc[p] = (const uint8_t*)(base + (int64_t)min(i0 + r, a.Tp - 1) * a.Ep + 8 * ((lane & 3) ^ ((r >> 2) & 3)));
+        } else {                                             // [32 t][BI e]
+            const int o = 512 * in + 8 * lane, r = o / BI, e = o % BI;
+            asrc[p] = (const uint8_t*)(base + (int64_t)r * a.Ep + min(i0 + e, a.Ep - 8));
+        }
+    }
+    astep = MODE == RT_DX ? C::BK * 2 : (int64_t)C::BK * a.Ep * 2;
+    const uint8_t* bsrc[C::B_INSTR];
+    int brow[C::B_INSTR];
+#pragma unroll
+    for (int p = 0; p < C::B_INSTR; ++p) {                   // [32 k][256 n]: two rows a piece
+        brow[p] = 2 * (C::B_INSTR * wv + p) + (lane >> 5);
+        bsrc[p] = (const uint8_t*)(B + min(n0 + 8 * (lane & 31), a.d - 8));
+    }
+    const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+    auto fetch = [&](int st) {
+        const uint32_t stage = __builtin_amdgcn_readfirstlane(base + (st & 1) * C::STAGE);
+#pragma unroll
+        for (int p = 0; p < C::A_INSTR; ++p) rt_dma16(asrc[p] + st * astep, stage + 1024 * (C::A_INSTR * wv + p));
+#pragma unroll
+        for (int p = 0; p < C::B_INSTR; ++p)                 // B rows past the end meet zeros of the planes
+            rt_dma16(bsrc[p] + (int64_t)min(C::BK * st + brow[p], rows_b - 1) * a.d * 2,
+                     stage + 3 * C::P_B + 1024 * (C::B_INSTR * wv + p));
+    };
+
+    floatx4 acc[4][NC];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) acc[i][c] = zero4();
+    if (s0 < s1) fetch(s0);
+    for (int st = s0; st < s1; ++st) {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (st + 1 < s1) fetch(st + 1);
+        const uint8_t* A = lds + (st & 1) * C::STAGE;
+        const uint8_t* Bt = A + 3 * C::P_B;
+        uint4 bf[NC];
+        {
+            uint32_t raw[8][NC / 2];
+            read_rows<NC>(raw, Bt + 8 * g * 512 + 2 * (16 * NC * wn + NC * m), 512);
+            transpose8<NC>(raw, bf);
+        }
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            uint4 af[4];
+            if constexpr (MODE == RT_DX) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 64 * wi + 16 * i + m;
+                    af[i] = *reinterpret_cast<const uint4*>(A + p * C::P_B + r * 64 + 16 * (g ^ ((r >> 2) & 3)));
+                }
+            } else {
+                uint32_t raw[8][2];
+                read_rows<4>(raw, A + p * C::P_B + 8 * g * (2 * BI) + 2 * (64 * wi + 4 * m), 2 * BI);
+                transpose8<4>(raw, af);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < NC; ++c) acc[i][c] = mfma_bf16(af[i], bf[c], acc[i][c]);
+        }
+    }
+
+    // ---- out: lane holds rows of subtile i (D row 4 g + v) and columns NC m .. + NC - 1
+    float* out = MODE == RT_DX ? a.dx : (a.slices > 1 ? a.part_w + (int64_t)z * a.E * a.d : a.dw_router);
+    const int n = n0 + 16 * NC * wn + NC * m;
+    if (n >= a.d) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int r = i0 + 64 * wi + (MODE == RT_DX ? 16 * i + 4 * g + v : 4 * (4 * g + v) + i);
+            if (r >= I) continue;
+            float* o = out + (int64_t)r * a.d + n;
+#pragma unroll
+            for (int c = 0; c < NC; c += 4)
+                *reinterpret_cast<float4*>(o + c) = make_float4(acc[i][c][v], acc[i][c + 1][v], acc[i][c + 2][v], acc[i][c + 3][v]);
+        }
+}
+
+// Token slices of dW_r in order (workgroups [0, wblocks)), then the chunks of
+// dbias: 64 experts a workgroup, 16 rows of threads over the chunks, float64.
+__global__ void __launch_bounds__(1024)
+rt_finish(RouterGrad a, int wblocks) {
+    __shared__ double sp[16][64];
+    if ((int)blockIdx.x < wblocks) {
+        const int64_t n = (int64_t)a.E * a.d, at = ((int64_t)blockIdx.x * 1024 + threadIdx.x) * 4;
+        if (at >= n) return;
+        float4 s = *reinterpret_cast<const float4*>(a.part_w + at);
+        for (int z = 1; z < a.slices; ++z) {
+            const float4 v = *reinterpret_cast<const float4*>(a.part_w + z * n + at);
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        }
+        *reinterpret_cast<float4*>(a.dw_router + at) = s;
+        return;
+    }
+    const int col = threadIdx.x & 63, row = threadIdx.x >> 6;
+    const int e = (blockIdx.x - wblocks) * 64 + col;
+    const int chunks = (a.T + DCH - 1) / DCH;
+    double s = 0.0;
+    if (e < a.E) {
+#pragma unroll 8
+        for (int c = row; c < chunks; c += 16) s += (double)a.part_b[(int64_t)c * a.E + e];
+    }
+    sp[row][col] = s;
+    __syncthreads();
+    if (row != 0 || e >= a.E) return;
+    for (int r = 1; r < 16; ++r) s += sp[r][col];
+    a.dbias[e] = (float)s;
+}
+
+// ------------------------------------------------------------------ host side ----
+namespace {
+
+constexpr size_t kAl = 256;
+size_t up(size_t v) { return (v + kAl - 1) & ~(kAl - 1); }
+
+struct LoadLayout { size_t p, c, z, dots, done, bytes; };
+LoadLayout load_layout(const RouterLoad& a) {
+    LoadLayout L{};
+    const size_t slots = (size_t)(a.T + LCH - 1) / LCH + a.S;
+    size_t off = 0;
+    auto take = [&](size_t n) { const size_t o = off; off = up(off + n); return o; };
+    L.p = take(slots * a.E * 4);
+    L.c = take(slots * a.E * 4);
+    L.z = take(slots * 8);
+    L.dots = take((size_t)a.S * ((a.E + 63) / 64) * 16);
+    L.done = take(4);
+    L.bytes = off;
+    return L;
+}
+
+struct GradLayout { size_t planes, part_w, part_b, bytes; };
+
+int pad32(int v) { return (v + 31) & ~31; }
+int tile_rows(int n) { return n > 128 ? 256 : 64; }
+
+// Token slices of dW_r: as many as give every CU a workgroup, of at least four
+// K steps each.
+int dw_slices(const RouterGrad& a) {
+    const int tiles = ((a.d + 255) / 256) * ((a.E + tile_rows(a.E) - 1) / tile_rows(a.E));
+    const int most = a.Tp / 32 / 4;
+    int z = 256 / tiles;
+    z = z < most ? z : most;
+    return z < 1 ? 1 : z > 16 ? 16 : z;
+}
+
+GradLayout grad_layout(const RouterGrad& a) {
+    GradLayout L{};
+    size_t off = 0;
+    auto take = [&](size_t n) { const size_t o = off; off = up(off + n); return o; };
+    L.planes = take((size_t)3 * a.Tp * a.Ep * 2);
+    L.part_w = take((size_t)dw_slices(a) * a.E * a.d * 4);
+    L.part_b = take((size_t)((a.Tp + DCH - 1) / DCH) * a.E * 4);
+    L.bytes = off;
+    return L;
+}
+
+template <int MODE>
+hipError_t launch_rt_gemm(const RouterGrad& a, hipStream_t s, const char* name) {
+    const int I = MODE == RT_DX ? a.T : a.E;
+    // DX: small tiles where large ones would leave compute units idle
+    const int bi = MODE == RT_DX ? ((int64_t)((I + 255) / 256) * ((a.d + 255) / 256) >= 192 ? 256 : 64) : tile_rows(I);
+    const int64_t tiles = (int64_t)((I + bi - 1) / bi) * ((a.d + 255) / 256) * (MODE == RT_DX ? 1 : a.slices);
+    const unsigned grid = (unsigned)((tiles + 7) & ~7ll);
+    prof_begin(s);
+    if (bi == 256) rt_gemm<MODE, 256><<<grid, RtCfg<256>::TH, 0, s>>>(a);
+    else rt_gemm<MODE, 64><<<grid, RtCfg<64>::TH, 0, s>>>(a);
+    prof_end(s, name);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t router_load_ws_bytes(const RouterLoad& a) { return load_layout(a).bytes; }
+
+hipError_t launch_router_load(RouterLoad a, void* ws, hipStream_t s) {
+    const LoadLayout L = load_layout(a);
+    char* base = static_cast<char*>(ws);
+    a.part_p = reinterpret_cast<float*>(base + L.p);
+    a.part_c = reinterpret_cast<int32_t*>(base + L.c);
+    a.part_z = reinterpret_cast<double*>(base + L.z);
+    a.dots = reinterpret_cast<double*>(base + L.dots);
+    a.done = reinterpret_cast<uint32_t*>(base + L.done);
+    const int chunks = (a.T + LCH - 1) / LCH;
+    prof_begin(s);
+    if (a.E <= 256) rt_load<1><<<chunks, 256, 0, s>>>(a);
+    else if (a.E <= 512) rt_load<2><<<chunks, 256, 0, s>>>(a);
+    else rt_load<4><<<chunks, 256, 0, s>>>(a);
+    prof_end(s, "rt_load");
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    prof_begin(s);
+    rt_load_reduce<<<dim3((a.E + 63) / 64, a.S), 1024, 0, s>>>(a);
+    prof_end(s, "rt_load_reduce");
+    return hipGetLastError();
+}
+
+static void pad_grad(RouterGrad& a) {
+    a.Tp = pad32(a.T);
+    a.Ep = pad32(a.E);
+}
+
+size_t router_grad_ws_bytes(RouterGrad a) {
+    pad_grad(a);
+    return grad_layout(a).bytes;
+}
+
+hipError_t launch_router_grad(RouterGrad a, void* ws, hipStream_t s) {
+    pad_grad(a);
+    const GradLayout L = grad_layout(a);
+    char* base = static_cast<char*>(ws);
+    a.slices = dw_slices(a);
+    a.planes = a.dx || a.dw_router ? reinterpret_cast<uint16_t*>(base + L.planes) : nullptr;
+    a.part_w = reinterpret_cast<float*>(base + L.part_w);
+    a.part_b = a.dbias ? reinterpret_cast<float*>(base + L.part_b) : nullptr;
+    const int chunks = (a.Tp + DCH - 1) / DCH;
+    prof_begin(s);
+    if (a.E <= 256) rt_dlogits<1><<<chunks, 256, 0, s>>>(a);
+    else if (a.E <= 512) rt_dlogits<2><<<chunks, 256, 0, s>>>(a);
+    else rt_dlogits<4><<<chunks, 256, 0, s>>>(a);
+    prof_end(s, "rt_dlogits");
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && a.dx) e = launch_rt_gemm<RT_DX>(a, s, "rt_dx");
+    if (e == hipSuccess && a.dw_router) e = launch_rt_gemm<RT_DW>(a, s, "rt_dw");
+    if (e != hipSuccess) return e;
+    const int wblocks = a.dw_router && a.slices > 1 ? (int)(((int64_t)a.E * a.d / 4 + 1023) / 1024) : 0;
+    const int bblocks = a.dbias ? (a.E + 63) / 64 : 0;
+    if (wblocks + bblocks == 0) return hipSuccess;
+    prof_begin(s);
+    rt_finish<<<wblocks + bblocks, 1024, 0, s>>>(a, wblocks);
+    prof_end(s, "rt_finish");
+    return hipGetLastError();
+}
+
+}  // namespace em
