@@ -13,6 +13,7 @@ library is required - calls raise if it is not built.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from typing import Optional
 
@@ -205,8 +206,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     return lib
 
 
+_dim_values = operator.attrgetter(*(n for n, _ in CDims._fields_))
+
+
 def cdims(dims) -> CDims:
-    return CDims(*(int(getattr(dims, f)) for f, _ in CDims._fields_))
+    return CDims(*map(int, _dim_values(dims)))
 
 
 def _ptr(t) -> Optional[int]:
@@ -221,8 +225,8 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:                  # the current stream's handle, without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -436,7 +440,7 @@ def _same_device(*tensors) -> None:
     import torch
     cur = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != cur):
+        if t is not None and t.get_device() != cur:
             raise ValueError(f"tensors must be on the current GPU (cuda:{cur}), got one on {t.device}")
 
 
@@ -455,6 +459,8 @@ def _row_stride(t) -> int:
     if t.dim() < 2:
         raise ValueError("expected rows: a tensor of at least two dimensions")
     K = t.shape[-1]
+    if t.is_contiguous():
+        return K
     if K != 1 and t.stride(-1) != 1:
         raise ValueError("the elements of a row must be contiguous")
     stride, span = None, 1
@@ -467,7 +473,7 @@ def _row_stride(t) -> int:
             elif s != stride * span:
                 raise ValueError("the rows must lie at one stride")
         span *= n
-    return max(K, 8) if stride is None else stride
+    return K if stride is None else stride
 
 
 def _mx_shape(fmt, dense, codes, scales):
@@ -531,7 +537,7 @@ def edge_moe_mx_product(x_format, x, codes, scales, y, ws, offsets=None, row_src
     _same_device(x, codes, scales, y, ws, offsets, row_src)
     st = load().edge_moe_mx_product(ctypes.byref(CMxDims(T, R, M, N, K, x_format)), x.data_ptr(), _row_stride(x),
                                     _ptr(row_src), _ptr(offsets), _ptr(codes), _ptr(scales), y.data_ptr(),
-                                    max(_row_stride(y), N), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
+                                    _row_stride(y), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
     if st != EDGE_MOE_OK:
         raise EdgeMoeError("edge_moe_mx_product", st)
 

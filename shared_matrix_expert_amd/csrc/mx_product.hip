@@ -40,6 +40,19 @@ EM_DEV floatx4 mfma_mx(const uint4& w, int ws, const i32x8& x, int xs, const flo
 // matrix by matrix; `total` is their count, r1 = 0 marks no tile.
 struct RowTile { int m, r0, r1, total; };
 
+// Inclusive sum over the lanes up to each one, with DPP row shifts and
+// broadcasts (no LDS).
+template <int CTRL, int ROWS>
+EM_DEV int dpp_add(int v) { return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false); }
+EM_DEV int scan_add(int v) {
+    v = dpp_add<0x111, 0xF>(v);       // row_shr:1, 2, 4, 8: sums within a row of 16 lanes
+    v = dpp_add<0x112, 0xF>(v);
+    v = dpp_add<0x114, 0xF>(v);
+    v = dpp_add<0x118, 0xF>(v);
+    v = dpp_add<0x142, 0xA>(v);       // row_bcast:15 into rows 1 and 3, then :31 into rows 2 and 3
+    return dpp_add<0x143, 0xC>(v);
+}
+
 // The row tile of this workgroup among tiles of BT rows: pick(total) names it,
 // or is negative for none.  With offsets (device memory) every wave counts the
 // tiles itself: each lane those of PER neighbouring matrices, then a scan over
@@ -60,12 +73,7 @@ EM_DEV RowTile find_tile(const int32_t* __restrict__ offsets, int M, int R, Pick
         at[i] = mine;
         mine += (hi[i] - lo[i] + BT - 1) / BT;
     }
-    int sum = mine;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int v = __shfl_up(sum, o, 64);
-        if (lane >= o) sum += v;
-    }
+    const int sum = scan_add(mine);
     RowTile t{0, 0, 0, __builtin_amdgcn_readlane(sum, 63)};
     const int rt = pick(t.total);
     if (rt < 0 || rt >= t.total) return t;
@@ -83,7 +91,10 @@ EM_DEV RowTile find_tile(const int32_t* __restrict__ offsets, int M, int R, Pick
 
 template <int BT, class Pick>
 EM_DEV RowTile row_tile(const int32_t* __restrict__ offsets, int M, int R, Pick pick) {
-    if (offsets) return M <= 64 ? find_tile<BT, 1>(offsets, M, R, pick) : find_tile<BT, 16>(offsets, M, R, pick);
+    if (offsets) {
+        if (M <= 64) return find_tile<BT, 1>(offsets, M, R, pick);
+        return M <= 512 ? find_tile<BT, 8>(offsets, M, R, pick) : find_tile<BT, 16>(offsets, M, R, pick);
+    }
     RowTile t{0, 0, 0, (R + BT - 1) / BT};
     const int rt = pick(t.total);
     if (rt < 0 || rt >= t.total) return t;
@@ -99,63 +110,43 @@ EM_DEV int x_row(const MxProduct& a, int r) {
     return (unsigned)s < (unsigned)a.T ? s : -1;
 }
 
-// Four consecutive columns of a y row.
-EM_DEV void store4(const MxProduct& a, int64_t r, int n, const floatx4& v) {
+// Four consecutive columns of a y row (`whole`: all four exist and take one store).
+EM_DEV void store4(const MxProduct& a, int64_t r, int n, const floatx4& v, bool whole) {
     uint16_t* p = a.y + r * a.y_stride + n;
     const f32x2 lo = {v.x, v.y}, hi = {v.z, v.w};
     const uint32_t w0 = __builtin_bit_cast(uint32_t, __builtin_convertvector(lo, bf16x2));
     const uint32_t w1 = __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, bf16x2));
-    if (a.vec && n + 4 <= a.N) {
+    if (whole) {
         *reinterpret_cast<uint2*>(p) = make_uint2(w0, w1);
         return;
     }
-    if (n < a.N) p[0] = (uint16_t)w0;
-    if (n + 1 < a.N) p[1] = (uint16_t)(w0 >> 16);
-    if (n + 2 < a.N) p[2] = (uint16_t)w1;
-    if (n + 3 < a.N) p[3] = (uint16_t)(w1 >> 16);
-}
-
-// ---- x rounded in registers -------------------------------------------------
-// One K step of an x row as an operand: the lane's raw bf16 elements in v (FP4:
-// its block's 32; FP8: K 16 g .. + 15 and 64 + 16 g .. + 15), the codes and this
-// lane's scale byte out.
-EM_DEV const uint16_t* x_piece(const uint16_t* row, int g, int h, int fmt) {
-    return row + (fmt == kMxFp4 ? 32 * g + 16 * h : 64 * h + 16 * g);
-}
-
-template <int FMT>
-EM_DEV void round_x(const uint4 (&v)[4], i32x8& q, int& xs) {
-    if constexpr (FMT == kMxFp4) {
-        const uint32_t a = max(max(amax8_bf16(v[0]), amax8_bf16(v[1])), max(amax8_bf16(v[2]), amax8_bf16(v[3])));
-        xs = e8m0_of<FMT>(a);
-        const bool bad = xs == 255;
-        const float sc = e8m0_f32(bad ? 127 : xs);
-        const i32x8 z = {0, 0, 0, 0, 0, 0, 0, 0};
-        const i32x8 c = {(int)fp4x8_bf16(v[0], sc), (int)fp4x8_bf16(v[1], sc), (int)fp4x8_bf16(v[2], sc),
-                         (int)fp4x8_bf16(v[3], sc), 0, 0, 0, 0};
-        q = bad ? z : c;
-    } else {
-        // the lanes 2 c and 2 c + 1 of a row share block c (first half of the
-        // codes) and block 2 + c (second half)
-        uint32_t a0 = max(amax8_bf16(v[0]), amax8_bf16(v[1]));
-        uint32_t a1 = max(amax8_bf16(v[2]), amax8_bf16(v[3]));
-        uint32_t both = a0 | (a1 << 16);
-        both = max_u16x2(both, (uint32_t)__shfl_xor((int)both, 16, 64));
-        const int X0 = e8m0_of<FMT>(both & 0xFFFFu), X1 = e8m0_of<FMT>(both >> 16);
-        const int l = lane_id();
-        // block g's byte: held by lanes of group 2 (g & 1) as X0 (g < 2) or X1
-        const int other = __shfl(X0 | (X1 << 8), (l & 15) + 32 * ((l >> 4) & 1), 64);
-        xs = (l & 32) ? other >> 8 : other & 255;
-        const bool b0 = X0 == 255, b1 = X1 == 255;
-        const float s0 = e8m0_f32(b0 ? 127 : X0), s1 = e8m0_f32(b1 ? 127 : X1);
-        const uint32_t l0 = e4m3_limit(b0 ? 127 : X0), l1 = e4m3_limit(b1 ? 127 : X1);
-        const uint32_t c[8] = {fp8x4_bf16(v[0].x, v[0].y, s0, l0), fp8x4_bf16(v[0].z, v[0].w, s0, l0),
-                               fp8x4_bf16(v[1].x, v[1].y, s0, l0), fp8x4_bf16(v[1].z, v[1].w, s0, l0),
-                               fp8x4_bf16(v[2].x, v[2].y, s1, l1), fp8x4_bf16(v[2].z, v[2].w, s1, l1),
-                               fp8x4_bf16(v[3].x, v[3].y, s1, l1), fp8x4_bf16(v[3].z, v[3].w, s1, l1)};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = (i < 4 ? b0 : b1) ? 0 : (int)c[i];
+    for (int i = 0; i < 4; ++i)
+        if (n + i < a.N) p[i] = (uint16_t)((i < 2 ? w0 : w1) >> (16 * (i & 1)));
+}
+
+// ---- x rounded by a wave ------------------------------------------------------
+// Codes of 16 neighbouring bf16 elements (a lane and its neighbour share a
+// block) and the block's scale byte.
+template <int FMT>
+EM_DEV void round16(const uint4 (&v)[2], uint32_t (&q)[4], int& X) {
+    const uint32_t mine = max(amax8_bf16(v[0]), amax8_bf16(v[1]));
+    const uint32_t a = max(mine, (uint32_t)__builtin_amdgcn_update_dpp((int)mine, (int)mine, 0xB1, 0xF, 0xF, false));
+    X = e8m0_of<FMT>(a);
+    const bool bad = X == 255;
+    const float sc = e8m0_f32(bad ? 127 : X);
+    if constexpr (FMT == kMxFp4) {
+        q[0] = fp4x8_bf16(v[0], sc);
+        q[1] = fp4x8_bf16(v[1], sc);
+        q[2] = q[3] = 0;
+    } else {
+        const uint32_t lim = e4m3_limit(bad ? 127 : X);
+        q[0] = fp8x4_bf16(v[0].x, v[0].y, sc, lim);
+        q[1] = fp8x4_bf16(v[0].z, v[0].w, sc, lim);
+        q[2] = fp8x4_bf16(v[1].x, v[1].y, sc, lim);
+        q[3] = fp8x4_bf16(v[1].z, v[1].w, sc, lim);
     }
+    if (bad) q[0] = q[1] = q[2] = q[3] = 0;
 }
 
 }  // namespace
@@ -163,12 +154,21 @@ EM_DEV void round_x(const uint4 (&v)[4], i32x8& q, int& xs) {
 // ------------------------------------------------------------------ few rows -----
 // A workgroup takes one row tile (16 NS rows of one matrix) and 16 NC columns;
 // its four waves split K into contiguous quarters and their partial sums are
-// added through LDS in wave order.  Weights and x run DEPTH steps ahead in
-// registers.
-template <int FMT, int NS, int NC>
+// added through LDS in wave order.  The weights run WD steps ahead in
+// registers: at K = 4096 and WD = 8 a wave's whole share is asked for at once.
+// x comes rounded from the workspace, or (FUSED, 16 rows) the wave rounds the
+// rows it has, 1024 elements of K at a time, into its own part of the LDS while
+// its weights are in flight.  (Rounding in operand registers instead, every lane
+// its own row's elements, costs 16 rows' work whatever their number: one token
+// through 8192 x 4096 took 9.4 us that way.)
+template <int FMT, int NS, int NC, bool FUSED>
 __global__ void __launch_bounds__(256)
 mxp_stream(MxProduct a) {
-    constexpr int DEPTH = NS == 1 ? 4 : 2;
+    constexpr int WD = NS == 4 ? 4 : 8, XD = NS == 4 ? 1 : 2;
+    constexpr int XB = FMT == kMxFp4 ? 64 : 128;                  // bytes of an x row per step
+    constexpr int RS = 8 * XB + 16, SS = 36;                      // LDS row strides: codes of 8 steps, scale bytes
+    constexpr int XL = FUSED ? 16 * (RS + SS) : 16;
+    __shared__ __attribute__((aligned(16))) uint8_t xl[4][XL];
     __shared__ __attribute__((aligned(16))) float red[4][NS * NC][256];
     const RowTile t = row_tile<16 * NS>(a.offsets, a.M, a.R, [](int) { return (int)blockIdx.y; });
     if (t.r1 == 0) return;
@@ -185,56 +185,105 @@ mxp_stream(MxProduct a) {
         wp[c] = a.codes + ((int64_t)t.m * a.N + col) * (a.K / 2) + 16 * g;
         sp[c] = a.scales + ((int64_t)t.m * steps * a.N + col) * 4 + g;
     }
-    const uint16_t* xp[NS];
-    bool live[NS];
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-        const int r = t.r0 + 16 * s + m;
-        const int src = r < t.r1 ? x_row(a, r) : -1;
-        live[s] = src >= 0;
-        xp[s] = a.x + (int64_t)max(src, 0) * a.x_stride;
-    }
-    floatx4 acc[NS][NC];
-#pragma unroll
-    for (int s = 0; s < NS; ++s)
-#pragma unroll
-        for (int c = 0; c < NC; ++c) acc[s][c] = zero4();
-
-    uint4 w[DEPTH][NC];
-    int ws[DEPTH][NC];
-    uint4 xv[DEPTH][NS][4];
-    auto load = [&](int d, int st) {
+    uint4 w[WD][NC];
+    int ws[WD][NC];
+    auto load_w = [&](int d, int st) {
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             w[d][c] = ldg16(wp[c] + (int64_t)st * (kMxStep / 2));
             ws[d][c] = sp[c][(int64_t)st * a.N * 4];
         }
-#pragma unroll
-        for (int s = 0; s < NS; ++s)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint16_t* p = x_piece(xp[s] + (int64_t)st * kMxStep, g, h, FMT);
-                xv[d][s][2 * h] = ldg16(p);
-                xv[d][s][2 * h + 1] = ldg16(p + 8);
-            }
     };
     if (s0 < s1) {
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) load(d, min(s0 + d, s1 - 1));
-        for (int st = s0; st < s1; st += DEPTH) {
+        for (int d = 0; d < WD; ++d) load_w(d, min(s0 + d, s1 - 1));
+    }
+    int src[NS];                                                  // x row of y row r0 + 16 s + m
 #pragma unroll
-            for (int d = 0; d < DEPTH; ++d) {
-                if (st + d < s1) {
+    for (int s = 0; s < NS; ++s) {
+        const int r = t.r0 + 16 * s + m;
+        src[s] = r < t.r1 ? x_row(a, r) : -1;
+    }
+    uint4 xv[XD][NS][2];
+    int xsv[XD][NS];
+    auto load_x = [&](int d, int st) {                            // (!FUSED) operand registers from the workspace
 #pragma unroll
-                    for (int s = 0; s < NS; ++s) {
-                        i32x8 q;
-                        int xs;
-                        round_x<FMT>(xv[d][s], q, xs);
+        for (int s = 0; s < NS; ++s) {
+            const int64_t row = max(src[s], 0);
+            const uint8_t* p = a.xq + row * (a.K / 128 * XB) + (int64_t)st * XB + 16 * g;
+            xv[d][s][0] = ldg16(p);
+            xv[d][s][1] = FMT == kMxFp8 ? ldg16(p + 64) : make_uint4(0u, 0u, 0u, 0u);
+            xsv[d][s] = a.xs[((int64_t)st * a.T + row) * 4 + g];
+        }
+    };
+    floatx4 acc[NS][NC];
 #pragma unroll
-                        for (int c = 0; c < NC; ++c) acc[s][c] = mfma_mx<FMT>(w[d][c], ws[d][c], q, xs, acc[s][c]);
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) acc[s][c] = zero4();
+    if constexpr (!FUSED) {
+        if (s0 < s1) {
+#pragma unroll
+            for (int d = 0; d < XD; ++d) load_x(d, min(s0 + d, s1 - 1));
+        }
+    }
+    for (int st = s0; st < s1; st += WD) {
+        if constexpr (FUSED) {
+            // rows in turn, 16 elements a lane: steps st .. st + 7 of this wave
+            const int left = min(8, s1 - st) * kMxStep;           // elements of K (the loads past them repeat the last)
+            const int at = min(16 * lane, left - 16);
+            const int rows = t.r1 - t.r0;
+            auto fetch = [&](int row, uint4 (&v)[2]) {
+                const uint16_t* p = a.x + (int64_t)max(__builtin_amdgcn_readlane(src[0], row), 0) * a.x_stride
+                                    + (int64_t)st * kMxStep + at;
+                v[0] = ldg16(p);
+                v[1] = ldg16(p + 8);
+            };
+            uint4 cur[2], nxt[2];
+            fetch(0, nxt);
+            asm volatile("" ::: "memory");                        // the steps before have read the buffer
+            for (int row = 0; row < rows; ++row) {
+                cur[0] = nxt[0];
+                cur[1] = nxt[1];
+                if (row + 1 < rows) fetch(row + 1, nxt);
+                uint32_t q[4];
+                int X;
+                round16<FMT>(cur, q, X);
+                uint8_t* o = &xl[wv][row * RS + lane * (XB / 8)];
+                if constexpr (FMT == kMxFp4) *reinterpret_cast<uint2*>(o) = make_uint2(q[0], q[1]);
+                else *reinterpret_cast<uint4*>(o) = make_uint4(q[0], q[1], q[2], q[3]);
+                if (!(lane & 1)) xl[wv][16 * RS + row * SS + (lane >> 1)] = (uint8_t)X;
+            }
+            __builtin_amdgcn_wave_barrier();                      // one wave's LDS accesses complete in order
+            asm volatile("" ::: "memory");
+        }
+#pragma unroll
+        for (int d = 0; d < WD; ++d) {
+            if (st + d < s1) {
+                i32x8 q[NS];
+                int xs[NS];
+#pragma unroll
+                for (int s = 0; s < NS; ++s) {
+                    uint4 lo, hi = make_uint4(0u, 0u, 0u, 0u);
+                    if constexpr (FUSED) {
+                        const uint8_t* p = &xl[wv][m * RS + d * XB + 16 * g];
+                        lo = ldg16(p);
+                        if constexpr (FMT == kMxFp8) hi = ldg16(p + 64);
+                        xs[s] = xl[wv][16 * RS + m * SS + 4 * d + g];
+                    } else {
+                        lo = xv[d % XD][s][0];
+                        hi = xv[d % XD][s][1];
+                        xs[s] = xsv[d % XD][s];
                     }
-                    if (st + d + DEPTH < s1) load(d, st + d + DEPTH);
+                    q[s] = i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
                 }
+#pragma unroll
+                for (int s = 0; s < NS; ++s)
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) acc[s][c] = mfma_mx<FMT>(w[d][c], ws[d][c], q[s], xs[s], acc[s][c]);
+                if constexpr (!FUSED)
+                    if (st + d + XD < s1) load_x(d % XD, st + d + XD);
+                if (st + d + WD < s1) load_w(d, st + d + WD);
             }
         }
     }
@@ -254,7 +303,7 @@ mxp_stream(MxProduct a) {
             v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
         }
         const int s = i / NC, c = i % NC, r = t.r0 + 16 * s + m;
-        if (r < t.r1) store4(a, r, n0 + 16 * c + 4 * g, live[s] ? v : zero4());
+        if (r < t.r1) store4(a, r, n0 + 16 * c + 4 * g, src[s] >= 0 ? v : zero4(), a.vec && n0 + 16 * (c + 1) <= a.N);
     }
 }
 
@@ -275,7 +324,8 @@ struct GemmCfg {
     static constexpr int NI = BN / WN / 16, NJ = BT / WT / 16;     // column and row subtiles of a wave
     static constexpr int XB = FMT == kMxFp4 ? 64 : 128;            // bytes of an x row per step
     static constexpr int X_B = BT * XB, W_B = BN * 64, XS_B = BT * 4, WS_B = BN * 4;
-    static constexpr int STAGE = X_B + W_B + XS_B + WS_B, STAGES = 3;
+    static constexpr int STAGE = X_B + W_B + XS_B + WS_B;
+    static constexpr int STAGES = 4 * STAGE <= 160 * 1024 ? 4 : 3;
     static constexpr int X_INSTR = (X_B / 1024 + 7) / 8;           // 1 KB loads of x per wave per stage
     static constexpr int W_INSTR = W_B / 1024 / 8;
     static constexpr int LOADS = X_INSTR + W_INSTR + 1;
@@ -297,6 +347,8 @@ template <int N>
 EM_DEV void wait_loads_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
 }
+
+template <int I> struct Set { static constexpr int value = I; };     // one of two register sets
 
 // Segment slot of row r's 16-byte segment s.
 template <int ROW_B>
@@ -379,36 +431,65 @@ mxp_gemm(MxProduct a) {
 #pragma unroll
         for (int j = 0; j < NJ; ++j) acc[p][j] = zero4();
 
-    fetch(0);
-    if (steps > 1) fetch(1);
-    for (int st = 0; st < steps; ++st) {
-        // step st has landed (the next one may be in flight), and every wave is
-        // done with the stage that step st + 2 overwrites
-        if (st + 1 < steps) wait_loads_barrier<C::LOADS>(); else wait_loads_barrier<0>();
-        if (st + 2 < steps) fetch(st + 2);
-        const uint8_t* X = lds + (st % C::STAGES) * C::STAGE;
-        const uint8_t* W = X + C::X_B;
-        const uint8_t* WS = W + C::W_B;
-        const uint8_t* XS = WS + C::WS_B;
-        i32x8 xf[NJ];
-        int xs[NJ];
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const int r = 16 * (NJ * wt + j) + m;
-            const uint4 lo = ldg16(X + r * XB + 16 * swz<XB>(r, g));
-            uint4 hi = make_uint4(0u, 0u, 0u, 0u);
-            if constexpr (FMT == kMxFp8) hi = ldg16(X + r * XB + 16 * swz<XB>(r, 4 + g));
-            xf[j] = i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-            xs[j] = XS[4 * r + g];
+    // Fragments of x and the first one of W are read a step ahead of their
+    // products, the others of W one column subtile ahead, so that the matrix
+    // cores have operands from the first cycle after a barrier and the LDS reads
+    // run under the products.
+    uint4 xlo[2][NJ], xhi[2][NJ], wf[2];
+    int xs[2][NJ];
+    int wsc[2];
+    auto stage_of = [&](int st) -> const uint8_t* { return lds + (st % C::STAGES) * C::STAGE; };
+    auto read_x = [&](auto set, const uint8_t* X, int u) {            // unit u of the XU reads of a step
+        constexpr int f = decltype(set)::value;
+        const int j = FMT == kMxFp8 ? u >> 1 : u, r = 16 * (NJ * wt + j) + m;
+        if (FMT == kMxFp4 || !(u & 1)) {
+            xlo[f][j] = ldg16(X + r * XB + 16 * swz<XB>(r, g));
+            xs[f][j] = X[C::X_B + C::W_B + C::WS_B + 4 * r + g];
+        } else {
+            xhi[f][j] = ldg16(X + r * XB + 16 * swz<XB>(r, 4 + g));
         }
+    };
+    auto read_w = [&](int i, const uint8_t* X, int p) {
+        const int r = 16 * (NI * wn + p) + m;
+        wf[i] = ldg16(X + C::X_B + r * 64 + 16 * swz<64>(r, g));
+        wsc[i] = X[C::X_B + C::W_B + 4 * r + g];
+    };
+    constexpr int XU = FMT == kMxFp8 ? 2 * NJ : NJ;
+    auto step = [&](int st, auto set) {
+        constexpr int f = decltype(set)::value;
+        // stage st + 1 has landed (the ones after it may be in flight), and every
+        // wave is done with the stage that the next fetch overwrites
+        if (st + C::STAGES - 2 < steps) wait_loads_barrier<C::LOADS * (C::STAGES - 3)>();
+        else wait_loads_barrier<0>();
+        if (st + C::STAGES - 1 < steps) fetch(st + C::STAGES - 1);
+        const uint8_t* X = stage_of(st);
+        const uint8_t* Xn = stage_of(st + 1);                         // past the last step: read, never used
 #pragma unroll
         for (int p = 0; p < NI; ++p) {
-            const int r = 16 * (NI * wn + p) + m;
-            const uint4 wf = ldg16(W + r * 64 + 16 * swz<64>(r, g));
-            const int wsc = WS[4 * r + g];
+            read_w((p + 1) & 1, p + 1 < NI ? X : Xn, (p + 1) % NI);
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) acc[p][j] = mfma_mx<FMT>(wf, wsc, xf[j], xs[j], acc[p][j]);
+            for (int u = p * XU / NI; u < (p + 1) * XU / NI; ++u) read_x(Set<1 - f>{}, Xn, u);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const uint4 lo = xlo[f][j], hi = xhi[f][j];
+                const i32x8 xf = {(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+                acc[p][j] = mfma_mx<FMT>(wf[p & 1], wsc[p & 1], xf, xs[f][j], acc[p][j]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    if constexpr (FMT == kMxFp4) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) xhi[0][j] = xhi[1][j] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    for (int st = 0; st < C::STAGES - 1 && st < steps; ++st) fetch(st);
+    wait_loads_barrier<0>();
+#pragma unroll
+    for (int u = 0; u < XU; ++u) read_x(Set<0>{}, stage_of(0), u);
+    read_w(0, stage_of(0), 0);
+    for (int st = 0; st < steps; st += 2) {
+        step(st, Set<0>{});
+        if (st + 1 < steps) step(st + 1, Set<1>{});
     }
 
     // ---- y: lane (g, m) holds columns 4 g .. 4 g + 3 of each column subtile, x row m
@@ -417,8 +498,13 @@ mxp_gemm(MxProduct a) {
         const int r = t.r0 + 16 * (NJ * wt + j) + m;
         if (r >= t.r1) continue;
         const bool live = x_row(a, r) >= 0;
+        if (a.vec && n0 + C::BN <= a.N) {
 #pragma unroll
-        for (int p = 0; p < NI; ++p) store4(a, r, n0 + 16 * (NI * wn + p) + 4 * g, live ? acc[p][j] : zero4());
+            for (int p = 0; p < NI; ++p) store4(a, r, n0 + 16 * (NI * wn + p) + 4 * g, live ? acc[p][j] : zero4(), true);
+        } else {
+#pragma unroll
+            for (int p = 0; p < NI; ++p) store4(a, r, n0 + 16 * (NI * wn + p) + 4 * g, live ? acc[p][j] : zero4(), false);
+        }
     }
 }
 
@@ -430,13 +516,13 @@ int64_t max_row_tiles(const MxProduct& a, int BT) {
     return a.offsets ? a.R / BT + (a.M < a.R ? a.M : a.R) : (a.R + BT - 1) / BT;
 }
 
-template <int NS>
+template <int NS, bool FUSED>
 hipError_t launch_stream(const MxProduct& a, hipStream_t s) {
     constexpr int NC = 2;
     const dim3 grid((a.N + 16 * NC - 1) / (16 * NC), (unsigned)max_row_tiles(a, 16 * NS));
     prof_begin(s);
-    if (a.fmt == kMxFp4) mxp_stream<kMxFp4, NS, NC><<<grid, 256, 0, s>>>(a);
-    else mxp_stream<kMxFp8, NS, NC><<<grid, 256, 0, s>>>(a);
+    if (a.fmt == kMxFp4) mxp_stream<kMxFp4, NS, NC, FUSED><<<grid, 256, 0, s>>>(a);
+    else mxp_stream<kMxFp8, NS, NC, FUSED><<<grid, 256, 0, s>>>(a);
     prof_end(s, "mxp_stream");
     return hipGetLastError();
 }
@@ -459,14 +545,16 @@ size_t mx_product_ws_bytes(const MxProduct& a) {
 }
 
 hipError_t launch_mx_product(MxProduct a, void* ws, hipStream_t s) {
-    const int live = a.offsets && a.M < a.R ? a.M : 1;      // matrices that the rows spread over
+    const int live = !a.offsets ? 1 : a.M < a.R ? a.M : a.R;   // matrices that the rows spread over
     const int64_t avg = ((int64_t)a.R + live - 1) / live;
-    if (avg <= 64) return avg <= 16 ? launch_stream<1>(a, s) : avg <= 32 ? launch_stream<2>(a, s) : launch_stream<4>(a, s);
+    if (a.T <= 16 && avg <= 16) return launch_stream<1, true>(a, s);
     a.xq = static_cast<uint8_t*>(ws);
     a.xs = a.xq + (((size_t)a.T * a.K / (a.fmt == kMxFp4 ? 2 : 1) + 255) & ~(size_t)255);
     const MxRows rows{a.T, a.T, a.K, a.x_stride, a.fmt, 0};
     const hipError_t e = launch_mx_quantize(rows, a.x, const_cast<uint8_t*>(a.xq), const_cast<uint8_t*>(a.xs), s);
     if (e != hipSuccess) return e;
+    if (avg <= 64)
+        return avg <= 16 ? launch_stream<1, false>(a, s) : avg <= 32 ? launch_stream<2, false>(a, s) : launch_stream<4, false>(a, s);
     return avg >= 192 ? launch_gemm<256>(a, s) : launch_gemm<64>(a, s);
 }
 
