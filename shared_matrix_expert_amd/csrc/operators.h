@@ -47,6 +47,7 @@ hipError_t launch_mx_product(MxProduct a, void* ws, hipStream_t s);
 // ---- router load and losses (router_train.hip)
 struct RouterLoad {
     int T, E, k, S, vec;            // vec: logit rows take 16-byte accesses
+    int chunk;                      // tokens per workgroup
     const float* logits;            // [T][E]
     const int32_t* topk_idx;        // [T][k]
     const int32_t* seq_offsets;     // [S + 1] or null (S = 1: every token)
@@ -67,6 +68,7 @@ struct RouterGrad {
     int T, E, k, S, d, vec;
     int Tp, Ep;                     // T and E up to multiples of 32
     int slices;                     // token slices of dW_r
+    int chunk;                      // tokens per workgroup of rt_dlogits
     const float* logits; const int32_t* topk_idx; const float* topk_w;
     const float* d_topk_w;          // [T][k] or null
     const float* d_loss;            // [2] or null
@@ -76,7 +78,7 @@ struct RouterGrad {
     // workspace
     uint16_t* planes;               // [3][Tp][Ep] bf16: dz = their sum
     float* part_w;                  // [slices][E][d]
-    float* part_b;                  // [Tp / 16][E]
+    float* part_b;                  // [Tp / chunk][E]
 };
 size_t router_grad_ws_bytes(RouterGrad a);
 hipError_t launch_router_grad(RouterGrad a, void* ws, hipStream_t s);

@@ -30,19 +30,44 @@ namespace {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int LCH = 32;        // tokens per workgroup of rt_load
-constexpr int DCH = 16;        // tokens per workgroup of rt_dlogits
+// Tokens per workgroup of rt_load and rt_dlogits (a multiple of its four waves):
+// few enough that small batches still spread over the compute units, where the
+// chain of one token's reductions is what takes the time.
+int load_chunk(int T) { return T <= 2048 ? 4 : T <= 8192 ? 16 : 32; }
+int grad_chunk(int T) { return T <= 4096 ? 4 : 16; }
 
-// ---- wave sums -----------------------------------------------------------------
+// ---- wave reductions: DPP within rows of 16 lanes, two broadcasts across them
+// (no LDS); the same value in every lane.
+template <int CTRL, int ROWS>
+EM_DEV float dpp_f(float v, float old) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp((int)__float_as_uint(old), (int)__float_as_uint(v), CTRL, ROWS, 0xF, false));
+}
+EM_DEV float lane63(float v) { return __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(v), 63)); }
+
 EM_DEV float wave_max(float v) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-    return v;
+    v = fmaxf(v, dpp_f<0xB1, 0xF>(v, v));        // quad_perm [1,0,3,2], [2,3,0,1]
+    v = fmaxf(v, dpp_f<0x4E, 0xF>(v, v));
+    v = fmaxf(v, dpp_f<0x141, 0xF>(v, v));       // row_half_mirror, row_mirror
+    v = fmaxf(v, dpp_f<0x140, 0xF>(v, v));
+    v = fmaxf(v, dpp_f<0x142, 0xA>(v, v));       // row_bcast:15, :31: lane 63 has seen every row
+    v = fmaxf(v, dpp_f<0x143, 0xC>(v, v));
+    return lane63(v);
 }
 EM_DEV float wave_sum(float v) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-    return v;
+    v += dpp_f<0xB1, 0xF>(v, 0.f);
+    v += dpp_f<0x4E, 0xF>(v, 0.f);
+    v += dpp_f<0x141, 0xF>(v, 0.f);
+    v += dpp_f<0x140, 0xF>(v, 0.f);
+    v += dpp_f<0x142, 0xA>(v, 0.f);
+    v += dpp_f<0x143, 0xC>(v, 0.f);
+    return lane63(v);
+}
+
+// A wave's own LDS accesses complete in order; this keeps the compiler from
+// reordering those of different lanes to one place.
+EM_DEV void wave_lds_order() {
+    __builtin_amdgcn_wave_barrier();
+    asm volatile("" ::: "memory");
 }
 
 // ---- sequences -----------------------------------------------------------------
@@ -143,7 +168,7 @@ EM_DEV float softmax_row(float (&v)[NV][4]) {
 }  // namespace
 
 // ------------------------------------------------------------------ the load -----
-// Chunk c of LCH tokens; its part of sequence s goes to slot c + s of the
+// Chunk c of a.chunk tokens; its part of sequence s goes to slot c + s of the
 // partial sums (both grow along the tokens, so a slot has one owner).  Bound by
 // reading the logits once.
 template <int NV>
@@ -154,7 +179,7 @@ rt_load(RouterLoad a) {
     __shared__ double zred[4];
     const Seqs q{a.seq_offsets, a.S, a.T};
     const int tid = threadIdx.x, lane = lane_id(), wv = wave_id();
-    const int t0 = blockIdx.x * LCH, t1 = min(a.T, t0 + LCH);
+    const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
     if (blockIdx.x == 0 && tid == 0) *a.done = 0;
     for (int s = find_seq(q, t0); s < a.S; ++s) {
         if (q.lo(s) >= t1) break;
@@ -214,7 +239,7 @@ rt_load_reduce(RouterLoad a) {
     const int col = threadIdx.x & 63, row = threadIdx.x >> 6;
     const int s = blockIdx.y, e = blockIdx.x * 64 + col;
     const int lo = q.lo(s), hi = q.hi(s), n = hi - lo;
-    const int c0 = lo / LCH, c1 = n > 0 ? (hi - 1) / LCH + 1 : c0;
+    const int c0 = lo / a.chunk, c1 = n > 0 ? (hi - 1) / a.chunk + 1 : c0;
     double p = 0.0;
     int cnt = 0;
     if (e < a.E) {
@@ -277,8 +302,9 @@ rt_load_reduce(RouterLoad a) {
 }
 
 // ------------------------------------------------------------------ dz -----------
-// One wave a token, DCH tokens a workgroup (each wave a run of neighbours, so
-// that the sequence's f stays in registers).  Rows T .. Tp - 1 and columns
+// One wave a token, a.chunk tokens a workgroup (each wave a run of neighbours, so
+// that the sequence's f stays in registers).  The picks' terms meet the row
+// through an LDS row that is zero between tokens.  Rows T .. Tp - 1 and columns
 // E .. Ep - 1 of the planes are zeros.
 template <int NV>
 __global__ void __launch_bounds__(256)
@@ -286,8 +312,8 @@ rt_dlogits(RouterGrad a) {
     __shared__ __attribute__((aligned(16))) float red[4][NV * 256];
     const Seqs q{a.seq_offsets, a.S, a.T};
     const int tid = threadIdx.x, lane = lane_id(), wv = wave_id();
-    constexpr int PER = DCH / 4;
-    const int t0 = blockIdx.x * DCH + wv * PER;
+    const int per = a.chunk / 4;
+    const int t0 = blockIdx.x * a.chunk + wv * per;
     float gb = 0.f, gz = 0.f;
     if (a.d_loss) {
         int live, tokens;
@@ -303,7 +329,11 @@ rt_dlogits(RouterGrad a) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) f[i][c] = acc[i][c] = 0.f;
     if (t0 < a.T) load_row<NV>(nxt, a.logits + (int64_t)t0 * a.E, a.E, a.vec);
-    for (int j = 0; j < PER; ++j) {
+    float* pick_row = red[wv];                          // this wave's picks (the column sums come after them)
+    if (a.d_topk_w)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) *reinterpret_cast<float4*>(&pick_row[256 * i + 4 * lane]) = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < per; ++j) {
         const int t = t0 + j;
         if (t >= a.Tp) break;
         float d[NV][4];
@@ -312,7 +342,7 @@ rt_dlogits(RouterGrad a) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) d[i][c] = t < a.T ? nxt[i][c] : 0.f;
         if (t < a.T) {
-            if (j + 1 < PER && t + 1 < a.T) load_row<NV>(nxt, a.logits + (int64_t)(t + 1) * a.E, a.E, a.vec);
+            if (j + 1 < per && t + 1 < a.T) load_row<NV>(nxt, a.logits + (int64_t)(t + 1) * a.E, a.E, a.vec);
             // the selection weights' gradient: lane j has the token's pick j
             int pick = -1;
             float pv = 0.f;
@@ -363,16 +393,27 @@ rt_dlogits(RouterGrad a) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) d[i][c] = 0.f;
             }
-            // picks in slot order: a fixed order also where one expert is named twice
-            if (a.d_topk_w)
+            // an expert's picks are added in slot order by every lane that names it
+            // (the order stays fixed where one is named twice), then written once
+            if (a.d_topk_w) {
+                float sum = 0.f;
                 for (int p = 0; p < a.k; ++p) {
                     const int e = __builtin_amdgcn_readlane(pick, p);
-                    const float v = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(pv), p));
-#pragma unroll
-                    for (int i = 0; i < NV; ++i)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) d[i][c] += 256 * i + 4 * lane + c == e ? v : 0.f;
+                    const float v = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(pv), p));
+                    sum += pick == e ? v : 0.f;
                 }
+                const bool named = (unsigned)pick < (unsigned)a.E;
+                if (named) pick_row[pick] = sum;
+                wave_lds_order();
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const float4 v = *reinterpret_cast<const float4*>(&pick_row[256 * i + 4 * lane]);
+                    d[i][0] += v.x; d[i][1] += v.y; d[i][2] += v.z; d[i][3] += v.w;
+                }
+                wave_lds_order();
+                if (named) pick_row[pick] = 0.f;
+                wave_lds_order();
+            }
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -438,7 +479,7 @@ enum RtMode { RT_DX = 0, RT_DW = 1 };
 template <int BI_>
 struct RtCfg {
     static constexpr int BI = BI_, BN = 256, BK = 32;
-    static constexpr int WI = BI / 64, WN = BI == 256 ? 2 : 4;      // waves: 64 rows x (256 / WN) columns each
+    static constexpr int WI = BI / 64, WN = 4;                      // waves: 64 rows x 64 columns each
     static constexpr int WAVES = WI * WN, TH = 64 * WAVES;
     static constexpr int NC = BN / WN / 16;                          // columns a lane ends with
     static constexpr int P_B = BI * BK * 2, B_B = BK * BN * 2;       // one plane's tile, B's tile
@@ -446,8 +487,11 @@ struct RtCfg {
     static constexpr int A_INSTR = 3 * P_B / 1024 / WAVES, B_INSTR = B_B / 1024 / WAVES;
 };
 
-EM_DEV void rt_dma16(const void* src, uint32_t dst) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(src), "s"(dst) : "memory", "m0");
+// Direct global -> LDS load of 16 bytes a lane, from base + off to dst + 16 lane
+// (counted by hand: see wait in rt_gemm; no register output).
+EM_DEV void rt_dma16(const void* base, uint32_t off, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 : : "v"(off), "s"(base), "s"(dst) : "memory", "m0");
 }
 
 // Eight K rows of C bf16 columns (C = 4: two words a row, C = 8: four) to C
@@ -481,7 +525,7 @@ EM_DEV void read_rows(uint32_t (&r)[8][C / 2], const uint8_t* p, int row_bytes) 
 }  // namespace
 
 template <int MODE, int BI>
-__global__ void __launch_bounds__(RtCfg<BI>::TH)
+__global__ void __launch_bounds__(RtCfg<BI>::TH) __attribute__((amdgpu_waves_per_eu(BI / 32)))
 rt_gemm(RouterGrad a) {
     using C = RtCfg<BI>;
     constexpr int NC = C::NC;
@@ -506,38 +550,29 @@ rt_gemm(RouterGrad a) {
     const int s0 = MODE == RT_DX ? 0 : (int)((int64_t)steps * z / a.slices);
     const int s1 = MODE == RT_DX ? steps : (int)((int64_t)steps * (z + 1) / a.slices);
 
-    // ---- load sources: 1 KB pieces of the planes' tiles, then of B's
-    const uint8_t* asrc[C::A_INSTR];
-    int64_t astep;
-#pragma unroll
-    for (int p = 0; p < C::A_INSTR; ++p) {
-        const int piece = C::A_INSTR * wv + p, plane = piece / (C::P_B / 1024), in = piece % (C::P_B / 1024);
-        const uint16_t* base = a.planes + (int64_t)plane * a.Tp * a.Ep;
-        if constexpr (MODE == RT_DX) {                       // [BI][32 e]: 64-byte rows, segments swizzled
-            const int r = 16 * in + (lane >> 2);
-            asrc[p] = (const uint8_t*)(base + (int64_t)min(i0 + r, a.Tp - 1) * a.Ep + 8 * ((lane & 3) ^ ((r >> 2) & 3)));
-        } else {                                             // [32 t][BI e]
-            const int o = 512 * in + 8 * lane, r = o / BI, e = o % BI;
-            asrc[p] = (const uint8_t*)(base + (int64_t)r * a.Ep + min(i0 + e, a.Ep - 8));
-        }
-    }
-    astep = MODE == RT_DX ? C::BK * 2 : (int64_t)C::BK * a.Ep * 2;
-    const uint8_t* bsrc[C::B_INSTR];
-    int brow[C::B_INSTR];
-#pragma unroll
-    for (int p = 0; p < C::B_INSTR; ++p) {                   // [32 k][256 n]: two rows a piece
-        brow[p] = 2 * (C::B_INSTR * wv + p) + (lane >> 5);
-        bsrc[p] = (const uint8_t*)(B + min(n0 + 8 * (lane & 31), a.d - 8));
-    }
+    // ---- loads: 1 KB pieces of the planes' tiles, then of B's, each a uniform
+    // base and a lane offset.  Tile rows and columns past the planes' (whose
+    // results are not stored) read on into the workspace's spare bytes.
+    const uint32_t aoff = MODE == RT_DX                      // [BI][32 e]: 64-byte rows, segments swizzled
+        ? (uint32_t)((lane >> 2) * a.Ep * 2 + 16 * ((lane & 3) ^ ((lane >> 4) & 3)))
+        : (uint32_t)((8 * lane / BI) * a.Ep * 2 + 2 * (8 * lane % BI));                   // [32 t][BI e]
+    const uint32_t boff = 2 * min(8 * (lane & 31), a.d - 8 - n0), boff2 = boff + (lane >> 5) * a.d * 2;   // two rows a piece
     const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
     auto fetch = [&](int st) {
         const uint32_t stage = __builtin_amdgcn_readfirstlane(base + (st & 1) * C::STAGE);
 #pragma unroll
-        for (int p = 0; p < C::A_INSTR; ++p) rt_dma16(asrc[p] + st * astep, stage + 1024 * (C::A_INSTR * wv + p));
+        for (int p = 0; p < C::A_INSTR; ++p) {
+            const int piece = C::A_INSTR * wv + p, plane = piece / (C::P_B / 1024), in = piece % (C::P_B / 1024);
+            const uint16_t* src = a.planes + (int64_t)plane * a.Tp * a.Ep
+                + (MODE == RT_DX ? (int64_t)(i0 + 16 * in) * a.Ep + C::BK * st
+                                 : ((int64_t)C::BK * st + 512 * in / BI) * a.Ep + i0);
+            rt_dma16(src, aoff, stage + 1024 * piece);
+        }
 #pragma unroll
-        for (int p = 0; p < C::B_INSTR; ++p)                 // B rows past the end meet zeros of the planes
-            rt_dma16(bsrc[p] + (int64_t)min(C::BK * st + brow[p], rows_b - 1) * a.d * 2,
-                     stage + 3 * C::P_B + 1024 * (C::B_INSTR * wv + p));
+        for (int p = 0; p < C::B_INSTR; ++p) {               // rows past the end repeat the last: they meet zeros
+            const int piece = C::B_INSTR * wv + p, row = min(C::BK * st + 2 * piece, rows_b - 1);
+            rt_dma16(B + (int64_t)row * a.d + n0, row + 1 < rows_b ? boff2 : boff, stage + 3 * C::P_B + 1024 * piece);
+        }
     };
 
     floatx4 acc[4][NC];
@@ -613,7 +648,7 @@ rt_finish(RouterGrad a, int wblocks) {
     }
     const int col = threadIdx.x & 63, row = threadIdx.x >> 6;
     const int e = (blockIdx.x - wblocks) * 64 + col;
-    const int chunks = (a.T + DCH - 1) / DCH;
+    const int chunks = (a.T + a.chunk - 1) / a.chunk;
     double s = 0.0;
     if (e < a.E) {
 #pragma unroll 8
@@ -635,7 +670,7 @@ size_t up(size_t v) { return (v + kAl - 1) & ~(kAl - 1); }
 struct LoadLayout { size_t p, c, z, dots, done, bytes; };
 LoadLayout load_layout(const RouterLoad& a) {
     LoadLayout L{};
-    const size_t slots = (size_t)(a.T + LCH - 1) / LCH + a.S;
+    const size_t slots = (size_t)(a.T + load_chunk(a.T) - 1) / load_chunk(a.T) + a.S;
     size_t off = 0;
     auto take = [&](size_t n) { const size_t o = off; off = up(off + n); return o; };
     L.p = take(slots * a.E * 4);
@@ -650,14 +685,14 @@ LoadLayout load_layout(const RouterLoad& a) {
 struct GradLayout { size_t planes, part_w, part_b, bytes; };
 
 int pad32(int v) { return (v + 31) & ~31; }
-int tile_rows(int n) { return n > 128 ? 256 : 64; }
+int tile_rows(int n) { return n > 64 ? 128 : 64; }
 
 // Token slices of dW_r: as many as give every CU a workgroup, of at least four
 // K steps each.
 int dw_slices(const RouterGrad& a) {
     const int tiles = ((a.d + 255) / 256) * ((a.E + tile_rows(a.E) - 1) / tile_rows(a.E));
     const int most = a.Tp / 32 / 4;
-    int z = 256 / tiles;
+    int z = 512 / tiles;
     z = z < most ? z : most;
     return z < 1 ? 1 : z > 16 ? 16 : z;
 }
@@ -666,9 +701,10 @@ GradLayout grad_layout(const RouterGrad& a) {
     GradLayout L{};
     size_t off = 0;
     auto take = [&](size_t n) { const size_t o = off; off = up(off + n); return o; };
-    L.planes = take((size_t)3 * a.Tp * a.Ep * 2);
+    // the last tile reads up to 255 rows past the last plane (DX), up to 255 columns past its last row (DW)
+    L.planes = take(((size_t)3 * a.Tp + 256) * a.Ep * 2 + 512);
     L.part_w = take((size_t)dw_slices(a) * a.E * a.d * 4);
-    L.part_b = take((size_t)((a.Tp + DCH - 1) / DCH) * a.E * 4);
+    L.part_b = take((size_t)((a.Tp + grad_chunk(a.T) - 1) / grad_chunk(a.T)) * a.E * 4);
     L.bytes = off;
     return L;
 }
@@ -677,11 +713,11 @@ template <int MODE>
 hipError_t launch_rt_gemm(const RouterGrad& a, hipStream_t s, const char* name) {
     const int I = MODE == RT_DX ? a.T : a.E;
     // DX: small tiles where large ones would leave compute units idle
-    const int bi = MODE == RT_DX ? ((int64_t)((I + 255) / 256) * ((a.d + 255) / 256) >= 192 ? 256 : 64) : tile_rows(I);
+    const int bi = MODE == RT_DX ? ((int64_t)((I + 127) / 128) * ((a.d + 255) / 256) >= 192 ? 128 : 64) : tile_rows(I);
     const int64_t tiles = (int64_t)((I + bi - 1) / bi) * ((a.d + 255) / 256) * (MODE == RT_DX ? 1 : a.slices);
     const unsigned grid = (unsigned)((tiles + 7) & ~7ll);
     prof_begin(s);
-    if (bi == 256) rt_gemm<MODE, 256><<<grid, RtCfg<256>::TH, 0, s>>>(a);
+    if (bi == 128) rt_gemm<MODE, 128><<<grid, RtCfg<128>::TH, 0, s>>>(a);
     else rt_gemm<MODE, 64><<<grid, RtCfg<64>::TH, 0, s>>>(a);
     prof_end(s, name);
     return hipGetLastError();
@@ -699,7 +735,8 @@ hipError_t launch_router_load(RouterLoad a, void* ws, hipStream_t s) {
     a.part_z = reinterpret_cast<double*>(base + L.z);
     a.dots = reinterpret_cast<double*>(base + L.dots);
     a.done = reinterpret_cast<uint32_t*>(base + L.done);
-    const int chunks = (a.T + LCH - 1) / LCH;
+    a.chunk = load_chunk(a.T);
+    const int chunks = (a.T + a.chunk - 1) / a.chunk;
     prof_begin(s);
     if (a.E <= 256) rt_load<1><<<chunks, 256, 0, s>>>(a);
     else if (a.E <= 512) rt_load<2><<<chunks, 256, 0, s>>>(a);
@@ -731,7 +768,8 @@ hipError_t launch_router_grad(RouterGrad a, void* ws, hipStream_t s) {
     a.planes = a.dx || a.dw_router ? reinterpret_cast<uint16_t*>(base + L.planes) : nullptr;
     a.part_w = reinterpret_cast<float*>(base + L.part_w);
     a.part_b = a.dbias ? reinterpret_cast<float*>(base + L.part_b) : nullptr;
-    const int chunks = (a.Tp + DCH - 1) / DCH;
+    a.chunk = grad_chunk(a.T);
+    const int chunks = ((a.planes ? a.Tp : a.T) + a.chunk - 1) / a.chunk;
     prof_begin(s);
     if (a.E <= 256) rt_dlogits<1><<<chunks, 256, 0, s>>>(a);
     else if (a.E <= 512) rt_dlogits<2><<<chunks, 256, 0, s>>>(a);
