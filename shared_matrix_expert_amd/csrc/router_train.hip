@@ -553,8 +553,8 @@ rt_gemm(RouterGrad a) {
     // ---- loads: 1 KB pieces of the planes' tiles, then of B's, each a uniform
     // base and a lane offset.  Tile rows and columns past the planes' (whose
     // results are not stored) read on into the workspace's spare bytes.
-    const uint32_t aoff = MODE == RT_DX                      // [BI][32 e]: 64-byte rows, segments swizzled
-        ? (uint32_t)((lane >> 2) * a.Ep * 2 + 16 * ((lane & 3) ^ ((lane >> 4) & 3)))
+    const uint32_t aoff = MODE == RT_DX                      // [BI][32 e]: 64-byte rows, segments swizzled (as mx_product.hip's)
+        ? (uint32_t)((lane >> 2) * a.Ep * 2 + 16 * ((lane & 3) ^ (-(lane >> 4) & 3)))
         : (uint32_t)((8 * lane / BI) * a.Ep * 2 + 2 * (8 * lane % BI));                   // [32 t][BI e]
     const uint32_t boff = 2 * min(8 * (lane & 31), a.d - 8 - n0), boff2 = boff + (lane >> 5) * a.d * 2;   // two rows a piece
     const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
@@ -599,7 +599,7 @@ rt_gemm(RouterGrad a) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = 64 * wi + 16 * i + m;
-                    af[i] = *reinterpret_cast<const uint4*>(A + p * C::P_B + r * 64 + 16 * (g ^ ((r >> 2) & 3)));
+                    af[i] = *reinterpret_cast<const uint4*>(A + p * C::P_B + r * 64 + 16 * (g ^ (-(r >> 2) & 3)));
                 }
             } else {
                 uint32_t raw[8][2];
@@ -625,8 +625,12 @@ rt_gemm(RouterGrad a) {
             if (r >= I) continue;
             float* o = out + (int64_t)r * a.d + n;
 #pragma unroll
-            for (int c = 0; c < NC; c += 4)
-                *reinterpret_cast<float4*>(o + c) = make_float4(acc[i][c][v], acc[i][c + 1][v], acc[i][c + 2][v], acc[i][c + 3][v]);
+            for (int c = 0; c < NC; c += 4) {
+                // dx streams out past the L2, where W_r and the planes stay
+                const floatx4 w = {acc[i][c][v], acc[i][c + 1][v], acc[i][c + 2][v], acc[i][c + 3][v]};
+                if constexpr (MODE == RT_DX) __builtin_nontemporal_store(w, reinterpret_cast<floatx4*>(o + c));
+                else *reinterpret_cast<floatx4*>(o + c) = w;
+            }
         }
 }
 
