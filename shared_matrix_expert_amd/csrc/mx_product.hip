@@ -24,6 +24,8 @@ namespace em {
 
 namespace {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 EM_DEV uint4 ldg16(const void* p) { return *reinterpret_cast<const uint4*>(p); }
 
 template <int FMT> constexpr int mx_code() { return FMT == kMxFp4 ? 4 : 0; }   // the instruction's format field
@@ -497,17 +499,47 @@ mxp_gemm(MxProduct a) {
     }
 
     // ---- y: lane (g, m) holds columns 4 g .. 4 g + 3 of each column subtile, x row m
+    if (a.vec > 1 && n0 + C::BN <= a.N) {
+        // through the LDS, so that a wave stores whole 256- or 128-byte row
+        // segments, past the L2: 32-byte pieces leave it half-written lines to
+        // merge, and the lines it keeps cost the next kernel their write-back
+        constexpr int RB = NI * 32, RSTR = RB + 16;          // bytes of a wave's row, their LDS stride
+        __syncthreads();                                     // every wave is done with the stages
+        uint8_t* o = lds + wv * (16 * NJ * RSTR);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const int r = t.r0 + 16 * (NJ * wt + j) + m;
+            const bool live = r < t.r1 && x_row(a, r) >= 0;
+#pragma unroll
+            for (int p = 0; p < NI; ++p) {
+                const floatx4 v = live ? acc[p][j] : zero4();
+                const f32x2 lo = {v.x, v.y}, hi = {v.z, v.w};
+                *reinterpret_cast<uint2*>(o + (16 * j + m) * RSTR + 32 * p + 8 * g) =
+                    make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector(lo, bf16x2)),
+                               __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, bf16x2)));
+            }
+        }
+        __builtin_amdgcn_wave_barrier();                     // one wave's LDS accesses complete in order
+        asm volatile("" ::: "memory");
+        constexpr int LPR = RB / 16, RPI = 64 / LPR;         // lanes per row, rows per store
+#pragma unroll
+        for (int i = 0; i < 16 * NJ / RPI; ++i) {
+            const int tr = RPI * i + lane / LPR, r = t.r0 + 16 * NJ * wt + tr;
+            if (r >= t.r1) continue;
+            const u32x4 v = *reinterpret_cast<const u32x4*>(o + tr * RSTR + 16 * (lane % LPR));
+            __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(a.y + (int64_t)r * a.y_stride + n0 + 16 * NI * wn + 8 * (lane % LPR)));
+        }
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
         const int r = t.r0 + 16 * (NJ * wt + j) + m;
         if (r >= t.r1) continue;
         const bool live = x_row(a, r) >= 0;
-        if (a.vec && n0 + C::BN <= a.N) {
 #pragma unroll
-            for (int p = 0; p < NI; ++p) store4(a, r, n0 + 16 * (NI * wn + p) + 4 * g, live ? acc[p][j] : zero4(), true);
-        } else {
-#pragma unroll
-            for (int p = 0; p < NI; ++p) store4(a, r, n0 + 16 * (NI * wn + p) + 4 * g, live ? acc[p][j] : zero4(), false);
+        for (int p = 0; p < NI; ++p) {
+            const int n = n0 + 16 * (NI * wn + p);
+            store4(a, r, n + 4 * g, live ? acc[p][j] : zero4(), a.vec && n + 16 <= a.N);
         }
     }
 }

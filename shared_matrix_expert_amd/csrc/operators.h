@@ -37,7 +37,7 @@ struct MxProduct {
     const uint8_t* scales;      // [M][K/128][N][4] E8M0
     uint16_t* y;                // [R] rows of N bf16, y_stride elements apart
     int64_t y_stride;
-    int vec;                    // y rows take 8-byte stores at every fourth column
+    int vec;                    // y rows take 8-byte (1) or 16-byte (2) stores at every fourth (eighth) column
     uint8_t* xq;                // workspace: x's codes [T][K] or [T][K/2] ...
     uint8_t* xs;                // ... and scales [K/128][T][4]
 };
