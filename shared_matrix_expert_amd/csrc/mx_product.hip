@@ -37,6 +37,34 @@ EM_DEV floatx4 mfma_mx(const uint4& w, int ws, const i32x8& x, int xs, const flo
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, x, acc, 4, mx_code<FMT>(), 0, ws, 0, xs);
 }
 
+// Four products of one W fragment with four x fragments, written out with the
+// accumulators in the accumulation registers: with 256 of them a wave the
+// compiler copies operands back and forth instead.  It sees the operands' loads
+// and waits for them; the block waits out vector writes of its operands itself.
+template <int FMT> struct XOp { typedef int type __attribute__((ext_vector_type(FMT == kMxFp4 ? 4 : 8))); };
+
+template <int FMT>
+EM_DEV void mfma_mx4(floatx4 (&c)[4], const uint4& w, int ws, const typename XOp<FMT>::type (&x)[4], const int (&xs)[4]) {
+#define EM_MX4(FIELDS)                                                                              \
+    asm volatile("s_nop 1\n\t"                                                                      \
+                 "v_mfma_scale_f32_16x16x128_f8f6f4 %0, %4, %5, %0, %9, %10 op_sel_hi:[0,0,0] " FIELDS "\n\t" \
+                 "v_mfma_scale_f32_16x16x128_f8f6f4 %1, %4, %6, %1, %9, %11 op_sel_hi:[0,0,0] " FIELDS "\n\t" \
+                 "v_mfma_scale_f32_16x16x128_f8f6f4 %2, %4, %7, %2, %9, %12 op_sel_hi:[0,0,0] " FIELDS "\n\t" \
+                 "v_mfma_scale_f32_16x16x128_f8f6f4 %3, %4, %8, %3, %9, %13 op_sel_hi:[0,0,0] " FIELDS \
+                 : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3])                                   \
+                 : "v"(w4), "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]), "v"(ws), "v"(xs[0]), "v"(xs[1]), "v"(xs[2]), "v"(xs[3]))
+    typedef int i32x4 __attribute__((ext_vector_type(4)));
+    const i32x4 w4 = {(int)w.x, (int)w.y, (int)w.z, (int)w.w};
+    if constexpr (FMT == kMxFp4) EM_MX4("cbsz:4 blgp:4");
+    else EM_MX4("cbsz:4");
+#undef EM_MX4
+}
+
+// Products in flight are done before what follows reads these accumulators.
+EM_DEV void mfma_settle(floatx4 (&c)[4]) {
+    asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3]));
+}
+
 // ---- rows ------------------------------------------------------------------
 // A row tile: rows [r0, r1) of y, all of matrix m.  Row tiles are numbered
 // matrix by matrix; `total` is their count, r1 = 0 marks no tile.
@@ -310,27 +338,32 @@ mxp_stream(MxProduct a) {
 }
 
 // ------------------------------------------------------------------ many rows ----
-// A workgroup of 8 waves takes BT rows x 256 columns, WN x (8 / WN) waves of
-// (256 / WN) columns x (BT WN / 8) rows.  Each K step's codes and scale words
-// arrive by direct global -> LDS loads, two steps ahead in three stages; every
-// wave issues the same number of loads a step, so one counted wait covers them.
-// A code row is 64 (E2M1) or 128 (E4M3) bytes; its 16-byte segments are stored
-// XOR-swizzled by the row, so that the 16 rows of a fragment read fall on
-// distinct bank groups.
+// A workgroup takes BT rows x 256 columns in WN x WT waves.  Each K step's codes
+// and scale words arrive by direct global -> LDS loads, STAGES - 1 steps ahead;
+// every wave issues the same number of loads a step, so one counted wait covers
+// them.  A code row is 64 (E2M1) or 128 (E4M3) bytes; its 16-byte segments are
+// stored XOR-swizzled by the row against bank conflicts.
+//
+// The 256-row tile runs one wave a SIMD on 128 x 128 of it each: the 256
+// accumulators fill half the register file and every operand read from the LDS
+// feeds eight products, so that the LDS delivers 96 (FP8) or 64 KB (FP4) a step
+// where eight waves of 128 x 64 would read 128 or 96.
 namespace {
+
+constexpr int gemm_threads(int BT) { return BT == 256 ? 256 : 512; }
 
 template <int FMT, int BT_>
 struct GemmCfg {
-    static constexpr int BT = BT_, BN = 256, TH = 512;
-    static constexpr int WN = BT == 256 ? 2 : 4, WT = 8 / WN;
+    static constexpr int BT = BT_, BN = 256;
+    static constexpr int WN = BT == 256 ? 2 : 4, WT = 2, NW = WN * WT;
     static constexpr int NI = BN / WN / 16, NJ = BT / WT / 16;     // column and row subtiles of a wave
     static constexpr int XB = FMT == kMxFp4 ? 64 : 128;            // bytes of an x row per step
     static constexpr int X_B = BT * XB, W_B = BN * 64, XS_B = BT * 4, WS_B = BN * 4;
     static constexpr int STAGE = X_B + W_B + XS_B + WS_B;
     static constexpr int STAGES = 4 * STAGE <= 160 * 1024 ? 4 : 3;
-    static constexpr int X_INSTR = (X_B / 1024 + 7) / 8;           // 1 KB loads of x per wave per stage
-    static constexpr int W_INSTR = W_B / 1024 / 8;
-    static constexpr int LOADS = X_INSTR + W_INSTR + 1;
+    static constexpr int X_P = X_B / 1024, W_P = W_B / 1024, S_P = (BN + BT) / 64;   // wave loads a stage
+    static constexpr int X_INSTR = (X_P + NW - 1) / NW, W_INSTR = W_P / NW, S_INSTR = (S_P + NW - 1) / NW;
+    static constexpr int LOADS = X_INSTR + W_INSTR + S_INSTR;
 };
 
 // Direct global -> LDS load of 16 (or 4) bytes a lane to `dst` + 16 (4) * lane.
@@ -340,8 +373,11 @@ struct GemmCfg {
 EM_DEV void dma16(const uint8_t* src, uint32_t dst) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(src), "s"(dst) : "memory", "m0");
 }
-EM_DEV void dma4(const uint8_t* src, uint32_t dst) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" : : "v"(src), "s"(dst) : "memory", "m0");
+EM_DEV void dma16(const uint8_t* base, uint32_t off, uint32_t dst) {     // base: the same for the wave
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "s"(dst) : "memory", "m0");
+}
+EM_DEV void dma4(const uint8_t* base, uint32_t off, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" : : "v"(off), "s"(base), "s"(dst) : "memory", "m0");
 }
 
 // At most N of this wave's loads in flight, its LDS reads done; then the barrier.
@@ -363,7 +399,7 @@ EM_DEV int swz(int r, int s) { return ROW_B == 128 ? s ^ ((r >> 1) & 7) : s ^ (-
 }  // namespace
 
 template <int FMT, int BT>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(gemm_threads(BT)) __attribute__((amdgpu_waves_per_eu(BT == 256 ? 1 : 2)))
 mxp_gemm(MxProduct a) {
     using C = GemmCfg<FMT, BT>;
     constexpr int NI = C::NI, NJ = C::NJ, XB = C::XB;
@@ -386,116 +422,137 @@ mxp_gemm(MxProduct a) {
     if (t.r1 == 0) return;
     const int n0 = tn * C::BN, nrow = t.r1 - t.r0;
 
-    // ---- load sources (one per wave instruction of a stage)
+    // ---- load sources (one per wave instruction of a stage; where the pieces run
+    // out before the waves, the first ones are loaded again)
     const int steps = a.K / kMxStep;
-    const uint8_t* xsrc[C::X_INSTR];
-    const uint8_t* wsrc[C::W_INSTR];
-    int xdst[C::X_INSTR];
+    const uint8_t* xsrc[C::X_INSTR];                    // x rows may lie anywhere in a workspace of any size
+    uint32_t woff[C::W_INSTR], soff[C::S_INSTR];
     constexpr int XR = 1024 / XB;                       // x rows per load
 #pragma unroll
     for (int q = 0; q < C::X_INSTR; ++q) {
-        const int piece = (C::X_INSTR * wv + q) % (C::X_B / 1024);   // a tile of fewer pieces than waves: loaded twice
-        const int tr = XR * piece + lane / (XB / 16), slot = lane % (XB / 16);
-        const int r = t.r0 + min(tr, nrow - 1);
-        xsrc[q] = a.xq + (int64_t)max(x_row(a, r), 0) * (a.K * XB / 128) + 16 * swz<XB>(tr, slot);
-        xdst[q] = piece * 1024;
+        const int tr = XR * ((C::X_INSTR * wv + q) % C::X_P) + lane / (XB / 16);
+        xsrc[q] = a.xq + (int64_t)max(x_row(a, t.r0 + min(tr, nrow - 1)), 0) * (a.K * XB / 128)
+                  + 16 * swz<XB>(tr, lane % (XB / 16));
     }
-    const uint8_t* wm = a.codes + (int64_t)t.m * a.N * (a.K / 2);
+    const uint8_t* wbase = a.codes + ((int64_t)t.m * a.N + n0) * (a.K / 2);
+    const uint8_t* wsbase = a.scales + ((int64_t)t.m * steps * a.N + n0) * 4;
 #pragma unroll
     for (int q = 0; q < C::W_INSTR; ++q) {
         const int tr = 16 * (C::W_INSTR * wv + q) + lane / 4;
-        wsrc[q] = wm + (int64_t)min(n0 + tr, a.N - 1) * (a.K / 2) + 16 * swz<64>(tr, lane % 4);
+        woff[q] = min(tr, a.N - 1 - n0) * (a.K / 2) + 16 * swz<64>(tr, lane % 4);
     }
-    // scale words: waves 0-3 the W rows', waves 4-7 the x rows' (BT = 64: the same 64)
-    const uint8_t* ssrc;
-    int64_t sstep;
-    int sdst;
-    if (wv < 4) {
-        ssrc = a.scales + ((int64_t)t.m * steps * a.N + min(n0 + 64 * wv + lane, a.N - 1)) * 4;
-        sstep = (int64_t)a.N * 4;
-        sdst = C::X_B + C::W_B + 256 * wv;
-    } else {
-        const int p = (wv - 4) % (BT / 64);
-        ssrc = a.xs + (int64_t)max(x_row(a, t.r0 + min(64 * p + lane, nrow - 1)), 0) * 4;
-        sstep = (int64_t)a.T * 4;
-        sdst = C::X_B + C::W_B + C::WS_B + 256 * p;
+    // scale words of 64 rows a piece: W's, then x's
+#pragma unroll
+    for (int q = 0; q < C::S_INSTR; ++q) {
+        const int piece = (C::S_INSTR * wv + q) % C::S_P, tr = 64 * piece + lane;
+        soff[q] = piece < C::BN / 64 ? 4 * min(tr, a.N - 1 - n0)
+                                     : 4 * max(x_row(a, t.r0 + min(tr - C::BN, nrow - 1)), 0);
     }
     const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
-    auto fetch = [&](int st) {
-        const uint32_t stage = __builtin_amdgcn_readfirstlane(base + (st % C::STAGES) * C::STAGE);
-#pragma unroll
-        for (int q = 0; q < C::X_INSTR; ++q) dma16(xsrc[q] + (int64_t)st * XB, stage + xdst[q]);
-#pragma unroll
-        for (int q = 0; q < C::W_INSTR; ++q) dma16(wsrc[q] + (int64_t)st * 64, stage + C::X_B + 1024 * (C::W_INSTR * wv + q));
-        dma4(ssrc + st * sstep, stage + sdst);
+    auto fetch = [&](int st, int to, int u) {           // load u of step st's, into the stage of step `to`
+        const uint32_t stage = __builtin_amdgcn_readfirstlane(base + (to % C::STAGES) * C::STAGE);
+        if (u < C::X_INSTR) {
+            dma16(xsrc[u] + (int64_t)st * XB, stage + 1024 * ((C::X_INSTR * wv + u) % C::X_P));
+        } else if (u < C::X_INSTR + C::W_INSTR) {
+            const int q = u - C::X_INSTR;
+            dma16(wbase + st * 64, woff[q], stage + C::X_B + 1024 * (C::W_INSTR * wv + q));
+        } else {
+            const int q = u - C::X_INSTR - C::W_INSTR, piece = (C::S_INSTR * wv + q) % C::S_P;
+            const uint8_t* src = piece < C::BN / 64 ? wsbase + (int64_t)st * a.N * 4 : a.xs + (int64_t)st * a.T * 4;
+            dma4(src, soff[q], stage + C::X_B + C::W_B + 256 * piece);
+        }
     };
 
     const int wn = wv / C::WT, wt = wv % C::WT;
-    floatx4 acc[NI][NJ];
+    constexpr int JB = NJ < 4 ? NJ : 4;                              // row subtiles of a product block
+    floatx4 acc[NI][NJ / JB][JB];
 #pragma unroll
     for (int p = 0; p < NI; ++p)
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[p][j] = zero4();
+        for (int j = 0; j < NJ; ++j) acc[p][j / JB][j % JB] = zero4();
 
-    // Fragments of x and the first one of W are read a step ahead of their
-    // products, the others of W one column subtile ahead, so that the matrix
-    // cores have operands from the first cycle after a barrier and the LDS reads
-    // run under the products.
-    uint4 xlo[2][NJ], xhi[2][NJ], wf[2];
-    int xs[2][NJ];
-    int wsc[2];
+    // Fragments of x are read a step ahead of their products, those of W two
+    // column subtiles ahead, so that the matrix cores have operands from the first
+    // cycle after a barrier and the LDS reads run under the products.
+    typename XOp<FMT>::type xf[2][NJ / JB][JB];
+    int xs[2][NJ / JB][JB];
+    uint4 wf[4];
+    int wsc[4];
+    // this lane's places in a subtile's rows (16 rows on, the swizzle is the same)
+    const int xlo = m * XB + 16 * swz<XB>(m, g), xhi = m * XB + 16 * swz<XB>(m, 4 + g), wlo = m * 64 + 16 * swz<64>(m, g);
+    const int sc = 4 * m + g;
     auto stage_of = [&](int st) -> const uint8_t* { return lds + (st % C::STAGES) * C::STAGE; };
     auto read_x = [&](auto set, const uint8_t* X, int u) {            // unit u of the XU reads of a step
         constexpr int f = decltype(set)::value;
-        const int j = FMT == kMxFp8 ? u >> 1 : u, r = 16 * (NJ * wt + j) + m;
-        if (FMT == kMxFp4 || !(u & 1)) {
-            xlo[f][j] = ldg16(X + r * XB + 16 * swz<XB>(r, g));
-            xs[f][j] = X[C::X_B + C::W_B + C::WS_B + 4 * r + g];
-        } else {
-            xhi[f][j] = ldg16(X + r * XB + 16 * swz<XB>(r, 4 + g));
-        }
+        const int j = FMT == kMxFp8 ? u >> 1 : u, h = FMT == kMxFp8 ? u & 1 : 0, r = 16 * (NJ * wt + j);
+        const uint4 v = ldg16(X + r * XB + (h ? xhi : xlo));
+        auto& o = xf[f][j / JB][j % JB];
+        o[4 * h] = (int)v.x; o[4 * h + 1] = (int)v.y; o[4 * h + 2] = (int)v.z; o[4 * h + 3] = (int)v.w;
+        if (h == 0) xs[f][j / JB][j % JB] = X[C::X_B + C::W_B + C::WS_B + 4 * r + sc];
     };
-    auto read_w = [&](int i, const uint8_t* X, int p) {
-        const int r = 16 * (NI * wn + p) + m;
-        wf[i] = ldg16(X + C::X_B + r * 64 + 16 * swz<64>(r, g));
-        wsc[i] = X[C::X_B + C::W_B + 4 * r + g];
+    auto read_w = [&](const uint8_t* X, int p) {
+        const int r = 16 * (NI * wn + p);
+        wf[p & 3] = ldg16(X + C::X_B + r * 64 + wlo);
+        wsc[p & 3] = X[C::X_B + C::W_B + 4 * r + sc];
     };
     constexpr int XU = FMT == kMxFp8 ? 2 * NJ : NJ;
     auto step = [&](int st, auto set) {
         constexpr int f = decltype(set)::value;
         // stage st + 1 has landed (the ones after it may be in flight), and every
-        // wave is done with the stage that the next fetch overwrites
-        if (st + C::STAGES - 2 < steps) wait_loads_barrier<C::LOADS * (C::STAGES - 3)>();
-        else wait_loads_barrier<0>();
-        if (st + C::STAGES - 1 < steps) fetch(st + C::STAGES - 1);
+        // wave is done with the stage that the next loads overwrite.  Past the last
+        // step the loads repeat it into stages that nothing reads: no branch here
+        // (with one, the accumulators are copied at its join).  They go out a few at
+        // a time between the products, which they would hold up together
+        wait_loads_barrier<C::LOADS * (C::STAGES - 3)>();
+        const int ahead = min(st + C::STAGES - 1, steps - 1);
         const uint8_t* X = stage_of(st);
         const uint8_t* Xn = stage_of(st + 1);                         // past the last step: read, never used
 #pragma unroll
         for (int p = 0; p < NI; ++p) {
-            read_w((p + 1) & 1, p + 1 < NI ? X : Xn, (p + 1) % NI);
+            read_w(p + 2 < NI ? X : Xn, (p + 2) % NI);
 #pragma unroll
             for (int u = p * XU / NI; u < (p + 1) * XU / NI; ++u) read_x(Set<1 - f>{}, Xn, u);
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const uint4 lo = xlo[f][j], hi = xhi[f][j];
-                const i32x8 xf = {(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-                acc[p][j] = mfma_mx<FMT>(wf[p & 1], wsc[p & 1], xf, xs[f][j], acc[p][j]);
+            for (int u = p * C::LOADS / NI; u < (p + 1) * C::LOADS / NI; ++u) fetch(ahead, st + C::STAGES - 1, u);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int b = 0; b < NJ / JB; ++b) {
+                if constexpr (JB == 4) {
+                    mfma_mx4<FMT>(acc[p][b], wf[p & 3], wsc[p & 3], xf[f][b], xs[f][b]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < JB; ++j) {
+                        const auto& x = xf[f][b][j];
+                        i32x8 x8 = {x[0], x[1], x[2], x[3], 0, 0, 0, 0};
+                        if constexpr (FMT == kMxFp8) x8 = x;
+                        acc[p][b][j] = mfma_mx<FMT>(wf[p & 3], wsc[p & 3], x8, xs[f][b][j], acc[p][b][j]);
+                    }
+                }
             }
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    if constexpr (FMT == kMxFp4) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) xhi[0][j] = xhi[1][j] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    for (int st = 0; st < C::STAGES - 1 && st < steps; ++st) fetch(st);
-    wait_loads_barrier<0>();
+    for (int st = 0; st < C::STAGES - 1; ++st)
+#pragma unroll
+        for (int u = 0; u < C::LOADS; ++u) fetch(min(st, steps - 1), st, u);
+    wait_loads_barrier<C::LOADS * (C::STAGES - 2)>();
 #pragma unroll
     for (int u = 0; u < XU; ++u) read_x(Set<0>{}, stage_of(0), u);
-    read_w(0, stage_of(0), 0);
-    for (int st = 0; st < steps; st += 2) {
+    read_w(stage_of(0), 0);
+    read_w(stage_of(0), 1);
+    int st = 0;
+    for (; st + 1 < steps; st += 2) {
         step(st, Set<0>{});
-        if (st + 1 < steps) step(st + 1, Set<1>{});
+        step(st + 1, Set<1>{});
+    }
+    if (st < steps) step(st, Set<0>{});
+    wait_loads_barrier<0>();                                          // nothing more lands in the stages
+    if constexpr (JB == 4) {
+#pragma unroll
+        for (int p = 0; p < NI; ++p)
+#pragma unroll
+            for (int b = 0; b < NJ / JB; ++b) mfma_settle(acc[p][b]);
     }
 
     // ---- y: lane (g, m) holds columns 4 g .. 4 g + 3 of each column subtile, x row m
@@ -504,7 +561,6 @@ mxp_gemm(MxProduct a) {
         // segments, past the L2: 32-byte pieces leave it half-written lines to
         // merge, and the lines it keeps cost the next kernel their write-back
         constexpr int RB = NI * 32, RSTR = RB + 16;          // bytes of a wave's row, their LDS stride
-        __syncthreads();                                     // every wave is done with the stages
         uint8_t* o = lds + wv * (16 * NJ * RSTR);
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
@@ -512,7 +568,7 @@ mxp_gemm(MxProduct a) {
             const bool live = r < t.r1 && x_row(a, r) >= 0;
 #pragma unroll
             for (int p = 0; p < NI; ++p) {
-                const floatx4 v = live ? acc[p][j] : zero4();
+                const floatx4 v = live ? acc[p][j / JB][j % JB] : zero4();
                 const f32x2 lo = {v.x, v.y}, hi = {v.z, v.w};
                 *reinterpret_cast<uint2*>(o + (16 * j + m) * RSTR + 32 * p + 8 * g) =
                     make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector(lo, bf16x2)),
@@ -539,7 +595,7 @@ mxp_gemm(MxProduct a) {
 #pragma unroll
         for (int p = 0; p < NI; ++p) {
             const int n = n0 + 16 * (NI * wn + p);
-            store4(a, r, n + 4 * g, live ? acc[p][j] : zero4(), a.vec && n + 16 <= a.N);
+            store4(a, r, n + 4 * g, live ? acc[p][j / JB][j % JB] : zero4(), a.vec && n + 16 <= a.N);
         }
     }
 }
@@ -567,8 +623,8 @@ template <int BT>
 hipError_t launch_gemm(const MxProduct& a, hipStream_t s) {
     const int64_t tiles = max_row_tiles(a, BT) * ((a.N + 255) / 256);
     prof_begin(s);
-    if (a.fmt == kMxFp4) mxp_gemm<kMxFp4, BT><<<(unsigned)((tiles + 7) & ~7ll), 512, 0, s>>>(a);
-    else mxp_gemm<kMxFp8, BT><<<(unsigned)((tiles + 7) & ~7ll), 512, 0, s>>>(a);
+    if (a.fmt == kMxFp4) mxp_gemm<kMxFp4, BT><<<(unsigned)((tiles + 7) & ~7ll), gemm_threads(BT), 0, s>>>(a);
+    else mxp_gemm<kMxFp8, BT><<<(unsigned)((tiles + 7) & ~7ll), gemm_threads(BT), 0, s>>>(a);
     prof_end(s, "mxp_gemm");
     return hipGetLastError();
 }
