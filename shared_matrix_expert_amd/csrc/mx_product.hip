@@ -37,33 +37,8 @@ EM_DEV floatx4 mfma_mx(const uint4& w, int ws, const i32x8& x, int xs, const flo
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, x, acc, 4, mx_code<FMT>(), 0, ws, 0, xs);
 }
 
-// Four products of one W fragment with four x fragments, written out with the
-// accumulators in the accumulation registers: with 256 of them a wave the
-// compiler copies operands back and forth instead.  It sees the operands' loads
-// and waits for them; the block waits out vector writes of its operands itself.
+// An x fragment's registers.
 template <int FMT> struct XOp { typedef int type __attribute__((ext_vector_type(FMT == kMxFp4 ? 4 : 8))); };
-
-template <int FMT>
-EM_DEV void mfma_mx4(floatx4 (&c)[4], const uint4& w, int ws, const typename XOp<FMT>::type (&x)[4], const int (&xs)[4]) {
-#define EM_MX4(FIELDS)                                                                              \
-    asm volatile("s_nop 1\n\t"                                                                      \
-                 "v_mfma_scale_f32_16x16x128_f8f6f4 %0, %4, %5, %0, %9, %10 op_sel_hi:[0,0,0] " FIELDS "\n\t" \
-                 "v_mfma_scale_f32_16x16x128_f8f6f4 %1, %4, %6, %1, %9, %11 op_sel_hi:[0,0,0] " FIELDS "\n\t" \
-                 "v_mfma_scale_f32_16x16x128_f8f6f4 %2, %4, %7, %2, %9, %12 op_sel_hi:[0,0,0] " FIELDS "\n\t" \
-                 "v_mfma_scale_f32_16x16x128_f8f6f4 %3, %4, %8, %3, %9, %13 op_sel_hi:[0,0,0] " FIELDS \
-                 : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3])                                   \
-                 : "v"(w4), "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]), "v"(ws), "v"(xs[0]), "v"(xs[1]), "v"(xs[2]), "v"(xs[3]))
-    typedef int i32x4 __attribute__((ext_vector_type(4)));
-    const i32x4 w4 = {(int)w.x, (int)w.y, (int)w.z, (int)w.w};
-    if constexpr (FMT == kMxFp4) EM_MX4("cbsz:4 blgp:4");
-    else EM_MX4("cbsz:4");
-#undef EM_MX4
-}
-
-// Products in flight are done before what follows reads these accumulators.
-EM_DEV void mfma_settle(floatx4 (&c)[4]) {
-    asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3]));
-}
 
 // ---- rows ------------------------------------------------------------------
 // A row tile: rows [r0, r1) of y, all of matrix m.  Row tiles are numbered
@@ -338,24 +313,20 @@ mxp_stream(MxProduct a) {
 }
 
 // ------------------------------------------------------------------ many rows ----
-// A workgroup takes BT rows x 256 columns in WN x WT waves.  Each K step's codes
-// and scale words arrive by direct global -> LDS loads, STAGES - 1 steps ahead;
-// every wave issues the same number of loads a step, so one counted wait covers
-// them.  A code row is 64 (E2M1) or 128 (E4M3) bytes; its 16-byte segments are
-// stored XOR-swizzled by the row against bank conflicts.
-//
-// The 256-row tile runs one wave a SIMD on 128 x 128 of it each: the 256
-// accumulators fill half the register file and every operand read from the LDS
-// feeds eight products, so that the LDS delivers 96 (FP8) or 64 KB (FP4) a step
-// where eight waves of 128 x 64 would read 128 or 96.
+// A workgroup of 8 waves takes BT rows x 256 columns in WN x WT waves.  Each K
+// step's codes and scale words arrive by direct global -> LDS loads, STAGES - 1
+// steps ahead; every wave issues the same number of loads a step, so one counted
+// wait covers them.  A code row is 64 (E2M1) or 128 (E4M3) bytes; its 16-byte
+// segments are stored XOR-swizzled by the row against bank conflicts.
+// (Four waves of 128 x 128, one a SIMD with 256 accumulators each, read a quarter
+// less from the LDS and measured 479 against 450 us on 16384 x 8192 x 4096 in FP8:
+// one wave's waits leave its matrix core idle.)
 namespace {
-
-constexpr int gemm_threads(int BT) { return BT == 256 ? 256 : 512; }
 
 template <int FMT, int BT_>
 struct GemmCfg {
     static constexpr int BT = BT_, BN = 256;
-    static constexpr int WN = BT == 256 ? 2 : 4, WT = 2, NW = WN * WT;
+    static constexpr int WN = BT == 256 ? 2 : 4, WT = 8 / WN, NW = WN * WT;
     static constexpr int NI = BN / WN / 16, NJ = BT / WT / 16;     // column and row subtiles of a wave
     static constexpr int XB = FMT == kMxFp4 ? 64 : 128;            // bytes of an x row per step
     static constexpr int X_B = BT * XB, W_B = BN * 64, XS_B = BT * 4, WS_B = BN * 4;
@@ -380,6 +351,8 @@ EM_DEV void dma4(const uint8_t* base, uint32_t off, uint32_t dst) {
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" : : "v"(off), "s"(base), "s"(dst) : "memory", "m0");
 }
 
+EM_DEV void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory"); }
+
 // At most N of this wave's loads in flight, its LDS reads done; then the barrier.
 template <int N>
 EM_DEV void wait_loads_barrier() {
@@ -399,7 +372,7 @@ EM_DEV int swz(int r, int s) { return ROW_B == 128 ? s ^ ((r >> 1) & 7) : s ^ (-
 }  // namespace
 
 template <int FMT, int BT>
-__global__ void __launch_bounds__(gemm_threads(BT)) __attribute__((amdgpu_waves_per_eu(BT == 256 ? 1 : 2)))
+__global__ void __launch_bounds__(512)
 mxp_gemm(MxProduct a) {
     using C = GemmCfg<FMT, BT>;
     constexpr int NI = C::NI, NJ = C::NJ, XB = C::XB;
@@ -464,20 +437,19 @@ mxp_gemm(MxProduct a) {
     };
 
     const int wn = wv / C::WT, wt = wv % C::WT;
-    constexpr int JB = NJ < 4 ? NJ : 4;                              // row subtiles of a product block
-    floatx4 acc[NI][NJ / JB][JB];
+    floatx4 acc[NI][NJ];
 #pragma unroll
     for (int p = 0; p < NI; ++p)
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[p][j / JB][j % JB] = zero4();
+        for (int j = 0; j < NJ; ++j) acc[p][j] = zero4();
 
-    // Fragments of x are read a step ahead of their products, those of W two
-    // column subtiles ahead, so that the matrix cores have operands from the first
-    // cycle after a barrier and the LDS reads run under the products.
-    typename XOp<FMT>::type xf[2][NJ / JB][JB];
-    int xs[2][NJ / JB][JB];
-    uint4 wf[4];
-    int wsc[4];
+    // Fragments of x are read before their step begins, those of W one column
+    // subtile ahead, so that the matrix cores have operands from a step's first
+    // cycle and the LDS reads run under the products.
+    typename XOp<FMT>::type xf[2][NJ];
+    int xs[2][NJ];
+    uint4 wf[2];
+    int wsc[2];
     // this lane's places in a subtile's rows (16 rows on, the swizzle is the same)
     const int xlo = m * XB + 16 * swz<XB>(m, g), xhi = m * XB + 16 * swz<XB>(m, 4 + g), wlo = m * 64 + 16 * swz<64>(m, g);
     const int sc = 4 * m + g;
@@ -486,48 +458,52 @@ mxp_gemm(MxProduct a) {
         constexpr int f = decltype(set)::value;
         const int j = FMT == kMxFp8 ? u >> 1 : u, h = FMT == kMxFp8 ? u & 1 : 0, r = 16 * (NJ * wt + j);
         const uint4 v = ldg16(X + r * XB + (h ? xhi : xlo));
-        auto& o = xf[f][j / JB][j % JB];
+        auto& o = xf[f][j];
         o[4 * h] = (int)v.x; o[4 * h + 1] = (int)v.y; o[4 * h + 2] = (int)v.z; o[4 * h + 3] = (int)v.w;
-        if (h == 0) xs[f][j / JB][j % JB] = X[C::X_B + C::W_B + C::WS_B + 4 * r + sc];
+        if (h == 0) xs[f][j] = X[C::X_B + C::W_B + C::WS_B + 4 * r + sc];
     };
     auto read_w = [&](const uint8_t* X, int p) {
         const int r = 16 * (NI * wn + p);
-        wf[p & 3] = ldg16(X + C::X_B + r * 64 + wlo);
-        wsc[p & 3] = X[C::X_B + C::W_B + 4 * r + sc];
+        wf[p & 1] = ldg16(X + C::X_B + r * 64 + wlo);
+        wsc[p & 1] = X[C::X_B + C::W_B + 4 * r + sc];
     };
     constexpr int XU = FMT == kMxFp8 ? 2 * NJ : NJ;
+    // Of the next step, x and the first of W are read from column subtile MID on,
+    // behind a barrier that knows its stage landed.  With three stages a second
+    // barrier, at the step's start, frees the stage of the step before for the loads
+    // right away and gives them almost two steps; with four, the one at the
+    // start does both and they have two.  Past the last step the loads repeat it
+    // into stages that nothing reads: no branch in the loop (with one, the
+    // accumulators are copied at its join).
+    constexpr int MID = C::STAGES == 3 ? NI * 3 / 4 : 0;
     auto step = [&](int st, auto set) {
         constexpr int f = decltype(set)::value;
-        // stage st + 1 has landed (the ones after it may be in flight), and every
-        // wave is done with the stage that the next loads overwrite.  Past the last
-        // step the loads repeat it into stages that nothing reads: no branch here
-        // (with one, the accumulators are copied at its join).  They go out a few at
-        // a time between the products, which they would hold up together
-        wait_loads_barrier<C::LOADS * (C::STAGES - 3)>();
-        const int ahead = min(st + C::STAGES - 1, steps - 1);
         const uint8_t* X = stage_of(st);
         const uint8_t* Xn = stage_of(st + 1);                         // past the last step: read, never used
+        const int ahead = min(st + C::STAGES - 1, steps - 1);
+        if constexpr (MID > 0) {
+            lds_barrier();
+#pragma unroll
+            for (int u = 0; u < C::LOADS; ++u) fetch(ahead, st + C::STAGES - 1, u);
+        }
 #pragma unroll
         for (int p = 0; p < NI; ++p) {
-            read_w(p + 2 < NI ? X : Xn, (p + 2) % NI);
+            if (p == MID) wait_loads_barrier<MID ? C::LOADS : C::LOADS * (C::STAGES - 3)>();
+            read_w(p + 1 < NI ? X : Xn, (p + 1) % NI);
+            if (p >= MID) {
 #pragma unroll
-            for (int u = p * XU / NI; u < (p + 1) * XU / NI; ++u) read_x(Set<1 - f>{}, Xn, u);
+                for (int u = (p - MID) * XU / (NI - MID); u < (p - MID + 1) * XU / (NI - MID); ++u) read_x(Set<1 - f>{}, Xn, u);
+            }
+            if constexpr (MID == 0) {                                 // spread between the products, which they would hold up together
 #pragma unroll
-            for (int u = p * C::LOADS / NI; u < (p + 1) * C::LOADS / NI; ++u) fetch(ahead, st + C::STAGES - 1, u);
-            __builtin_amdgcn_sched_barrier(0);
+                for (int u = p * C::LOADS / NI; u < (p + 1) * C::LOADS / NI; ++u) fetch(ahead, st + C::STAGES - 1, u);
+            }
 #pragma unroll
-            for (int b = 0; b < NJ / JB; ++b) {
-                if constexpr (JB == 4) {
-                    mfma_mx4<FMT>(acc[p][b], wf[p & 3], wsc[p & 3], xf[f][b], xs[f][b]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < JB; ++j) {
-                        const auto& x = xf[f][b][j];
-                        i32x8 x8 = {x[0], x[1], x[2], x[3], 0, 0, 0, 0};
-                        if constexpr (FMT == kMxFp8) x8 = x;
-                        acc[p][b][j] = mfma_mx<FMT>(wf[p & 3], wsc[p & 3], x8, xs[f][b][j], acc[p][b][j]);
-                    }
-                }
+            for (int j = 0; j < NJ; ++j) {
+                const auto& x = xf[f][j];
+                i32x8 x8 = {x[0], x[1], x[2], x[3], 0, 0, 0, 0};
+                if constexpr (FMT == kMxFp8) x8 = x;
+                acc[p][j] = mfma_mx<FMT>(wf[p & 1], wsc[p & 1], x8, xs[f][j], acc[p][j]);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -540,7 +516,6 @@ mxp_gemm(MxProduct a) {
 #pragma unroll
     for (int u = 0; u < XU; ++u) read_x(Set<0>{}, stage_of(0), u);
     read_w(stage_of(0), 0);
-    read_w(stage_of(0), 1);
     int st = 0;
     for (; st + 1 < steps; st += 2) {
         step(st, Set<0>{});
@@ -548,12 +523,6 @@ mxp_gemm(MxProduct a) {
     }
     if (st < steps) step(st, Set<0>{});
     wait_loads_barrier<0>();                                          // nothing more lands in the stages
-    if constexpr (JB == 4) {
-#pragma unroll
-        for (int p = 0; p < NI; ++p)
-#pragma unroll
-            for (int b = 0; b < NJ / JB; ++b) mfma_settle(acc[p][b]);
-    }
 
     // ---- y: lane (g, m) holds columns 4 g .. 4 g + 3 of each column subtile, x row m
     if (a.vec > 1 && n0 + C::BN <= a.N) {
@@ -568,7 +537,7 @@ mxp_gemm(MxProduct a) {
             const bool live = r < t.r1 && x_row(a, r) >= 0;
 #pragma unroll
             for (int p = 0; p < NI; ++p) {
-                const floatx4 v = live ? acc[p][j / JB][j % JB] : zero4();
+                const floatx4 v = live ? acc[p][j] : zero4();
                 const f32x2 lo = {v.x, v.y}, hi = {v.z, v.w};
                 *reinterpret_cast<uint2*>(o + (16 * j + m) * RSTR + 32 * p + 8 * g) =
                     make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector(lo, bf16x2)),
@@ -595,7 +564,7 @@ mxp_gemm(MxProduct a) {
 #pragma unroll
         for (int p = 0; p < NI; ++p) {
             const int n = n0 + 16 * (NI * wn + p);
-            store4(a, r, n + 4 * g, live ? acc[p][j / JB][j % JB] : zero4(), a.vec && n + 16 <= a.N);
+            store4(a, r, n + 4 * g, live ? acc[p][j] : zero4(), a.vec && n + 16 <= a.N);
         }
     }
 }
@@ -623,8 +592,8 @@ template <int BT>
 hipError_t launch_gemm(const MxProduct& a, hipStream_t s) {
     const int64_t tiles = max_row_tiles(a, BT) * ((a.N + 255) / 256);
     prof_begin(s);
-    if (a.fmt == kMxFp4) mxp_gemm<kMxFp4, BT><<<(unsigned)((tiles + 7) & ~7ll), gemm_threads(BT), 0, s>>>(a);
-    else mxp_gemm<kMxFp8, BT><<<(unsigned)((tiles + 7) & ~7ll), gemm_threads(BT), 0, s>>>(a);
+    if (a.fmt == kMxFp4) mxp_gemm<kMxFp4, BT><<<(unsigned)((tiles + 7) & ~7ll), 512, 0, s>>>(a);
+    else mxp_gemm<kMxFp8, BT><<<(unsigned)((tiles + 7) & ~7ll), 512, 0, s>>>(a);
     prof_end(s, "mxp_gemm");
     return hipGetLastError();
 }
