@@ -577,15 +577,48 @@ int64_t max_row_tiles(const MxProduct& a, int BT) {
     return a.offsets ? a.R / BT + (a.M < a.R ? a.M : a.R) : (a.R + BT - 1) / BT;
 }
 
-template <int NS, bool FUSED>
-hipError_t launch_stream(const MxProduct& a, hipStream_t s) {
-    constexpr int NC = 2;
+template <int NS, int NC, bool FUSED>
+hipError_t launch_stream_nc(const MxProduct& a, hipStream_t s) {
     const dim3 grid((a.N + 16 * NC - 1) / (16 * NC), (unsigned)max_row_tiles(a, 16 * NS));
     prof_begin(s);
     if (a.fmt == kMxFp4) mxp_stream<kMxFp4, NS, NC, FUSED><<<grid, 256, 0, s>>>(a);
     else mxp_stream<kMxFp8, NS, NC, FUSED><<<grid, 256, 0, s>>>(a);
     prof_end(s, "mxp_stream");
     return hipGetLastError();
+}
+
+// 32 columns a workgroup, 16 where that leaves half of the compute units idle.
+template <int NS, bool FUSED>
+hipError_t launch_stream(const MxProduct& a, hipStream_t s) {
+    if constexpr (NS == 1)
+        if (max_row_tiles(a, 16) * ((a.N + 31) / 32) <= 128) return launch_stream_nc<1, 1, FUSED>(a, s);
+    return launch_stream_nc<NS, 2, FUSED>(a, s);
+}
+
+// How many times 16 rows of a matrix mxp_stream takes at once (0: not mxp_stream).
+// Measured at K = 4096 and 8192, FP8 (us a call, streams of 16 / 32 / 64 rows
+// against 64-row tiles): one matrix of 8192 columns 32 rows 14.2 / 12.3 / 12.1 /
+// 16.6, 64 rows 23.6 / 18.4 / 16.6 / 16.9, 128 rows 41 / 31 / 27 / 18; 1024
+// columns 128 rows 10.8 / 11.9 / 15.7 / 17.4, 1024 rows 46 / 35 / 31 / 20: the
+// fewest rows that make one workgroup a CU, and tiles where 64 do not.  512
+// matrices of 128 columns, 64 rows in all 11.9 against 23, 256 rows 24 / 24; 64 of
+// 1024 columns, 64 rows 28 / 25, 512 rows 42 / 27: tiles once they number about
+// half of the CUs, since a tile's loads keep more of a matrix in flight.
+int stream_rows(const MxProduct& a) {
+    const int live = !a.offsets ? 1 : a.M < a.R ? a.M : a.R;       // matrices that the rows spread over
+    const int64_t avg = ((int64_t)a.R + live - 1) / live, cols = (a.N + 31) / 32;
+    if (max_row_tiles(a, 64) * a.N / 256 >= 130) return 0;
+    for (int ns = 1; ns <= 4; ns *= 2)
+        if (max_row_tiles(a, 16 * ns) * cols <= 256 || (avg <= 16 * ns && (a.offsets || ns == 1))) return ns;
+    return 0;
+}
+
+// Tiles of 256 rows where they fill the CUs and most of their rows are used; else
+// 64 rows (8192 columns, K = 4096: 1024 rows 41 against 54 us, 2048 rows 87 / 67;
+// 64 matrices of 1024 columns: 128 rows each 57 / 70, 256 each 134 / 135).
+bool big_tiles(const MxProduct& a) {
+    const int live = !a.offsets ? 1 : a.M < a.R ? a.M : a.R;
+    return a.R >= 192ll * live && max_row_tiles(a, 256) * ((a.N + 255) / 256) >= 192;
 }
 
 template <int BT>
@@ -606,17 +639,20 @@ size_t mx_product_ws_bytes(const MxProduct& a) {
 }
 
 hipError_t launch_mx_product(MxProduct a, void* ws, hipStream_t s) {
-    const int live = !a.offsets ? 1 : a.M < a.R ? a.M : a.R;   // matrices that the rows spread over
-    const int64_t avg = ((int64_t)a.R + live - 1) / live;
-    if (a.T <= 16 && avg <= 16) return launch_stream<1, true>(a, s);
+    const int ns = stream_rows(a);
+    // few x rows: every workgroup rounds the ones it needs, which spares a launch
+    if (a.T <= 16 && ns == 1) return launch_stream<1, true>(a, s);
     a.xq = static_cast<uint8_t*>(ws);
     a.xs = a.xq + (((size_t)a.T * a.K / (a.fmt == kMxFp4 ? 2 : 1) + 255) & ~(size_t)255);
     const MxRows rows{a.T, a.T, a.K, a.x_stride, a.fmt, 0};
     const hipError_t e = launch_mx_quantize(rows, a.x, const_cast<uint8_t*>(a.xq), const_cast<uint8_t*>(a.xs), s);
     if (e != hipSuccess) return e;
-    if (avg <= 64)
-        return avg <= 16 ? launch_stream<1, false>(a, s) : avg <= 32 ? launch_stream<2, false>(a, s) : launch_stream<4, false>(a, s);
-    return avg >= 192 ? launch_gemm<256>(a, s) : launch_gemm<64>(a, s);
+    switch (ns) {
+        case 1: return launch_stream<1, false>(a, s);
+        case 2: return launch_stream<2, false>(a, s);
+        case 4: return launch_stream<4, false>(a, s);
+        default: return big_tiles(a) ? launch_gemm<256>(a, s) : launch_gemm<64>(a, s);
+    }
 }
 
 }  // namespace em

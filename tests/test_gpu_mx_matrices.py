@@ -221,7 +221,8 @@ def i32(v):
 @fmt_of
 @pytest.mark.parametrize("T,N,K", [(1, 16, 128), (1, 2048, 4096), (2, 1, 256), (3, 37, 384), (16, 64, 640),
                                    (17, 100, 512), (33, 50, 1024), (64, 96, 128), (65, 257, 256), (127, 33, 384),
-                                   (191, 512, 512), (192, 256, 128), (257, 300, 1152), (700, 1030, 256)])
+                                   (191, 512, 512), (192, 256, 128), (257, 300, 1152), (700, 1030, 256),
+                                   (20, 4096, 256), (50, 2080, 256), (40, 8192, 128), (3000, 4608, 256), (2800, 5000, 128)])
 def test_product_dense(fmt, T, N, K):
     say(f"case: product {T} x {N} x {K}")
     q, e, W = matrices(1, N, K, T + N)
@@ -260,16 +261,16 @@ def test_product_grouped(fmt, sizes, T):
 
 
 @fmt_of
-@pytest.mark.parametrize("R,T", [(40, 7), (500, 60)])
-def test_product_gathered_rows(fmt, R, T):
+@pytest.mark.parametrize("R,T,N", [(40, 7, 48), (500, 60, 48), (90, 17, 640), (900, 300, 512), (1400, 200, 8192)])
+def test_product_gathered_rows(fmt, R, T, N):
     """Shared x rows, and entries that name no row: zeros."""
     rng = np.random.default_rng(2)
     src = rng.integers(0, T, R)
     src[[0, 5, R - 1]] = [-1, T, 2 ** 31 - 1]
-    q, e, W = matrices(2, 48, 384, 1)
+    q, e, W = matrices(2, N, 384, 1)
     off = [0, R // 3, R]
     x = rows_of(T, 384, 3)
-    y = torch.full((R, 48), float("nan"), dtype=torch.bfloat16, device=DEV)
+    y = torch.full((R, N), float("nan"), dtype=torch.bfloat16, device=DEV)
     product(fmt, x.to(DEV), q, e, y, offsets=i32(off), row_src=i32(src))
     within(y, *ops.product(x.double().numpy(), fmt, W, off, src), 384)
     assert bool((y[[0, 5, R - 1]] == 0).all())
