@@ -16,10 +16,11 @@
 //   rt_load         softmax rows of a chunk of tokens, column sums and counts
 //   rt_load_reduce  chunks added in order (float64) per sequence; the losses
 //   rt_dlogits      dz by rows, float32 and / or as three bf16 planes
-//   rt_gemm         dx and dW_r on the bf16 matrix cores: dz is the exact sum of
+//   rt_products     dx and dW_r on the bf16 matrix cores: dz is the exact sum of
 //                   its planes (hi + mid + lo: 24 bits), x and W_r are bf16, every
-//                   product is exact in float32 and the sums are float32
-//   rt_finish       the token slices of dW_r and the chunks of dbias, in order
+//                   product is exact in float32 and the sums are float32; and dbias,
+//                   the chunks of rt_dlogits added in order
+//   rt_finish       the token slices of dW_r added in order
 #include "common.h"
 #include "operators.h"
 
@@ -470,8 +471,12 @@ rt_dlogits(RouterGrad a) {
 // loads, one step ahead in two stages.  An operand whose K runs down the rows is
 // transposed in registers: a lane reads a short run of columns of its eight K
 // rows, and byte permutes pair the rows; operand c of lane m is then column
-// C m + c of the run of 16 C, so that a lane ends with C neighbouring columns of
-// out.  Bound by the matrix cores (three products an element).
+// 4 m + c of the run of 64, so that a lane ends with four neighbouring columns of
+// out.  Three products an element, so the matrix cores bound it, with the LDS
+// (16 KB a wave and step) and dx's stores close behind: waves of 64 x 64, four a
+// SIMD, overlap them.  (Waves of 64 x 128, two a SIMD, read less from the LDS and
+// measured the same to 5% slower, a 256-row workgroup the same.)  Both products
+// and dbias share a launch: at T = 1501 neither fills the chip by itself.
 namespace {
 
 enum RtMode { RT_DX = 0, RT_DW = 1 };
@@ -479,27 +484,31 @@ enum RtMode { RT_DX = 0, RT_DW = 1 };
 template <int BI_>
 struct RtCfg {
     static constexpr int BI = BI_, BN = 256, BK = 32;
-    static constexpr int WI = BI / 64, WN = 4;                      // waves: 64 rows x 64 columns each
-    static constexpr int WAVES = WI * WN, TH = 64 * WAVES;
-    static constexpr int NC = BN / WN / 16;                          // columns a lane ends with
+    static constexpr int WN = 4, WAVES = BI / 64 * WN, TH = 64 * WAVES;   // waves of 64 rows x 64 columns
+    static constexpr int NC = 4;                                     // columns a lane ends with
     static constexpr int P_B = BI * BK * 2, B_B = BK * BN * 2;       // one plane's tile, B's tile
     static constexpr int STAGE = 3 * P_B + B_B;
     static constexpr int A_INSTR = 3 * P_B / 1024 / WAVES, B_INSTR = B_B / 1024 / WAVES;
 };
 
 // Direct global -> LDS load of 16 bytes a lane, from base + off to dst + 16 lane
-// (counted by hand: see wait in rt_gemm; no register output).
+// (waited for by hand in rt_tile; no register output).
 EM_DEV void rt_dma16(const void* base, uint32_t off, uint32_t dst) {
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                  : : "v"(off), "s"(base), "s"(dst) : "memory", "m0");
 }
 
-// Eight K rows of C bf16 columns (C = 4: two words a row, C = 8: four) to C
-// operands of eight K elements.
-template <int C>
-EM_DEV void transpose8(const uint32_t (&r)[8][C / 2], uint4 (&o)[C]) {
+// Eight K rows of four bf16 columns (two words a row) to four operands of eight
+// K elements.
+EM_DEV void transpose8(const uint2 (&v)[8], uint4 (&o)[4]) {
+    uint32_t r[8][2];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
+    for (int i = 0; i < 8; ++i) {
+        r[i][0] = v[i].x;
+        r[i][1] = v[i].y;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
         const uint32_t sel = c & 1 ? 0x07060302u : 0x05040100u;
         o[c].x = __builtin_amdgcn_perm(r[1][c / 2], r[0][c / 2], sel);
         o[c].y = __builtin_amdgcn_perm(r[3][c / 2], r[2][c / 2], sel);
@@ -508,38 +517,28 @@ EM_DEV void transpose8(const uint32_t (&r)[8][C / 2], uint4 (&o)[C]) {
     }
 }
 
-template <int C>
-EM_DEV void read_rows(uint32_t (&r)[8][C / 2], const uint8_t* p, int row_bytes) {
+EM_DEV void read_rows(uint2 (&r)[8], const uint8_t* p, int row_bytes) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if constexpr (C == 8) {
-            const uint4 v = *reinterpret_cast<const uint4*>(p + i * row_bytes);
-            r[i][0] = v.x; r[i][1] = v.y; r[i][2] = v.z; r[i][3] = v.w;
-        } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(p + i * row_bytes);
-            r[i][0] = v.x; r[i][1] = v.y;
-        }
-    }
+    for (int i = 0; i < 8; ++i) r[i] = *reinterpret_cast<const uint2*>(p + i * row_bytes);
 }
 
-}  // namespace
+// Tiles of one product: out's row and column tiles, for DW by token slice.
+EM_DEV int rt_row_tiles(int mode, int BI, const RouterGrad& a) { return ((mode == RT_DX ? a.T : a.E) + BI - 1) / BI; }
 
 template <int MODE, int BI>
-__global__ void __launch_bounds__(RtCfg<BI>::TH) __attribute__((amdgpu_waves_per_eu(BI / 32)))
-rt_gemm(RouterGrad a) {
+EM_DEV void rt_tile(const RouterGrad& a, int block, uint8_t* lds) {
     using C = RtCfg<BI>;
     constexpr int NC = C::NC;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * C::STAGE];
     const int lane = lane_id(), wv = wave_id(), g = lane >> 4, m = lane & 15;
     const int wi = wv / C::WN, wn = wv % C::WN;
     const int I = MODE == RT_DX ? a.T : a.E;                 // rows of out
     const int rows_b = MODE == RT_DX ? a.E : a.T;            // rows of B
     const uint16_t* B = MODE == RT_DX ? a.w_router : a.x;
-    // XCD x = blockIdx % 8 takes neighbouring tiles
-    const int nn = (a.d + C::BN - 1) / C::BN, ni = (I + BI - 1) / BI;
+    // XCD x = block % 8 takes neighbouring tiles
+    const int nn = (a.d + C::BN - 1) / C::BN, ni = rt_row_tiles(MODE, BI, a);
     const int total = nn * ni * (MODE == RT_DX ? 1 : a.slices);
-    const int per = (total + 7) >> 3, at = blockIdx.x >> 3;
-    const int b = (blockIdx.x & 7) * per + at;
+    const int per = (total + 7) >> 3, at = block >> 3;
+    const int b = (block & 7) * per + at;
     if (at >= per || b >= total) return;
     // DX: rows slowest; DW: token slices slowest (a slice's x and dz are shared by its tiles)
     const int z = MODE == RT_DX ? 0 : b / (nn * ni);
@@ -588,9 +587,9 @@ rt_gemm(RouterGrad a) {
         const uint8_t* Bt = A + 3 * C::P_B;
         uint4 bf[NC];
         {
-            uint32_t raw[8][NC / 2];
-            read_rows<NC>(raw, Bt + 8 * g * 512 + 2 * (16 * NC * wn + NC * m), 512);
-            transpose8<NC>(raw, bf);
+            uint2 raw[8];
+            read_rows(raw, Bt + 8 * g * 512 + 2 * (16 * NC * wn + NC * m), 512);
+            transpose8(raw, bf);
         }
 #pragma unroll
         for (int p = 0; p < 3; ++p) {
@@ -602,9 +601,9 @@ rt_gemm(RouterGrad a) {
                     af[i] = *reinterpret_cast<const uint4*>(A + p * C::P_B + r * 64 + 16 * (g ^ (-(r >> 2) & 3)));
                 }
             } else {
-                uint32_t raw[8][2];
-                read_rows<4>(raw, A + p * C::P_B + 8 * g * (2 * BI) + 2 * (64 * wi + 4 * m), 2 * BI);
-                transpose8<4>(raw, af);
+                uint2 raw[8];
+                read_rows(raw, A + p * C::P_B + 8 * g * (2 * BI) + 2 * (64 * wi + 4 * m), 2 * BI);
+                transpose8(raw, af);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -624,45 +623,56 @@ rt_gemm(RouterGrad a) {
             const int r = i0 + 64 * wi + (MODE == RT_DX ? 16 * i + 4 * g + v : 4 * (4 * g + v) + i);
             if (r >= I) continue;
             float* o = out + (int64_t)r * a.d + n;
-#pragma unroll
-            for (int c = 0; c < NC; c += 4) {
-                // dx streams out past the L2, where W_r and the planes stay
-                const floatx4 w = {acc[i][c][v], acc[i][c + 1][v], acc[i][c + 2][v], acc[i][c + 3][v]};
-                if constexpr (MODE == RT_DX) __builtin_nontemporal_store(w, reinterpret_cast<floatx4*>(o + c));
-                else *reinterpret_cast<floatx4*>(o + c) = w;
-            }
+            // dx streams out past the L2, where W_r and the planes stay
+            const floatx4 w = {acc[i][0][v], acc[i][1][v], acc[i][2][v], acc[i][3][v]};
+            if constexpr (MODE == RT_DX) __builtin_nontemporal_store(w, reinterpret_cast<floatx4*>(o));
+            else *reinterpret_cast<floatx4*>(o) = w;
         }
 }
 
-// Token slices of dW_r in order (workgroups [0, wblocks)), then the chunks of
-// dbias: 64 experts a workgroup, 16 rows of threads over the chunks, float64.
-__global__ void __launch_bounds__(1024)
-rt_finish(RouterGrad a, int wblocks) {
-    __shared__ double sp[16][64];
-    if ((int)blockIdx.x < wblocks) {
-        const int64_t n = (int64_t)a.E * a.d, at = ((int64_t)blockIdx.x * 1024 + threadIdx.x) * 4;
-        if (at >= n) return;
-        float4 s = *reinterpret_cast<const float4*>(a.part_w + at);
-        for (int z = 1; z < a.slices; ++z) {
-            const float4 v = *reinterpret_cast<const float4*>(a.part_w + z * n + at);
-            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-        }
-        *reinterpret_cast<float4*>(a.dw_router + at) = s;
-        return;
-    }
-    const int col = threadIdx.x & 63, row = threadIdx.x >> 6;
-    const int e = (blockIdx.x - wblocks) * 64 + col;
+// 64 experts of dbias from the chunks of rt_dlogits: rows of 64 threads over
+// interleaved chunks in float64, then the rows in order.
+template <int TH>
+EM_DEV void rt_bias(const RouterGrad& a, int block, uint8_t* lds) {
+    double(*sp)[64] = reinterpret_cast<double(*)[64]>(lds);
+    const int col = threadIdx.x & 63, row = threadIdx.x >> 6, e = block * 64 + col;
     const int chunks = (a.T + a.chunk - 1) / a.chunk;
     double s = 0.0;
     if (e < a.E) {
 #pragma unroll 8
-        for (int c = row; c < chunks; c += 16) s += (double)a.part_b[(int64_t)c * a.E + e];
+        for (int c = row; c < chunks; c += TH / 64) s += (double)a.part_b[(int64_t)c * a.E + e];
     }
     sp[row][col] = s;
     __syncthreads();
     if (row != 0 || e >= a.E) return;
-    for (int r = 1; r < 16; ++r) s += sp[r][col];
+    for (int r = 1; r < TH / 64; ++r) s += sp[r][col];
     a.dbias[e] = (float)s;
+}
+
+}  // namespace
+
+// Workgroups: dbias (bblocks), then the tiles of dW_r (wblocks), then those of dx.
+template <int BI>
+__global__ void __launch_bounds__(RtCfg<BI>::TH) __attribute__((amdgpu_waves_per_eu(BI / 32)))
+rt_products(RouterGrad a, int bblocks, int wblocks) {
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * RtCfg<BI>::STAGE];
+    const int b = blockIdx.x;
+    if (b < bblocks) rt_bias<RtCfg<BI>::TH>(a, b, lds);
+    else if (b < bblocks + wblocks) rt_tile<RT_DW, BI>(a, b - bblocks, lds);
+    else rt_tile<RT_DX, BI>(a, b - bblocks - wblocks, lds);
+}
+
+// Token slices of dW_r, in order.
+__global__ void __launch_bounds__(256)
+rt_finish(RouterGrad a) {
+    const int64_t n = (int64_t)a.E * a.d, at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (at >= n) return;
+    float4 s = *reinterpret_cast<const float4*>(a.part_w + at);
+    for (int z = 1; z < a.slices; ++z) {
+        const float4 v = *reinterpret_cast<const float4*>(a.part_w + z * n + at);
+        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
+    *reinterpret_cast<float4*>(a.dw_router + at) = s;
 }
 
 // ------------------------------------------------------------------ host side ----
@@ -689,16 +699,20 @@ LoadLayout load_layout(const RouterLoad& a) {
 struct GradLayout { size_t planes, part_w, part_b, bytes; };
 
 int pad32(int v) { return (v + 31) & ~31; }
-int tile_rows(int n) { return n > 64 ? 128 : 64; }
+int tile_rows(const RouterGrad& a) { return a.E > 64 ? 128 : 64; }
+int64_t tiles(int rows, int bi, int d) { return (int64_t)((rows + bi - 1) / bi) * ((d + 255) / 256); }
 
-// Token slices of dW_r: as many as give every CU a workgroup, of at least four
-// K steps each.
+// Token slices of dW_r: as many as give every CU a workgroup, or two where each
+// still has 32 K steps (T = 16384: 8 slices 170, 4 slices 190 us); at least four
+// steps each.  Every slice writes dW_r once and rt_finish reads it (T = 1501:
+// 8 slices 29 + 16, 4 slices 27 + 12, 2 slices 37 + 10 us).
 int dw_slices(const RouterGrad& a) {
-    const int tiles = ((a.d + 255) / 256) * ((a.E + tile_rows(a.E) - 1) / tile_rows(a.E));
-    const int most = a.Tp / 32 / 4;
-    int z = 512 / tiles;
-    z = z < most ? z : most;
-    return z < 1 ? 1 : z > 16 ? 16 : z;
+    const int64_t t = tiles(a.E, tile_rows(a), a.d);
+    const int steps = a.Tp / 32;
+    int64_t z = 512 / t;
+    if (z > 0 && steps / z < 32) z = 256 / t;
+    z = z < steps / 4 ? z : steps / 4;
+    return z < 1 ? 1 : z > 16 ? 16 : (int)z;
 }
 
 GradLayout grad_layout(const RouterGrad& a) {
@@ -711,20 +725,6 @@ GradLayout grad_layout(const RouterGrad& a) {
     L.part_b = take((size_t)((a.Tp + grad_chunk(a.T) - 1) / grad_chunk(a.T)) * a.E * 4);
     L.bytes = off;
     return L;
-}
-
-template <int MODE>
-hipError_t launch_rt_gemm(const RouterGrad& a, hipStream_t s, const char* name) {
-    const int I = MODE == RT_DX ? a.T : a.E;
-    // DX: small tiles where large ones would leave compute units idle
-    const int bi = MODE == RT_DX ? ((int64_t)((I + 127) / 128) * ((a.d + 255) / 256) >= 192 ? 128 : 64) : tile_rows(I);
-    const int64_t tiles = (int64_t)((I + bi - 1) / bi) * ((a.d + 255) / 256) * (MODE == RT_DX ? 1 : a.slices);
-    const unsigned grid = (unsigned)((tiles + 7) & ~7ll);
-    prof_begin(s);
-    if (bi == 128) rt_gemm<MODE, 128><<<grid, RtCfg<128>::TH, 0, s>>>(a);
-    else rt_gemm<MODE, 64><<<grid, RtCfg<64>::TH, 0, s>>>(a);
-    prof_end(s, name);
-    return hipGetLastError();
 }
 
 }  // namespace
@@ -780,14 +780,20 @@ hipError_t launch_router_grad(RouterGrad a, void* ws, hipStream_t s) {
     else rt_dlogits<4><<<chunks, 256, 0, s>>>(a);
     prof_end(s, "rt_dlogits");
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess && a.dx) e = launch_rt_gemm<RT_DX>(a, s, "rt_dx");
-    if (e == hipSuccess && a.dw_router) e = launch_rt_gemm<RT_DW>(a, s, "rt_dw");
-    if (e != hipSuccess) return e;
-    const int wblocks = a.dw_router && a.slices > 1 ? (int)(((int64_t)a.E * a.d / 4 + 1023) / 1024) : 0;
-    const int bblocks = a.dbias ? (a.E + 63) / 64 : 0;
-    if (wblocks + bblocks == 0) return hipSuccess;
+    if (e != hipSuccess || !(a.dx || a.dw_router || a.dbias)) return e;
+    const int bi = tile_rows(a);
+    const auto up8 = [](int64_t n) { return (int)((n + 7) & ~7ll); };
+    const int bblocks = a.dbias ? up8((a.E + 63) / 64) : 0;
+    const int wblocks = a.dw_router ? up8(tiles(a.E, bi, a.d) * a.slices) : 0;
+    const int xblocks = a.dx ? up8(tiles(a.T, bi, a.d)) : 0;
     prof_begin(s);
-    rt_finish<<<wblocks + bblocks, 1024, 0, s>>>(a, wblocks);
+    if (bi == 128) rt_products<128><<<bblocks + wblocks + xblocks, RtCfg<128>::TH, 0, s>>>(a, bblocks, wblocks);
+    else rt_products<64><<<bblocks + wblocks + xblocks, RtCfg<64>::TH, 0, s>>>(a, bblocks, wblocks);
+    prof_end(s, "rt_products");
+    e = hipGetLastError();
+    if (e != hipSuccess || !a.dw_router || a.slices == 1) return e;
+    prof_begin(s);
+    rt_finish<<<(unsigned)(((int64_t)a.E * a.d / 4 + 255) / 256), 256, 0, s>>>(a);
     prof_end(s, "rt_finish");
     return hipGetLastError();
 }
