@@ -41,6 +41,8 @@ EXPORTED = ("edge_moe_workspace_bytes", "edge_moe_route", "edge_moe_forward",
 # element formats and dense types of the MX matrix operators
 MX_FP4, MX_FP8 = 0, 1
 _BF16, _FLOAT = 0, 1
+_dtypes: dict = {}             # torch's types by name, and those of dense matrices (filled by load())
+_dense_types: dict = {}
 
 
 class CDims(ctypes.Structure):
@@ -126,7 +128,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                            "`python -m shared_matrix_expert_amd.build`")
     # PyTorch-ROCm ships its own HIP runtime; load it first so that the library
     # binds to the same runtime instance as the streams and memory it is given.
-    import torch  # noqa: F401
+    import torch
+    _dtypes.update({n: getattr(torch, n) for n in ("uint8", "int32", "float32")})
+    _dense_types.update({torch.bfloat16: _BF16, torch.int16: _BF16, torch.uint16: _BF16, torch.float32: _FLOAT})
     lib = ctypes.CDLL(path)
     vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
     lib.edge_moe_workspace_bytes.argtypes = [ctypes.POINTER(CDims)]
@@ -376,15 +380,17 @@ def _sized(t, dtype: str, count: int, what: str) -> Optional[int]:
     """Address of a contiguous tensor of `count` values of dtype (None passes)."""
     if t is None:
         return None
-    if str(t.dtype) != dtype or t.numel() != count:
-        raise ValueError(f"{what}: expected {count} values of {dtype}, got {t.numel()} of {t.dtype}")
-    return _ptr(t)
+    if t.dtype is not _dtypes[dtype] or t.numel() != count or not t.is_contiguous():
+        raise ValueError(f"{what}: expected {count} contiguous {dtype} values, got {t.numel()} of {t.dtype}")
+    return t.data_ptr()
 
 
 def _bf16_sized(t, count: int, what: str) -> Optional[int]:
-    if t is not None and (_dense_type(t) != _BF16 or t.numel() != count):
-        raise ValueError(f"{what}: expected {count} bfloat16 values (or int16 bits), got {t.numel()} of {t.dtype}")
-    return _ptr(t)
+    if t is None:
+        return None
+    if _dense_type(t) != _BF16 or t.numel() != count or not t.is_contiguous():
+        raise ValueError(f"{what}: expected {count} contiguous bfloat16 values (or int16 bits), got {t.numel()} of {t.dtype}")
+    return t.data_ptr()
 
 
 def edge_moe_balance_ws_bytes(dims, n_seq=1) -> int:
@@ -397,12 +403,13 @@ def edge_moe_balance(dims, logits, topk_idx, counts, probs, loss, ws, seq_offset
     seq_offsets int32 [S + 1]: the sequences' tokens (None: one sequence)."""
     T, E, k = dims.T, dims.n_experts, dims.top_k
     S = 1 if seq_offsets is None else seq_offsets.numel() - 1
-    f, i = "torch.float32", "torch.int32"
-    _same_device(logits, topk_idx, counts, probs, loss, ws, seq_offsets)
-    st = load().edge_moe_balance(ctypes.byref(cdims(dims)), _sized(logits, f, T * E, "logits"),
+    f, i = "float32", "int32"
+    lib = load()
+    dev = _same_device(logits, topk_idx, counts, probs, loss, ws, seq_offsets)
+    st = lib.edge_moe_balance(cdims(dims), _sized(logits, f, T * E, "logits"),
                                  _sized(topk_idx, i, T * k, "topk_idx"), _sized(seq_offsets, i, S + 1, "seq_offsets"),
                                  S, _sized(counts, i, S * E, "counts"), _sized(probs, f, S * E, "probs"),
-                                 _sized(loss, f, 2, "loss"), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
+                                 _sized(loss, f, 2, "loss"), _ptr(ws), ws.numel() * ws.element_size(), _stream_on(dev, stream))
     if st != EDGE_MOE_OK:
         raise EdgeMoeError("edge_moe_balance", st)
 
@@ -420,38 +427,45 @@ def edge_moe_route_backward(dims, logits, topk_idx, ws, topk_w=None, d_topk_w=No
     w_router, dw_router needs x (bf16)."""
     T, E, k, d = dims.T, dims.n_experts, dims.top_k, dims.d
     S = 1 if seq_offsets is None else seq_offsets.numel() - 1
-    f, i = "torch.float32", "torch.int32"
-    _same_device(logits, topk_idx, ws, topk_w, d_topk_w, d_loss, counts, seq_offsets, x, w_router, dlogits, dx,
-                 dw_router, dbias)
+    f, i = "float32", "int32"
+    lib = load()
+    dev = _same_device(logits, topk_idx, ws, topk_w, d_topk_w, d_loss, counts, seq_offsets, x, w_router, dlogits, dx,
+                       dw_router, dbias)
     g = CRouteGrad(_sized(logits, f, T * E, "logits"), _sized(topk_idx, i, T * k, "topk_idx"),
                    _sized(topk_w, f, T * k, "topk_w"), _sized(d_topk_w, f, T * k, "d_topk_w"),
                    _sized(d_loss, f, 2, "d_loss"), _sized(counts, i, S * E, "counts"),
                    _sized(seq_offsets, i, S + 1, "seq_offsets"), S, _bf16_sized(x, T * d, "x"),
                    _bf16_sized(w_router, E * d, "w_router"), _sized(dlogits, f, T * E, "dlogits"),
                    _sized(dx, f, T * d, "dx"), _sized(dw_router, f, E * d, "dw_router"), _sized(dbias, f, E, "dbias"))
-    st = load().edge_moe_route_backward(ctypes.byref(cdims(dims)), ctypes.byref(g), _ptr(ws),
-                                        ws.numel() * ws.element_size(), _stream(stream))
+    st = lib.edge_moe_route_backward(cdims(dims), g, _ptr(ws), ws.numel() * ws.element_size(), _stream_on(dev, stream))
     if st != EDGE_MOE_OK:
         raise EdgeMoeError("edge_moe_route_backward", st)
 
 
-def _same_device(*tensors) -> None:
-    """Every tensor on the current GPU: the library launches there."""
+def _same_device(*tensors) -> int:
+    """Every tensor on the current GPU, where the library launches; its index."""
     import torch
     cur = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != cur:
             raise ValueError(f"tensors must be on the current GPU (cuda:{cur}), got one on {t.device}")
+    return cur
+
+
+def _stream_on(device: int, stream) -> int:
+    """The stream's handle; None: the device's current stream."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(device)
+    return _stream(stream)
 
 
 def _dense_type(t) -> int:
     """bf16 (bfloat16, or int16 / uint16 bit patterns) or float32."""
-    name = str(t.dtype)
-    if name in ("torch.bfloat16", "torch.int16", "torch.uint16"):
-        return _BF16
-    if name == "torch.float32":
-        return _FLOAT
-    raise ValueError(f"expected bfloat16 (or its int16 bits) or float32, got {name}")
+    kind = _dense_types.get(t.dtype)
+    if kind is None:
+        raise ValueError(f"expected bfloat16 (or its int16 bits) or float32, got {t.dtype}")
+    return kind
 
 
 def _row_stride(t) -> int:
@@ -477,41 +491,38 @@ def _row_stride(t) -> int:
 
 
 def _mx_shape(fmt, dense, codes, scales):
-    """(M, N, K) of a dense tensor and its MX codes and scales, checked against each other."""
+    """(M, N, K) of a dense tensor and the addresses of its MX codes and scales,
+    checked against each other."""
     if fmt not in (MX_FP4, MX_FP8):
         raise ValueError("format must be MX_FP4 or MX_FP8")
     if dense.dim() < 2:
         raise ValueError("expected rows: a tensor of at least two dimensions")
     N, K = dense.shape[-2], dense.shape[-1]
     M = dense.numel() // max(1, N * K)
-    _uint8(codes, M * N * (K // 2 if fmt == MX_FP4 else K), "codes")
-    _uint8(scales, M * N * (K // 32), "scales")
-    return M, N, K
-
-
-def _uint8(t, count: int, what: str) -> None:
-    if str(t.dtype) != "torch.uint8" or t.numel() != count:
-        raise ValueError(f"{what}: expected {count} uint8 values, got {t.numel()} of {t.dtype}")
+    return (M, N, K, _sized(codes, "uint8", M * N * (K // 2 if fmt == MX_FP4 else K), "codes"),
+            _sized(scales, "uint8", M * N * (K // 32), "scales"))
 
 
 def edge_moe_mx_quantize(fmt, src, codes, scales, stream=None) -> None:
     """Dense matrices src [..., N, K] (bf16 or float32, rows at one stride) to
     MX codes [..., N, K/2] (MX_FP4) or [..., N, K] (MX_FP8) and E8M0 scales
     [..., K/128, N, 4], both uint8."""
-    M, N, K = _mx_shape(fmt, src, codes, scales)
-    _same_device(src, codes, scales)
-    st = load().edge_moe_mx_quantize(M, N, K, fmt, _dense_type(src), src.data_ptr(), _row_stride(src), _ptr(codes),
-                                     _ptr(scales), _stream(stream))
+    lib = load()
+    M, N, K, q, e = _mx_shape(fmt, src, codes, scales)
+    dev = _same_device(src, codes, scales)
+    st = lib.edge_moe_mx_quantize(M, N, K, fmt, _dense_type(src), src.data_ptr(), _row_stride(src), q, e,
+                                     _stream_on(dev, stream))
     if st != EDGE_MOE_OK:
         raise EdgeMoeError("edge_moe_mx_quantize", st)
 
 
 def edge_moe_mx_dequantize(fmt, codes, scales, dst, stream=None) -> None:
     """MX codes and scales back to dense dst [..., N, K] (bf16 or float32)."""
-    M, N, K = _mx_shape(fmt, dst, codes, scales)
-    _same_device(dst, codes, scales)
-    st = load().edge_moe_mx_dequantize(M, N, K, fmt, _dense_type(dst), _ptr(codes), _ptr(scales), dst.data_ptr(),
-                                       _row_stride(dst), _stream(stream))
+    lib = load()
+    M, N, K, q, e = _mx_shape(fmt, dst, codes, scales)
+    dev = _same_device(dst, codes, scales)
+    st = lib.edge_moe_mx_dequantize(M, N, K, fmt, _dense_type(dst), q, e, dst.data_ptr(), _row_stride(dst),
+                                       _stream_on(dev, stream))
     if st != EDGE_MOE_OK:
         raise EdgeMoeError("edge_moe_mx_dequantize", st)
 
@@ -525,19 +536,18 @@ def edge_moe_mx_product(x_format, x, codes, scales, y, ws, offsets=None, row_src
     MXFP4 matrices codes [M][N][K/2], scales [M][K/128][N][4] (or one matrix
     without the leading dimension).  offsets int32 [M + 1]: the y rows of each
     matrix; row_src int32 [R]: the x row of each y row."""
+    lib = load()
     if x.dim() != 2 or y.dim() != 2 or _dense_type(x) != _BF16 or _dense_type(y) != _BF16:
         raise ValueError("x and y must be bfloat16 (or int16 bits) [rows][columns]")
     (T, K), (R, N) = x.shape, y.shape
     M = 1 if codes.dim() == 2 else codes.shape[0]
-    _uint8(codes, M * N * (K // 2), "codes")
-    _uint8(scales, M * N * (K // 32), "scales")
-    for t, n, what in ((offsets, M + 1, "offsets"), (row_src, R, "row_src")):
-        if t is not None and (str(t.dtype) != "torch.int32" or t.numel() != n):
-            raise ValueError(f"{what}: expected {n} int32 values, got {t.numel()} of {t.dtype}")
-    _same_device(x, codes, scales, y, ws, offsets, row_src)
-    st = load().edge_moe_mx_product(ctypes.byref(CMxDims(T, R, M, N, K, x_format)), x.data_ptr(), _row_stride(x),
-                                    _ptr(row_src), _ptr(offsets), _ptr(codes), _ptr(scales), y.data_ptr(),
-                                    _row_stride(y), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
+    q = _sized(codes, "uint8", M * N * (K // 2), "codes")
+    e = _sized(scales, "uint8", M * N * (K // 32), "scales")
+    off, src = _sized(offsets, "int32", M + 1, "offsets"), _sized(row_src, "int32", R, "row_src")
+    dev = _same_device(x, codes, scales, y, ws, offsets, row_src)
+    st = lib.edge_moe_mx_product(CMxDims(T, R, M, N, K, x_format), x.data_ptr(), _row_stride(x), src, off, q, e,
+                                    y.data_ptr(), _row_stride(y), _ptr(ws), ws.numel() * ws.element_size(),
+                                    _stream_on(dev, stream))
     if st != EDGE_MOE_OK:
         raise EdgeMoeError("edge_moe_mx_product", st)
 

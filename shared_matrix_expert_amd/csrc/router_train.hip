@@ -31,11 +31,12 @@ namespace {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-// Tokens per workgroup of rt_load and rt_dlogits (a multiple of its four waves):
-// few enough that small batches still spread over the compute units, where the
-// chain of one token's reductions is what takes the time.
-int load_chunk(int T) { return T <= 2048 ? 4 : T <= 8192 ? 16 : 32; }
-int grad_chunk(int T) { return T <= 4096 ? 4 : 16; }
+// Tokens per workgroup of rt_load and rt_dlogits, one or four a wave (whose rows
+// are all asked for at once): few enough that small batches spread over the
+// compute units, where the chain of one token's reductions is what takes the time.
+constexpr int WT = 4;          // tokens a wave takes at most
+int load_chunk(int T) { return T <= 2048 ? 4 : 4 * WT; }
+int grad_chunk(int T) { return T <= 4096 ? 4 : 4 * WT; }
 
 // ---- wave reductions: DPP within rows of 16 lanes, two broadcasts across them
 // (no LDS); the same value in every lane.
@@ -192,24 +193,24 @@ rt_load(RouterLoad a) {
             const int e = a.topk_idx[(int64_t)lo * a.k + i];
             if ((unsigned)e < (unsigned)a.E) atomicAdd(&hist[e], 1);
         }
-        float acc[NV][4], cur[NV][4], nxt[NV][4];
+        float acc[NV][4], row[WT][NV][4];
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) acc[i][c] = 0.f;
         double z2 = 0.0;
-        if (lo + wv < hi) load_row<NV>(cur, a.logits + (int64_t)(lo + wv) * a.E, a.E, a.vec);
-        for (int t = lo + wv; t < hi; t += 4) {
-            if (t + 4 < hi) load_row<NV>(nxt, a.logits + (int64_t)(t + 4) * a.E, a.E, a.vec);
-            const float lse = softmax_row<NV>(cur);
+#pragma unroll
+        for (int j = 0; j < WT; ++j)
+            if (lo + wv + 4 * j < hi) load_row<NV>(row[j], a.logits + (int64_t)(lo + wv + 4 * j) * a.E, a.E, a.vec);
+#pragma unroll
+        for (int j = 0; j < WT; ++j) {
+            if (lo + wv + 4 * j >= hi) break;
+            const float lse = softmax_row<NV>(row[j]);
             z2 += (double)lse * (double)lse;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    acc[i][c] += cur[i][c];
-                    cur[i][c] = nxt[i][c];
-                }
+                for (int c = 0; c < 4; ++c) acc[i][c] += row[j][i][c];
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -324,26 +325,29 @@ rt_dlogits(RouterGrad a) {
     }
     int s = a.d_loss ? find_seq(q, t0) : 0, have = -1;
     int slo = a.d_loss ? q.lo(s) : 0, shi = a.d_loss ? q.hi(s) : 0;
-    float f[NV][4], acc[NV][4], nxt[NV][4];
+    float f[NV][4], acc[NV][4], row[WT][NV][4];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int c = 0; c < 4; ++c) f[i][c] = acc[i][c] = 0.f;
-    if (t0 < a.T) load_row<NV>(nxt, a.logits + (int64_t)t0 * a.E, a.E, a.vec);
+#pragma unroll
+    for (int j = 0; j < WT; ++j)
+        if (j < per && t0 + j < a.T) load_row<NV>(row[j], a.logits + (int64_t)(t0 + j) * a.E, a.E, a.vec);
     float* pick_row = red[wv];                          // this wave's picks (the column sums come after them)
     if (a.d_topk_w)
 #pragma unroll
         for (int i = 0; i < NV; ++i) *reinterpret_cast<float4*>(&pick_row[256 * i + 4 * lane]) = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j = 0; j < per; ++j) {
+#pragma unroll
+    for (int j = 0; j < WT; ++j) {
         const int t = t0 + j;
-        if (t >= a.Tp) break;
-        float d[NV][4];
+        if (j >= per || t >= a.Tp) break;
+        float(&d)[NV][4] = row[j];
+        if (t >= a.T) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) d[i][c] = t < a.T ? nxt[i][c] : 0.f;
-        if (t < a.T) {
-            if (j + 1 < per && t + 1 < a.T) load_row<NV>(nxt, a.logits + (int64_t)(t + 1) * a.E, a.E, a.vec);
+                for (int c = 0; c < 4; ++c) d[i][c] = 0.f;
+        } else {
             // the selection weights' gradient: lane j has the token's pick j
             int pick = -1;
             float pv = 0.f;

@@ -77,7 +77,7 @@ def check_balance(D, z, idx, off=None):
 
 
 SHAPES = [(1, 8, 1), (2, 10, 3), (31, 64, 4), (33, 130, 2), (64, 257, 8), (130, 512, 10), (300, 1000, 6), (700, 33, 32),
-          (1025, 1024, 5)]
+          (1025, 1024, 5), (2100, 128, 3)]
 
 
 @pytest.mark.parametrize("T,E,k", SHAPES)
