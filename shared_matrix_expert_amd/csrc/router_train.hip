@@ -138,6 +138,18 @@ EM_DEV void load_row(float (&v)[NV][4], const float* __restrict__ row, int E, bo
     }
 }
 
+// e^v for v <= 0 from the hardware base-2 exponential: the rounding error of
+// v log2(e) (up to |v| units in the last place of the result) is taken along as
+// a first-order factor, which leaves that instruction's unit.  Below 2^-126: 0.
+EM_DEV float exp_neg(float v) {
+    constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.69314718f;
+    v = v < -200.f ? -200.f : v;                        // -infinity too; NaN stays
+    const float t = v * kLog2e;
+    const float lo = fmaf(v, kLog2eLow, fmaf(v, kLog2e, -t));
+    const float e = __builtin_amdgcn_exp2f(t);
+    return fmaf(e, lo * kLn2, e);
+}
+
 // v becomes softmax(v); the row's log sum exp is returned.  A row of -infinity
 // alone (every expert masked) has no distribution: probabilities and lse 0.
 template <int NV>
@@ -155,7 +167,7 @@ EM_DEV float softmax_row(float (&v)[NV][4]) {
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            v[i][c] = expf(v[i][c] - b);
+            v[i][c] = exp_neg(v[i][c] - b);
             s += v[i][c];
         }
     s = wave_sum(s);
@@ -172,7 +184,8 @@ EM_DEV float softmax_row(float (&v)[NV][4]) {
 // ------------------------------------------------------------------ the load -----
 // Chunk c of a.chunk tokens; its part of sequence s goes to slot c + s of the
 // partial sums (both grow along the tokens, so a slot has one owner).  Bound by
-// reading the logits once.
+// reading the logits once; they and the picks are asked for before the sequences
+// are looked up.
 template <int NV>
 __global__ void __launch_bounds__(256)
 rt_load(RouterLoad a) {
@@ -183,30 +196,43 @@ rt_load(RouterLoad a) {
     const int tid = threadIdx.x, lane = lane_id(), wv = wave_id();
     const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
     if (blockIdx.x == 0 && tid == 0) *a.done = 0;
-    for (int s = find_seq(q, t0); s < a.S; ++s) {
+    float row[WT][NV][4], lse[WT];                     // token t0 + wv + 4 j
+#pragma unroll
+    for (int j = 0; j < WT; ++j)
+        if (t0 + wv + 4 * j < t1) load_row<NV>(row[j], a.logits + (int64_t)(t0 + wv + 4 * j) * a.E, a.E, a.vec);
+    constexpr int PICKS = 4 * WT * 32 / 256;           // picks of a chunk per thread, at most
+    int pick[PICKS];
+#pragma unroll
+    for (int u = 0; u < PICKS; ++u) {
+        const int i = tid + 256 * u;
+        pick[u] = i < (t1 - t0) * a.k ? a.topk_idx[(int64_t)t0 * a.k + i] : -1;
+    }
+    const int first = find_seq(q, t0);
+#pragma unroll
+    for (int j = 0; j < WT; ++j)
+        if (t0 + wv + 4 * j < t1) lse[j] = softmax_row<NV>(row[j]);
+    for (int s = first; s < a.S; ++s) {
         if (q.lo(s) >= t1) break;
         const int lo = max(q.lo(s), t0), hi = min(q.hi(s), t1);
         if (lo >= hi) continue;
         for (int e = tid; e < NV * 256; e += 256) hist[e] = 0;
         __syncthreads();
-        for (int i = tid; i < (hi - lo) * a.k; i += 256) {
-            const int e = a.topk_idx[(int64_t)lo * a.k + i];
-            if ((unsigned)e < (unsigned)a.E) atomicAdd(&hist[e], 1);
+#pragma unroll
+        for (int u = 0; u < PICKS; ++u) {
+            const int i = tid + 256 * u;
+            if ((unsigned)pick[u] < (unsigned)a.E && i >= (lo - t0) * a.k && i < (hi - t0) * a.k) atomicAdd(&hist[pick[u]], 1);
         }
-        float acc[NV][4], row[WT][NV][4];
+        float acc[NV][4];
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) acc[i][c] = 0.f;
         double z2 = 0.0;
 #pragma unroll
-        for (int j = 0; j < WT; ++j)
-            if (lo + wv + 4 * j < hi) load_row<NV>(row[j], a.logits + (int64_t)(lo + wv + 4 * j) * a.E, a.E, a.vec);
-#pragma unroll
         for (int j = 0; j < WT; ++j) {
-            if (lo + wv + 4 * j >= hi) break;
-            const float lse = softmax_row<NV>(row[j]);
-            z2 += (double)lse * (double)lse;
+            const int t = t0 + wv + 4 * j;
+            if (t < lo || t >= hi) continue;
+            z2 += (double)lse[j] * (double)lse[j];
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -316,6 +342,22 @@ rt_dlogits(RouterGrad a) {
     const int tid = threadIdx.x, lane = lane_id(), wv = wave_id();
     const int per = a.chunk / 4;
     const int t0 = blockIdx.x * a.chunk + wv * per;
+    float f[NV][4], acc[NV][4], row[WT][NV][4];
+    int picks[WT];                                      // lane p has pick p, its weight and the weight's gradient
+    float pw[WT], pd[WT];
+#pragma unroll
+    for (int j = 0; j < WT; ++j) {
+        const int t = t0 + j;
+        picks[j] = -1;
+        pw[j] = pd[j] = 0.f;
+        if (j >= per || t >= a.T) continue;
+        load_row<NV>(row[j], a.logits + (int64_t)t * a.E, a.E, a.vec);
+        if (a.d_topk_w && lane < a.k) {
+            picks[j] = a.topk_idx[(int64_t)t * a.k + lane];
+            pw[j] = a.topk_w[(int64_t)t * a.k + lane];
+            pd[j] = a.d_topk_w[(int64_t)t * a.k + lane];
+        }
+    }
     float gb = 0.f, gz = 0.f;
     if (a.d_loss) {
         int live, tokens;
@@ -325,14 +367,10 @@ rt_dlogits(RouterGrad a) {
     }
     int s = a.d_loss ? find_seq(q, t0) : 0, have = -1;
     int slo = a.d_loss ? q.lo(s) : 0, shi = a.d_loss ? q.hi(s) : 0;
-    float f[NV][4], acc[NV][4], row[WT][NV][4];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int c = 0; c < 4; ++c) f[i][c] = acc[i][c] = 0.f;
-#pragma unroll
-    for (int j = 0; j < WT; ++j)
-        if (j < per && t0 + j < a.T) load_row<NV>(row[j], a.logits + (int64_t)(t0 + j) * a.E, a.E, a.vec);
     float* pick_row = red[wv];                          // this wave's picks (the column sums come after them)
     if (a.d_topk_w)
 #pragma unroll
@@ -348,19 +386,9 @@ rt_dlogits(RouterGrad a) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) d[i][c] = 0.f;
         } else {
-            // the selection weights' gradient: lane j has the token's pick j
-            int pick = -1;
-            float pv = 0.f;
-            if (a.d_topk_w) {
-                float w = 0.f, dw = 0.f;
-                if (lane < a.k) {
-                    pick = a.topk_idx[(int64_t)t * a.k + lane];
-                    w = a.topk_w[(int64_t)t * a.k + lane];
-                    dw = a.d_topk_w[(int64_t)t * a.k + lane];
-                }
-                const float mean = wave_sum(w * dw);
-                pv = w * (dw - mean);
-            }
+            // the selection weights' gradient
+            const int pick = picks[j];
+            const float pv = a.d_topk_w ? pw[j] * (pd[j] - wave_sum(pw[j] * pd[j])) : 0.f;
             while (t >= shi && s + 1 < a.S) {           // the token's sequence (none: neither loss has it)
                 ++s;
                 slo = q.lo(s);
