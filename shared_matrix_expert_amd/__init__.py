@@ -41,6 +41,10 @@ EXPORTED = ("edge_moe_workspace_bytes", "edge_moe_route", "edge_moe_forward",
 # element formats and dense types of the MX matrix operators
 MX_FP4, MX_FP8 = 0, 1
 _BF16, _FLOAT = 0, 1
+class _cuda:                   # torch's current device and stream handle, without the objects around them
+    getDevice = getRawStream = None
+
+
 _dtypes: dict = {}             # torch's types by name, and those of dense matrices (filled by load())
 _dense_types: dict = {}
 
@@ -129,6 +133,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     # PyTorch-ROCm ships its own HIP runtime; load it first so that the library
     # binds to the same runtime instance as the streams and memory it is given.
     import torch
+    _cuda.getDevice, _cuda.getRawStream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     _dtypes.update({n: getattr(torch, n) for n in ("uint8", "int32", "float32")})
     _dense_types.update({torch.bfloat16: _BF16, torch.int16: _BF16, torch.uint16: _BF16, torch.float32: _FLOAT})
     lib = ctypes.CDLL(path)
@@ -442,22 +447,20 @@ def edge_moe_route_backward(dims, logits, topk_idx, ws, topk_w=None, d_topk_w=No
         raise EdgeMoeError("edge_moe_route_backward", st)
 
 
-def _same_device(*tensors) -> int:
+def _same_device(first, *rest) -> int:
     """Every tensor on the current GPU, where the library launches; its index."""
-    import torch
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != cur:
-            raise ValueError(f"tensors must be on the current GPU (cuda:{cur}), got one on {t.device}")
-    return cur
+    dev = first.get_device()
+    for t in rest:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors must be on one GPU, got {first.device} and {t.device}")
+    if dev < 0 or dev != _cuda.getDevice():
+        raise ValueError(f"tensors must be on the current GPU, got {first.device}")
+    return dev
 
 
 def _stream_on(device: int, stream) -> int:
     """The stream's handle; None: the device's current stream."""
-    if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(device)
-    return _stream(stream)
+    return _cuda.getRawStream(device) if stream is None else _stream(stream)
 
 
 def _dense_type(t) -> int:
@@ -497,8 +500,8 @@ def _mx_shape(fmt, dense, codes, scales):
         raise ValueError("format must be MX_FP4 or MX_FP8")
     if dense.dim() < 2:
         raise ValueError("expected rows: a tensor of at least two dimensions")
-    N, K = dense.shape[-2], dense.shape[-1]
-    M = dense.numel() // max(1, N * K)
+    N, K = dense.shape[-2:]
+    M = dense.numel() // (N * K or 1)
     return (M, N, K, _sized(codes, "uint8", M * N * (K // 2 if fmt == MX_FP4 else K), "codes"),
             _sized(scales, "uint8", M * N * (K // 32), "scales"))
 
