@@ -302,7 +302,7 @@ int edge_moe_forward_mx(const edge_moe_dims* dims, const uint16_t* x, const int3
  * -infinity has no distribution and adds zeros.  NaN and +infinity give NaN.
  * logits: [T][E] as edge_moe_route writes logits_out.  Of dims, T, n_experts and
  * top_k are used (all must pass the layer's checks).  Sums over tokens are kept in
- * float64 past 32 tokens; results are bitwise reproducible. */
+ * float64 past 16 tokens; results are bitwise reproducible. */
 size_t edge_moe_balance_ws_bytes(const edge_moe_dims* dims, int32_t n_seq);
 int edge_moe_balance(const edge_moe_dims* dims, const float* logits, const int32_t* topk_idx,
                      const int32_t* seq_offsets, int32_t n_seq, int32_t* counts, float* probs, float* loss, void* ws,
@@ -337,8 +337,10 @@ typedef struct edge_moe_route_grad {
 /* Workspace bytes of edge_moe_route_backward (0 for invalid dims). */
 size_t edge_moe_route_backward_ws_bytes(const edge_moe_dims* dims);
 
-/* dz is kept to all 24 bits of its float32 (the sum of three bf16 terms), x and
- * W_r enter exactly and the sums are float32; bitwise reproducible.  An infinite
+/* dz is kept to all 24 bits of its float32 (the sum of three bf16 terms; fewer
+ * where a value is so small that the last term leaves bf16's normal range, below
+ * about 2^-110), x and W_r enter exactly and the sums are float32; bitwise
+ * reproducible.  An infinite
  * or NaN dz, x or W_r gives unspecified values in the sums it enters. */
 int edge_moe_route_backward(const edge_moe_dims* dims, const edge_moe_route_grad* grad, void* ws, size_t ws_bytes,
                             void* stream);

@@ -128,3 +128,18 @@ def test_product_binding_checks():
         a = {**ok, **bad}
         with pytest.raises((ValueError, RuntimeError, AssertionError)):     # the last: host tensors
             em.edge_moe_mx_product(em.MX_FP8, a.pop("x"), a.pop("codes"), a.pop("scales"), a.pop("y"), ws, **a)
+
+
+def test_tensors_must_be_on_the_current_gpu(monkeypatch):
+    class On:
+        def __init__(self, dev):
+            self.dev, self.device = dev, f"cuda:{dev}"
+
+        def get_device(self):
+            return self.dev
+    em.load()
+    monkeypatch.setattr(em._cuda, "getDevice", lambda: 1)
+    assert em._same_device(On(1), None, On(1)) == 1
+    for bad in ((On(0), On(0)), (On(1), On(0)), (On(-1), On(-1)), (On(1), None, On(-1))):
+        with pytest.raises(ValueError):
+            em._same_device(*bad)
