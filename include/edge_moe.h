@@ -361,7 +361,7 @@ int edge_moe_route_backward(const edge_moe_dims* dims, const edge_moe_route_grad
  * NaN or an infinity gets X = 255 and zero codes: it reads back as NaN.
  *   src         rows of K elements of src_type, src_stride elements apart
  *               (row n of matrix m is row m N + n; src_stride >= K)
- * K a multiple of 128 up to 32768, M N up to 2^30 rows (EDGE_MOE_EUNSUPPORTED
+ * K a multiple of 128 up to 32768, M N up to 2^27 rows (EDGE_MOE_EUNSUPPORTED
  * otherwise); src and its row stride in bytes, and codes, 16-byte aligned,
  * scales 4-byte aligned.  Makes the matrices of edge_moe_forward_mx and
  * edge_moe_mx_product from dense weights; results are those of the layer's own

@@ -543,6 +543,8 @@ def edge_moe_mx_product(x_format, x, codes, scales, y, ws, offsets=None, row_src
     if x.dim() != 2 or y.dim() != 2 or _dense_type(x) != _BF16 or _dense_type(y) != _BF16:
         raise ValueError("x and y must be bfloat16 (or int16 bits) [rows][columns]")
     (T, K), (R, N) = x.shape, y.shape
+    if max(T, R) >= 1 << 31:            # the library's sizes are 32 bits
+        raise ValueError(f"x and y have too many rows: {T}, {R}")
     M = 1 if codes.dim() == 2 else codes.shape[0]
     q = _sized(codes, "uint8", M * N * (K // 2), "codes")
     e = _sized(scales, "uint8", M * N * (K // 32), "scales")

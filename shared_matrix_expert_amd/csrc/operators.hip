@@ -9,10 +9,11 @@ namespace {
 
 bool aligned(const void* p, size_t a) { return p && ((uintptr_t)p % a) == 0; }
 
-// M matrices of N rows x K in the MX layouts.
+// M matrices of N rows x K in the MX layouts.  2^27 rows are 2^31 threads of the
+// quantiser; a launch holds fewer than 2^32.
 int mx_shape_status(int32_t M, int32_t N, int32_t K) {
     if (M < 1 || N < 1 || K < 1) return EDGE_MOE_EINVAL;
-    if (K % 128 || K > 32768 || (int64_t)M * N > (1ll << 30)) return EDGE_MOE_EUNSUPPORTED;
+    if (K % 128 || K > 32768 || (int64_t)M * N > (1ll << 27)) return EDGE_MOE_EUNSUPPORTED;
     return EDGE_MOE_OK;
 }
 

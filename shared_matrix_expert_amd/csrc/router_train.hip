@@ -151,7 +151,8 @@ EM_DEV float exp_neg(float v) {
 }
 
 // v becomes softmax(v); the row's log sum exp is returned.  A row of -infinity
-// alone (every expert masked) has no distribution: probabilities and lse 0.
+// alone (every expert masked) has no distribution: probabilities and lse 0, which
+// is then the sum s; a NaN among them makes s and both NaN.
 template <int NV>
 EM_DEV float softmax_row(float (&v)[NV][4]) {
     float m = -INFINITY;
@@ -171,12 +172,12 @@ EM_DEV float softmax_row(float (&v)[NV][4]) {
             s += v[i][c];
         }
     s = wave_sum(s);
-    const float inv = none ? 0.f : 1.f / s;
+    const float inv = none ? s : 1.f / s;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int c = 0; c < 4; ++c) v[i][c] *= inv;
-    return none ? 0.f : m + logf(s);
+    return none ? s : m + logf(s);
 }
 
 }  // namespace

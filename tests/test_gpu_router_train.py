@@ -1,9 +1,10 @@
 """The router-training operators on the GPU against the float64 oracle.
 
 Tolerances, in units u = 2^-24 (half a float32 step): a probability carries the
-rounding of z - max (|z - max| u), expf and the reciprocal (4 u), and the sum of
-E terms (each lane's E / 64, then six butterfly steps); the column sums add at
-most LCH / 4 + 2 more roundings before float64.  LOAD below bounds their sum for
+rounding of z - max (|z - max| u), the exponential and the reciprocal (4 u), and
+the sum of E terms (each lane's E / 64, then six steps across the lanes); the
+column sums add at most the roundings of 16 tokens' sums (four a wave, then four
+waves) before float64.  LOAD below bounds their sum for
 |z - max| <= 40 and E <= 1024: 40 + 4 + 22 + 10 < 100.
 """
 from types import SimpleNamespace
@@ -122,6 +123,17 @@ def test_balance_masked_experts_and_dropped_slots():
     assert np.isinf(float(loss[1])) and np.isfinite(float(loss[0]))
     z[20, 3] = np.nan
     assert np.isnan(run_balance(dims(T, E, k), z, idx)[2].cpu().numpy()).all()
+
+
+@pytest.mark.parametrize("rest", [float("nan"), -float("inf")])
+def test_balance_rows_of_nan(rest):
+    """A row of NaN alone, or of NaN among masked experts, is no masked token."""
+    T, E, k = 20, 300, 2
+    z, idx, *_ = case(T, E, k, 5)
+    z[7] = rest
+    z[7, 11] = np.nan
+    _, p, loss = run_balance(dims(T, E, k), z, idx)
+    assert bool(torch.isnan(p).all()) and bool(torch.isnan(loss).all())
 
 
 def run_backward(D, z, idx, **kw):

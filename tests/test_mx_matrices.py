@@ -70,7 +70,8 @@ def test_round_validation_before_any_device_call(name):
                 dict(scales=BASE + 2), dict(stride=255), dict(stride=260), dict(stride=-256),
                 dict(type=1, stride=258)):
         assert call(**bad) == em.EDGE_MOE_EINVAL, bad
-    for bad in (dict(K=96, stride=96), dict(K=32896, stride=32896), dict(M=1 << 20, N=1 << 20)):
+    for bad in (dict(K=96, stride=96), dict(K=32896, stride=32896), dict(M=1 << 20, N=1 << 20),
+                dict(M=1 << 9, N=(1 << 18) + 1, K=128, stride=128)):       # more rows than a launch holds
         assert call(**bad) == em.EDGE_MOE_EUNSUPPORTED, bad
 
 
@@ -128,6 +129,14 @@ def test_product_binding_checks():
         a = {**ok, **bad}
         with pytest.raises((ValueError, RuntimeError, AssertionError)):     # the last: host tensors
             em.edge_moe_mx_product(em.MX_FP8, a.pop("x"), a.pop("codes"), a.pop("scales"), a.pop("y"), ws, **a)
+
+
+def test_product_refuses_rows_past_32_bits():
+    y = torch.empty((1 << 32) + 4, 1, dtype=torch.bfloat16, device="meta")
+    x = torch.zeros(4, 128, dtype=torch.bfloat16)
+    q, e = torch.zeros(1, 1, 64, dtype=torch.uint8), torch.zeros(1, 1, 1, 4, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="too many rows"):
+        em.edge_moe_mx_product(em.MX_FP8, x, q, e, y, torch.zeros(4096, dtype=torch.uint8))
 
 
 def test_tensors_must_be_on_the_current_gpu(monkeypatch):
