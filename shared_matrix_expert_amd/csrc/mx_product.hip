@@ -115,6 +115,9 @@ EM_DEV int x_row(const MxProduct& a, int r) {
     return (unsigned)s < (unsigned)a.T ? s : -1;
 }
 
+// Row of the rounded x in the workspace for y row r (row 0 where row_src names none).
+EM_DEV int xq_row(const MxProduct& a, int r) { return a.gathered ? r : max(x_row(a, r), 0); }
+
 // Four consecutive columns of a y row (`whole`: all four exist and take one store).
 EM_DEV void store4(const MxProduct& a, int64_t r, int n, const floatx4& v, bool whole) {
     uint16_t* p = a.y + r * a.y_stride + n;
@@ -203,22 +206,23 @@ mxp_stream(MxProduct a) {
 #pragma unroll
         for (int d = 0; d < WD; ++d) load_w(d, min(s0 + d, s1 - 1));
     }
-    int src[NS];                                                  // x row of y row r0 + 16 s + m
+    int src[NS], qrow[NS];                                        // x row of y row r0 + 16 s + m; its row in the workspace
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
         const int r = t.r0 + 16 * s + m;
         src[s] = r < t.r1 ? x_row(a, r) : -1;
+        qrow[s] = a.gathered ? min(r, t.r1 - 1) : max(src[s], 0);
     }
     uint4 xv[XD][NS][2];
     int xsv[XD][NS];
     auto load_x = [&](int d, int st) {                            // (!FUSED) operand registers from the workspace
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-            const int64_t row = max(src[s], 0);
+            const int64_t row = qrow[s];
             const uint8_t* p = a.xq + row * (a.K / 128 * XB) + (int64_t)st * XB + 16 * g;
             xv[d][s][0] = ldg16(p);
             xv[d][s][1] = FMT == kMxFp8 ? ldg16(p + 64) : make_uint4(0u, 0u, 0u, 0u);
-            xsv[d][s] = a.xs[((int64_t)st * a.T + row) * 4 + g];
+            xsv[d][s] = a.xs[((int64_t)st * a.xrows + row) * 4 + g];
         }
     };
     floatx4 acc[NS][NC];
@@ -232,7 +236,11 @@ mxp_stream(MxProduct a) {
             for (int d = 0; d < XD; ++d) load_x(d, min(s0 + d, s1 - 1));
         }
     }
-    for (int st = s0; st < s1; st += WD) {
+    // WD steps; but for the last ones (`more`) without a branch, which would make
+    // each step wait for the loads it has just issued (one row through 8192 x 32768:
+    // 34.2 us with branches, 27.1 without)
+    auto run = [&](int st, auto more) {
+        constexpr bool MORE = decltype(more)::value;
         if constexpr (FUSED) {
             // rows in turn, 16 elements a lane: steps st .. st + 7 of this wave
             const int left = min(8, s1 - st) * kMxStep;           // elements of K (the loads past them repeat the last)
@@ -264,7 +272,7 @@ mxp_stream(MxProduct a) {
         }
 #pragma unroll
         for (int d = 0; d < WD; ++d) {
-            if (st + d < s1) {
+            if (MORE || st + d < s1) {
                 i32x8 q[NS];
                 int xs[NS];
 #pragma unroll
@@ -287,11 +295,14 @@ mxp_stream(MxProduct a) {
 #pragma unroll
                     for (int c = 0; c < NC; ++c) acc[s][c] = mfma_mx<FMT>(w[d][c], ws[d][c], q[s], xs[s], acc[s][c]);
                 if constexpr (!FUSED)
-                    if (st + d + XD < s1) load_x(d % XD, st + d + XD);
-                if (st + d + WD < s1) load_w(d, st + d + WD);
+                    load_x(d % XD, min(st + d + XD, s1 - 1));
+                if constexpr (MORE) load_w(d, min(st + d + WD, s1 - 1));
             }
         }
-    }
+    };
+    int st = s0;
+    for (; st + WD < s1; st += WD) run(st, std::true_type{});
+    if (st < s1) run(st, std::false_type{});
 #pragma unroll
     for (int s = 0; s < NS; ++s)
 #pragma unroll
@@ -404,7 +415,7 @@ mxp_gemm(MxProduct a) {
 #pragma unroll
     for (int q = 0; q < C::X_INSTR; ++q) {
         const int tr = XR * ((C::X_INSTR * wv + q) % C::X_P) + lane / (XB / 16);
-        xsrc[q] = a.xq + (int64_t)max(x_row(a, t.r0 + min(tr, nrow - 1)), 0) * (a.K * XB / 128)
+        xsrc[q] = a.xq + (int64_t)xq_row(a, t.r0 + min(tr, nrow - 1)) * (a.K * XB / 128)
                   + 16 * swz<XB>(tr, lane % (XB / 16));
     }
     const uint8_t* wbase = a.codes + ((int64_t)t.m * a.N + n0) * (a.K / 2);
@@ -419,7 +430,7 @@ mxp_gemm(MxProduct a) {
     for (int q = 0; q < C::S_INSTR; ++q) {
         const int piece = (C::S_INSTR * wv + q) % C::S_P, tr = 64 * piece + lane;
         soff[q] = piece < C::BN / 64 ? 4 * min(tr, a.N - 1 - n0)
-                                     : 4 * max(x_row(a, t.r0 + min(tr - C::BN, nrow - 1)), 0);
+                                     : 4 * xq_row(a, t.r0 + min(tr - C::BN, nrow - 1));
     }
     const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
     auto fetch = [&](int st, int to, int u) {           // load u of step st's, into the stage of step `to`
@@ -431,7 +442,7 @@ mxp_gemm(MxProduct a) {
             dma16(wbase + st * 64, woff[q], stage + C::X_B + 1024 * (C::W_INSTR * wv + q));
         } else {
             const int q = u - C::X_INSTR - C::W_INSTR, piece = (C::S_INSTR * wv + q) % C::S_P;
-            const uint8_t* src = piece < C::BN / 64 ? wsbase + (int64_t)st * a.N * 4 : a.xs + (int64_t)st * a.T * 4;
+            const uint8_t* src = piece < C::BN / 64 ? wsbase + (int64_t)st * a.N * 4 : a.xs + (int64_t)st * a.xrows * 4;
             dma4(src, soff[q], stage + C::X_B + C::W_B + 256 * piece);
         }
     };
@@ -613,6 +624,18 @@ int stream_rows(const MxProduct& a) {
     return 0;
 }
 
+// Whether mxp_stream's workgroups round the x rows that they need, which spares a
+// launch of 3 to 4 us, but costs each of them 0.25 us per row and 4096 of K (the
+// conversions): taken while a matrix's average rows times K are at most 16 x 4096.
+// Measured (us a call, rounded there / before it, FP8): one matrix of 8192 x 4096
+// 1 row 7.6 / 10.4, 16 rows 10.4 / 10.8; 4096 x 8192 8 rows 10.7 / 11.0, 16 rows
+// 15.1 / 12.1; 1024 x 32768 1 row 12.7 / 18.4, 4 rows 20 / 21, 16 rows 47 / 29;
+// 512 of 128 x 4096 80 rows 9.4 / 14.1.
+bool rounds_in_stream(const MxProduct& a) {
+    const int live = !a.offsets ? 1 : a.M < a.R ? a.M : a.R;
+    return ((int64_t)a.R + live - 1) / live * a.K <= 16 * 4096;
+}
+
 // Tiles of 256 rows where they fill the CUs and most of their rows are used; else
 // 64 rows (8192 columns, K = 4096: 1024 rows 41 against 54 us, 2048 rows 87 / 67;
 // 64 matrices of 1024 columns: 128 rows each 57 / 70, 256 each 134 / 135).
@@ -633,18 +656,23 @@ hipError_t launch_gemm(const MxProduct& a, hipStream_t s) {
 
 }  // namespace
 
+// Rows of x that the workspace holds: of a longer x only those that y's rows read
+// (rows that several y rows share are rounded once).
+static int x_rows(const MxProduct& a) { return a.R < a.T ? a.R : a.T; }
+
 size_t mx_product_ws_bytes(const MxProduct& a) {
     const size_t row = (size_t)a.K * (a.fmt == kMxFp4 ? 1 : 2) / 2 + (size_t)a.K / 32;
-    return (a.T * row + 511) & ~(size_t)255;
+    return ((size_t)x_rows(a) * row + 511) & ~(size_t)255;
 }
 
 hipError_t launch_mx_product(MxProduct a, void* ws, hipStream_t s) {
     const int ns = stream_rows(a);
-    // few x rows: every workgroup rounds the ones it needs, which spares a launch
-    if (a.T <= 16 && ns == 1) return launch_stream<1, true>(a, s);
+    if (ns == 1 && rounds_in_stream(a)) return launch_stream<1, true>(a, s);
+    a.xrows = x_rows(a);
+    a.gathered = a.row_src && a.xrows < a.T;
     a.xq = static_cast<uint8_t*>(ws);
-    a.xs = a.xq + (((size_t)a.T * a.K / (a.fmt == kMxFp4 ? 2 : 1) + 255) & ~(size_t)255);
-    const MxRows rows{a.T, a.T, a.K, a.x_stride, a.fmt, 0};
+    a.xs = a.xq + (((size_t)a.xrows * a.K / (a.fmt == kMxFp4 ? 2 : 1) + 255) & ~(size_t)255);
+    const MxRows rows{a.xrows, a.xrows, a.K, a.x_stride, a.fmt, 0, a.gathered ? a.row_src : nullptr, a.T};
     const hipError_t e = launch_mx_quantize(rows, a.x, const_cast<uint8_t*>(a.xq), const_cast<uint8_t*>(a.xs), s);
     if (e != hipSuccess) return e;
     switch (ns) {

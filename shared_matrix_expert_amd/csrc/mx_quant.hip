@@ -43,21 +43,28 @@ EM_DEV uint32_t quad_max(uint32_t v) {
 
 }  // namespace
 
-template <int FMT, bool F32>
+// GATHER: row r of the result is src row row_src[r] (row 0 for one outside
+// 0..src_rows - 1).
+template <int FMT, bool F32, bool GATHER>
 __global__ void __launch_bounds__(256)
 mxq_quantize(const void* __restrict__ src, int64_t stride, int64_t rows, int N, int K, uint8_t* __restrict__ codes,
-             uint8_t* __restrict__ scales) {
+             uint8_t* __restrict__ scales, const int32_t* __restrict__ row_src, int src_rows) {
     const int l16 = threadIdx.x & 15;
     const int64_t row = (int64_t)blockIdx.x * QR + (threadIdx.x >> 4);
     if (row >= rows) return;
     const int steps = K / kMxStep, s0 = blockIdx.y * QS;
     const int64_t m = row / N, n = row - m * N;
     uint8_t* srow = scales + (m * steps * N + n) * 4;          // + step * N * 4 + block
+    int64_t from = row;
+    if constexpr (GATHER) {
+        const int r = row_src[row];
+        from = (unsigned)r < (unsigned)src_rows ? r : 0;
+    }
     uint4 v[QS][F32 ? 2 : 1];
 #pragma unroll
     for (int i = 0; i < QS; ++i) {
         const int64_t k = (int64_t)min(s0 + i, steps - 1) * kMxStep + 8 * l16;
-        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(src) + (row * stride + k) * (F32 ? 4 : 2));
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(src) + (from * stride + k) * (F32 ? 4 : 2));
         v[i][0] = ld16_once(p);
         if constexpr (F32) v[i][1] = ld16_once(p + 1);
     }
@@ -176,13 +183,19 @@ dim3 quant_grid(const MxRows& r) {
 
 hipError_t launch_mx_quantize(const MxRows& r, const void* src, uint8_t* codes, uint8_t* scales, hipStream_t s) {
     const dim3 g = quant_grid(r);
+    const auto launch = [&](auto kernel) {
+        kernel<<<g, 256, 0, s>>>(src, r.stride, r.rows, r.N, r.K, codes, scales, r.row_src, r.src_rows);
+    };
     prof_begin(s);
-    if (r.fmt == kMxFp4) {
-        if (r.f32) mxq_quantize<kMxFp4, true><<<g, 256, 0, s>>>(src, r.stride, r.rows, r.N, r.K, codes, scales);
-        else mxq_quantize<kMxFp4, false><<<g, 256, 0, s>>>(src, r.stride, r.rows, r.N, r.K, codes, scales);
+    if (r.row_src) {                                            // bf16 (the product's x)
+        if (r.fmt == kMxFp4) launch(mxq_quantize<kMxFp4, false, true>);
+        else launch(mxq_quantize<kMxFp8, false, true>);
+    } else if (r.fmt == kMxFp4) {
+        if (r.f32) launch(mxq_quantize<kMxFp4, true, false>);
+        else launch(mxq_quantize<kMxFp4, false, false>);
     } else {
-        if (r.f32) mxq_quantize<kMxFp8, true><<<g, 256, 0, s>>>(src, r.stride, r.rows, r.N, r.K, codes, scales);
-        else mxq_quantize<kMxFp8, false><<<g, 256, 0, s>>>(src, r.stride, r.rows, r.N, r.K, codes, scales);
+        if (r.f32) launch(mxq_quantize<kMxFp8, true, false>);
+        else launch(mxq_quantize<kMxFp8, false, false>);
     }
     prof_end(s, "mxq_quantize");
     return hipGetLastError();

@@ -21,6 +21,8 @@ struct MxRows {
     int64_t stride;      // elements between rows of the dense side
     int fmt;             // kMxFp4, kMxFp8
     int f32;             // dense side float32 (else bf16)
+    const int32_t* row_src = nullptr;   // (quantise, bf16) the src row of each row, of src_rows
+    int src_rows = 0;
 };
 hipError_t launch_mx_quantize(const MxRows& r, const void* src, uint8_t* codes, uint8_t* scales, hipStream_t s);
 hipError_t launch_mx_dequantize(const MxRows& r, const uint8_t* codes, const uint8_t* scales, void* dst, hipStream_t s);
@@ -38,8 +40,9 @@ struct MxProduct {
     uint16_t* y;                // [R] rows of N bf16, y_stride elements apart
     int64_t y_stride;
     int vec;                    // y rows take 8-byte (1) or 16-byte (2) stores at every fourth (eighth) column
-    uint8_t* xq;                // workspace: x's codes [T][K] or [T][K/2] ...
-    uint8_t* xs;                // ... and scales [K/128][T][4]
+    int xrows, gathered;        // rows of x in the workspace; gathered: row r is y row r's, else x row r
+    uint8_t* xq;                // workspace: x's codes [xrows][K] or [xrows][K/2] ...
+    uint8_t* xs;                // ... and scales [K/128][xrows][4]
 };
 size_t mx_product_ws_bytes(const MxProduct& a);
 hipError_t launch_mx_product(MxProduct a, void* ws, hipStream_t s);

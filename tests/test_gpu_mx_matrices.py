@@ -277,6 +277,28 @@ def test_product_gathered_rows(fmt, R, T, N):
 
 
 @fmt_of
+@pytest.mark.parametrize("R,T,N", [(1, 400, 64), (3, 17, 40), (40, 700, 48), (60, 900, 640), (300, 2000, 512), (700, 1501, 8192)])
+@pytest.mark.parametrize("gather", [True, False])
+def test_product_of_few_rows_of_a_long_x(fmt, R, T, N, gather):
+    """Fewer y rows than x rows: gathered ones (two the same, one that names no
+    row), or x's first; the workspace is that of R rows."""
+    rng = np.random.default_rng(R)
+    src = rng.integers(0, T, R) if gather else None
+    if gather and R > 2:
+        src[0], src[1], src[R - 1] = src[2], T, T - 1
+    q, e, W = matrices(2, N, 384, 1)
+    off = [0, R // 3, R]
+    x = rows_of(T, 384, 3)
+    y = torch.full((R, N), float("nan"), dtype=torch.bfloat16, device=DEV)
+    ws = torch.full((em.edge_moe_mx_product_ws_bytes(T, R, 2, N, 384, fmt) + 4096,), 0xA5, dtype=torch.uint8, device=DEV)
+    assert ws.numel() <= 4096 + 512 + R * (384 + 12)
+    em.edge_moe_mx_product(fmt, x.to(DEV), q, e, y, ws[:-4096], offsets=i32(off), row_src=None if src is None else i32(src))
+    ref = ops.product(x[:R].double().numpy(), fmt, W, off) if src is None else ops.product(x.double().numpy(), fmt, W, off, src)
+    within(y, *ref, 384)
+    assert bool((ws[-4096:] == 0xA5).all())
+
+
+@fmt_of
 @pytest.mark.parametrize("T", [5, 90, 230])
 def test_product_strided_rows(fmt, T):
     q, e, W = matrices(1, 44, 256, 8)
