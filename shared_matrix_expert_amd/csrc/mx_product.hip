@@ -337,7 +337,7 @@ namespace {
 template <int FMT, int BT_>
 struct GemmCfg {
     static constexpr int BT = BT_, BN = 256;
-    static constexpr int WN = BT == 256 ? 2 : 4, WT = 8 / WN, NW = WN * WT;
+    static constexpr int WN = BT >= 192 ? 2 : 4, WT = 8 / WN, NW = WN * WT;
     static constexpr int NI = BN / WN / 16, NJ = BT / WT / 16;     // column and row subtiles of a wave
     static constexpr int XB = FMT == kMxFp4 ? 64 : 128;            // bytes of an x row per step
     static constexpr int X_B = BT * XB, W_B = BN * 64, XS_B = BT * 4, WS_B = BN * 4;
@@ -636,12 +636,29 @@ bool rounds_in_stream(const MxProduct& a) {
     return ((int64_t)a.R + live - 1) / live * a.K <= 16 * 4096;
 }
 
-// Tiles of 256 rows where they fill the CUs and most of their rows are used; else
-// 64 rows (8192 columns, K = 4096: 1024 rows 41 against 54 us, 2048 rows 87 / 67;
-// 64 matrices of 1024 columns: 128 rows each 57 / 70, 256 each 134 / 135).
-bool big_tiles(const MxProduct& a) {
-    const int live = !a.offsets ? 1 : a.M < a.R ? a.M : a.R;
-    return a.R >= 192ll * live && max_row_tiles(a, 256) * ((a.N + 255) / 256) >= 192;
+// Rows of mxp_gemm's tiles.  A CU holds one workgroup, so a product takes as many
+// rounds of tiles as 256 CUs need, each as long as a tile: measured at K = 4096,
+// 64 / 128 / 192 / 256 rows 18 / 27 / 36 / 44 us in FP4 and 20 / 31 / 45 / 59 in
+// FP8.  The rows with the least rounds times length are taken; each matrix with
+// rows is counted half a tile more.  (8192 columns, K = 4096, FP4, us a call by
+// rows: 1000 40 / 30 / 32 / 35, 1536 58 / 49 / 39 / 41, 2048 76 / 57 / 62 / 48;
+// 8 matrices of 4096 x 8192 in FP8, 5001 rows: 235 / 180 / 183 / 207.)
+int tile_rows(const MxProduct& a) {
+    static constexpr int kTile[2][4] = {{18, 27, 36, 44}, {20, 31, 45, 59}};
+    const int live = !a.offsets ? 0 : a.M < a.R ? a.M : a.R;
+    const int64_t cols = (a.N + 255) / 256;
+    int64_t best = 0;
+    int rows = 0;
+    for (int i = 0; i < 4; ++i) {
+        const int bt = 64 * (i + 1);
+        const int64_t halves = a.offsets ? 2ll * a.R / bt + live : 2ll * ((a.R + bt - 1) / bt);
+        const int64_t cost = (halves * cols + 511) / 512 * kTile[a.fmt == kMxFp8][i];
+        if (!rows || cost < best) {
+            best = cost;
+            rows = bt;
+        }
+    }
+    return rows;
 }
 
 template <int BT>
@@ -679,7 +696,13 @@ hipError_t launch_mx_product(MxProduct a, void* ws, hipStream_t s) {
         case 1: return launch_stream<1, false>(a, s);
         case 2: return launch_stream<2, false>(a, s);
         case 4: return launch_stream<4, false>(a, s);
-        default: return big_tiles(a) ? launch_gemm<256>(a, s) : launch_gemm<64>(a, s);
+        default: break;
+    }
+    switch (tile_rows(a)) {
+        case 64: return launch_gemm<64>(a, s);
+        case 128: return launch_gemm<128>(a, s);
+        case 192: return launch_gemm<192>(a, s);
+        default: return launch_gemm<256>(a, s);
     }
 }
 

@@ -222,7 +222,8 @@ def i32(v):
 @pytest.mark.parametrize("T,N,K", [(1, 16, 128), (1, 2048, 4096), (2, 1, 256), (3, 37, 384), (16, 64, 640),
                                    (17, 100, 512), (33, 50, 1024), (64, 96, 128), (65, 257, 256), (127, 33, 384),
                                    (191, 512, 512), (192, 256, 128), (257, 300, 1152), (700, 1030, 256),
-                                   (20, 4096, 256), (50, 2080, 256), (40, 8192, 128), (3000, 4608, 256), (2800, 5000, 128)])
+                                   (20, 4096, 256), (50, 2080, 256), (40, 8192, 128), (3000, 4608, 256), (2800, 5000, 128),
+                                   (1000, 7937, 128), (997, 7920, 384), (1530, 8000, 256), (1400, 8191, 128)])
 def test_product_dense(fmt, T, N, K):
     say(f"case: product {T} x {N} x {K}")
     q, e, W = matrices(1, N, K, T + N)
@@ -258,6 +259,21 @@ def test_product_grouped(fmt, sizes, T):
     ref, mag = ops.product(x.double().numpy(), fmt, W, off, src, R)
     within(y, ref, mag, K)
     assert bool((y[:head] == 3.25).all()) and bool((y[head + n:] == 3.25).all())
+
+
+@fmt_of
+@pytest.mark.parametrize("sizes", [[600, 0, 700, 65], [1500, 3, 0, 700, 129], [2050, 0, 1, 1300], [90] * 12])
+def test_product_grouped_tiles(fmt, sizes):
+    """Groups that the tiled kernel takes by 64 to 256 rows, odd columns."""
+    N, K, R = 4101, 256, sum(sizes)
+    q, e, W = matrices(len(sizes), N, K, 11)
+    x = rows_of(R, K, 12)
+    y = torch.full((R + 2, N), 3.25, dtype=torch.bfloat16, device=DEV)
+    say(f"case: groups of {sizes}")
+    off = np.concatenate([[0], np.cumsum(sizes)])
+    product(fmt, x.to(DEV), q, e, y[:R], offsets=i32(off))
+    within(y[:R], *ops.product(x.double().numpy(), fmt, W, off), K)
+    assert bool((y[R:] == 3.25).all())
 
 
 @fmt_of
