@@ -169,6 +169,9 @@ EM_DEV void round16(const uint4 (&v)[2], uint32_t (&q)[4], int& X) {
 // its weights are in flight.  (Rounding in operand registers instead, every lane
 // its own row's elements, costs 16 rows' work whatever their number: one token
 // through 8192 x 4096 took 9.4 us that way.)
+// One row through 8192 x 4096: 6.5 us for 17.8 MB, the launch and three dependent
+// trips to memory; through 8192 x 32768: 27 us a call, 5.2 TB/s.  80 rows over 512
+// matrices of 128 x 4096: 10 us, five trips (offsets, row list, x, W, y).
 template <int FMT, int NS, int NC, bool FUSED>
 __global__ void __launch_bounds__(256)
 mxp_stream(MxProduct a) {
@@ -329,6 +332,9 @@ mxp_stream(MxProduct a) {
 // steps ahead; every wave issues the same number of loads a step, so one counted
 // wait covers them.  A code row is 64 (E2M1) or 128 (E4M3) bytes; its 16-byte
 // segments are stored XOR-swizzled by the row against bank conflicts.
+// 16384 x 8192 x 4096 in FP8: 430 to 450 us at the clock that the load leaves, 2.5
+// PFLOP/s (a large library product in FP8: 2.65); 5001 rows in 8 groups through
+// 4096 x 8192 in FP4: 116 to 124 us, two rounds of 192-row tiles, 2.8 PFLOP/s.
 // (Four waves of 128 x 128, one a SIMD with 256 accumulators each, read a quarter
 // less from the LDS and measured 479 against 450 us on 16384 x 8192 x 4096 in FP8:
 // one wave's waits leave its matrix core idle.)
