@@ -70,7 +70,7 @@ hipError_t launch_router_load(RouterLoad a, void* ws, hipStream_t s);
 struct RouterGrad {
     int T, E, k, S, d, vec;
     int Tp, Ep;                     // T and E up to multiples of 32
-    int slices;                     // token slices of dW_r
+    int bi, slices;                 // tile rows of the products, token slices of dW_r
     int chunk;                      // tokens per workgroup of rt_dlogits
     const float* logits; const int32_t* topk_idx; const float* topk_w;
     const float* d_topk_w;          // [T][k] or null

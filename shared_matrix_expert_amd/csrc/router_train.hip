@@ -617,36 +617,68 @@ EM_DEV void rt_tile(const RouterGrad& a, int block, uint8_t* lds) {
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int c = 0; c < NC; ++c) acc[i][c] = zero4();
+    // A wave's LDS reads of a plane: DX the operands themselves, DW rows to transpose.
+    struct Plane { uint4 v[4]; };
+    auto read_plane = [&](const uint8_t* A, int p) {
+        Plane o;
+        if constexpr (MODE == RT_DX) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 64 * wi + 16 * i + m;
+                o.v[i] = *reinterpret_cast<const uint4*>(A + p * C::P_B + r * 64 + 16 * (g ^ (-(r >> 2) & 3)));
+            }
+        } else {
+            uint2 raw[8];
+            read_rows(raw, A + p * C::P_B + 8 * g * (2 * BI) + 2 * (64 * wi + 4 * m), 2 * BI);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o.v[i] = make_uint4(raw[2 * i].x, raw[2 * i].y, raw[2 * i + 1].x, raw[2 * i + 1].y);
+        }
+        return o;
+    };
+    auto products = [&](const Plane& a, const uint4 (&bf)[NC]) {
+        uint4 af[4];
+        if constexpr (MODE == RT_DX) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) af[i] = a.v[i];
+        } else {
+            uint2 raw[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) raw[i] = i & 1 ? make_uint2(a.v[i / 2].z, a.v[i / 2].w) : make_uint2(a.v[i / 2].x, a.v[i / 2].y);
+            transpose8(raw, af);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) acc[i][c] = mfma_bf16(af[i], bf[c], acc[i][c]);
+    };
     if (s0 < s1) fetch(s0);
     for (int st = s0; st < s1; ++st) {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (st + 1 < s1) fetch(st + 1);
         const uint8_t* A = lds + (st & 1) * C::STAGE;
         const uint8_t* Bt = A + 3 * C::P_B;
+        const int bat = 8 * g * 512 + 2 * (16 * NC * wn + NC * m);
         uint4 bf[NC];
-        {
-            uint2 raw[8];
-            read_rows(raw, Bt + 8 * g * 512 + 2 * (16 * NC * wn + NC * m), 512);
+        uint2 raw[8];
+        if constexpr (BI == 64) {
+            // one or two waves a SIMD: the next plane is read, and the next step asked
+            // for, under this plane's products
+            read_rows(raw, Bt + bat, 512);
+            const Plane p0 = read_plane(A, 0);
+            if (st + 1 < s1) fetch(st + 1);
             transpose8(raw, bf);
-        }
+            const Plane p1 = read_plane(A, 1);
+            __builtin_amdgcn_sched_barrier(0);
+            products(p0, bf);
+            const Plane p2 = read_plane(A, 2);
+            __builtin_amdgcn_sched_barrier(0);
+            products(p1, bf);
+            products(p2, bf);
+        } else {
+            if (st + 1 < s1) fetch(st + 1);
+            read_rows(raw, Bt + bat, 512);
+            transpose8(raw, bf);
 #pragma unroll
-        for (int p = 0; p < 3; ++p) {
-            uint4 af[4];
-            if constexpr (MODE == RT_DX) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 64 * wi + 16 * i + m;
-                    af[i] = *reinterpret_cast<const uint4*>(A + p * C::P_B + r * 64 + 16 * (g ^ (-(r >> 2) & 3)));
-                }
-            } else {
-                uint2 raw[8];
-                read_rows(raw, A + p * C::P_B + 8 * g * (2 * BI) + 2 * (64 * wi + 4 * m), 2 * BI);
-                transpose8(raw, af);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int c = 0; c < NC; ++c) acc[i][c] = mfma_bf16(af[i], bf[c], acc[i][c]);
+            for (int p = 0; p < 3; ++p) products(read_plane(A, p), bf);
         }
     }
 
@@ -700,17 +732,28 @@ rt_products(RouterGrad a, int bblocks, int wblocks) {
     else rt_tile<RT_DX, BI>(a, b - bblocks - wblocks, lds);
 }
 
-// Token slices of dW_r, in order: HBM and the Infinity Cache (512 x 4096, 8 slices:
-// 12 us, 75 MB; 4 slices 7.2 us, 42 MB).
+// Token slices of dW_r, in order, eight asked for at once (four where there are no
+// more): HBM and the Infinity Cache (512 x 4096, 4 slices: 7.2 us, 42 MB).
+template <int N>
+EM_DEV void rt_add_slices(float4& s, const RouterGrad& a, int64_t n, int64_t at, int z) {
+    float4 v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = *reinterpret_cast<const float4*>(a.part_w + min(z + i, a.slices - 1) * n + at);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (z + i < a.slices) {
+            s.x += v[i].x; s.y += v[i].y; s.z += v[i].z; s.w += v[i].w;
+        }
+}
+
 __global__ void __launch_bounds__(256)
 rt_finish(RouterGrad a) {
     const int64_t n = (int64_t)a.E * a.d, at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (at >= n) return;
-    float4 s = *reinterpret_cast<const float4*>(a.part_w + at);
-    for (int z = 1; z < a.slices; ++z) {
-        const float4 v = *reinterpret_cast<const float4*>(a.part_w + z * n + at);
-        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-    }
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.slices <= 4) rt_add_slices<4>(s, a, n, at, 0);
+    else
+        for (int z = 0; z < a.slices; z += 8) rt_add_slices<8>(s, a, n, at, z);
     *reinterpret_cast<float4*>(a.dw_router + at) = s;
 }
 
@@ -738,20 +781,39 @@ LoadLayout load_layout(const RouterLoad& a) {
 struct GradLayout { size_t planes, part_w, part_b, bytes; };
 
 int pad32(int v) { return (v + 31) & ~31; }
-int tile_rows(const RouterGrad& a) { return a.E > 64 ? 128 : 64; }
 int64_t tiles(int rows, int bi, int d) { return (int64_t)((rows + bi - 1) / bi) * ((d + 255) / 256); }
 
-// Token slices of dW_r: as many as give every CU a workgroup, or two where each
-// still has 32 K steps (T = 16384: 8 slices 170, 4 slices 190 us); at least four
-// steps each.  Every slice writes dW_r once and rt_finish reads it (T = 1501:
-// 8 slices 29 + 16, 4 slices 27 + 12, 2 slices 37 + 10 us).
-int dw_slices(const RouterGrad& a) {
-    const int64_t t = tiles(a.E, tile_rows(a), a.d);
-    const int steps = a.Tp / 32;
-    int64_t z = 512 / t;
-    if (z > 0 && steps / z < 32) z = 256 / t;
-    z = z < steps / 4 ? z : steps / 4;
-    return z < 1 ? 1 : z > 16 ? 16 : (int)z;
+// Tile rows of rt_products and token slices of dW_r: the least of an estimate (us)
+// from measured step times (32 of K).  A workgroup alone on a CU takes 0.85 us a
+// step with 64 rows and 1.06 with 128, two 1.25 and 2.2 each, and a full chip 0.85
+// and 1.2 us a step and CU; dx has E / 32 steps a tile, dW_r T / 32 split into the
+// slices, whose sums rt_finish adds in a launch more.  Measured passes, 64 rows
+// against 128 (T x E x d, us): 7 x 913 x 640 30 / 40, 751 x 480 x 2560 30 / 33,
+// 16384 x 512 x 4096 362 / 333; slices 1, 8 and 32 of 11764 x 48 x 384 282 / 52 / 30,
+// 1, 2 and 4 of 761 x 936 x 1024 36 / 38 / 41.
+void plan_grad(RouterGrad& a) {
+    static constexpr double kAlone[2] = {0.85, 1.06}, kTwo[2] = {1.25, 2.2}, kFull[2] = {0.85, 1.2};
+    a.Tp = pad32(a.T);
+    a.Ep = pad32(a.E);
+    const int tsteps = a.Tp / 32, esteps = a.Ep / 32;
+    double least = 0;
+    a.bi = 0;
+    for (int i = 0; i < 2; ++i) {
+        const int bi = 64 << i;
+        const int64_t dx = tiles(a.T, bi, a.d), dw = tiles(a.E, bi, a.d);
+        for (int z = 1; z <= 64 && z <= tsteps; z *= 2) {
+            const int slice = (tsteps + z - 1) / z, longest = slice > esteps ? slice : esteps;
+            const double chain = longest * (dx + dw * z <= 256 ? kAlone[i] : kTwo[i]);
+            const double all = ((double)dx * esteps + (double)dw * tsteps) * kFull[i] / 256;
+            const double finish = z == 1 ? 0 : 3.5 + 0.3 * z + (z + 1.0) * a.E * a.d * 4 / 6e6;
+            const double us = (chain > all ? chain : all) + finish;
+            if (!a.bi || us < least) {
+                least = us;
+                a.bi = bi;
+                a.slices = z;
+            }
+        }
+    }
 }
 
 GradLayout grad_layout(const RouterGrad& a) {
@@ -760,7 +822,7 @@ GradLayout grad_layout(const RouterGrad& a) {
     auto take = [&](size_t n) { const size_t o = off; off = up(off + n); return o; };
     // the last tile reads up to 255 rows past the last plane (DX), up to 255 columns past its last row (DW)
     L.planes = take(((size_t)3 * a.Tp + 256) * a.Ep * 2 + 512);
-    L.part_w = take((size_t)dw_slices(a) * a.E * a.d * 4);
+    L.part_w = take((size_t)(a.slices > 1 ? a.slices : 0) * a.E * a.d * 4);
     L.part_b = take((size_t)((a.Tp + grad_chunk(a.T) - 1) / grad_chunk(a.T)) * a.E * 4);
     L.bytes = off;
     return L;
@@ -793,21 +855,15 @@ hipError_t launch_router_load(RouterLoad a, void* ws, hipStream_t s) {
     return hipGetLastError();
 }
 
-static void pad_grad(RouterGrad& a) {
-    a.Tp = pad32(a.T);
-    a.Ep = pad32(a.E);
-}
-
 size_t router_grad_ws_bytes(RouterGrad a) {
-    pad_grad(a);
+    plan_grad(a);
     return grad_layout(a).bytes;
 }
 
 hipError_t launch_router_grad(RouterGrad a, void* ws, hipStream_t s) {
-    pad_grad(a);
+    plan_grad(a);
     const GradLayout L = grad_layout(a);
     char* base = static_cast<char*>(ws);
-    a.slices = dw_slices(a);
     a.planes = a.dx || a.dw_router ? reinterpret_cast<uint16_t*>(base + L.planes) : nullptr;
     a.part_w = reinterpret_cast<float*>(base + L.part_w);
     a.part_b = a.dbias ? reinterpret_cast<float*>(base + L.part_b) : nullptr;
@@ -820,7 +876,7 @@ hipError_t launch_router_grad(RouterGrad a, void* ws, hipStream_t s) {
     prof_end(s, "rt_dlogits");
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !(a.dx || a.dw_router || a.dbias)) return e;
-    const int bi = tile_rows(a);
+    const int bi = a.bi;
     const auto up8 = [](int64_t n) { return (int)((n + 7) & ~7ll); };
     const int bblocks = a.dbias ? up8((a.E + 63) / 64) : 0;
     const int wblocks = a.dw_router ? up8(tiles(a.E, bi, a.d) * a.slices) : 0;

@@ -186,7 +186,8 @@ def check_backward(T, E, k, d, off=None, weights=True, losses=True, edit=None, s
 
 @pytest.mark.parametrize("T,E,k,d", [(1, 8, 1, 128), (2, 10, 3, 384), (31, 64, 4, 512), (65, 130, 2, 128), (96, 64, 4, 512),
                                      (130, 512, 10, 640), (257, 1000, 6, 256), (300, 257, 5, 1024), (1025, 128, 2, 128),
-                                     (1501, 512, 10, 512)])
+                                     (1501, 512, 10, 512), (5, 913, 6, 640), (751, 480, 7, 1280), (2273, 80, 4, 128),
+                                     (1531, 10, 2, 3200), (7181, 16, 3, 384), (11764, 48, 4, 128)])
 def test_backward_shapes(T, E, k, d):
     say(f"case: backward {T} x {E} x {d}, top {k}")
     check_backward(T, E, k, d)
