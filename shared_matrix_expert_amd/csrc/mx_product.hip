@@ -322,7 +322,7 @@ mxp_stream(MxProduct a) {
             v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
         }
         const int s = i / NC, c = i % NC, r = t.r0 + 16 * s + m;
-        if (r < t.r1) store4(a, r, n0 + 16 * c + 4 * g, src[s] >= 0 ? v : zero4(), a.vec && n0 + 16 * (c + 1) <= a.N);
+        if (r < t.r1) store4(a, r, n0 + 16 * c + 4 * g, src[s] >= 0 ? v : zero4(), a.vec >= 2 && n0 + 16 * (c + 1) <= a.N);
     }
 }
 
@@ -541,47 +541,56 @@ mxp_gemm(MxProduct a) {
     if (st < steps) step(st, Set<0>{});
     wait_loads_barrier<0>();                                          // nothing more lands in the stages
 
-    // ---- y: lane (g, m) holds columns 4 g .. 4 g + 3 of each column subtile, x row m
-    if (a.vec > 1 && n0 + C::BN <= a.N) {
-        // through the LDS, so that a wave stores whole 256- or 128-byte row
-        // segments, past the L2: 32-byte pieces leave it half-written lines to
-        // merge, and the lines it keeps cost the next kernel their write-back
-        constexpr int RB = NI * 32, RSTR = RB + 16;          // bytes of a wave's row, their LDS stride
-        uint8_t* o = lds + wv * (16 * NJ * RSTR);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const int r = t.r0 + 16 * (NJ * wt + j) + m;
-            const bool live = r < t.r1 && x_row(a, r) >= 0;
-#pragma unroll
-            for (int p = 0; p < NI; ++p) {
-                const floatx4 v = live ? acc[p][j] : zero4();
-                const f32x2 lo = {v.x, v.y}, hi = {v.z, v.w};
-                *reinterpret_cast<uint2*>(o + (16 * j + m) * RSTR + 32 * p + 8 * g) =
-                    make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector(lo, bf16x2)),
-                               __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, bf16x2)));
-            }
-        }
-        __builtin_amdgcn_wave_barrier();                     // one wave's LDS accesses complete in order
-        asm volatile("" ::: "memory");
-        constexpr int LPR = RB / 16, RPI = 64 / LPR;         // lanes per row, rows per store
-#pragma unroll
-        for (int i = 0; i < 16 * NJ / RPI; ++i) {
-            const int tr = RPI * i + lane / LPR, r = t.r0 + 16 * NJ * wt + tr;
-            if (r >= t.r1) continue;
-            const u32x4 v = *reinterpret_cast<const u32x4*>(o + tr * RSTR + 16 * (lane % LPR));
-            __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(a.y + (int64_t)r * a.y_stride + n0 + 16 * NI * wn + 8 * (lane % LPR)));
-        }
-        return;
-    }
+    // ---- y: lane (g, m) holds columns 4 g .. 4 g + 3 of each column subtile, x row m.
+    // Through the LDS, so that a wave stores whole 256- or 128-byte row segments: 32-byte
+    // pieces leave the L2 half-written lines to merge.  Aligned ones go past it, since the
+    // lines that it keeps cost the next kernel their write-back; rows at odd places and
+    // the last columns in words or halves (11845 rows of 4222 columns, K = 384: 117 us
+    // with 2-byte stores from the accumulators, 60 here).
+    constexpr int RB = NI * 32, RSTR = RB + 16;              // bytes of a wave's row, their LDS stride
+    uint8_t* o = lds + wv * (16 * NJ * RSTR);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
         const int r = t.r0 + 16 * (NJ * wt + j) + m;
-        if (r >= t.r1) continue;
-        const bool live = x_row(a, r) >= 0;
+        const bool live = r < t.r1 && x_row(a, r) >= 0;
 #pragma unroll
         for (int p = 0; p < NI; ++p) {
-            const int n = n0 + 16 * (NI * wn + p);
-            store4(a, r, n + 4 * g, live ? acc[p][j] : zero4(), a.vec && n + 16 <= a.N);
+            const floatx4 v = live ? acc[p][j] : zero4();
+            const f32x2 lo = {v.x, v.y}, hi = {v.z, v.w};
+            *reinterpret_cast<uint2*>(o + (16 * j + m) * RSTR + 32 * p + 8 * g) =
+                make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector(lo, bf16x2)),
+                           __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, bf16x2)));
+        }
+    }
+    __builtin_amdgcn_wave_barrier();                         // one wave's LDS accesses complete in order
+    asm volatile("" ::: "memory");
+    const int r0 = t.r0 + 16 * NJ * wt, c0 = n0 + 16 * NI * wn, left = a.N - c0;   // the wave's rows, columns and those that exist
+    if (a.vec == 3 && left >= 16 * NI) {
+        constexpr int LPR = RB / 16, RPI = 64 / LPR;         // lanes per row, rows per store
+#pragma unroll
+        for (int i = 0; i < 16 * NJ / RPI; ++i) {
+            const int tr = RPI * i + lane / LPR;
+            if (r0 + tr >= t.r1) continue;
+            const u32x4 v = *reinterpret_cast<const u32x4*>(o + tr * RSTR + 16 * (lane % LPR));
+            __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(a.y + (int64_t)(r0 + tr) * a.y_stride + c0 + 8 * (lane % LPR)));
+        }
+    } else if (a.vec) {
+        constexpr int LPR = RB / 4, RPI = 64 / LPR;
+        const int n = 2 * (lane % LPR);
+#pragma unroll 8
+        for (int i = 0; i < 16 * NJ / RPI; ++i) {
+            const int tr = RPI * i + lane / LPR;
+            if (r0 + tr >= t.r1 || n >= left) continue;
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(o + tr * RSTR + 2 * n);
+            uint16_t* p = a.y + (int64_t)(r0 + tr) * a.y_stride + c0 + n;
+            if (n + 1 < left) *reinterpret_cast<uint32_t*>(p) = v;
+            else *p = (uint16_t)v;
+        }
+    } else {
+#pragma unroll 8
+        for (int i = 0; i < 16 * NJ * (RB / 128); ++i) {
+            const int tr = i / (RB / 128), n = lane + 64 * (i % (RB / 128));
+            if (r0 + tr < t.r1 && n < left) a.y[(int64_t)(r0 + tr) * a.y_stride + c0 + n] = *reinterpret_cast<const uint16_t*>(o + tr * RSTR + 2 * n);
         }
     }
 }

@@ -39,7 +39,7 @@ struct MxProduct {
     const uint8_t* scales;      // [M][K/128][N][4] E8M0
     uint16_t* y;                // [R] rows of N bf16, y_stride elements apart
     int64_t y_stride;
-    int vec;                    // y rows take 8-byte (1) or 16-byte (2) stores at every fourth (eighth) column
+    int vec;                    // y rows take 4-, 8- or 16-byte stores (1, 2, 3) at every second, fourth or eighth column
     int xrows, gathered;        // rows of x in the workspace; gathered: row r is y row r's, else x row r
     uint8_t* xq;                // workspace: x's codes [xrows][K] or [xrows][K/2] ...
     uint8_t* xs;                // ... and scales [K/128][xrows][4]

@@ -108,7 +108,7 @@ int edge_moe_mx_product(const edge_moe_mx_dims* dims, const uint16_t* x, int64_t
     if (d.R == 0) return EDGE_MOE_OK;
     a.x = x; a.x_stride = x_stride; a.row_src = row_src; a.offsets = offsets; a.codes = codes; a.scales = scales;
     a.y = y; a.y_stride = y_stride;
-    a.vec = y_stride % 8 == 0 && aligned(y, 16) ? 2 : y_stride % 4 == 0 && aligned(y, 8) ? 1 : 0;
+    a.vec = y_stride % 8 == 0 && aligned(y, 16) ? 3 : y_stride % 4 == 0 && aligned(y, 8) ? 2 : y_stride % 2 == 0 && aligned(y, 4) ? 1 : 0;
     return hip_status(em::launch_mx_product(a, ws, (hipStream_t)stream));
 }
 
