@@ -62,13 +62,12 @@ EM_DEV uint32_t fp4x8_bf16(const uint4& v, float scale) {
     r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, v.w), scale, 3);
     return r;
 }
-EM_DEV uint32_t fp4x8_f32(const float (&v)[8], float scale) {
+// Four float32 values, as 16 bits.
+EM_DEV uint16_t fp4x4_f32(const float (&v)[4], float scale) {
     uint32_t r = 0;
     r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[0], v[1], scale, 0);
     r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[2], v[3], scale, 1);
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[4], v[5], scale, 2);
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[6], v[7], scale, 3);
-    return r;
+    return (uint16_t)r;
 }
 
 // Two bf16 values with magnitudes limited to 448 * 2^(X - 127): the E4M3

@@ -5,15 +5,17 @@
 //
 // Both directions read each input once and write each output once with a
 // handful of conversions per element, so they are bound by HBM.  Sixteen lanes
-// take one 128-element step of a row (8 elements each): a scale block is four
-// neighbouring lanes, its maximum two quad permutes, and a wave's accesses are
-// whole 256-byte (bf16) or 512-byte (float32) row segments.  A workgroup takes
-// 16 rows x 4 steps: the four steps' loads are in flight together, and the
-// scale words of its 16 rows fall in one 64-byte run per step.  The dense side is
-// read and written past the caches: 8 matrices of 8192 x 4096 (537 MB dense, 143
-// packed) there and back 321 -> 288 us (4.7 TB/s), 16384 rows of 4096 in FP8 92 ->
-// 72 us (39 there, 5.2 TB/s).
-// Eight steps a workgroup measured no faster.
+// take one 128-element step of a row.  bf16: 8 elements in a row each, a scale
+// block four neighbouring lanes, its maximum two quad permutes.  float32: 4
+// elements in each half of the step, a block eight lanes; every access of the
+// sixteen lanes is then 256 bytes in a row (with 8 neighbours each, two accesses
+// of half the bytes of every line, 65536 x 4096 back from FP4 took 526 us, 203
+// here).  A workgroup takes 16 rows x 4 steps: the four steps' loads are in flight
+// together, and the scale words of its 16 rows fall in one 64-byte run per step.
+// The dense side is read and written past the caches: 8 matrices of 8192 x 4096
+// (537 MB dense, 143 packed) there and back 321 -> 288 us (4.7 TB/s), 16384 rows of
+// 4096 in FP8 92 -> 72 us (39 there, 5.2 TB/s).  Eight steps a workgroup measured
+// no faster.
 #include "mx_format.h"
 #include "operators.h"
 
@@ -41,6 +43,14 @@ EM_DEV uint32_t quad_max(uint32_t v) {
     v = max(v, quad<0xB1>(v));
     return max(v, quad<0x4E>(v));
 }
+EM_DEV uint32_t oct_max(uint32_t v) {
+    v = quad_max(v);
+    return max(v, quad<0x141>(v));                              // row_half_mirror: the other quad of the eight lanes
+}
+
+// A lane's first float32 element in half h of a 128-element step: four neighbours
+// each, so that an access of the sixteen lanes is 256 bytes in a row.
+EM_DEV int f32_at(int l16, int h) { return 64 * h + 4 * l16; }
 
 }  // namespace
 
@@ -64,50 +74,64 @@ mxq_quantize(const void* __restrict__ src, int64_t stride, int64_t rows, int N, 
     uint4 v[QS][F32 ? 2 : 1];
 #pragma unroll
     for (int i = 0; i < QS; ++i) {
-        const int64_t k = (int64_t)min(s0 + i, steps - 1) * kMxStep + 8 * l16;
-        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(src) + (from * stride + k) * (F32 ? 4 : 2));
-        v[i][0] = ld16_once(p);
-        if constexpr (F32) v[i][1] = ld16_once(p + 1);
+        const int64_t k = (int64_t)min(s0 + i, steps - 1) * kMxStep;
+        if constexpr (F32) {
+            const float* p = static_cast<const float*>(src) + from * stride + k;
+            v[i][0] = ld16_once(reinterpret_cast<const uint4*>(p + f32_at(l16, 0)));
+            v[i][1] = ld16_once(reinterpret_cast<const uint4*>(p + f32_at(l16, 1)));
+        } else {
+            v[i][0] = ld16_once(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + from * stride + k + 8 * l16));
+        }
     }
 #pragma unroll
     for (int i = 0; i < QS; ++i) {
         if (s0 + i >= steps) break;
-        uint32_t hi;                                            // upper 16 bits of the block's largest magnitude
-        float f[8];
+        uint8_t* sc_out = srow + (int64_t)(s0 + i) * N * 4;
+        const int64_t at = row * K + (int64_t)(s0 + i) * kMxStep;
         if constexpr (F32) {
-            const uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
-            uint32_t a = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                a = max(a, w[j] & 0x7FFFFFFFu);
-                f[j] = __uint_as_float(w[j]);
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t w[4] = {v[i][h].x, v[i][h].y, v[i][h].z, v[i][h].w};
+                float f[4];
+                uint32_t a = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    a = max(a, w[j] & 0x7FFFFFFFu);
+                    f[j] = __uint_as_float(w[j]);
+                }
+                const int X = e8m0_of<FMT>(oct_max(a) >> 16);
+                const bool bad = X == 255;
+                const float sc = e8m0_f32(bad ? 127 : X);
+                const int64_t c = at + f32_at(l16, h);
+                if constexpr (FMT == kMxFp4) *reinterpret_cast<uint16_t*>(codes + (c >> 1)) = bad ? 0 : fp4x4_f32(f, sc);
+                else *reinterpret_cast<uint32_t*>(codes + c) = bad ? 0u : fp8x4_f32(f, sc);
+                if ((l16 & 7) == 0) sc_out[2 * h + (l16 >> 3)] = (uint8_t)X;
             }
-            hi = quad_max(a) >> 16;
         } else {
-            hi = quad_max(amax8_bf16(v[i][0]));
-        }
-        const int X = e8m0_of<FMT>(hi);
-        const bool bad = X == 255;
-        const float sc = e8m0_f32(bad ? 127 : X);
-        const int64_t at = row * K + (int64_t)(s0 + i) * kMxStep + 8 * l16;
-        if constexpr (FMT == kMxFp4) {
-            const uint32_t c = F32 ? fp4x8_f32(f, sc) : fp4x8_bf16(v[i][0], sc);
-            *reinterpret_cast<uint32_t*>(codes + (at >> 1)) = bad ? 0u : c;
-        } else {
-            uint32_t c0, c1;
-            if constexpr (F32) {
-                c0 = fp8x4_f32(f, sc);
-                c1 = fp8x4_f32(f + 4, sc);
+            const int X = e8m0_of<FMT>(quad_max(amax8_bf16(v[i][0])));
+            const bool bad = X == 255;
+            const float sc = e8m0_f32(bad ? 127 : X);
+            const int64_t c = at + 8 * l16;
+            if constexpr (FMT == kMxFp4) {
+                const uint32_t q = fp4x8_bf16(v[i][0], sc);
+                *reinterpret_cast<uint32_t*>(codes + (c >> 1)) = bad ? 0u : q;
             } else {
                 const uint32_t lim = e4m3_limit(bad ? 127 : X);
-                c0 = fp8x4_bf16(v[i][0].x, v[i][0].y, sc, lim);
-                c1 = fp8x4_bf16(v[i][0].z, v[i][0].w, sc, lim);
+                const uint32_t q0 = fp8x4_bf16(v[i][0].x, v[i][0].y, sc, lim), q1 = fp8x4_bf16(v[i][0].z, v[i][0].w, sc, lim);
+                *reinterpret_cast<uint2*>(codes + c) = bad ? make_uint2(0u, 0u) : make_uint2(q0, q1);
             }
-            *reinterpret_cast<uint2*>(codes + at) = bad ? make_uint2(0u, 0u) : make_uint2(c0, c1);
+            if ((l16 & 3) == 0) sc_out[l16 >> 2] = (uint8_t)X;
         }
-        if ((l16 & 3) == 0) srow[(int64_t)(s0 + i) * N * 4 + (l16 >> 2)] = (uint8_t)X;
     }
 }
+
+// Codes 2 I and 2 I + 1 of a word as floats, and a block's scale (X = 255: NaN).
+template <int FMT, int I>
+EM_DEV f32x2 mx_pair(uint32_t q) {
+    if constexpr (FMT == kMxFp4) return __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, I);
+    else return __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q, 1.0f, I == 1);
+}
+EM_DEV float mx_scale(int X) { return X == 255 ? __uint_as_float(0x7FC00000u) : e8m0_f32(X); }
 
 // Back: value(code) * 2^(X - 127), exact in float32, then rounded once to the
 // dense type (a code has at most four significant bits, so bf16 rounds only
@@ -122,8 +146,36 @@ mxq_dequantize(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ sc
     if (row >= rows) return;
     const int steps = K / kMxStep, s0 = blockIdx.y * QS;
     const int64_t m = row / N, n = row - m * N;
-    const uint8_t* srow = scales + (m * steps * N + n) * 4 + (l16 >> 2);
-    uint32_t q[QS][FMT == kMxFp4 ? 1 : 2];
+    const uint8_t* srow = scales + (m * steps * N + n) * 4;
+    if constexpr (F32) {                                        // four codes in each half of a step
+        uint32_t q[QS][2];
+        int X[QS][2];
+#pragma unroll
+        for (int i = 0; i < QS; ++i) {
+            const int st = min(s0 + i, steps - 1);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t c = row * K + (int64_t)st * kMxStep + f32_at(l16, h);
+                if constexpr (FMT == kMxFp4) q[i][h] = *reinterpret_cast<const uint16_t*>(codes + (c >> 1));
+                else q[i][h] = *reinterpret_cast<const uint32_t*>(codes + c);
+                X[i][h] = srow[(int64_t)st * N * 4 + 2 * h + (l16 >> 3)];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < QS; ++i) {
+            if (s0 + i >= steps) break;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float sc = mx_scale(X[i][h]);
+                const f32x2 lo = mx_pair<FMT, 0>(q[i][h]), hi = mx_pair<FMT, 1>(q[i][h]);
+                const f32x4 o = {lo.x * sc, lo.y * sc, hi.x * sc, hi.y * sc};
+                __builtin_nontemporal_store(__builtin_bit_cast(u32x4, o),
+                                            reinterpret_cast<u32x4*>(static_cast<float*>(dst) + row * stride + (int64_t)(s0 + i) * kMxStep + f32_at(l16, h)));
+            }
+        }
+        return;
+    }
+    uint32_t q[QS][FMT == kMxFp4 ? 1 : 2];                      // bf16: eight codes in a row
     int X[QS];
 #pragma unroll
     for (int i = 0; i < QS; ++i) {
@@ -136,43 +188,27 @@ mxq_dequantize(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ sc
             q[i][0] = w.x;
             q[i][1] = w.y;
         }
-        X[i] = srow[(int64_t)st * N * 4];
+        X[i] = srow[(int64_t)st * N * 4 + (l16 >> 2)];
     }
 #pragma unroll
     for (int i = 0; i < QS; ++i) {
         if (s0 + i >= steps) break;
-        const float sc = X[i] == 255 ? __uint_as_float(0x7FC00000u) : e8m0_f32(X[i]);
-        float f[8];
+        const float sc = mx_scale(X[i]);
+        f32x2 f[4];
         if constexpr (FMT == kMxFp4) {
-            const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i][0], 1.0f, 0);
-            const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i][0], 1.0f, 1);
-            const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i][0], 1.0f, 2);
-            const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i][0], 1.0f, 3);
-            f[0] = a.x * sc; f[1] = a.y * sc; f[2] = b.x * sc; f[3] = b.y * sc;
-            f[4] = c.x * sc; f[5] = c.y * sc; f[6] = d.x * sc; f[7] = d.y * sc;
+            f[0] = mx_pair<FMT, 0>(q[i][0]); f[1] = mx_pair<FMT, 1>(q[i][0]);
+            f[2] = mx_pair<FMT, 2>(q[i][0]); f[3] = mx_pair<FMT, 3>(q[i][0]);
         } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q[i][h], 1.0f, false);
-                const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q[i][h], 1.0f, true);
-                f[4 * h] = a.x * sc; f[4 * h + 1] = a.y * sc; f[4 * h + 2] = b.x * sc; f[4 * h + 3] = b.y * sc;
-            }
+            f[0] = mx_pair<FMT, 0>(q[i][0]); f[1] = mx_pair<FMT, 1>(q[i][0]);
+            f[2] = mx_pair<FMT, 0>(q[i][1]); f[3] = mx_pair<FMT, 1>(q[i][1]);
         }
-        const int64_t at = row * stride + (int64_t)(s0 + i) * kMxStep + 8 * l16;
-        if constexpr (F32) {
-            u32x4* o = reinterpret_cast<u32x4*>(static_cast<float*>(dst) + at);
-            const f32x4 lo = {f[0], f[1], f[2], f[3]}, hi = {f[4], f[5], f[6], f[7]};
-            __builtin_nontemporal_store(__builtin_bit_cast(u32x4, lo), o);
-            __builtin_nontemporal_store(__builtin_bit_cast(u32x4, hi), o + 1);
-        } else {
-            u32x4 w;
+        u32x4 w;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const f32x2 v = {f[2 * j], f[2 * j + 1]};
-                w[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
-            }
-            __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(dst) + at));
+        for (int j = 0; j < 4; ++j) {
+            const f32x2 v = {f[j].x * sc, f[j].y * sc};
+            w[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
         }
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(dst) + row * stride + (int64_t)(s0 + i) * kMxStep + 8 * l16));
     }
 }
 
