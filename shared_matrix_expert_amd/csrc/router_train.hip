@@ -120,22 +120,61 @@ EM_DEV void live_seqs(const Seqs& q, int& live, int& tokens) {
 
 // ---- logit rows ----------------------------------------------------------------
 // A wave holds a row: lane l has experts 256 i + 4 l + c (c < 4).  Experts past
-// E read as -infinity (probability 0).
+// E read as -infinity (probability 0).  Rows that are not 16-byte aligned (E no
+// multiple of 4) arrive as 64 neighbours a load, expert 256 i + 64 c + l, and are
+// turned through the wave's LDS row (loads of every fourth expert took 44 us for
+// load and gradient of 14311 x 399, 35 this way).
 template <int NV>
 EM_DEV void load_row(float (&v)[NV][4], const float* __restrict__ row, int E, bool vec) {
     const int lane = lane_id();
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int e = 256 * i + 4 * lane;
         if (vec) {
+            const int e = 256 * i + 4 * lane;
             const float4 f = e < E ? *reinterpret_cast<const float4*>(row + e)
                                    : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
             v[i][0] = f.x; v[i][1] = f.y; v[i][2] = f.z; v[i][3] = f.w;
         } else {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) v[i][c] = e + c < E ? row[e + c] : -INFINITY;
+            for (int c = 0; c < 4; ++c) {
+                const int e = 256 * i + 64 * c + lane;
+                v[i][c] = e < E ? row[e] : -INFINITY;
+            }
         }
     }
+}
+
+// 64 neighbours a load to four a lane, and back.
+template <int NV>
+EM_DEV void turn_in(float (&v)[NV][4], float* lds) {
+    const int lane = lane_id();
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) lds[256 * i + 64 * c + lane] = v[i][c];
+    wave_lds_order();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const float4 f = *reinterpret_cast<const float4*>(&lds[256 * i + 4 * lane]);
+        v[i][0] = f.x; v[i][1] = f.y; v[i][2] = f.z; v[i][3] = f.w;
+    }
+    wave_lds_order();
+}
+template <int NV>
+EM_DEV void store_turned(float* __restrict__ row, int E, const float (&v)[NV][4], float* lds) {
+    const int lane = lane_id();
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        *reinterpret_cast<float4*>(&lds[256 * i + 4 * lane]) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+    wave_lds_order();
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int e = 256 * i + 64 * c + lane;
+            if (e < E) row[e] = lds[e];
+        }
+    wave_lds_order();
 }
 
 // e^v for v <= 0 from the hardware base-2 exponential: the rounding error of
@@ -212,7 +251,10 @@ rt_load(RouterLoad a) {
     const int first = find_seq(q, t0);
 #pragma unroll
     for (int j = 0; j < WT; ++j)
-        if (t0 + wv + 4 * j < t1) lse[j] = softmax_row<NV>(row[j]);
+        if (t0 + wv + 4 * j < t1) {
+            if (!a.vec) turn_in<NV>(row[j], red[wv]);
+            lse[j] = softmax_row<NV>(row[j]);
+        }
     for (int s = first; s < a.S; ++s) {
         if (q.lo(s) >= t1) break;
         const int lo = max(q.lo(s), t0), hi = min(q.hi(s), t1);
@@ -342,6 +384,7 @@ template <int NV>
 __global__ void __launch_bounds__(256)
 rt_dlogits(RouterGrad a) {
     __shared__ __attribute__((aligned(16))) float red[4][NV * 256];
+    __shared__ __attribute__((aligned(16))) float turn[4][NV * 256];
     const Seqs q{a.seq_offsets, a.S, a.T};
     const int tid = threadIdx.x, lane = lane_id(), wv = wave_id();
     const int per = a.chunk / 4;
@@ -400,6 +443,7 @@ rt_dlogits(RouterGrad a) {
             }
             const bool in = a.d_loss && t >= slo && t < shi;
             if (in) {
+                if (!a.vec) turn_in<NV>(d, turn[wv]);
                 const float lse = softmax_row<NV>(d);
                 const int n = shi - slo;
                 if (have != s) {
@@ -456,18 +500,14 @@ rt_dlogits(RouterGrad a) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) acc[i][c] += d[i][c];
             if (a.dlogits) {
-                float* row = a.dlogits + (int64_t)t * a.E;
+                float* out = a.dlogits + (int64_t)t * a.E;
+                if (!a.vec) store_turned<NV>(out, a.E, d, turn[wv]);
+                else
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int e = 256 * i + 4 * lane;
-                    if (a.vec) {
-                        if (e < a.E) *reinterpret_cast<float4*>(row + e) = make_float4(d[i][0], d[i][1], d[i][2], d[i][3]);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            if (e + c < a.E) row[e + c] = d[i][c];
+                    for (int i = 0; i < NV; ++i) {
+                        const int e = 256 * i + 4 * lane;
+                        if (e < a.E) *reinterpret_cast<float4*>(out + e) = make_float4(d[i][0], d[i][1], d[i][2], d[i][3]);
                     }
-                }
             }
         }
         if (a.planes) {
