@@ -327,7 +327,7 @@ mxp_stream(MxProduct a) {
 }
 
 // ------------------------------------------------------------------ many rows ----
-// A workgroup of 8 waves takes BT rows x 256 columns in WN x WT waves.  Each K
+// A workgroup of 8 waves takes BT rows x BN columns in WN x WT waves.  Each K
 // step's codes and scale words arrive by direct global -> LDS loads, STAGES - 1
 // steps ahead; every wave issues the same number of loads a step, so one counted
 // wait covers them.  A code row is 64 (E2M1) or 128 (E4M3) bytes; its 16-byte
@@ -340,10 +340,10 @@ mxp_stream(MxProduct a) {
 // one wave's waits leave its matrix core idle.)
 namespace {
 
-template <int FMT, int BT_>
+template <int FMT, int BT_, int BN_>
 struct GemmCfg {
-    static constexpr int BT = BT_, BN = 256;
-    static constexpr int WN = BT >= 192 ? 2 : 4, WT = 8 / WN, NW = WN * WT;
+    static constexpr int BT = BT_, BN = BN_;
+    static constexpr int WN = BT >= 192 || BN == 128 ? 2 : 4, WT = 8 / WN, NW = WN * WT;
     static constexpr int NI = BN / WN / 16, NJ = BT / WT / 16;     // column and row subtiles of a wave
     static constexpr int XB = FMT == kMxFp4 ? 64 : 128;            // bytes of an x row per step
     static constexpr int X_B = BT * XB, W_B = BN * 64, XS_B = BT * 4, WS_B = BN * 4;
@@ -388,10 +388,10 @@ EM_DEV int swz(int r, int s) { return ROW_B == 128 ? s ^ ((r >> 1) & 7) : s ^ (-
 
 }  // namespace
 
-template <int FMT, int BT>
+template <int FMT, int BT, int BN>
 __global__ void __launch_bounds__(512)
 mxp_gemm(MxProduct a) {
-    using C = GemmCfg<FMT, BT>;
+    using C = GemmCfg<FMT, BT, BN>;
     constexpr int NI = C::NI, NJ = C::NJ, XB = C::XB;
     __shared__ __attribute__((aligned(16))) uint8_t lds[C::STAGES * C::STAGE];
     const int lane = lane_id(), wv = wave_id(), g = lane >> 4, m = lane & 15;
@@ -651,24 +651,29 @@ bool rounds_in_stream(const MxProduct& a) {
     return ((int64_t)a.R + live - 1) / live * a.K <= 16 * 4096;
 }
 
-// Rows of mxp_gemm's tiles.  A CU holds one workgroup, so a product takes as many
-// rounds of tiles as 256 CUs need, each as long as a tile: measured at K = 4096,
-// 64 / 128 / 192 / 256 rows 18 / 27 / 36 / 44 us in FP4 and 20 / 31 / 45 / 59 in
-// FP8.  The rows with the least rounds times length are taken; each matrix with
+// Rows of mxp_gemm's tiles.  A product takes as many rounds of tiles as 256 CUs
+// need, each as long as a tile: measured at K = 4096, tiles of 64 / 128 / 192 / 256
+// rows x 256 columns 18 / 27 / 36 / 44 us in FP4 and 20 / 31 / 45 / 59 in FP8; of 64 /
+// 128 / 256 rows x 128 columns, for matrices of no more, 12 / 17.5 / 26 and 13.5 / 20 /
+// 34.  The rows with the least rounds times length are taken; each matrix with
 // rows is counted half a tile more.  (8192 columns, K = 4096, FP4, us a call by
 // rows: 1000 40 / 30 / 32 / 35, 1536 58 / 49 / 39 / 41, 2048 76 / 57 / 62 / 48;
-// 8 matrices of 4096 x 8192 in FP8, 5001 rows: 235 / 180 / 183 / 207.)
+// 8 matrices of 4096 x 8192 in FP8, 5001 rows: 235 / 180 / 183 / 207; 512 of 128 x
+// 4096, 20480 rows: 53 with 256 columns, 43 with 128.)
 int tile_rows(const MxProduct& a) {
-    static constexpr int kTile[2][4] = {{18, 27, 36, 44}, {20, 31, 45, 59}};
+    static constexpr int kRows[4] = {64, 128, 192, 256};
+    static constexpr int kWide[2][4] = {{36, 54, 72, 88}, {40, 62, 90, 118}};       // half microseconds
+    static constexpr int kNarrow[2][4] = {{24, 35, 0, 52}, {27, 40, 0, 68}};
     const int live = !a.offsets ? 0 : a.M < a.R ? a.M : a.R;
     const int64_t cols = (a.N + 255) / 256;
+    const int* length = (a.N <= 128 ? kNarrow : kWide)[a.fmt == kMxFp8];
     int64_t best = 0;
     int rows = 0;
     for (int i = 0; i < 4; ++i) {
-        const int bt = 64 * (i + 1);
+        const int bt = kRows[i];
         const int64_t halves = a.offsets ? 2ll * a.R / bt + live : 2ll * ((a.R + bt - 1) / bt);
-        const int64_t cost = (halves * cols + 511) / 512 * kTile[a.fmt == kMxFp8][i];
-        if (!rows || cost < best) {
+        const int64_t cost = (halves * cols + 511) / 512 * length[i];
+        if (cost && (!rows || cost < best)) {
             best = cost;
             rows = bt;
         }
@@ -676,12 +681,12 @@ int tile_rows(const MxProduct& a) {
     return rows;
 }
 
-template <int BT>
+template <int BT, int BN>
 hipError_t launch_gemm(const MxProduct& a, hipStream_t s) {
-    const int64_t tiles = max_row_tiles(a, BT) * ((a.N + 255) / 256);
+    const int64_t tiles = max_row_tiles(a, BT) * ((a.N + BN - 1) / BN);
     prof_begin(s);
-    if (a.fmt == kMxFp4) mxp_gemm<kMxFp4, BT><<<(unsigned)((tiles + 7) & ~7ll), 512, 0, s>>>(a);
-    else mxp_gemm<kMxFp8, BT><<<(unsigned)((tiles + 7) & ~7ll), 512, 0, s>>>(a);
+    if (a.fmt == kMxFp4) mxp_gemm<kMxFp4, BT, BN><<<(unsigned)((tiles + 7) & ~7ll), 512, 0, s>>>(a);
+    else mxp_gemm<kMxFp8, BT, BN><<<(unsigned)((tiles + 7) & ~7ll), 512, 0, s>>>(a);
     prof_end(s, "mxp_gemm");
     return hipGetLastError();
 }
@@ -713,11 +718,19 @@ hipError_t launch_mx_product(MxProduct a, void* ws, hipStream_t s) {
         case 4: return launch_stream<4, false>(a, s);
         default: break;
     }
-    switch (tile_rows(a)) {
-        case 64: return launch_gemm<64>(a, s);
-        case 128: return launch_gemm<128>(a, s);
-        case 192: return launch_gemm<192>(a, s);
-        default: return launch_gemm<256>(a, s);
+    const int rows_a_tile = tile_rows(a);
+    if (a.N <= 128) {
+        switch (rows_a_tile) {
+            case 64: return launch_gemm<64, 128>(a, s);
+            case 128: return launch_gemm<128, 128>(a, s);
+            default: return launch_gemm<256, 128>(a, s);
+        }
+    }
+    switch (rows_a_tile) {
+        case 64: return launch_gemm<64, 256>(a, s);
+        case 128: return launch_gemm<128, 256>(a, s);
+        case 192: return launch_gemm<192, 256>(a, s);
+        default: return launch_gemm<256, 256>(a, s);
     }
 }
 

@@ -277,6 +277,24 @@ def test_product_grouped_tiles(fmt, sizes):
 
 
 @fmt_of
+@pytest.mark.parametrize("M,N,K,R", [(40, 128, 384, 3000), (20, 123, 128, 9000), (3, 100, 512, 20000), (1, 128, 256, 9000),
+                                     (1, 77, 128, 40000), (1, 2, 384, 50000)])
+def test_product_narrow_matrices(fmt, M, N, K, R):
+    """Many rows through matrices of at most 128 columns, sharing x rows, some rows of no x."""
+    rng = np.random.default_rng(M)
+    off = np.sort(np.concatenate([[0, R], rng.integers(0, R + 1, M - 1)]))
+    T = 500
+    src = rng.integers(-1, T, R)
+    q, e, W = matrices(M, N, K, 13)
+    x = rows_of(T, K, 14)
+    y = torch.full((R + 1, N), 3.25, dtype=torch.bfloat16, device=DEV)
+    say(f"case: {R} rows, {M} x {N} x {K}")
+    product(fmt, x.to(DEV), q, e, y[:R], offsets=i32(off), row_src=i32(src))
+    within(y[:R], *ops.product(x.double().numpy(), fmt, W, off, src), K)
+    assert bool((y[R:] == 3.25).all()) and bool((y[:R][i32(src) < 0] == 0).all())
+
+
+@fmt_of
 @pytest.mark.parametrize("R,T,N", [(40, 7, 48), (500, 60, 48), (90, 17, 640), (900, 300, 512), (1400, 200, 8192)])
 def test_product_gathered_rows(fmt, R, T, N):
     """Shared x rows, and entries that name no row: zeros."""
