@@ -70,7 +70,7 @@ hipError_t launch_router_load(RouterLoad a, void* ws, hipStream_t s);
 struct RouterGrad {
     int T, E, k, S, d, vec;
     int Tp, Ep;                     // T and E up to multiples of 32
-    int bi, slices;                 // tile rows of the products, token slices of dW_r
+    int bi, slices, xslices;        // tile rows of the products, token slices of dW_r, expert slices of dx
     int chunk;                      // tokens per workgroup of rt_dlogits
     const float* logits; const int32_t* topk_idx; const float* topk_w;
     const float* d_topk_w;          // [T][k] or null
@@ -80,7 +80,7 @@ struct RouterGrad {
     float* dlogits; float* dx; float* dw_router; float* dbias;   // each may be null
     // workspace
     uint16_t* planes;               // [3][Tp][Ep] bf16: dz = their sum
-    float* part_w;                  // [slices][E][d]
+    float* part_w; float* part_x;   // [slices][E][d]; [xslices][T][d] (unless 1)
     float* part_b;                  // [Tp / chunk][E]
 };
 size_t router_grad_ws_bytes(RouterGrad a);

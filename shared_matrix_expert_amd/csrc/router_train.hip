@@ -20,7 +20,7 @@
 //                   its planes (hi + mid + lo: 24 bits), x and W_r are bf16, every
 //                   product is exact in float32 and the sums are float32; and dbias,
 //                   the chunks of rt_dlogits added in order
-//   rt_finish       the token slices of dW_r added in order
+//   rt_finish       the slices of dW_r and dx added in order
 #include "common.h"
 #include "operators.h"
 
@@ -600,7 +600,7 @@ EM_DEV void read_rows(uint2 (&r)[8], const uint8_t* p, int row_bytes) {
     for (int i = 0; i < 8; ++i) r[i] = *reinterpret_cast<const uint2*>(p + i * row_bytes);
 }
 
-// Tiles of one product: out's row and column tiles, for DW by token slice.
+// Tiles of one product: out's row and column tiles, by slice of K.
 EM_DEV int rt_row_tiles(int mode, int BI, const RouterGrad& a) { return ((mode == RT_DX ? a.T : a.E) + BI - 1) / BI; }
 
 template <int MODE, int BI>
@@ -614,18 +614,17 @@ EM_DEV void rt_tile(const RouterGrad& a, int block, uint8_t* lds) {
     const uint16_t* B = MODE == RT_DX ? a.w_router : a.x;
     // XCD x = block % 8 takes neighbouring tiles
     const int nn = (a.d + C::BN - 1) / C::BN, ni = rt_row_tiles(MODE, BI, a);
-    const int total = nn * ni * (MODE == RT_DX ? 1 : a.slices);
+    const int slices = MODE == RT_DX ? a.xslices : a.slices, total = nn * ni * slices;
     const int per = (total + 7) >> 3, at = block >> 3;
     const int b = (block & 7) * per + at;
     if (at >= per || b >= total) return;
-    // DX: rows slowest; DW: token slices slowest (a slice's x and dz are shared by its tiles)
-    const int z = MODE == RT_DX ? 0 : b / (nn * ni);
-    const int i0 = (MODE == RT_DX ? b / nn : (b % (nn * ni)) % ni) * BI;
-    const int n0 = (MODE == RT_DX ? b % nn : (b % (nn * ni)) / ni) * C::BN;
+    // slices slowest (a slice's operands are shared by its tiles), then DX rows, DW columns
+    const int z = slices == 1 ? 0 : b / (nn * ni), in = b - z * (nn * ni);
+    const int i0 = (MODE == RT_DX ? in / nn : in % ni) * BI, n0 = (MODE == RT_DX ? in % nn : in / ni) * C::BN;
     const int K = MODE == RT_DX ? a.Ep : a.Tp;
     const int steps = K / C::BK;
-    const int s0 = MODE == RT_DX ? 0 : (int)((int64_t)steps * z / a.slices);
-    const int s1 = MODE == RT_DX ? steps : (int)((int64_t)steps * (z + 1) / a.slices);
+    const int s0 = MODE == RT_DX && slices == 1 ? 0 : (int)((unsigned)(steps * z) / (unsigned)slices);       // steps up to 2^15
+    const int s1 = MODE == RT_DX && slices == 1 ? steps : (int)((unsigned)(steps * (z + 1)) / (unsigned)slices);
 
     // ---- loads: 1 KB pieces of the planes' tiles, then of B's, each a uniform
     // base and a lane offset.  Tile rows and columns past the planes' (whose
@@ -723,21 +722,26 @@ EM_DEV void rt_tile(const RouterGrad& a, int block, uint8_t* lds) {
     }
 
     // ---- out: lane holds rows of subtile i (D row 4 g + v) and columns NC m .. + NC - 1
-    float* out = MODE == RT_DX ? a.dx : (a.slices > 1 ? a.part_w + (int64_t)z * a.E * a.d : a.dw_router);
+    float* whole = MODE == RT_DX ? a.dx : a.dw_router;
+    float* out = slices > 1 ? (MODE == RT_DX ? a.part_x : a.part_w) + (int64_t)z * I * a.d : whole;
     const int n = n0 + 16 * NC * wn + NC * m;
     if (n >= a.d) return;
+    auto store = [&](auto past) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const int r = i0 + 64 * wi + (MODE == RT_DX ? 16 * i + 4 * g + v : 4 * (4 * g + v) + i);
-            if (r >= I) continue;
-            float* o = out + (int64_t)r * a.d + n;
-            // dx streams out past the L2, where W_r and the planes stay
-            const floatx4 w = {acc[i][0][v], acc[i][1][v], acc[i][2][v], acc[i][3][v]};
-            if constexpr (MODE == RT_DX) __builtin_nontemporal_store(w, reinterpret_cast<floatx4*>(o));
-            else *reinterpret_cast<floatx4*>(o) = w;
-        }
+            for (int v = 0; v < 4; ++v) {
+                const int r = i0 + 64 * wi + (MODE == RT_DX ? 16 * i + 4 * g + v : 4 * (4 * g + v) + i);
+                if (r >= I) continue;
+                float* o = out + (int64_t)r * a.d + n;
+                const floatx4 w = {acc[i][0][v], acc[i][1][v], acc[i][2][v], acc[i][3][v]};
+                if constexpr (decltype(past)::value) __builtin_nontemporal_store(w, reinterpret_cast<floatx4*>(o));
+                else *reinterpret_cast<floatx4*>(o) = w;
+            }
+    };
+    // a whole dx streams out past the L2, where W_r and the planes stay
+    if (MODE == RT_DX && slices == 1) store(std::true_type{});
+    else store(std::false_type{});
 }
 
 // 64 experts of dbias from the chunks of rt_dlogits: rows of 64 threads over
@@ -772,29 +776,33 @@ rt_products(RouterGrad a, int bblocks, int wblocks) {
     else rt_tile<RT_DX, BI>(a, b - bblocks - wblocks, lds);
 }
 
-// Token slices of dW_r, in order, eight asked for at once (four where there are no
-// more): HBM and the Infinity Cache (512 x 4096, 4 slices: 7.2 us, 42 MB).
+// The slices of dW_r (wblocks workgroups) and of dx, in order, eight asked for at
+// once (four where there are no more): HBM and the Infinity Cache (512 x 4096, 4
+// slices: 7.2 us, 42 MB).
 template <int N>
-EM_DEV void rt_add_slices(float4& s, const RouterGrad& a, int64_t n, int64_t at, int z) {
+EM_DEV void rt_add_slices(float4& s, const float* part, int slices, int64_t n, int64_t at, int z) {
     float4 v[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = *reinterpret_cast<const float4*>(a.part_w + min(z + i, a.slices - 1) * n + at);
+    for (int i = 0; i < N; ++i) v[i] = *reinterpret_cast<const float4*>(part + min(z + i, slices - 1) * n + at);
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        if (z + i < a.slices) {
+        if (z + i < slices) {
             s.x += v[i].x; s.y += v[i].y; s.z += v[i].z; s.w += v[i].w;
         }
 }
 
 __global__ void __launch_bounds__(256)
-rt_finish(RouterGrad a) {
-    const int64_t n = (int64_t)a.E * a.d, at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+rt_finish(RouterGrad a, unsigned wblocks) {
+    const bool w = blockIdx.x < wblocks;
+    const int64_t n = (int64_t)(w ? a.E : a.T) * a.d, at = ((int64_t)(blockIdx.x - (w ? 0 : wblocks)) * 256 + threadIdx.x) * 4;
+    const float* part = w ? a.part_w : a.part_x;
+    const int slices = w ? a.slices : a.xslices;
     if (at >= n) return;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (a.slices <= 4) rt_add_slices<4>(s, a, n, at, 0);
+    if (slices <= 4) rt_add_slices<4>(s, part, slices, n, at, 0);
     else
-        for (int z = 0; z < a.slices; z += 8) rt_add_slices<8>(s, a, n, at, z);
-    *reinterpret_cast<float4*>(a.dw_router + at) = s;
+        for (int z = 0; z < slices; z += 8) rt_add_slices<8>(s, part, slices, n, at, z);
+    *reinterpret_cast<float4*>((w ? a.dw_router : a.dx) + at) = s;
 }
 
 // ------------------------------------------------------------------ host side ----
@@ -818,19 +826,19 @@ LoadLayout load_layout(const RouterLoad& a) {
     return L;
 }
 
-struct GradLayout { size_t planes, part_w, part_b, bytes; };
+struct GradLayout { size_t planes, part_w, part_x, part_b, bytes; };
 
 int pad32(int v) { return (v + 31) & ~31; }
 int64_t tiles(int rows, int bi, int d) { return (int64_t)((rows + bi - 1) / bi) * ((d + 255) / 256); }
 
-// Tile rows of rt_products and token slices of dW_r: the least of an estimate (us)
-// from measured step times (32 of K).  A workgroup alone on a CU takes 0.85 us a
-// step with 64 rows and 1.06 with 128, two 1.25 and 2.2 each, and a full chip 0.85
-// and 1.2 us a step and CU; dx has E / 32 steps a tile, dW_r T / 32 split into the
-// slices, whose sums rt_finish adds in a launch more.  Measured passes, 64 rows
-// against 128 (T x E x d, us): 7 x 913 x 640 30 / 40, 751 x 480 x 2560 30 / 33,
-// 16384 x 512 x 4096 362 / 333; slices 1, 8 and 32 of 11764 x 48 x 384 282 / 52 / 30,
-// 1, 2 and 4 of 761 x 936 x 1024 36 / 38 / 41.
+// Tile rows of rt_products and slices of K (tokens for dW_r, experts for dx): the
+// least of an estimate (us) from measured step times (32 of K).  A workgroup alone
+// on a CU takes 0.85 us a step with 64 rows and 1.06 with 128, two 1.25 and 2.2
+// each, and a full chip 0.85 and 1.2 us a step and CU; dx has E / 32 steps a tile,
+// dW_r T / 32, split into the slices, whose sums rt_finish adds in a launch more.
+// Measured passes, 64 rows against 128 (T x E x d, us): 7 x 913 x 640 30 / 40,
+// 751 x 480 x 2560 30 / 33, 16384 x 512 x 4096 362 / 333; 1, 8 and 32 slices of
+// 11764 x 48 x 384 282 / 52 / 30, 1, 2 and 4 of 761 x 936 x 1024 36 / 38 / 41.
 void plan_grad(RouterGrad& a) {
     static constexpr double kAlone[2] = {0.85, 1.06}, kTwo[2] = {1.25, 2.2}, kFull[2] = {0.85, 1.2};
     a.Tp = pad32(a.T);
@@ -841,18 +849,23 @@ void plan_grad(RouterGrad& a) {
     for (int i = 0; i < 2; ++i) {
         const int bi = 64 << i;
         const int64_t dx = tiles(a.T, bi, a.d), dw = tiles(a.E, bi, a.d);
-        for (int z = 1; z <= 64 && z <= tsteps; z *= 2) {
-            const int slice = (tsteps + z - 1) / z, longest = slice > esteps ? slice : esteps;
-            const double chain = longest * (dx + dw * z <= 256 ? kAlone[i] : kTwo[i]);
-            const double all = ((double)dx * esteps + (double)dw * tsteps) * kFull[i] / 256;
-            const double finish = z == 1 ? 0 : 3.5 + 0.3 * z + (z + 1.0) * a.E * a.d * 4 / 6e6;
-            const double us = (chain > all ? chain : all) + finish;
-            if (!a.bi || us < least) {
-                least = us;
-                a.bi = bi;
-                a.slices = z;
+        const double all = ((double)dx * esteps + (double)dw * tsteps) * kFull[i] / 256;
+        for (int x = 1; x <= 8 && (x == 1 || 4 * x <= esteps); x *= 2)
+            for (int z = 1; z <= 64 && z <= tsteps; z *= 2) {
+                const int w_steps = (tsteps + z - 1) / z, x_steps = (esteps + x - 1) / x;
+                const double chain = (w_steps > x_steps ? w_steps : x_steps) * (dx * x + dw * z <= 256 ? kAlone[i] : kTwo[i]);
+                double finish = 0;
+                if (x > 1 || z > 1)
+                    finish = 3.5 + 0.3 * (z > x ? z : x) +
+                             ((z > 1 ? (z + 1.0) * a.E : 0.0) + (x > 1 ? (x + 1.0) * a.T : 0.0)) * a.d * 4 / 6e6;
+                const double us = (chain > all ? chain : all) + finish;
+                if (!a.bi || us < least) {
+                    least = us;
+                    a.bi = bi;
+                    a.slices = z;
+                    a.xslices = x;
+                }
             }
-        }
     }
 }
 
@@ -863,6 +876,7 @@ GradLayout grad_layout(const RouterGrad& a) {
     // the last tile reads up to 255 rows past the last plane (DX), up to 255 columns past its last row (DW)
     L.planes = take(((size_t)3 * a.Tp + 256) * a.Ep * 2 + 512);
     L.part_w = take((size_t)(a.slices > 1 ? a.slices : 0) * a.E * a.d * 4);
+    L.part_x = take((size_t)(a.xslices > 1 ? a.xslices : 0) * a.T * a.d * 4);
     L.part_b = take((size_t)((a.Tp + grad_chunk(a.T) - 1) / grad_chunk(a.T)) * a.E * 4);
     L.bytes = off;
     return L;
@@ -906,6 +920,7 @@ hipError_t launch_router_grad(RouterGrad a, void* ws, hipStream_t s) {
     char* base = static_cast<char*>(ws);
     a.planes = a.dx || a.dw_router ? reinterpret_cast<uint16_t*>(base + L.planes) : nullptr;
     a.part_w = reinterpret_cast<float*>(base + L.part_w);
+    a.part_x = reinterpret_cast<float*>(base + L.part_x);
     a.part_b = a.dbias ? reinterpret_cast<float*>(base + L.part_b) : nullptr;
     a.chunk = grad_chunk(a.T);
     const int chunks = ((a.planes ? a.Tp : a.T) + a.chunk - 1) / a.chunk;
@@ -920,15 +935,19 @@ hipError_t launch_router_grad(RouterGrad a, void* ws, hipStream_t s) {
     const auto up8 = [](int64_t n) { return (int)((n + 7) & ~7ll); };
     const int bblocks = a.dbias ? up8((a.E + 63) / 64) : 0;
     const int wblocks = a.dw_router ? up8(tiles(a.E, bi, a.d) * a.slices) : 0;
-    const int xblocks = a.dx ? up8(tiles(a.T, bi, a.d)) : 0;
+    const int xblocks = a.dx ? up8(tiles(a.T, bi, a.d) * a.xslices) : 0;
     prof_begin(s);
     if (bi == 128) rt_products<128><<<bblocks + wblocks + xblocks, RtCfg<128>::TH, 0, s>>>(a, bblocks, wblocks);
     else rt_products<64><<<bblocks + wblocks + xblocks, RtCfg<64>::TH, 0, s>>>(a, bblocks, wblocks);
     prof_end(s, "rt_products");
     e = hipGetLastError();
-    if (e != hipSuccess || !a.dw_router || a.slices == 1) return e;
+    const auto joins = [&](const float* out, int slices, int rows) {
+        return out && slices > 1 ? (unsigned)(((int64_t)rows * a.d / 4 + 255) / 256) : 0u;
+    };
+    const unsigned wj = joins(a.dw_router, a.slices, a.E), xj = joins(a.dx, a.xslices, a.T);
+    if (e != hipSuccess || !(wj + xj)) return e;
     prof_begin(s);
-    rt_finish<<<(unsigned)(((int64_t)a.E * a.d / 4 + 255) / 256), 256, 0, s>>>(a);
+    rt_finish<<<wj + xj, 256, 0, s>>>(a, wj);
     prof_end(s, "rt_finish");
     return hipGetLastError();
 }
