@@ -12,6 +12,7 @@ library is required - calls raise if it is not built.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import operator
 import os
@@ -239,6 +240,19 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _made_on(stream):
+    """Context in which new tensors belong to the stream that fills them: torch
+    hands out memory in the order of the stream it was asked on, so a block of
+    the current stream's may still be read or written there when a kernel on
+    another stream fills it."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
 def cweights(weights: dict) -> CWeights:
     return CWeights(*(_ptr(weights.get(k) if k in _OPTIONAL_KEYS else weights[k]) for k in _WEIGHT_KEYS))
 
@@ -290,7 +304,8 @@ def edge_moe_tile_shared(dims, which, src_q, dst_q, stream=None) -> None:
 def tile_weights(dims, weights: dict, stream=None) -> dict:
     """A copy of the weight dict with the decode-tiled codes added (new device
     tensors of the sizes of s_up / s_dn / a_up / a_dn; a_up only when its rank
-    is a multiple of 128, a_dn only when its rank is 128)."""
+    is a multiple of 128, a_dn only when its rank is 128).  The new tensors
+    belong to `stream`; what uses them on another one waits for it."""
     import torch
     out = dict(weights)
     for which, key in ((0, "s_up"), (1, "s_dn"), (2, "a_up"), (3, "a_dn")):
@@ -298,7 +313,8 @@ def tile_weights(dims, weights: dict, stream=None) -> dict:
             continue
         if which == 3 and dims.delta_rank != 128:
             continue
-        q = torch.empty_like(weights[key])
+        with _made_on(stream):
+            q = torch.empty_like(weights[key])
         edge_moe_tile_shared(dims, which, weights[key], q, stream)
         out[key + "_t"] = q
     return out
@@ -561,14 +577,16 @@ def mx_weights(dense: dict, stream=None) -> dict:
     """The MX weight dict of edge_moe_forward_mx from dense matrices: "s_up"
     [G][h][d], "s_dn" [G][d][h], "a_up" [E][r][d], "b_up" [E][h][r], "a_dn"
     [E][r][h], "b_dn" [E][d][r] (bf16 or float32) are quantised to MXFP4; the
-    LoRA factors, bf16, are taken as they are."""
+    LoRA factors, bf16, are taken as they are.  The new tensors belong to
+    `stream`; what uses them on another one waits for it."""
     import torch
     out = {}
     for key in _WEIGHT_KEYS[:12:2]:
         src = dense[key]
         M, N, K = src.shape
-        out[key] = torch.empty(M, N, K // 2, dtype=torch.uint8, device=src.device)
-        out[key + "_scale"] = torch.empty(M, K // 128, N, 4, dtype=torch.uint8, device=src.device)
+        with _made_on(stream):
+            out[key] = torch.empty(M, N, K // 2, dtype=torch.uint8, device=src.device)
+            out[key + "_scale"] = torch.empty(M, K // 128, N, 4, dtype=torch.uint8, device=src.device)
         edge_moe_mx_quantize(MX_FP4, src, out[key], out[key + "_scale"], stream)
     for key in _WEIGHT_KEYS[12:16]:
         out[key] = dense[key]
