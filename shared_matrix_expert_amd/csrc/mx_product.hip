@@ -17,6 +17,7 @@
 //               and rounds the x rows it needs on the way.
 //   mxp_gemm    many rows: x rounded once (mxq_quantize into the workspace),
 //               LDS-tiled, bound by the matrix cores and the LDS reads.
+#include "lds_load.h"
 #include "mx_format.h"
 #include "operators.h"
 
@@ -354,20 +355,6 @@ struct GemmCfg {
     static constexpr int LOADS = X_INSTR + W_INSTR + S_INSTR;
 };
 
-// Direct global -> LDS load of 16 (or 4) bytes a lane to `dst` + 16 (4) * lane.
-// Written out because the compiler, which cannot tell the stages of the ring
-// apart, waits for every such load of its own before the next LDS read; these
-// are counted by wait_loads instead.  They have no register output.
-EM_DEV void dma16(const uint8_t* src, uint32_t dst) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(src), "s"(dst) : "memory", "m0");
-}
-EM_DEV void dma16(const uint8_t* base, uint32_t off, uint32_t dst) {     // base: the same for the wave
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "s"(dst) : "memory", "m0");
-}
-EM_DEV void dma4(const uint8_t* base, uint32_t off, uint32_t dst) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" : : "v"(off), "s"(base), "s"(dst) : "memory", "m0");
-}
-
 EM_DEV void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory"); }
 
 // At most N of this wave's loads in flight, its LDS reads done; then the barrier.
@@ -442,14 +429,14 @@ mxp_gemm(MxProduct a) {
     auto fetch = [&](int st, int to, int u) {           // load u of step st's, into the stage of step `to`
         const uint32_t stage = __builtin_amdgcn_readfirstlane(base + (to % C::STAGES) * C::STAGE);
         if (u < C::X_INSTR) {
-            dma16(xsrc[u] + (int64_t)st * XB, stage + 1024 * ((C::X_INSTR * wv + u) % C::X_P));
+            lds_load16(xsrc[u] + (int64_t)st * XB, stage + 1024 * ((C::X_INSTR * wv + u) % C::X_P));
         } else if (u < C::X_INSTR + C::W_INSTR) {
             const int q = u - C::X_INSTR;
-            dma16(wbase + st * 64, woff[q], stage + C::X_B + 1024 * (C::W_INSTR * wv + q));
+            lds_load16(wbase + st * 64, woff[q], stage + C::X_B + 1024 * (C::W_INSTR * wv + q));
         } else {
             const int q = u - C::X_INSTR - C::W_INSTR, piece = (C::S_INSTR * wv + q) % C::S_P;
             const uint8_t* src = piece < C::BN / 64 ? wsbase + (int64_t)st * a.N * 4 : a.xs + (int64_t)st * a.xrows * 4;
-            dma4(src, soff[q], stage + C::X_B + C::W_B + 256 * piece);
+            lds_load4(src, soff[q], stage + C::X_B + C::W_B + 256 * piece);
         }
     };
 

@@ -22,6 +22,7 @@
 //                   the chunks of rt_dlogits added in order
 //   rt_finish       the slices of dW_r and dx added in order
 #include "common.h"
+#include "lds_load.h"
 #include "operators.h"
 
 namespace em {
@@ -571,13 +572,6 @@ struct RtCfg {
     static constexpr int A_INSTR = 3 * P_B / 1024 / WAVES, B_INSTR = B_B / 1024 / WAVES;
 };
 
-// Direct global -> LDS load of 16 bytes a lane, from base + off to dst + 16 lane
-// (waited for by hand in rt_tile; no register output).
-EM_DEV void rt_dma16(const void* base, uint32_t off, uint32_t dst) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-                 : : "v"(off), "s"(base), "s"(dst) : "memory", "m0");
-}
-
 // Eight K rows of four bf16 columns (two words a row) to four operands of eight
 // K elements.
 EM_DEV void transpose8(const uint2 (&v)[8], uint4 (&o)[4]) {
@@ -644,12 +638,12 @@ EM_DEV void rt_tile(const RouterGrad& a, int block, uint8_t* lds) {
             const uint16_t* src = a.planes + (int64_t)plane * a.Tp * a.Ep
                 + (MODE == RT_DX ? (int64_t)(i0 + 16 * in) * a.Ep + C::BK * st
                                  : ((int64_t)C::BK * st + 512 * in / BI) * a.Ep + i0);
-            rt_dma16(src, aoff, stage + 1024 * piece);
+            lds_load16(src, aoff, stage + 1024 * piece);
         }
 #pragma unroll
         for (int p = 0; p < C::B_INSTR; ++p) {               // rows past the end repeat the last: they meet zeros
             const int piece = C::B_INSTR * wv + p, row = min(C::BK * st + 2 * piece, rows_b - 1);
-            rt_dma16(B + (int64_t)row * a.d + n0, row + 1 < rows_b ? boff2 : boff, stage + 3 * C::P_B + 1024 * piece);
+            lds_load16(B + (int64_t)row * a.d + n0, row + 1 < rows_b ? boff2 : boff, stage + 3 * C::P_B + 1024 * piece);
         }
     };
 
