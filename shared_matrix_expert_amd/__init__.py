@@ -42,7 +42,9 @@ EXPORTED = ("edge_moe_workspace_bytes", "edge_moe_route", "edge_moe_forward",
 # element formats and dense types of the MX matrix operators
 MX_FP4, MX_FP8 = 0, 1
 _BF16, _FLOAT = 0, 1
-class _cuda:                   # torch's current device and stream handle, without the objects around them
+
+
+class _cuda:                   # torch's current device, and a device's stream handle (filled by load())
     getDevice = getRawStream = None
 
 
@@ -134,9 +136,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     # PyTorch-ROCm ships its own HIP runtime; load it first so that the library
     # binds to the same runtime instance as the streams and memory it is given.
     import torch
-    _cuda.getDevice, _cuda.getRawStream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    # Where this torch has them, the calls that build no device or stream object
+    # (0.1 us against 1); host-only calls need neither.
+    _cuda.getDevice = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _cuda.getRawStream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_handle)
     _dtypes.update({n: getattr(torch, n) for n in ("uint8", "int32", "float32")})
-    _dense_types.update({torch.bfloat16: _BF16, torch.int16: _BF16, torch.uint16: _BF16, torch.float32: _FLOAT})
+    _dense_types.update({getattr(torch, n): kind for n, kind in
+                         (("bfloat16", _BF16), ("int16", _BF16), ("uint16", _BF16), ("float32", _FLOAT)) if hasattr(torch, n)})
     lib = ctypes.CDLL(path)
     vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
     lib.edge_moe_workspace_bytes.argtypes = [ctypes.POINTER(CDims)]
@@ -233,10 +239,15 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+def _stream_handle(device: int) -> int:
+    import torch
+    return torch.cuda.current_stream(device).cuda_stream
+
+
 def _stream(stream) -> Optional[int]:
     import torch
-    if stream is None:                  # the current stream's handle, without a Stream object around it
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        return _cuda.getRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
