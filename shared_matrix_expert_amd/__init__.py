@@ -16,6 +16,7 @@ import contextlib
 import ctypes
 import operator
 import os
+import struct
 from typing import Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -225,8 +226,22 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
 _dim_values = operator.attrgetter(*(n for n, _ in CDims._fields_))
 
 
+def _i32(v: int) -> int:
+    """A size as the library's int32: one past it becomes the largest, which no
+    limit of the library allows (ctypes would cut the upper bits off)."""
+    return min(max(int(v), -1 << 31), (1 << 31) - 1)
+
+
+def _int32s(kind, values):
+    """Struct of int32 sizes."""
+    try:
+        return kind.from_buffer_copy(struct.pack(f"{len(values)}i", *map(int, values)))
+    except struct.error:
+        return kind(*map(_i32, values))
+
+
 def cdims(dims) -> CDims:
-    return CDims(*map(int, _dim_values(dims)))
+    return _int32s(CDims, _dim_values(dims))
 
 
 def _ptr(t) -> Optional[int]:
@@ -426,7 +441,7 @@ def _bf16_sized(t, count: int, what: str) -> Optional[int]:
 
 
 def edge_moe_balance_ws_bytes(dims, n_seq=1) -> int:
-    return int(load().edge_moe_balance_ws_bytes(ctypes.byref(cdims(dims)), int(n_seq)))
+    return int(load().edge_moe_balance_ws_bytes(ctypes.byref(cdims(dims)), _i32(n_seq)))
 
 
 def edge_moe_balance(dims, logits, topk_idx, counts, probs, loss, ws, seq_offsets=None, stream=None) -> None:
@@ -440,7 +455,7 @@ def edge_moe_balance(dims, logits, topk_idx, counts, probs, loss, ws, seq_offset
     dev = _same_device(logits, topk_idx, counts, probs, loss, ws, seq_offsets)
     st = lib.edge_moe_balance(cdims(dims), _sized(logits, f, T * E, "logits"),
                                  _sized(topk_idx, i, T * k, "topk_idx"), _sized(seq_offsets, i, S + 1, "seq_offsets"),
-                                 S, _sized(counts, i, S * E, "counts"), _sized(probs, f, S * E, "probs"),
+                                 _i32(S), _sized(counts, i, S * E, "counts"), _sized(probs, f, S * E, "probs"),
                                  _sized(loss, f, 2, "loss"), _ptr(ws), ws.numel() * ws.element_size(), _stream_on(dev, stream))
     if st != EDGE_MOE_OK:
         raise EdgeMoeError("edge_moe_balance", st)
@@ -466,7 +481,7 @@ def edge_moe_route_backward(dims, logits, topk_idx, ws, topk_w=None, d_topk_w=No
     g = CRouteGrad(_sized(logits, f, T * E, "logits"), _sized(topk_idx, i, T * k, "topk_idx"),
                    _sized(topk_w, f, T * k, "topk_w"), _sized(d_topk_w, f, T * k, "d_topk_w"),
                    _sized(d_loss, f, 2, "d_loss"), _sized(counts, i, S * E, "counts"),
-                   _sized(seq_offsets, i, S + 1, "seq_offsets"), S, _bf16_sized(x, T * d, "x"),
+                   _sized(seq_offsets, i, S + 1, "seq_offsets"), _i32(S), _bf16_sized(x, T * d, "x"),
                    _bf16_sized(w_router, E * d, "w_router"), _sized(dlogits, f, T * E, "dlogits"),
                    _sized(dx, f, T * d, "dx"), _sized(dw_router, f, E * d, "dw_router"), _sized(dbias, f, E, "dbias"))
     st = lib.edge_moe_route_backward(cdims(dims), g, _ptr(ws), ws.numel() * ws.element_size(), _stream_on(dev, stream))
@@ -529,7 +544,7 @@ def _mx_shape(fmt, dense, codes, scales):
         raise ValueError("expected rows: a tensor of at least two dimensions")
     N, K = dense.shape[-2:]
     M = dense.numel() // (N * K or 1)
-    return (M, N, K, _sized(codes, "uint8", M * N * (K // 2 if fmt == MX_FP4 else K), "codes"),
+    return (_i32(M), _i32(N), _i32(K), _sized(codes, "uint8", M * N * (K // 2 if fmt == MX_FP4 else K), "codes"),
             _sized(scales, "uint8", M * N * (K // 32), "scales"))
 
 
@@ -558,7 +573,7 @@ def edge_moe_mx_dequantize(fmt, codes, scales, dst, stream=None) -> None:
 
 
 def edge_moe_mx_product_ws_bytes(T, R, M, N, K, x_format) -> int:
-    return int(load().edge_moe_mx_product_ws_bytes(ctypes.byref(CMxDims(T, R, M, N, K, x_format))))
+    return int(load().edge_moe_mx_product_ws_bytes(ctypes.byref(_int32s(CMxDims, (T, R, M, N, K, x_format)))))
 
 
 def edge_moe_mx_product(x_format, x, codes, scales, y, ws, offsets=None, row_src=None, stream=None) -> None:
@@ -577,7 +592,7 @@ def edge_moe_mx_product(x_format, x, codes, scales, y, ws, offsets=None, row_src
     e = _sized(scales, "uint8", M * N * (K // 32), "scales")
     off, src = _sized(offsets, "int32", M + 1, "offsets"), _sized(row_src, "int32", R, "row_src")
     dev = _same_device(x, codes, scales, y, ws, offsets, row_src)
-    st = lib.edge_moe_mx_product(CMxDims(T, R, M, N, K, x_format), x.data_ptr(), _row_stride(x), src, off, q, e,
+    st = lib.edge_moe_mx_product(_int32s(CMxDims, (T, R, M, N, K, x_format)), x.data_ptr(), _row_stride(x), src, off, q, e,
                                     y.data_ptr(), _row_stride(y), _ptr(ws), ws.numel() * ws.element_size(),
                                     _stream_on(dev, stream))
     if st != EDGE_MOE_OK:
