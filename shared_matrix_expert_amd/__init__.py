@@ -232,16 +232,19 @@ def _i32(v: int) -> int:
     return min(max(int(v), -1 << 31), (1 << 31) - 1)
 
 
-def _int32s(kind, values):
-    """Struct of int32 sizes."""
+def _int32s(kind, pack, *values):
+    """Struct of int32 sizes; `pack` refuses what does not fit (or is no int)."""
     try:
-        return kind.from_buffer_copy(struct.pack(f"{len(values)}i", *map(int, values)))
+        return kind.from_buffer_copy(pack(*values))
     except struct.error:
         return kind(*map(_i32, values))
 
 
+_pack_dims, _pack_mx_dims = struct.Struct("9i").pack, struct.Struct("6i").pack
+
+
 def cdims(dims) -> CDims:
-    return _int32s(CDims, _dim_values(dims))
+    return _int32s(CDims, _pack_dims, *_dim_values(dims))
 
 
 def _ptr(t) -> Optional[int]:
@@ -573,7 +576,7 @@ def edge_moe_mx_dequantize(fmt, codes, scales, dst, stream=None) -> None:
 
 
 def edge_moe_mx_product_ws_bytes(T, R, M, N, K, x_format) -> int:
-    return int(load().edge_moe_mx_product_ws_bytes(ctypes.byref(_int32s(CMxDims, (T, R, M, N, K, x_format)))))
+    return int(load().edge_moe_mx_product_ws_bytes(ctypes.byref(_int32s(CMxDims, _pack_mx_dims, T, R, M, N, K, x_format))))
 
 
 def edge_moe_mx_product(x_format, x, codes, scales, y, ws, offsets=None, row_src=None, stream=None) -> None:
@@ -592,7 +595,7 @@ def edge_moe_mx_product(x_format, x, codes, scales, y, ws, offsets=None, row_src
     e = _sized(scales, "uint8", M * N * (K // 32), "scales")
     off, src = _sized(offsets, "int32", M + 1, "offsets"), _sized(row_src, "int32", R, "row_src")
     dev = _same_device(x, codes, scales, y, ws, offsets, row_src)
-    st = lib.edge_moe_mx_product(_int32s(CMxDims, (T, R, M, N, K, x_format)), x.data_ptr(), _row_stride(x), src, off, q, e,
+    st = lib.edge_moe_mx_product(_int32s(CMxDims, _pack_mx_dims, T, R, M, N, K, x_format), x.data_ptr(), _row_stride(x), src, off, q, e,
                                     y.data_ptr(), _row_stride(y), _ptr(ws), ws.numel() * ws.element_size(),
                                     _stream_on(dev, stream))
     if st != EDGE_MOE_OK:
