@@ -504,8 +504,13 @@ def _same_device(first, *rest) -> int:
 
 
 def _stream_on(device: int, stream) -> int:
-    """The stream's handle; None: the device's current stream."""
-    return _cuda.getRawStream(device) if stream is None else _stream(stream)
+    """The stream's handle; None: the device's current stream.  A stream of
+    another GPU would run the kernels there, on memory of this one."""
+    if stream is None:
+        return _cuda.getRawStream(device)
+    if getattr(stream, "device_index", device) != device:
+        raise ValueError(f"the stream must be of the tensors' GPU {device}, got one of GPU {stream.device_index}")
+    return _stream(stream)
 
 
 def _dense_type(t) -> int:
