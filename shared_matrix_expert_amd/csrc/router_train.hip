@@ -824,7 +824,8 @@ LoadLayout load_layout(const RouterLoad& a) {
 
 struct GradLayout { size_t planes, part_w, part_x, part_b, bytes; };
 
-int pad32(int v) { return (v + 31) & ~31; }
+constexpr int kTileRows = 128, kPad = 32;   // largest tile of rt_products; T and E are padded to a step of K
+int pad32(int v) { return (v + kPad - 1) & ~(kPad - 1); }
 int64_t tiles(int rows, int bi, int d) { return (int64_t)((rows + bi - 1) / bi) * ((d + 255) / 256); }
 
 // Tile rows of rt_products and slices of K (tokens for dW_r, experts for dx): the
@@ -869,8 +870,9 @@ GradLayout grad_layout(const RouterGrad& a) {
     GradLayout L{};
     size_t off = 0;
     auto take = [&](size_t n) { const size_t o = off; off = up(off + n); return o; };
-    // the last tile reads up to 255 rows past the last plane (DX), up to 255 columns past its last row (DW)
-    L.planes = take(((size_t)3 * a.Tp + 256) * a.Ep * 2 + 512);
+    // Tiles of up to 128 rows of a T or E padded to 32: the last one reads up to 96 rows
+    // past the last plane (DX), or 96 columns past its last row (DW), which is less.
+    L.planes = take(((size_t)3 * a.Tp + kTileRows - kPad) * a.Ep * 2);
     L.part_w = take((size_t)(a.slices > 1 ? a.slices : 0) * a.E * a.d * 4);
     L.part_x = take((size_t)(a.xslices > 1 ? a.xslices : 0) * a.T * a.d * 4);
     L.part_b = take((size_t)((a.Tp + grad_chunk(a.T) - 1) / grad_chunk(a.T)) * a.E * 4);
