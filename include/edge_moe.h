@@ -63,6 +63,8 @@
 extern "C" {
 #endif
 
+/* Raised when a declaration changes.  Entry points can be added under one
+ * version: a caller that may meet an older library looks them up by name. */
 #define EDGE_MOE_ABI_VERSION 5
 
 /* Status codes. */

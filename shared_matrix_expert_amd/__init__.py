@@ -145,6 +145,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     _dense_types.update({getattr(torch, n): kind for n, kind in
                          (("bfloat16", _BF16), ("int16", _BF16), ("uint16", _BF16), ("float32", _FLOAT)) if hasattr(torch, n)})
     lib = ctypes.CDLL(path)
+    missing = [n for n in EXPORTED if not hasattr(lib, n)]
+    if missing:
+        raise RuntimeError(f"{path} was built from other sources, it lacks {', '.join(missing)}: run "
+                           "`python -m shared_matrix_expert_amd.build`")
     vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
     lib.edge_moe_workspace_bytes.argtypes = [ctypes.POINTER(CDims)]
     lib.edge_moe_workspace_bytes.restype = sz
