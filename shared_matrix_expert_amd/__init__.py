@@ -233,7 +233,9 @@ _dim_values = operator.attrgetter(*(n for n, _ in CDims._fields_))
 def _i32(v: int) -> int:
     """A size as the library's int32: one past it becomes the largest, which no
     limit of the library allows (ctypes would cut the upper bits off)."""
-    return min(max(int(v), -1 << 31), (1 << 31) - 1)
+    if -0x80000000 <= v <= 0x7FFFFFFF:
+        return int(v)
+    return 0x7FFFFFFF if v > 0 else -0x80000000
 
 
 def _int32s(kind, pack, *values):
