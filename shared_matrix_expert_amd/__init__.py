@@ -558,8 +558,11 @@ def _mx_shape(fmt, dense, codes, scales):
         raise ValueError("expected rows: a tensor of at least two dimensions")
     N, K = dense.shape[-2:]
     M = dense.numel() // (N * K or 1)
-    return (_i32(M), _i32(N), _i32(K), _sized(codes, "uint8", M * N * (K // 2 if fmt == MX_FP4 else K), "codes"),
-            _sized(scales, "uint8", M * N * (K // 32), "scales"))
+    q = _sized(codes, "uint8", M * N * (K // 2 if fmt == MX_FP4 else K), "codes")
+    e = _sized(scales, "uint8", M * N * (K // 32), "scales")
+    if max(M, N, K) > 0x7FFFFFFF:
+        M, N, K = _i32(M), _i32(N), _i32(K)
+    return M, N, K, q, e
 
 
 def edge_moe_mx_quantize(fmt, src, codes, scales, stream=None) -> None:
