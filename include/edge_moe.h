@@ -300,8 +300,10 @@ int edge_moe_forward_mx(const edge_moe_dims* dims, const uint16_t* x, const int3
  *           have tokens of sum_e f_se P_se with f_se = E c_se / (k n_s) (1 for an
  *           even load), and the z loss, the mean of lse_t^2 over their tokens
  * An empty sequence has zero counts and probabilities; no token at all: losses 0.
- * A logit of -infinity is an expert of probability 0; a token whose logits are all
- * -infinity has no distribution and adds zeros.  NaN and +infinity give NaN.
+ * A logit of -infinity is an expert of probability 0 (any more than 87 below the
+ * token's largest may come out as one: probabilities under 2^-126); a token whose
+ * logits are all -infinity has no distribution and adds zeros.  NaN and +infinity
+ * give NaN.
  * logits: [T][E] as edge_moe_route writes logits_out.  Of dims, T, n_experts and
  * top_k are used (all must pass the layer's checks).  Sums over tokens are kept in
  * float64 past 16 tokens; results are bitwise reproducible. */
@@ -317,6 +319,11 @@ int edge_moe_balance(const edge_moe_dims* dims, const float* logits, const int32
  * (S' sequences with tokens, n tokens in them; the counts are constants, as the
  * selection is), and from it
  *   dx = dz W_r,   dW_r = dz^T x,   dbias = sum_t dz_t
+ * dx is the router's share of the gradient at the layer's input: the library has no
+ * backward pass through the experts, whose share the caller adds.  An entry of
+ * topk_idx outside 0..E-1 has no term of its own; its weight and gradient stay in
+ * the sum over i.  The first term is every token's: a padded batch gives the tokens
+ * of no sequence d_topk_w = 0, and finite x (their dz = 0 meets it in dW_r).
  * A host struct of device pointers; each output may be NULL and is then not
  * computed.  d_topk_w or d_loss (or both) must be given. */
 typedef struct edge_moe_route_grad {
@@ -362,7 +369,7 @@ int edge_moe_route_backward(const edge_moe_dims* dims, const edge_moe_route_grad
  * at 6 (FP4) or 448 (FP8), the sign kept (also a zero's).  A block that holds a
  * NaN or an infinity gets X = 255 and zero codes: it reads back as NaN.
  *   src         rows of K elements of src_type, src_stride elements apart
- *               (row n of matrix m is row m N + n; src_stride >= K)
+ *               (row n of matrix m is row m N + n; K <= src_stride <= 2^32)
  * K a multiple of 128 up to 32768, M N up to 2^27 rows (EDGE_MOE_EUNSUPPORTED
  * otherwise); src and its row stride in bytes, and codes, 16-byte aligned,
  * scales 4-byte aligned.  Makes the matrices of edge_moe_forward_mx and
@@ -396,7 +403,7 @@ typedef struct edge_moe_mx_dims {
 /* Workspace bytes of edge_moe_mx_product (0 for dims it does not take). */
 size_t edge_moe_mx_product_ws_bytes(const edge_moe_mx_dims* dims);
 
-/*   x        T rows of K bf16, x_stride elements apart (x_stride >= K, a
+/*   x        T rows of K bf16, x_stride elements apart (K <= x_stride <= 2^32, a
  *            multiple of 8; 16-byte aligned)
  *   row_src  int32[R]: the x row of each y row (any number of y rows may share
  *            one), or NULL: y row r reads x row r (R <= T).  An entry outside
@@ -409,8 +416,8 @@ size_t edge_moe_mx_product_ws_bytes(const edge_moe_mx_dims* dims);
  *            never write outside y.
  *   codes, scales  the matrices as edge_moe_mx_quantize writes them (FP4);
  *            16- and 4-byte aligned
- *   y        R rows of N bf16, y_stride elements apart (y_stride >= N); only N
- *            elements of a row are written
+ *   y        R rows of N bf16, y_stride elements apart (N <= y_stride <= 2^32);
+ *            only N elements of a row are written
  *   ws       256-byte aligned, at least edge_moe_mx_product_ws_bytes(dims)
  * The matrix cores sum the 128 products of one instruction to about 2^-13.5 of
  * their magnitude sum and the instructions' sums in float32; y is rounded once to

@@ -16,7 +16,8 @@
 //               streams its part of K from HBM straight into operand registers
 //               and rounds the x rows it needs on the way.
 //   mxp_gemm    many rows: x rounded once (mxq_quantize into the workspace),
-//               LDS-tiled, bound by the matrix cores and the LDS reads.
+//               LDS-tiled.  An instruction takes 32 cycles with x in E4M3, 16 with
+//               x in E2M1; the matrix cores are busy 61% and 47% of the cycles.
 #include "lds_load.h"
 #include "mx_format.h"
 #include "operators.h"
@@ -170,9 +171,11 @@ EM_DEV void round16(const uint4 (&v)[2], uint32_t (&q)[4], int& X) {
 // its weights are in flight.  (Rounding in operand registers instead, every lane
 // its own row's elements, costs 16 rows' work whatever their number: one token
 // through 8192 x 4096 took 9.4 us that way.)
-// One row through 8192 x 4096: 6.5 us for 17.8 MB, the launch and three dependent
-// trips to memory; through 8192 x 32768: 27 us a call, 5.2 TB/s.  80 rows over 512
-// matrices of 128 x 4096: 10 us, five trips (offsets, row list, x, W, y).
+// One row through 8192 x 4096: 6.3 us for 17.8 MB, the launch, one trip to memory (W
+// and x are asked for together) and the chain behind it (rounding, products, the
+// sum of four waves); through 8192 x 32768: 27 us a call, 5.2 TB/s.  80 rows over 512
+// matrices of 128 x 4096: 10 us, three trips in turn: the offsets; W and then the row
+// list, which comes back behind all of W since loads return in order; x.
 template <int FMT, int NS, int NC, bool FUSED>
 __global__ void __launch_bounds__(256)
 mxp_stream(MxProduct a) {
@@ -333,9 +336,10 @@ mxp_stream(MxProduct a) {
 // steps ahead; every wave issues the same number of loads a step, so one counted
 // wait covers them.  A code row is 64 (E2M1) or 128 (E4M3) bytes; its 16-byte
 // segments are stored XOR-swizzled by the row against bank conflicts.
-// 16384 x 8192 x 4096 in FP8: 430 to 450 us at the clock that the load leaves, 2.5
-// PFLOP/s (a large library product in FP8: 2.65); 5001 rows in 8 groups through
-// 4096 x 8192 in FP4: 116 to 124 us, two rounds of 192-row tiles, 2.8 PFLOP/s.
+// 16384 x 8192 x 4096 in FP8: 419 to 433 us in a long run of launches (440 to 500 in
+// its first twenty), 2.6 PFLOP/s (a large library product in FP8: 2.65);
+// 5001 rows in 8 groups through 4096 x 8192 in FP4: 118 to 128 us, two rounds of
+// 192-row tiles, 2.7 PFLOP/s, half of what the instruction's 16 cycles would allow.
 // (Four waves of 128 x 128, one a SIMD with 256 accumulators each, read a quarter
 // less from the LDS and measured 479 against 450 us on 16384 x 8192 x 4096 in FP8:
 // one wave's waits leave its matrix core idle.)
@@ -369,7 +373,8 @@ template <int I> struct Set { static constexpr int value = I; };     // one of t
 // at a time, but not 16 neighbours: lanes 0-3, 12-15 and 20-27 go together.  So
 // the 64-byte rows of one segment (four to a 256-byte line of banks) and the
 // middle ones of the next segment have to fall on different slots, which the
-// plain s ^ (r / 4) does not give (measured: 4 conflict cycles a read, none here).
+// plain s ^ (r / 4) does not give (4 conflict cycles a read with it; here 0.1 to 0.2
+// over all of the kernel's LDS instructions, y's way out among them).
 template <int ROW_B>
 EM_DEV int swz(int r, int s) { return ROW_B == 128 ? s ^ ((r >> 1) & 7) : s ^ (-(r >> 2) & 3); }
 
@@ -642,8 +647,9 @@ bool rounds_in_stream(const MxProduct& a) {
 // need, each as long as a tile: measured at K = 4096, tiles of 64 / 128 / 192 / 256
 // rows x 256 columns 18 / 27 / 36 / 44 us in FP4 and 20 / 31 / 45 / 59 in FP8; of 64 /
 // 128 / 256 rows x 128 columns, for matrices of no more, 12 / 17.5 / 26 and 13.5 / 20 /
-// 34.  The rows with the least rounds times length are taken; each matrix with
-// rows is counted half a tile more.  (8192 columns, K = 4096, FP4, us a call by
+// 34.  The rows with the least rounds times length are taken, at 256 columns, or 128
+// for matrices of no more (narrow tiles of wider matrices are not weighed); each matrix
+// with rows is counted half a tile more.  (8192 columns, K = 4096, FP4, us a call by
 // rows: 1000 40 / 30 / 32 / 35, 1536 58 / 49 / 39 / 41, 2048 76 / 57 / 62 / 48;
 // 8 matrices of 4096 x 8192 in FP8, 5001 rows: 235 / 180 / 183 / 207; 512 of 128 x
 // 4096, 20480 rows: 53 with 256 columns, 43 with 128.)

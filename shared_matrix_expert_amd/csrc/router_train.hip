@@ -32,8 +32,8 @@ namespace {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-// Tokens per workgroup of rt_load and rt_dlogits, one or four a wave (whose rows
-// are all asked for at once): few enough that small batches spread over the
+// Tokens per workgroup of rt_load and rt_dlogits, one or four a wave (whose aligned
+// rows are all asked for at once): few enough that small batches spread over the
 // compute units, where the chain of one token's reductions is what takes the time.
 constexpr int WT = 4;          // tokens a wave takes at most
 int load_chunk(int T) { return T <= 2048 ? 4 : 4 * WT; }
@@ -124,7 +124,8 @@ EM_DEV void live_seqs(const Seqs& q, int& live, int& tokens) {
 // E read as -infinity (probability 0).  Rows that are not 16-byte aligned (E no
 // multiple of 4) arrive as 64 neighbours a load, expert 256 i + 64 c + l, and are
 // turned through the wave's LDS row (loads of every fourth expert took 44 us for
-// load and gradient of 14311 x 399, 35 this way).
+// load and gradient of 14311 x 399, 35 this way).  Both forms in one kernel cost the
+// unaligned one: the compiler waits for the loads before at each 256 experts of it.
 template <int NV>
 EM_DEV void load_row(float (&v)[NV][4], const float* __restrict__ row, int E, bool vec) {
     const int lane = lane_id();
@@ -226,8 +227,9 @@ EM_DEV float softmax_row(float (&v)[NV][4]) {
 // Chunk c of a.chunk tokens; its part of sequence s goes to slot c + s of the
 // partial sums (both grow along the tokens, so a slot has one owner).  Bound by
 // reading the logits once; they and the picks are asked for before the sequences
-// are looked up.  16384 x 512: 12.5 us, 33.5 MB of logits in and 4 MB of sums out in
-// one round of workgroups; 333 x 64: 4.2 us, a launch and one token's chain.
+// are looked up.  16384 x 512: 12.8 us, 33.5 MB of logits in and 4 MB of sums out in
+// one round of workgroups (2.9 TB/s: a launch and the chain of four tokens, beside
+// the bytes); 333 x 64: 4.1 us, a launch and one token's chain.
 template <int NV>
 __global__ void __launch_bounds__(256)
 rt_load(RouterLoad a) {
@@ -302,7 +304,7 @@ rt_load(RouterLoad a) {
 // float64, the rows are added in order.  The last workgroup to arrive forms the
 // losses from every workgroup's dot product.  Those are passed with
 // device-coherent accesses and a counted wait, not fences (a fence writes back
-// the XCD's whole L2).  6.3 us at 16384 x 512, 5.3 us at 333 x 64: the launch and
+// the XCD's whole L2).  6.1 us at 16384 x 512, 5.2 us at 333 x 64: the launch and
 // five dependent trips to memory.
 __global__ void __launch_bounds__(1024)
 rt_load_reduce(RouterLoad a) {
@@ -380,7 +382,7 @@ rt_load_reduce(RouterLoad a) {
 // that the sequence's f stays in registers).  The picks' terms meet the row
 // through an LDS row that is zero between tokens.  Rows T .. Tp - 1 and columns
 // E .. Ep - 1 of the planes are zeros.  Bound by HBM: 16384 x 512 logits in and dz
-// out 16.5 us (67 MB, 4.1 TB/s), in and three planes out 24 to 30 us (84 MB).
+// out 16 us (67 MB, 4.2 TB/s), in and three planes out 24 to 29 us (84 MB).
 template <int NV>
 __global__ void __launch_bounds__(256)
 rt_dlogits(RouterGrad a) {
@@ -554,8 +556,9 @@ rt_dlogits(RouterGrad a) {
 // SIMD, overlap them.  (Waves of 64 x 128, two a SIMD, read less from the LDS and
 // measured the same to 5% slower, a 256-row workgroup the same.)  Both products
 // and dbias share a launch: at T = 1501 neither fills the chip by itself.
-// T = 16384, E = 512, d = 4096: 311 us, 412 GFLOP at 1.3 PFLOP/s (a large library
-// product in bf16: 1.2); T = 1501: 39 us, 0.97 PFLOP/s, 448 tiles on 512 places.
+// T = 16384, E = 512, d = 4096: 316 to 322 us in a long run of launches, 412 GFLOP at
+// 1.3 PFLOP/s (a large library product in bf16: 1.2), the matrix cores busy 74% of the
+// cycles; T = 1501: 39 to 44 us, 0.9 PFLOP/s, 448 tiles on 512 places.
 // With 64 rows a SIMD has one or two waves, which then read a plane ahead of the
 // products (a step 0.85 -> 0.78 us); a third and fourth LDS stage changed nothing.
 namespace {
@@ -774,7 +777,7 @@ rt_products(RouterGrad a, int bblocks, int wblocks) {
 
 // The slices of dW_r (wblocks workgroups) and of dx, in order, eight asked for at
 // once (four where there are no more): HBM and the Infinity Cache (512 x 4096, 4
-// slices: 7.2 us, 42 MB).
+// slices: 7.6 us, 42 MB).
 template <int N>
 EM_DEV void rt_add_slices(float4& s, const float* part, int slices, int64_t n, int64_t at, int z) {
     float4 v[N];
