@@ -12,7 +12,7 @@ Five kinds of pass:
 * ``dense_backward``: its gradients at x and at the matrices
   (edge_moe_dense_product_backward);
 * ``int4``: the product of token rows with int4 matrices in the layer's own
-  storage (edge_moe_int4_product).
+  storage (edge_moe_packed_product).
 
 ``run`` computes a pass in plain torch operations, or through the library
 where ``own`` is true; ``exact`` gives the definition in float64.
@@ -285,8 +285,8 @@ def _own(s):
     T, M, N, K = (s[n] for n in ("T", "M", "N", "K"))
     R = T * max(1, s["k"])
     if kind == "int4":
-        ws = _ws(s, lambda: em.edge_moe_int4_product_ws_bytes(T, R, M, N, K, s["gq"]))
-        em.edge_moe_int4_product(s["gq"], s["x"], s["codes"], s["scales"], s["y"], ws, offsets=s["offsets"], row_src=s["row_src"])
+        ws = _ws(s, lambda: em.edge_moe_packed_product_ws_bytes(T, R, M, N, K, s["gq"]))
+        em.edge_moe_packed_product(s["gq"], s["x"], s["codes"], s["scales"], s["y"], ws, offsets=s["offsets"], row_src=s["row_src"])
         return s["y"]
     if kind == "dense":
         ws = _ws(s, lambda: em.edge_moe_dense_product_ws_bytes(T, R, M, N, K))
