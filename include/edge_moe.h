@@ -427,6 +427,158 @@ int edge_moe_mx_product(const edge_moe_mx_dims* dims, const uint16_t* x, int64_t
                         const int32_t* offsets, const uint8_t* codes, const uint8_t* scales, uint16_t* y,
                         int64_t y_stride, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------ norm, dense and int4 matrices --
+ * Root-mean-square norm with the residual's addition, between two layers:
+ *   r = bf16(x + add)                    (the exact sum rounded once, as
+ *                                         edge_moe_residual's; x where add is NULL)
+ *   rstd = 1 / sqrt(mean_i r_i^2 + eps)
+ *   y = bf16(r rstd gain)
+ *   codes, scales = MXFP8 of y           (the rule of edge_moe_mx_quantize)
+ * A host struct of device pointers.  Rows are 16-byte aligned: bases 16-byte
+ * aligned, strides (in elements, d .. 2^32) multiples of 8 (bf16) or 4
+ * (float32); only the d elements of a row are read and written.  Of x_out, y,
+ * codes with scales, and rstd at least one must be given.  x_out may be x. */
+typedef struct edge_moe_norm_args {
+    int32_t         T;             /* rows, 0..2^25                              */
+    int32_t         d;             /* a multiple of 8 up to 32768                */
+    float           eps;           /* above 0                                    */
+    int32_t         add_type;      /* EDGE_MOE_BF16 or EDGE_MOE_FLOAT, with add  */
+    int32_t         gain_type;     /* EDGE_MOE_BF16 or EDGE_MOE_FLOAT            */
+    const uint16_t* x;        int64_t x_stride;      /* bf16                     */
+    const void*     add;      int64_t add_stride;    /* or NULL                  */
+    const void*     gain;          /* [d], 16-byte aligned                       */
+    uint16_t*       x_out;    int64_t x_out_stride;  /* bf16: r, or NULL         */
+    uint16_t*       y;        int64_t y_stride;      /* bf16, or NULL            */
+    uint8_t*        codes;         /* [T][d] E4M3, 16-byte aligned, or NULL; d a multiple of 128 */
+    uint8_t*        scales;        /* [d/128][T][4] E8M0, 4-byte aligned, with codes */
+    float*          rstd;          /* [T] or NULL                                */
+} edge_moe_norm_args;
+
+/* The mean is summed in float64: no row of finite bf16 overflows it.  A NaN or
+ * an infinity in r makes its own row NaN or zero.  codes and scales are the x
+ * that edge_moe_mx_product_coded takes, and the rounding that edge_moe_mx_product
+ * would make of y.  Bitwise reproducible. */
+int edge_moe_norm(const edge_moe_norm_args* args, void* stream);
+
+/* Its backward pass, with v = r rstd and dv = dy gain:
+ *   dx = dres + rstd (dv - v mean_i(dv_i v_i)),   dgain = sum_t dy_t v_t
+ * dx is the gradient at x and at add alike.  Rows as edge_moe_norm's; dx may be
+ * dres or dy. */
+typedef struct edge_moe_norm_grad {
+    int32_t         T;             /* rows, 0..2^25                              */
+    int32_t         d;             /* a multiple of 8 up to 32768                */
+    int32_t         gain_type;     /* EDGE_MOE_BF16 or EDGE_MOE_FLOAT            */
+    int32_t         grad_type;     /* of dy, dres and dx                         */
+    const uint16_t* x;        int64_t x_stride;      /* bf16: r, the x_out of the forward pass */
+    const void*     gain;          /* [d], 16-byte aligned                       */
+    const float*    rstd;          /* [T] of the forward pass                    */
+    const void*     dy;       int64_t dy_stride;
+    const void*     dres;     int64_t dres_stride;   /* gradient at r from elsewhere, or NULL */
+    void*           dx;       int64_t dx_stride;     /* or NULL                  */
+    float*          dgain;         /* [d] float32, or NULL                       */
+} edge_moe_norm_grad;
+
+/* Workspace bytes of edge_moe_norm_backward (0 for a shape it does not take; T = 0
+ * is taken: dgain is then zero). */
+size_t edge_moe_norm_backward_ws_bytes(int32_t T, int32_t d);
+
+/* Sums over a row and over rows are float32 in a fixed order, the workgroups'
+ * sums float64: bitwise reproducible.  ws 256-byte aligned. */
+int edge_moe_norm_backward(const edge_moe_norm_grad* grad, void* ws, size_t ws_bytes, void* stream);
+
+/* Product of bf16 rows with bf16 matrices, dense or grouped over a routed
+ * batch's experts (experts before they are quantised, LoRA factors):
+ *   y[r] = sum_k x[src(r)][k] W_m[k],   r = 0..R-1
+ * with m the matrix whose rows offsets[m] .. offsets[m + 1] - 1 hold r. */
+typedef struct edge_moe_dense_dims {
+    int32_t T;          /* rows of x, 1..2^20                                     */
+    int32_t R;          /* rows of y, 0..2^25                                     */
+    int32_t M;          /* matrices, 1..1024                                      */
+    int32_t N;          /* rows of a matrix = columns of y, a multiple of 8 up to 32768 */
+    int32_t K;          /* columns of a matrix and of x, a multiple of 8 up to 32768 */
+} edge_moe_dense_dims;
+
+/* Workspace bytes of edge_moe_dense_product (0 for dims it does not take). */
+size_t edge_moe_dense_product_ws_bytes(const edge_moe_dense_dims* dims);
+
+/*   x        T rows of K bf16, x_stride elements apart (K .. 2^32, a multiple of
+ *            8; 16-byte aligned)
+ *   row_src, offsets  as edge_moe_mx_product's: the x row of each y row, or NULL
+ *            (R <= T); the first y row of each matrix, or NULL with M = 1.  A
+ *            row_src entry outside 0..T-1 gives a row of zeros; y rows outside
+ *            offsets[0] .. offsets[M] - 1 are left as they were; offsets that
+ *            descend leave rows unwritten or take them twice.
+ *   w        [M][N][K] bf16, 16-byte aligned
+ *   y        R rows of N of y_type, y_stride elements apart (N .. 2^32), rows
+ *            16-byte aligned; only N elements of a row are written
+ *   ws       256-byte aligned
+ * Products are exact, their sums float32, y is rounded once.  A NaN or infinity
+ * reaches only the sums it enters.  Bitwise reproducible. */
+int edge_moe_dense_product(const edge_moe_dense_dims* dims, const uint16_t* x, int64_t x_stride, const int32_t* row_src,
+                           const int32_t* offsets, const uint16_t* w, int32_t y_type, void* y, int64_t y_stride, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/* Its backward pass:
+ *   dx[r] = sum_n dy[r][n] W_m[n]                      (token_rows NULL: R rows)
+ *   dx[t] = sum_j of that over the rows token_rows[t][j]   (T rows)
+ *   dW_m[n] = sum over m's rows r of dy[r][n] x[src(r)]
+ * A host struct of device pointers; dx or dw (or both) must be given. */
+typedef struct edge_moe_dense_grad {
+    const uint16_t* dy;       int64_t dy_stride;     /* R rows of N bf16, 16-byte aligned       */
+    const uint16_t* x;        int64_t x_stride;      /* with dw: T rows of K bf16               */
+    const int32_t*  row_src;       /* with dw: as in the forward pass, or NULL (R <= T)         */
+    const int32_t*  offsets;       /* as in the forward pass                                    */
+    const int32_t*  token_rows;    /* [T][per_token] rows of each token, or NULL; an entry that
+                                      is no row of a matrix adds nothing                        */
+    int32_t         per_token;     /* 1..1024, with token_rows                                  */
+    const uint16_t* w;             /* with dx: [M][N][K] bf16, 16-byte aligned                  */
+    void*           dx;       int64_t dx_stride;     /* rows of K, or NULL                      */
+    int32_t         dx_type;
+    int32_t         dw_type;
+    void*           dw;            /* [M][N][K], 16-byte aligned, or NULL                       */
+} edge_moe_dense_grad;
+
+/* Workspace bytes of edge_moe_dense_product_backward, with token_rows and without
+ * (0 for dims it does not take). */
+size_t edge_moe_dense_product_backward_ws_bytes(const edge_moe_dense_dims* dims);
+
+/* Without token_rows, dx rows outside offsets[0] .. offsets[M] - 1 are left as they
+ * were; with them every dx row is written.  A row whose row_src entry is outside
+ * 0..T-1 adds nothing to dW; the dW of a matrix without rows is zero.  Types, sums
+ * and rounding as edge_moe_dense_product's (a token's rows are added in float32, in
+ * slot order).  Bitwise reproducible. */
+int edge_moe_dense_product_backward(const edge_moe_dense_dims* dims, const edge_moe_dense_grad* grad, void* ws,
+                                    size_t ws_bytes, void* stream);
+
+/* Product of bf16 rows with int4 matrices in the layer's storage (s_up, a_dn, ...,
+ * or any other matrix of it), dense or grouped over a routed batch's experts:
+ *   y[r][n] = sum_k x[src(r)][k] q_m[n][k] s_m[n][k / Gq_eff],   r = 0..R-1
+ * with m the matrix whose rows offsets[m] .. offsets[m + 1] - 1 hold r. */
+typedef struct edge_moe_packed_dims {
+    int32_t T;            /* rows of x, 1..2^20                                       */
+    int32_t R;            /* rows of y, 0..2^25                                       */
+    int32_t M;            /* matrices, 1..1024                                        */
+    int32_t N;            /* rows of a matrix = columns of y, 1..32768                */
+    int32_t K;            /* a multiple of 32 up to 32768, and of Gq_eff              */
+    int32_t quant_group;  /* a power of two in [32, 4096]; Gq_eff = min(quant_group, K) */
+} edge_moe_packed_dims;
+
+/* Workspace bytes of edge_moe_packed_product (0 for dims it does not take). */
+size_t edge_moe_packed_product_ws_bytes(const edge_moe_packed_dims* dims);
+
+/*   x, row_src, offsets  as edge_moe_dense_product's
+ *   codes    [M][N][K/2] packed int4, 16-byte aligned
+ *   scales   [M][N][K/Gq_eff] fp16, 4-byte aligned
+ *   y        R rows of N of y_type, y_stride elements apart (N .. 2^32); only N
+ *            elements of a row are written
+ *   ws       256-byte aligned
+ * Weights are q s exactly; a group's products are exact and summed in float32, the
+ * groups' sums scaled and added in float32, y is rounded once.  A NaN or infinity
+ * reaches only the sums it enters.  Bitwise reproducible. */
+int edge_moe_packed_product(const edge_moe_packed_dims* dims, const uint16_t* x, int64_t x_stride, const int32_t* row_src,
+                          const int32_t* offsets, const uint8_t* codes, const uint16_t* scales, int32_t y_type, void* y,
+                          int64_t y_stride, void* ws, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------ expert streaming from host --
  * The pages keep the expert library in host memory and bring the experts a
  * batch routes to into a small GPU memory, evicting the least recently used,

@@ -38,7 +38,9 @@ EXPORTED = ("edge_moe_workspace_bytes", "edge_moe_route", "edge_moe_forward",
             "edge_moe_cache_prefetch", "edge_moe_cache_totals", "edge_moe_cache_slot_of",
             "edge_moe_mx_quantize", "edge_moe_mx_dequantize", "edge_moe_mx_product_ws_bytes", "edge_moe_mx_product",
             "edge_moe_balance_ws_bytes", "edge_moe_balance", "edge_moe_route_backward_ws_bytes",
-            "edge_moe_route_backward")
+            "edge_moe_route_backward", "edge_moe_norm", "edge_moe_norm_backward_ws_bytes", "edge_moe_norm_backward",
+            "edge_moe_dense_product_ws_bytes", "edge_moe_dense_product", "edge_moe_dense_product_backward_ws_bytes",
+            "edge_moe_dense_product_backward", "edge_moe_packed_product_ws_bytes", "edge_moe_packed_product")
 
 # element formats and dense types of the MX matrix operators
 MX_FP4, MX_FP8 = 0, 1
@@ -51,6 +53,7 @@ class _cuda:                   # torch's current device, and a device's stream h
 
 _dtypes: dict = {}             # torch's types by name, and those of dense matrices (filled by load())
 _dense_types: dict = {}
+_half_types: set = set()
 
 
 class CDims(ctypes.Structure):
@@ -117,6 +120,35 @@ class CRouteGrad(ctypes.Structure):
                 + [(n, ctypes.c_void_p) for n in ("x", "w_router", "dlogits", "dx", "dw_router", "dbias")])
 
 
+def _fields(spec: str) -> list:
+    """ctypes fields of a struct: names by kind (i int32, f float, p pointer, s int64 stride)."""
+    kinds = {"i": ctypes.c_int32, "f": ctypes.c_float, "p": ctypes.c_void_p, "s": ctypes.c_int64}
+    return [(n, kinds[k]) for k, n in (w.split(":") for w in spec.split())]
+
+
+class CNormArgs(ctypes.Structure):
+    _fields_ = _fields("i:T i:d f:eps i:add_type i:gain_type p:x s:x_stride p:add s:add_stride p:gain p:x_out s:x_out_stride "
+                       "p:y s:y_stride p:codes p:scales p:rstd")
+
+
+class CNormGrad(ctypes.Structure):
+    _fields_ = _fields("i:T i:d i:gain_type i:grad_type p:x s:x_stride p:gain p:rstd p:dy s:dy_stride p:dres s:dres_stride "
+                       "p:dx s:dx_stride p:dgain")
+
+
+class CDenseDims(ctypes.Structure):
+    _fields_ = _fields("i:T i:R i:M i:N i:K")
+
+
+class CPackedDims(ctypes.Structure):
+    _fields_ = _fields("i:T i:R i:M i:N i:K i:quant_group")
+
+
+class CDenseGrad(ctypes.Structure):
+    _fields_ = _fields("p:dy s:dy_stride p:x s:x_stride p:row_src p:offsets p:token_rows i:per_token p:w p:dx s:dx_stride "
+                       "i:dx_type i:dw_type p:dw")
+
+
 class EdgeMoeError(RuntimeError):
     def __init__(self, fn: str, status: int):
         super().__init__(f"{fn} failed: status {status} ({status_string(status)})")
@@ -144,6 +176,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     _dtypes.update({n: getattr(torch, n) for n in ("uint8", "int32", "float32")})
     _dense_types.update({getattr(torch, n): kind for n, kind in
                          (("bfloat16", _BF16), ("int16", _BF16), ("uint16", _BF16), ("float32", _FLOAT)) if hasattr(torch, n)})
+    _half_types.update(getattr(torch, n) for n in ("float16", "int16", "uint16") if hasattr(torch, n))
     lib = ctypes.CDLL(path)
     missing = [n for n in EXPORTED if not hasattr(lib, n)]
     if missing:
@@ -207,6 +240,24 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.edge_moe_route_backward_ws_bytes.restype = sz
     lib.edge_moe_route_backward.argtypes = [ctypes.POINTER(CDims), ctypes.POINTER(CRouteGrad), vp, sz, vp]
     lib.edge_moe_route_backward.restype = i32
+    lib.edge_moe_norm.argtypes = [ctypes.POINTER(CNormArgs), vp]
+    lib.edge_moe_norm.restype = i32
+    lib.edge_moe_norm_backward_ws_bytes.argtypes = [i32, i32]
+    lib.edge_moe_norm_backward_ws_bytes.restype = sz
+    lib.edge_moe_norm_backward.argtypes = [ctypes.POINTER(CNormGrad), vp, sz, vp]
+    lib.edge_moe_norm_backward.restype = i32
+    lib.edge_moe_dense_product_ws_bytes.argtypes = [ctypes.POINTER(CDenseDims)]
+    lib.edge_moe_dense_product_ws_bytes.restype = sz
+    lib.edge_moe_dense_product.argtypes = [ctypes.POINTER(CDenseDims), vp, i64, vp, vp, vp, i32, vp, i64, vp, sz, vp]
+    lib.edge_moe_dense_product.restype = i32
+    lib.edge_moe_dense_product_backward_ws_bytes.argtypes = [ctypes.POINTER(CDenseDims)]
+    lib.edge_moe_dense_product_backward_ws_bytes.restype = sz
+    lib.edge_moe_dense_product_backward.argtypes = [ctypes.POINTER(CDenseDims), ctypes.POINTER(CDenseGrad), vp, sz, vp]
+    lib.edge_moe_dense_product_backward.restype = i32
+    lib.edge_moe_packed_product_ws_bytes.argtypes = [ctypes.POINTER(CPackedDims)]
+    lib.edge_moe_packed_product_ws_bytes.restype = sz
+    lib.edge_moe_packed_product.argtypes = [ctypes.POINTER(CPackedDims), vp, i64, vp, vp, vp, vp, i32, vp, i64, vp, sz, vp]
+    lib.edge_moe_packed_product.restype = i32
     lib.edge_moe_residual.argtypes = [ctypes.c_int32, ctypes.c_int32, vp, vp, vp, vp]
     lib.edge_moe_residual.restype = i32
     lib.edge_moe_copy.argtypes = [vp, vp, sz, vp]
@@ -246,7 +297,7 @@ def _int32s(kind, pack, *values):
         return kind(*map(_i32, values))
 
 
-_pack_dims, _pack_mx_dims = struct.Struct("9i").pack, struct.Struct("6i").pack
+_pack_dims, _pack_mx_dims, _pack_dense_dims = struct.Struct("9i").pack, struct.Struct("6i").pack, struct.Struct("5i").pack
 
 
 def cdims(dims) -> CDims:
@@ -634,6 +685,183 @@ def mx_weights(dense: dict, stream=None) -> dict:
     for key in _WEIGHT_KEYS[12:16]:
         out[key] = dense[key]
     return out
+
+
+# ------------------------------------------------ norm, dense and int4 matrices ----
+
+def _rows(t, count: int, cols: int, what: str):
+    """(address, stride) of a tensor of `count` rows of `cols`, at one stride; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.dim() < 2 or t.shape[-1] != cols or t.numel() != count * cols:
+        raise ValueError(f"{what}: expected {count} rows of {cols}, got {tuple(t.shape)}")
+    return t.data_ptr(), _row_stride(t)
+
+
+def _bf16_rows(t, count: int, cols: int, what: str):
+    if t is not None and _dense_type(t) != _BF16:
+        raise ValueError(f"{what}: expected bfloat16 (or int16 bits), got {t.dtype}")
+    return _rows(t, count, cols, what)
+
+
+def _vector(t, count: int, what: str) -> int:
+    """Address of a contiguous bf16 or float32 vector."""
+    if t.numel() != count or not t.is_contiguous():
+        raise ValueError(f"{what}: expected {count} contiguous values, got {t.numel()}")
+    return t.data_ptr()
+
+
+def edge_moe_norm(x, gain, eps, add=None, x_out=None, y=None, codes=None, scales=None, rstd=None, stream=None) -> None:
+    """r = bf16(x + add) to x_out, y = bf16(r rstd gain) with rstd = 1 / sqrt(mean r^2
+    + eps), and y's MXFP8 codes [..., T, d] and scales [..., d/128, T, 4]: those of
+    the outputs that are given.  x, x_out, y bf16 rows [T][d] at one stride, add bf16
+    or float32, gain [d] bf16 or float32."""
+    lib = load()
+    if x.dim() < 2:
+        raise ValueError("x must be rows: a tensor of at least two dimensions")
+    d = x.shape[-1]
+    T = x.numel() // (d or 1)
+    dev = _same_device(x, gain, add, x_out, y, codes, scales, rstd)
+    a = CNormArgs(_i32(T), _i32(d), eps, 0 if add is None else _dense_type(add), _dense_type(gain), *_bf16_rows(x, T, d, "x"),
+                  *_rows(add, T, d, "add"), _vector(gain, d, "gain"), *_bf16_rows(x_out, T, d, "x_out"),
+                  *_bf16_rows(y, T, d, "y"), _sized(codes, "uint8", T * d, "codes"),
+                  _sized(scales, "uint8", T * (d // 32), "scales"), _sized(rstd, "float32", T, "rstd"))
+    st = lib.edge_moe_norm(a, _stream_on(dev, stream))
+    if st != EDGE_MOE_OK:
+        raise EdgeMoeError("edge_moe_norm", st)
+
+
+def edge_moe_norm_backward_ws_bytes(T, d) -> int:
+    return int(load().edge_moe_norm_backward_ws_bytes(_i32(T), _i32(d)))
+
+
+def edge_moe_norm_backward(x, gain, rstd, dy, ws, dres=None, dx=None, dgain=None, stream=None) -> None:
+    """The norm's backward pass at x (the forward pass's x_out, or its x where nothing
+    was added): dx = dres + the gradient through y, dgain [d] float32.  dy, dres and
+    dx rows of one type, bf16 or float32."""
+    lib = load()
+    if x.dim() < 2:
+        raise ValueError("x must be rows: a tensor of at least two dimensions")
+    d = x.shape[-1]
+    T = x.numel() // (d or 1)
+    kind = _dense_type(dy)
+    for t, what in ((dres, "dres"), (dx, "dx")):
+        if t is not None and _dense_type(t) != kind:
+            raise ValueError(f"{what} must be of dy's type, got {t.dtype} and {dy.dtype}")
+    dev = _same_device(x, gain, rstd, dy, ws, dres, dx, dgain)
+    g = CNormGrad(_i32(T), _i32(d), _dense_type(gain), kind, *_bf16_rows(x, T, d, "x"), _vector(gain, d, "gain"),
+                  _sized(rstd, "float32", T, "rstd"), *_rows(dy, T, d, "dy"), *_rows(dres, T, d, "dres"),
+                  *_rows(dx, T, d, "dx"), _sized(dgain, "float32", d, "dgain"))
+    st = lib.edge_moe_norm_backward(g, _ptr(ws), ws.numel() * ws.element_size(), _stream_on(dev, stream))
+    if st != EDGE_MOE_OK:
+        raise EdgeMoeError("edge_moe_norm_backward", st)
+
+
+def _dense_dims(T, R, M, N, K) -> CDenseDims:
+    return _int32s(CDenseDims, _pack_dense_dims, T, R, M, N, K)
+
+
+def _matrices(w, what: str):
+    """(M, N, K) and address of contiguous bf16 matrices [M][N][K] or one [N][K]."""
+    if w.dim() not in (2, 3) or _dense_type(w) != _BF16 or not w.is_contiguous():
+        raise ValueError(f"{what}: expected contiguous bfloat16 matrices [M][N][K]")
+    return (1 if w.dim() == 2 else w.shape[0]), w.shape[-2], w.shape[-1], w.data_ptr()
+
+
+def edge_moe_dense_product_ws_bytes(T, R, M, N, K) -> int:
+    return int(load().edge_moe_dense_product_ws_bytes(_dense_dims(T, R, M, N, K)))
+
+
+def edge_moe_dense_product(x, w, y, ws, offsets=None, row_src=None, stream=None) -> None:
+    """y [R][N] (bf16 or float32) = the rows of x [T][K] (bf16) times bf16 matrices w
+    [M][N][K] (or one matrix [N][K]).  offsets int32 [M + 1]: the y rows of each
+    matrix; row_src int32 [R]: the x row of each y row."""
+    lib = load()
+    M, N, K, wp = _matrices(w, "w")
+    if x.dim() != 2 or y.dim() != 2:
+        raise ValueError("x and y must be rows: [rows][columns]")
+    T, R = x.shape[0], y.shape[0]
+    dev = _same_device(x, w, y, ws, offsets, row_src)
+    st = lib.edge_moe_dense_product(_dense_dims(T, R, M, N, K), *_bf16_rows(x, T, K, "x"), _sized(row_src, "int32", R, "row_src"),
+                                    _sized(offsets, "int32", M + 1, "offsets"), wp, _dense_type(y), *_rows(y, R, N, "y"),
+                                    _ptr(ws), ws.numel() * ws.element_size(), _stream_on(dev, stream))
+    if st != EDGE_MOE_OK:
+        raise EdgeMoeError("edge_moe_dense_product", st)
+
+
+def edge_moe_dense_product_backward_ws_bytes(T, R, M, N, K) -> int:
+    return int(load().edge_moe_dense_product_backward_ws_bytes(_dense_dims(T, R, M, N, K)))
+
+
+def edge_moe_dense_product_backward(dy, ws, x=None, w=None, dx=None, dw=None, offsets=None, row_src=None, token_rows=None,
+                                    stream=None) -> None:
+    """Gradients of edge_moe_dense_product from dy [R][N] (bf16), bf16 or float32 each:
+    dx from w, [R][K] by rows or, with token_rows int32 [T][k] (the rows of each
+    token, -1 for none), [T][K] by tokens; dw [M][N][K] from x and row_src."""
+    lib = load()
+    if dy.dim() != 2 or (dx is None and dw is None):
+        raise ValueError("dy must be rows [R][N], and dx or dw given")
+    if (dx is not None and w is None) or (dw is not None and x is None):
+        raise ValueError("dx needs w, dw needs x")
+    R, N = dy.shape
+    M, K = None, None
+    for t, what in ((dw, "dw"), (w if dx is not None else None, "w")):
+        if t is None:
+            continue
+        if t.dim() not in (2, 3) or not t.is_contiguous() or (M is not None and (M, K) != ((1 if t.dim() == 2 else t.shape[0]), t.shape[-1])):
+            raise ValueError("w and dw must be contiguous matrices [M][N][K] of one shape")
+        M, K = (1 if t.dim() == 2 else t.shape[0]), t.shape[-1]
+        if t.shape[-2] != N:
+            raise ValueError(f"{what}: expected {N} rows a matrix, got {t.shape[-2]}")
+    if dx is not None and _dense_type(w) != _BF16:
+        raise ValueError(f"w: expected bfloat16 (or int16 bits), got {w.dtype}")
+    k = 0
+    if token_rows is not None:
+        if token_rows.dim() != 2:
+            raise ValueError("token_rows must be [T][k]")
+        k = token_rows.shape[1]
+    T = x.shape[0] if dw is not None else token_rows.shape[0] if token_rows is not None else 1
+    if dw is not None and x.dim() != 2:
+        raise ValueError("x must be rows [T][K]")
+    dev = _same_device(dy, ws, x, w, dx, dw, offsets, row_src, token_rows)
+    g = CDenseGrad(*_bf16_rows(dy, R, N, "dy"), *(_bf16_rows(x, T, K, "x") if dw is not None else (None, 0)),
+                   _sized(row_src, "int32", R, "row_src"), _sized(offsets, "int32", M + 1, "offsets"),
+                   _sized(token_rows, "int32", T * k, "token_rows"), k, None if dx is None else w.data_ptr(),
+                   *_rows(dx, T if k else R, K, "dx"), 0 if dx is None else _dense_type(dx),
+                   0 if dw is None else _dense_type(dw), None if dw is None else dw.data_ptr())
+    st = lib.edge_moe_dense_product_backward(_dense_dims(T, R, M, N, K), g, _ptr(ws), ws.numel() * ws.element_size(),
+                                             _stream_on(dev, stream))
+    if st != EDGE_MOE_OK:
+        raise EdgeMoeError("edge_moe_dense_product_backward", st)
+
+
+def _packed_dims(T, R, M, N, K, quant_group) -> CPackedDims:
+    return _int32s(CPackedDims, _pack_mx_dims, T, R, M, N, K, quant_group)
+
+
+def edge_moe_packed_product_ws_bytes(T, R, M, N, K, quant_group) -> int:
+    return int(load().edge_moe_packed_product_ws_bytes(_packed_dims(T, R, M, N, K, quant_group)))
+
+
+def edge_moe_packed_product(quant_group, x, codes, scales, y, ws, offsets=None, row_src=None, stream=None) -> None:
+    """y [R][N] (bf16 or float32) = the rows of x [T][K] (bf16) times int4 matrices:
+    codes uint8 [M][N][K/2] and fp16 scales [M][N][K/min(quant_group, K)] (or one
+    matrix without the leading dimension), as in the layer's weight dicts.  offsets
+    int32 [M + 1]: the y rows of each matrix; row_src int32 [R]: the x row of each."""
+    lib = load()
+    if x.dim() != 2 or y.dim() != 2 or quant_group < 1:
+        raise ValueError("x and y must be rows: [rows][columns], quant_group a group's elements")
+    (T, K), (R, N) = x.shape, y.shape
+    M = 1 if codes.dim() == 2 else codes.shape[0]
+    if scales.dtype not in _half_types or not scales.is_contiguous() or scales.numel() != M * N * (K // (min(quant_group, K) or 1)):
+        raise ValueError(f"scales: expected {M} x {N} x {K} / {quant_group} contiguous float16 values (or int16 bits)")
+    dev = _same_device(x, codes, scales, y, ws, offsets, row_src)
+    st = lib.edge_moe_packed_product(_packed_dims(T, R, M, N, K, quant_group), *_bf16_rows(x, T, K, "x"),
+                                   _sized(row_src, "int32", R, "row_src"), _sized(offsets, "int32", M + 1, "offsets"),
+                                   _sized(codes, "uint8", M * N * (K // 2), "codes"), scales.data_ptr(), _dense_type(y),
+                                   *_rows(y, R, N, "y"), _ptr(ws), ws.numel() * ws.element_size(), _stream_on(dev, stream))
+    if st != EDGE_MOE_OK:
+        raise EdgeMoeError("edge_moe_packed_product", st)
 
 
 def edge_moe_residual(x, y, x_out, stream=None) -> None:

@@ -21,7 +21,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libedge_moe.so")
 SOURCES = ["api.hip", "router.hip", "dispatch.hip", "gemm.hip", "decode.hip", "layer.hip",
            "prefill.hip", "calib.hip", "mx.hip", "prefetch.hip", "cache.hip", "mx_quant.hip",
-           "mx_product.hip", "router_train.hip", "operators.hip"]
+           "mx_product.hip", "router_train.hip", "norm.hip", "dense_product.hip",
+           "int4_product.hip", "operators.hip"]
 ARCH = "gfx950"
 
 
@@ -32,6 +33,7 @@ KERNEL_SOURCES = (("dec_layer", "layer.hip"), ("pl_", "layer.hip"), ("dec_", "de
                   ("router_", "router.hip"), ("perm_", "dispatch.hip"), ("pf_", "prefill.hip"),
                   ("mfma_peak", "calib.hip"), ("mx_", "mx.hip"), ("prefetch_", "prefetch.hip"), ("cache_", "cache.hip"),
                   ("mxq_", "mx_quant.hip"), ("mxp_", "mx_product.hip"), ("rt_", "router_train.hip"),
+                  ("norm_", "norm.hip"), ("dp_", "dense_product.hip"), ("ip_", "int4_product.hip"),
                   ("copy_bytes", "gemm.hip"))
 
 

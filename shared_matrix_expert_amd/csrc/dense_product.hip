@@ -1,0 +1,640 @@
+// Products of token rows with bf16 matrices, grouped by matrix with ragged rows, and
+// their gradients:
+//   DP_Y    y[r][n]     = sum_k x[src(r)][k] W_m[n][k]       (m the matrix of row r)
+//   DP_DX   dx[r][k]    = sum_n dy[r][n] W_m[n][k]           (or summed over a token's rows)
+//   DP_DW   dW_m[n][k]  = sum over m's rows r of dy[r][n] x[src(r)][k]
+// All three are out[i][j] = sum_c P[i][c] Q[j][c].  An operand whose c lies along its
+// rows comes from the LDS as it is; one whose c runs down the rows (W in dx, both in dW)
+// is transposed on the way out of the LDS (ds_read_b64_tr_b16).  The matrix cores take
+// Q as their row operand, so that a lane holds four neighbouring j of one i.
+//
+//   dp_stream  y of few rows a matrix: bound by the weight bytes.  Four waves split K and
+//              stream W straight into operand registers.
+//   dp_tile    everything else: LDS tiles by direct global -> LDS loads, counted by hand.
+//   dp_join    slices of c, and the rows of a token, added in a fixed order (float32).
+#include <type_traits>
+
+#include "common.h"
+#include "lds_load.h"
+#include "operators.h"
+#include "row_tile.h"
+
+namespace em {
+
+namespace {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+
+EM_DEV uint4 ldg16(const void* p) { return *reinterpret_cast<const uint4*>(p); }
+
+EM_DEV uint32_t pack2(float a, float b) {
+    const f32x2 v = {a, b};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
+enum DpMode { DP_Y = 0, DP_DX = 1, DP_DW = 2, DP_DWG = 3 };       // DWG: dW with gathered x rows
+
+// What lanes without an element read: rows and columns past an operand's end.
+__device__ const uint4 dp_zero = {0u, 0u, 0u, 0u};
+
+// x row of y row r, -1 where row_src names none.
+EM_DEV int x_row(const DenseProduct& a, int r) {
+    if (!a.row_src) return r;
+    const int s = a.row_src[r];
+    return (unsigned)s < (unsigned)a.T ? s : -1;
+}
+
+// Four neighbouring columns of an out row.
+EM_DEV void store4(void* out, int f32, int64_t at, const floatx4& v) {
+    if (f32) *reinterpret_cast<floatx4*>(static_cast<float*>(out) + at) = v;
+    else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------ few rows -----
+// A workgroup takes one row tile (16 NS rows of one matrix) and 16 NC columns; its four
+// waves split K into contiguous quarters, WD steps of 32 ahead, and their partial sums
+// are added through LDS in wave order.
+template <int NS, int NC>
+__global__ void __launch_bounds__(256)
+dp_stream(DenseProduct a) {
+    constexpr int WD = NS == 4 ? 4 : 8, XD = NS == 4 ? 1 : 2;
+    __shared__ __attribute__((aligned(16))) float red[4][NS * NC][256];
+    const RowTile t = row_tile<16 * NS>(a.offsets, a.M, a.R, [](int) { return (int)blockIdx.y; });
+    if (t.r1 == 0) return;
+    const int lane = lane_id(), wv = wave_id(), g = lane >> 4, m = lane & 15;
+    const int n0 = blockIdx.x * (16 * NC);
+    const int steps = a.K / 32, rest = a.K % 32;
+    const int s0 = steps * wv / 4, s1 = steps * (wv + 1) / 4;
+
+    const uint16_t* wp[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) wp[c] = a.w + ((int64_t)t.m * a.N + min(n0 + 16 * c + m, a.N - 1)) * a.K + 8 * g;
+    uint4 w[WD][NC], x[XD][NS];
+    auto load_w = [&](int d, int st) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) w[d][c] = ldg16(wp[c] + 32 * st);
+    };
+    if (s0 < s1) {
+#pragma unroll
+        for (int d = 0; d < WD; ++d) load_w(d, min(s0 + d, s1 - 1));
+    }
+    bool live[NS];
+    const uint16_t* xp[NS];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+        const int r = t.r0 + 16 * s + m, src = x_row(a, min(r, t.r1 - 1));
+        live[s] = src >= 0;
+        xp[s] = a.x + (int64_t)max(src, 0) * a.x_stride + 8 * g;
+    }
+    auto load_x = [&](int d, int st) {
+#pragma unroll
+        for (int s = 0; s < NS; ++s) x[d][s] = ldg16(xp[s] + 32 * st);
+    };
+    floatx4 acc[NS][NC];
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) acc[s][c] = zero4();
+    if (s0 < s1) {
+#pragma unroll
+        for (int d = 0; d < XD; ++d) load_x(d, min(s0 + d, s1 - 1));
+    }
+    auto run = [&](int st, auto more) {                       // WD steps, without a branch but for the last ones
+        constexpr bool MORE = decltype(more)::value;
+#pragma unroll
+        for (int d = 0; d < WD; ++d) {
+            if (MORE || st + d < s1) {
+#pragma unroll
+                for (int s = 0; s < NS; ++s)
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) acc[s][c] = mfma_bf16(w[d][c], x[d % XD][s], acc[s][c]);
+                load_x(d % XD, min(st + d + XD, s1 - 1));
+                if constexpr (MORE) load_w(d, min(st + d + WD, s1 - 1));
+            }
+        }
+    };
+    int st = s0;
+    for (; st + WD < s1; st += WD) run(st, std::true_type{});
+    if (st < s1) run(st, std::false_type{});
+    if (rest && wv == 3) {                                    // the last 8, 16 or 24 of K: zeros past them on both sides
+        const bool in = 8 * g < rest;
+        const int off = in ? 32 * steps : -8 * g;             // else the row's first elements, not used
+        uint4 xr[NS];
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            const uint4 v = ldg16(xp[s] + off);
+            xr[s] = in ? v : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const uint4 v = ldg16(wp[c] + off);
+            const uint4 wr = in ? v : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int s = 0; s < NS; ++s) acc[s][c] = mfma_bf16(wr, xr[s], acc[s][c]);
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) *reinterpret_cast<floatx4*>(&red[wv][s * NC + c][4 * lane]) = acc[s][c];
+    __syncthreads();
+    // tile i = (subtile s, column tile c) is summed by wave i % 4
+#pragma unroll
+    for (int i = 0; i < NS * NC; ++i) {
+        if ((i & 3) != wv) continue;
+        floatx4 v = *reinterpret_cast<const floatx4*>(&red[0][i][4 * lane]);
+#pragma unroll
+        for (int q = 1; q < 4; ++q) v += *reinterpret_cast<const floatx4*>(&red[q][i][4 * lane]);
+        const int s = i / NC, r = t.r0 + 16 * s + m, n = n0 + 16 * (i % NC) + 4 * g;
+        if (r < t.r1 && n < a.N) store4(a.out, a.out_f32, (int64_t)r * a.out_stride + n, live[s] ? v : zero4());
+    }
+}
+
+// ------------------------------------------------------------------ LDS tiles ----
+// A workgroup takes BT i x BN j of out in WT x WN waves.  Each step of 32 c arrives by
+// direct global -> LDS loads, three steps ahead in four stages; every wave issues the
+// same number of loads a step, so that one counted wait covers them.  Lanes without an
+// element (past the rows, columns or c of an operand, or a row that row_src does not
+// name) load zeros from dp_zero, so that nothing outside an operand meets a product.
+//
+// An operand with c along its rows: 64-byte rows of 32 c, 16-byte segments XOR-swizzled
+// by the row (mx_product.hip's rule).  One with c down the rows: 32 rows of BX elements,
+// segments swizzled in pairs by the row, so that the four rows that sixteen lanes read
+// together fall on different banks.
+namespace {
+
+template <int MODE, int BT_, int BN_>
+struct DpCfg {
+    static constexpr bool JT = MODE != DP_Y, IT = MODE >= DP_DW;      // c runs down the rows of Q, of P
+    static constexpr bool GATHER = MODE == DP_DWG;
+    static constexpr int BT = BT_, BN = BN_;
+    static constexpr int NW = BN == 256 || (BN == 128 && BT == 256) ? 8 : 4;
+    static constexpr int WN = BN == 256 ? (BT == 256 ? 2 : 4) : BN == 128 ? 2 : (BT == 256 ? 1 : 2), WT = NW / WN;
+    static constexpr int NI = BN / WN / 16, NJ = BT / WT / 16;        // j and i subtiles of a wave
+    static constexpr int J_B = BN * 64, I_B = BT * 64, STAGE = J_B + I_B, STAGES = 4;
+    static constexpr int J_P = J_B / 1024, P = STAGE / 1024;          // wave loads of Q, of a stage
+    static constexpr int LOADS = (P + NW - 1) / NW;
+    static constexpr int OUT_B = 16 * (NI * 64 + 16);                 // a wave's sixteen out rows on their way out
+    static constexpr int IDX_B = GATHER ? NW * 8 * 256 : 0;           // x rows of the next steps, eight slots a wave
+    static constexpr int LDS_B = (STAGES * STAGE > NW * OUT_B ? STAGES * STAGE : NW * OUT_B) + IDX_B;
+    static constexpr int VM = LOADS + (GATHER ? 1 : 0);               // vector-memory instructions a step
+};
+
+template <int N>
+EM_DEV void wait_loads_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
+}
+
+template <int I> struct Set { static constexpr int value = I; };
+
+// Slot of 16-byte segment s: of row r of 64 bytes; of c row r of BX elements.
+EM_DEV int swz_row(int r, int s) { return s ^ (-(r >> 2) & 3); }
+template <int BX>
+EM_DEV int swz_col(int r, int s) { return s ^ 2 * ((r & 3) | (BX >= 128 ? (r >> 1) & 4 : 0)); }
+
+// One load of a stage: where a lane's 16 bytes come from.
+struct DpSrc {
+    const char* base;        // at step 0
+    int64_t adv;             // bytes a step
+    int lim;                 // first step without an element
+};
+
+}  // namespace
+
+template <int MODE, int BT, int BN>
+__global__ void __launch_bounds__((DpCfg<MODE, BT, BN>::NW * 64))
+dp_tile(DenseProduct a) {
+    using C = DpCfg<MODE, BT, BN>;
+    constexpr int NI = C::NI, NJ = C::NJ;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[C::LDS_B];
+    const int lane = lane_id(), wv = wave_id(), g = lane >> 4, m = lane & 15;
+
+    // ---- the tile: i0 .. i1 of P's rows, j0 of Q's, steps s0 .. s1 of c; XCD x = blockIdx % 8
+    // takes neighbouring tiles
+    const int J = MODE == DP_Y ? a.N : a.K, nn = (J + BN - 1) / BN;
+    int mat, i0, i1, j0, z = 0, c0 = 0, clen;
+    if constexpr (MODE >= DP_DW) {
+        const int ni = (a.N + BT - 1) / BT, each = a.M * ni * nn, total = each * a.slices, per = (total + 7) >> 3;
+        const int at = blockIdx.x >> 3, b = (blockIdx.x & 7) * per + at;
+        if (at >= per || b >= total) return;
+        z = b / each;
+        const int in = b - z * each;
+        mat = in / (ni * nn);
+        const int tile = in - mat * (ni * nn);
+        i0 = tile / nn * BT;
+        i1 = min(a.N, i0 + BT);
+        j0 = tile % nn * BN;
+        c0 = a.offsets ? min(max(a.offsets[mat], 0), a.R) : 0;
+        clen = (a.offsets ? min(max(a.offsets[mat + 1], c0), a.R) : a.R) - c0;
+    } else {
+        int tn = 0;
+        const RowTile t = row_tile<BT>(a.offsets, a.M, a.R, [&](int rows) {
+            rows = min(rows, a.row_tiles);                       // more only where offsets descend
+            const int each = rows * nn, total = each * a.slices, per = (total + 7) >> 3, at = blockIdx.x >> 3;
+            int b = (blockIdx.x & 7) * per + at;
+            if (at >= per || b >= total) return -1;
+            z = b / each;
+            b -= z * each;
+            const int grp = b / (8 * nn), left = min(8, rows - 8 * grp), in = b - grp * 8 * nn;
+            tn = in / left;
+            return 8 * grp + in % left;
+        });
+        if (t.r1 == 0) return;
+        mat = t.m;
+        i0 = t.r0;
+        i1 = t.r1;
+        j0 = tn * BN;
+        clen = MODE == DP_Y ? a.K : a.N;
+    }
+    const int steps = (clen + 31) >> 5;
+    const int s0 = (int)((int64_t)steps * z / a.slices), s1 = (int)((int64_t)steps * (z + 1) / a.slices);
+
+    // ---- load sources
+    DpSrc src[C::LOADS];
+    int idx_at[C::LOADS];                                         // (GATHER) the load's row in a step's x rows, -1: dy
+#pragma unroll
+    for (int u = 0; u < C::LOADS; ++u) {
+        const int piece = (C::LOADS * wv + u) % C::P;
+        const bool isj = piece < C::J_P;
+        DpSrc o;
+        idx_at[u] = -1;
+        if (isj ? C::JT : C::IT) {                                // c down the rows
+            const int bx = isj ? BN : BT, row = (isj ? piece : piece - C::J_P) * (512 / bx) + lane / (bx / 8);
+            const int slot = lane % (bx / 8);
+            const int col = (isj ? j0 : i0) + 8 * (isj ? swz_col<BN>(row, slot) : swz_col<BT>(row, slot));
+            const int cols = isj ? a.K : a.N;                     // of x and W; of dy
+            const int64_t stride = isj ? (MODE == DP_DX ? (int64_t)a.K : a.x_stride) : a.dy_stride;
+            const uint16_t* p = isj ? (MODE == DP_DX ? a.w + (int64_t)mat * a.N * a.K : a.x) : a.dy;
+            const int64_t first = isj && C::GATHER ? 0 : (int64_t)(c0 + row) * stride;
+            o.base = reinterpret_cast<const char*>(p + first + min(col, cols - 8));
+            o.adv = 64 * stride;
+            o.lim = col < cols ? (clen - row + 31) >> 5 : 0;
+            if (isj && C::GATHER) {
+                idx_at[u] = row;
+                o.adv = 2 * stride;                               // times the x row
+            }
+        } else {                                                  // c along the rows
+            const int row = (isj ? piece : piece - C::J_P) * 16 + lane / 4, seg = swz_row(row, lane % 4);
+            const uint16_t* p;
+            bool in = true;
+            if (isj) {                                            // W of y
+                in = j0 + row < a.N;
+                p = a.w + ((int64_t)mat * a.N + min(j0 + row, a.N - 1)) * a.K;
+            } else if (MODE == DP_Y) {
+                const int s = x_row(a, min(i0 + row, i1 - 1));
+                in = s >= 0;
+                p = a.x + (int64_t)max(s, 0) * a.x_stride;
+            } else {
+                p = a.dy + (int64_t)min(i0 + row, i1 - 1) * a.dy_stride;
+            }
+            o.base = reinterpret_cast<const char*>(p + 8 * seg);
+            o.adv = 64;
+            o.lim = in ? (clen - 8 * seg + 31) >> 5 : 0;
+        }
+        src[u] = o;
+    }
+    const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+    const int* ring = reinterpret_cast<const int*>(lds + C::LDS_B - C::IDX_B) + wv * (8 * 64);
+    const char* zero = reinterpret_cast<const char*>(&dp_zero);
+    auto fetch_rows = [&](int st) {                               // (GATHER) the x rows of step st
+        const int r = min(c0 + 32 * st + (lane & 31), c0 + clen - 1);
+        lds_load4(a.row_src, 4u * (uint32_t)r,
+                  __builtin_amdgcn_readfirstlane(base + C::LDS_B - C::IDX_B + wv * 2048 + (st & 7) * 256));
+    };
+    auto fetch = [&](int st, int u) {
+        const int piece = (C::LOADS * wv + u) % C::P;
+        const uint32_t dst = __builtin_amdgcn_readfirstlane(base + (st & 3) * C::STAGE + 1024 * piece);
+        const char* p;
+        if (C::GATHER && piece < C::J_P) {
+            const int s = ring[(st & 7) * 64 + idx_at[u]];
+            p = st < src[u].lim && (unsigned)s < (unsigned)a.T ? src[u].base + s * src[u].adv : zero;
+        } else {
+            p = st < src[u].lim ? src[u].base + st * src[u].adv : zero;
+        }
+        lds_load16(p, dst);
+    };
+
+    const int wn = wv / C::WT, wt = wv % C::WT;
+    floatx4 acc[NI][NJ];
+#pragma unroll
+    for (int p = 0; p < NI; ++p)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[p][j] = zero4();
+
+    // ---- operand reads.  Transposed: lanes 4 q .. 4 q + 3 of sixteen read 16 columns of c
+    // row q, and lane m gets column m's four c; two reads make the eight c of its slot.
+    const int row_at = m * 64 + 16 * swz_row(m, g);               // (16 rows on, the swizzle is the same)
+    auto read_t = [&](const uint8_t* tile, int sub, auto bx) {
+        constexpr int BX = decltype(bx)::value;
+        uint4 o;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = 8 * g + 4 * h + (m >> 2);
+            const uint8_t* p = tile + k * (2 * BX) + 16 * swz_col<BX>(k, 2 * sub + ((m >> 1) & 1)) + 8 * (m & 1);
+            const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)p);
+            const uint2 w = __builtin_bit_cast(uint2, v);
+            if (h == 0) { o.x = w.x; o.y = w.y; }
+            else { o.z = w.x; o.w = w.y; }
+        }
+        return o;
+    };
+    auto read_j = [&](const uint8_t* stage, int p) {
+        if constexpr (C::JT) return read_t(stage, NI * wn + p, std::integral_constant<int, BN>{});
+        else return ldg16(stage + 16 * (NI * wn + p) * 64 + row_at);
+    };
+    auto read_i = [&](const uint8_t* stage, int j) {
+        if constexpr (C::IT) return read_t(stage + C::J_B, NJ * wt + j, std::integral_constant<int, BT>{});
+        else return ldg16(stage + C::J_B + 16 * (NJ * wt + j) * 64 + row_at);
+    };
+    uint4 fi[2][NJ], fj[2];
+    auto stage_of = [&](int st) -> const uint8_t* { return lds + (st & 3) * C::STAGE; };
+    // P's fragments are read a step ahead and Q's one subtile ahead, so that the matrix
+    // cores have operands from a step's first cycle.  A step's barrier says that the next
+    // step's stage has landed and that the one before is free.
+    auto step = [&](int st, auto set) {
+        constexpr int f = decltype(set)::value;
+        const uint8_t* X = stage_of(st);
+        const uint8_t* Xn = stage_of(st + 1);
+        wait_loads_barrier<C::VM>();
+        if constexpr (C::GATHER) fetch_rows(st + 5);
+#pragma unroll
+        for (int p = 0; p < NI; ++p) {
+            fj[(p + 1) & 1] = read_j(p + 1 < NI ? X : Xn, (p + 1) % NI);
+#pragma unroll
+            for (int u = p * NJ / NI; u < (p + 1) * NJ / NI; ++u) fi[1 - f][u] = read_i(Xn, u);
+#pragma unroll
+            for (int u = p * C::LOADS / NI; u < (p + 1) * C::LOADS / NI; ++u) fetch(st + 3, u);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) acc[p][j] = mfma_bf16(fj[p & 1], fi[f][j], acc[p][j]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    if (s0 < s1) {
+        if constexpr (C::GATHER) {
+#pragma unroll
+            for (int st = 0; st < 5; ++st) fetch_rows(s0 + st);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+#pragma unroll
+        for (int st = 0; st < 3; ++st) {
+#pragma unroll
+            for (int u = 0; u < C::LOADS; ++u) fetch(s0 + st, u);
+        }
+        wait_loads_barrier<C::GATHER ? C::LOADS : 2 * C::LOADS>();      // (a gathering step's own wait allows for its row load)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) fi[0][j] = read_i(stage_of(s0), j);
+        fj[0] = read_j(stage_of(s0), 0);
+        int st = s0;
+        for (; st + 1 < s1; st += 2) {
+            step(st, Set<0>{});
+            step(st + 1, Set<1>{});
+        }
+        if (st < s1) step(st, Set<0>{});
+        wait_loads_barrier<0>();                                  // nothing more lands in the stages
+    }
+
+    // ---- out, sixteen rows of a wave at a time through the LDS, so that whole row segments
+    // are stored: lane (g, m) holds columns 4 g .. 4 g + 3 of each j subtile, row m
+    const int rows = MODE >= DP_DW ? a.M * a.N : a.R;
+    const bool whole = a.slices == 1 && !a.to_part;
+    void* out = whole ? a.out : a.part + (int64_t)z * rows * J;
+    const int64_t stride = whole ? a.out_stride : J;
+    const int f32 = whole ? a.out_f32 : 1;
+    const int64_t r0 = (MODE >= DP_DW ? (int64_t)mat * a.N : 0) + i0 + 16 * NJ * wt;
+    const int left = i1 - i0 - 16 * NJ * wt, col0 = j0 + 16 * NI * wn;
+    constexpr int RS = NI * 64 + 16;
+    uint8_t* o = lds + wv * C::OUT_B;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+#pragma unroll
+        for (int p = 0; p < NI; ++p) *reinterpret_cast<floatx4*>(o + m * RS + 64 * p + 16 * g) = acc[p][j];
+        __builtin_amdgcn_wave_barrier();                          // one wave's LDS accesses complete in order
+        asm volatile("" ::: "memory");
+        if (f32) {
+            constexpr int LPR = NI * 4, RPI = 64 / LPR;
+#pragma unroll
+            for (int i = 0; i < 16 / RPI; ++i) {
+                const int tr = RPI * i + lane / LPR, col = col0 + 4 * (lane % LPR);
+                const floatx4 v = *reinterpret_cast<const floatx4*>(o + tr * RS + 16 * (lane % LPR));
+                if (16 * j + tr < left && col < J)
+                    *reinterpret_cast<floatx4*>(static_cast<float*>(out) + (r0 + 16 * j + tr) * stride + col) = v;
+            }
+        } else {
+            constexpr int LPR = NI * 2, RPI = 64 / LPR;
+#pragma unroll
+            for (int i = 0; i < (16 + RPI - 1) / RPI; ++i) {
+                const int tr = RPI * i + lane / LPR, col = col0 + 8 * (lane % LPR);
+                if (tr >= 16) continue;
+                const floatx4 u = *reinterpret_cast<const floatx4*>(o + tr * RS + 32 * (lane % LPR));
+                const floatx4 v = *reinterpret_cast<const floatx4*>(o + tr * RS + 32 * (lane % LPR) + 16);
+                if (16 * j + tr < left && col < J)
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + (r0 + 16 * j + tr) * stride + col) =
+                        make_uint4(pack2(u.x, u.y), pack2(u.z, u.w), pack2(v.x, v.y), pack2(v.z, v.w));
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+        asm volatile("" ::: "memory");
+    }
+}
+
+// ------------------------------------------------------------------ sums ---------
+// out[i] = the slices of row i, or of the rows of token i in slot order, added in
+// order.  Rows past the matrices' (which no tile has written) are left as they were, or
+// add nothing to a token.
+struct DpJoin {
+    const float* part;
+    int slices;
+    int64_t rows;                   // of a slice
+    int cols;
+    void* out;
+    int64_t out_stride;
+    int out_f32;
+    int64_t out_rows;
+    const int32_t* offsets; int M;  // rows offsets[0] .. offsets[M] - 1 are written; null: all
+    const int32_t* token_rows; int per_token;
+};
+
+__global__ void __launch_bounds__(256)
+dp_join(DpJoin a) {
+    const int quads = a.cols / 4;
+    const int64_t i = blockIdx.x * 256ll + threadIdx.x;
+    const int64_t row = i / quads;
+    const int col = (int)(i - row * quads) * 4;
+    if (row >= a.out_rows) return;
+    int64_t lo = 0, hi = a.rows;
+    if (a.offsets) {
+        lo = min(max((int64_t)a.offsets[0], (int64_t)0), a.rows);
+        hi = min(max((int64_t)a.offsets[a.M], lo), a.rows);
+    }
+    floatx4 s = zero4();
+    if (a.token_rows) {
+        for (int j = 0; j < a.per_token; ++j) {
+            const int64_t r = a.token_rows[row * a.per_token + j];
+            if (r < lo || r >= hi) continue;
+            for (int z = 0; z < a.slices; ++z) s += *reinterpret_cast<const floatx4*>(a.part + (z * a.rows + r) * a.cols + col);
+        }
+    } else {
+        if (row < lo || row >= hi) return;
+        for (int z = 0; z < a.slices; ++z) s += *reinterpret_cast<const floatx4*>(a.part + (z * a.rows + row) * a.cols + col);
+    }
+    store4(a.out, a.out_f32, row * a.out_stride + col, s);
+}
+
+// ------------------------------------------------------------------ host side ----
+namespace {
+
+// Row tiles of BT rows that R rows in M matrices can make at most.
+int64_t max_row_tiles(const DenseProduct& a, int BT) {
+    const int live = a.M < a.R ? a.M : a.R;
+    return a.M > 1 ? a.R / BT + live : (a.R + BT - 1) / BT;
+}
+
+struct DpPlan { int bt, bn, slices; };
+
+DpPlan plan(const DenseProduct& a, int mode) {
+    DpPlan p{};
+    const int J = mode == DP_Y ? a.N : a.K;
+    const int live = a.M < a.R ? a.M : (a.R ? a.R : 1);
+    const int64_t avg = mode == DP_DW ? a.N : ((int64_t)a.R + live - 1) / live;
+    p.bt = avg <= 64 ? 64 : avg <= 128 ? 128 : 256;
+    p.bn = J <= 64 ? 64 : J <= 128 ? 128 : 256;
+    const auto tiles = [&] {
+        const int64_t nn = (J + p.bn - 1) / p.bn;
+        return mode == DP_DW ? (int64_t)a.M * ((a.N + p.bt - 1) / p.bt) * nn : max_row_tiles(a, p.bt) * nn;
+    };
+    while (tiles() < 200 && p.bt > 64) p.bt /= 2;
+    const int64_t c = mode == DP_Y ? a.K : mode == DP_DX ? a.N : ((int64_t)a.R + live - 1) / live;
+    const int steps = (int)((c + 31) / 32);
+    p.slices = 1;
+    while (tiles() * p.slices * 2 <= 512 && p.slices < 16 && steps >= 16 * p.slices) p.slices *= 2;
+    return p;
+}
+
+template <int MODE, int BT, int BN>
+hipError_t launch_tile(const DenseProduct& a, int64_t blocks, hipStream_t s) {
+    prof_begin(s);
+    dp_tile<MODE, BT, BN><<<(unsigned)((blocks + 7) & ~7ll), DpCfg<MODE, BT, BN>::NW * 64, 0, s>>>(a);
+    prof_end(s, MODE == DP_Y ? "dp_tile_y" : MODE == DP_DX ? "dp_tile_dx" : "dp_tile_dw");
+    return hipGetLastError();
+}
+
+template <int MODE, int BT>
+hipError_t launch_tile(const DenseProduct& a, int bn, int64_t blocks, hipStream_t s) {
+    switch (bn) {
+        case 64: return launch_tile<MODE, BT, 64>(a, blocks, s);
+        case 128: return launch_tile<MODE, BT, 128>(a, blocks, s);
+        default: return launch_tile<MODE, BT, 256>(a, blocks, s);
+    }
+}
+
+template <int MODE>
+hipError_t launch_tile(DenseProduct a, const DpPlan& p, hipStream_t s) {
+    const int J = MODE == DP_Y ? a.N : a.K, nn = (J + p.bn - 1) / p.bn;
+    a.slices = p.slices;
+    a.row_tiles = (int)max_row_tiles(a, p.bt);
+    const int64_t rows = MODE >= DP_DW ? (int64_t)a.M * ((a.N + p.bt - 1) / p.bt) : a.row_tiles;
+    const int64_t blocks = rows * nn * p.slices;
+    switch (p.bt) {
+        case 64: return launch_tile<MODE, 64>(a, p.bn, blocks, s);
+        case 128: return launch_tile<MODE, 128>(a, p.bn, blocks, s);
+        default: return launch_tile<MODE, 256>(a, p.bn, blocks, s);
+    }
+}
+
+hipError_t launch_join(const DpJoin& j, hipStream_t s) {
+    const int64_t n = j.out_rows * (j.cols / 4);
+    if (!n) return hipSuccess;
+    prof_begin(s);
+    dp_join<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(j);
+    prof_end(s, "dp_join");
+    return hipGetLastError();
+}
+
+// How many times 16 rows of a matrix dp_stream takes at once (0: not dp_stream).
+int stream_rows(const DenseProduct& a) {
+    const int live = a.M < a.R ? a.M : a.R;
+    const int64_t avg = ((int64_t)a.R + live - 1) / live, cols = (a.N + 31) / 32;
+    for (int ns = 1; ns <= 4; ns *= 2)
+        if (max_row_tiles(a, 16 * ns) * cols <= 256 || avg <= 16 * ns) return ns;
+    return 0;
+}
+
+template <int NS>
+hipError_t launch_stream(const DenseProduct& a, hipStream_t s) {
+    const int64_t tiles = max_row_tiles(a, 16 * NS);
+    prof_begin(s);
+    if (NS == 1 && tiles * ((a.N + 31) / 32) <= 128) dp_stream<NS, 1><<<dim3((a.N + 15) / 16, (unsigned)tiles), 256, 0, s>>>(a);
+    else dp_stream<NS, 2><<<dim3((a.N + 31) / 32, (unsigned)tiles), 256, 0, s>>>(a);
+    prof_end(s, "dp_stream");
+    return hipGetLastError();
+}
+
+size_t up(size_t v) { return (v + 255) & ~(size_t)255; }
+
+size_t part_bytes(const DenseProduct& a, int mode, int slices) {
+    return up((size_t)slices * (mode == DP_DW ? (size_t)a.M * a.N * a.K : (size_t)a.R * (mode == DP_Y ? a.N : a.K)) * 4);
+}
+
+}  // namespace
+
+size_t dense_product_ws_bytes(const DenseProduct& a) {
+    if (!a.R || stream_rows(a)) return 256;
+    const DpPlan p = plan(a, DP_Y);
+    return p.slices > 1 ? part_bytes(a, DP_Y, p.slices) : 256;
+}
+
+hipError_t launch_dense_product(DenseProduct a, void* ws, hipStream_t s) {
+    switch (stream_rows(a)) {
+        case 1: return launch_stream<1>(a, s);
+        case 2: return launch_stream<2>(a, s);
+        case 4: return launch_stream<4>(a, s);
+        default: break;
+    }
+    const DpPlan p = plan(a, DP_Y);
+    a.part = static_cast<float*>(ws);
+    const hipError_t e = launch_tile<DP_Y>(a, p, s);
+    if (e != hipSuccess || p.slices == 1) return e;
+    return launch_join(DpJoin{a.part, p.slices, a.R, a.N, a.out, a.out_stride, a.out_f32, a.R, a.offsets, a.M, nullptr, 0}, s);
+}
+
+// dx's partial sums (or rows, for tokens) and dW's share the workspace: dW runs first.
+size_t dense_backward_ws_bytes(const DenseProduct& a) {
+    const DpPlan pw = plan(a, DP_DW);
+    const size_t w = pw.slices > 1 ? part_bytes(a, DP_DW, pw.slices) : 256;
+    if (!a.R) return w;
+    const size_t x = part_bytes(a, DP_DX, plan(a, DP_DX).slices);
+    return w > x ? w : x;
+}
+
+hipError_t launch_dense_backward(const DenseGrad& gr, void* ws, hipStream_t s) {
+    DenseProduct a = gr.p;
+    a.part = static_cast<float*>(ws);
+    if (gr.dw) {
+        const DpPlan p = plan(a, DP_DW);
+        a.out = gr.dw; a.out_stride = a.K; a.out_f32 = gr.dw_f32;
+        hipError_t e = a.row_src ? launch_tile<DP_DWG>(a, p, s) : launch_tile<DP_DW>(a, p, s);
+        if (e == hipSuccess && p.slices > 1) {
+            const int64_t rows = (int64_t)a.M * a.N;
+            e = launch_join(DpJoin{a.part, p.slices, rows, a.K, gr.dw, a.K, gr.dw_f32, rows, nullptr, 0, nullptr, 0}, s);
+        }
+        if (e != hipSuccess) return e;
+    }
+    if (!gr.dx) return hipSuccess;
+    const DpPlan p = plan(a, DP_DX);
+    a.out = gr.dx; a.out_stride = gr.dx_stride; a.out_f32 = gr.dx_f32;
+    a.to_part = gr.token_rows != nullptr;
+    if (a.R) {
+        const hipError_t e = launch_tile<DP_DX>(a, p, s);
+        if (e != hipSuccess) return e;
+    }
+    if (p.slices == 1 && !a.to_part) return hipSuccess;
+    return launch_join(DpJoin{a.part, p.slices, a.R, a.K, gr.dx, gr.dx_stride, gr.dx_f32, a.to_part ? a.T : a.R, a.offsets, a.M,
+                              gr.token_rows, gr.per_token}, s);
+}
+
+}  // namespace em

@@ -1,0 +1,434 @@
+// Root-mean-square norm between layers, forward and backward.
+//
+//   forward   r = bf16(x + add);  rstd = 1 / sqrt(mean r^2 + eps)
+//             y = bf16(r rstd gain);  codes, scales = MXFP8 of y (mx_quant.hip's rule)
+//   backward  v = r rstd, dv = dy gain:  dr = rstd (dv - v mean(dv v))
+//             dx = dres + dr,  dgain = sum_t dy v
+//
+// Each row is read once, kept in registers over the reduction and written once, so
+// both directions are bound by HBM.  W waves share a row, each lane NV runs of eight
+// neighbours; an MX block is then four neighbouring lanes.  A workgroup takes a run
+// of neighbouring rows and asks for the next row before it reduces the present one;
+// the gain stays in registers.  The squares are summed in float64: no bf16 row
+// overflows there, and the sum's order does not show.
+#include <type_traits>
+
+#include "mx_format.h"
+#include "operators.h"
+
+namespace em {
+
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+EM_DEV uint4 ldv(const void* p) { return *reinterpret_cast<const uint4*>(p); }
+
+// Eight neighbouring elements as loaded: bf16 in one word, float32 in two.
+template <bool F32> struct Raw8 { uint4 v[F32 ? 2 : 1]; };
+
+template <bool F32>
+EM_DEV void load8(Raw8<F32>& o, const void* row, int e) {
+    if constexpr (F32) {
+        const float* p = static_cast<const float*>(row) + e;
+        o.v[0] = ldv(p);
+        o.v[1] = ldv(p + 4);
+    } else {
+        o.v[0] = ldv(static_cast<const uint16_t*>(row) + e);
+    }
+}
+
+template <bool F32>
+EM_DEV void widen8(const Raw8<F32>& r, float (&f)[8]) {
+    if constexpr (F32) {
+        f[0] = __uint_as_float(r.v[0].x); f[1] = __uint_as_float(r.v[0].y);
+        f[2] = __uint_as_float(r.v[0].z); f[3] = __uint_as_float(r.v[0].w);
+        f[4] = __uint_as_float(r.v[1].x); f[5] = __uint_as_float(r.v[1].y);
+        f[6] = __uint_as_float(r.v[1].z); f[7] = __uint_as_float(r.v[1].w);
+    } else {
+        const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+}
+
+// Eight elements of a gain of either type.
+EM_DEV void load_gain(float (&f)[8], const void* gain, int f32, int e) {
+    if (f32) {
+        Raw8<true> r;
+        load8(r, gain, e);
+        widen8(r, f);
+    } else {
+        Raw8<false> r;
+        load8(r, gain, e);
+        widen8(r, f);
+    }
+}
+
+EM_DEV uint32_t pack2(float a, float b) {
+    const f32x2 v = {a, b};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+EM_DEV uint4 pack8(const float (&f)[8]) {
+    return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+}
+
+// x + a on its way to bf16: the float32 sum, moved one unit towards the exact one
+// where it lies on the middle of two bf16 values, so that rounding it gives the
+// exact sum's bf16 (edge_moe_residual's).
+EM_DEV float sum_for_bf16(float x, float a) {
+    const float s = x + a;
+    const float xs = s - a, as = s - xs;
+    const float lost = (x - xs) + (a - as);                 // s + lost = x + a exactly
+    int32_t b = __float_as_int(s);
+    if ((b & 0xFFFF) == 0x8000 && lost != 0.f) b += (lost > 0.f) == (s > 0.f) ? 1 : -1;
+    return __int_as_float(b);
+}
+
+template <int CTRL, int ROWS>
+EM_DEV double dpp_add_f64(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xF, false);
+    return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Sum over the wave's lanes, the same in every lane (a fixed order).
+EM_DEV double wave_sum_f64(double v) {
+    v = dpp_add_f64<0x111, 0xF>(v);       // row_shr:1, 2, 4, 8, then row_bcast:15 and :31
+    v = dpp_add_f64<0x112, 0xF>(v);
+    v = dpp_add_f64<0x114, 0xF>(v);
+    v = dpp_add_f64<0x118, 0xF>(v);
+    v = dpp_add_f64<0x142, 0xA>(v);
+    v = dpp_add_f64<0x143, 0xC>(v);
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// Sum over the row's W waves; `turn` alternates, so that one barrier a row is enough.
+template <int W>
+EM_DEV double row_sum(double v, double (&slots)[2][W], int turn) {
+    v = wave_sum_f64(v);
+    if constexpr (W == 1) return v;
+    const int wv = wave_id();
+    if (lane_id() == 0) slots[turn][wv] = v;
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) s += slots[turn][i];
+    return s;
+}
+
+// 1 / sqrt(m) in float64: the hardware's estimate and two steps towards the root.
+EM_DEV double rsqrt_f64(double m) {
+    double r = __builtin_amdgcn_rsq(m);
+    r = r * fma(-0.5 * m * r, r, 1.5);
+    return r * fma(-0.5 * m * r, r, 1.5);
+}
+
+// Rows of a workgroup: W > 1 one at a time, W = 1 one a wave.
+template <int W> constexpr int rows_at_once() { return W == 1 ? 4 : 1; }
+template <int W> constexpr int norm_threads() { return W == 1 ? 256 : 64 * W; }
+
+}  // namespace
+
+// ADD: nothing, bf16 or float32 to add (0, 1, 2).
+template <int W, int NV, int ADD>
+__global__ void __launch_bounds__(norm_threads<W>())
+norm_forward(NormFwd a) {
+    __shared__ double slots[2][W];
+    const int in_row = W == 1 ? lane_id() : (int)threadIdx.x;
+    const int first = blockIdx.x * a.chunk + (W == 1 ? wave_id() : 0);
+    const int last = min(a.T, (int)(blockIdx.x + 1) * a.chunk);
+    constexpr int STEP = rows_at_once<W>();
+    if (first >= last) return;                                 // W = 1 only: a wave without rows (no barrier there)
+    bool live[NV];
+    int at[NV];                                                // lanes past the row read its first elements again
+    float gain[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = 8 * (in_row + 64 * W * i);
+        live[i] = e < a.d;
+        at[i] = live[i] ? e : 0;
+        load_gain(gain[i], a.gain, a.gain_f32, at[i]);
+    }
+    Raw8<false> xr[NV];
+    Raw8<ADD == 2> ar[NV];
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            load8(xr[i], a.x + t * a.x_stride, at[i]);
+            if constexpr (ADD == 2) load8(ar[i], static_cast<const float*>(a.add) + t * a.add_stride, at[i]);
+            if constexpr (ADD == 1) load8(ar[i], static_cast<const uint16_t*>(a.add) + t * a.add_stride, at[i]);
+        }
+    };
+    fetch(first);
+    int turn = 0;
+    for (int t = first; t < last; t += STEP) {
+        uint4 r[NV];                                           // the row in bf16
+        double sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float f[8];
+            widen8(xr[i], f);
+            if constexpr (ADD != 0) {
+                float g[8];
+                widen8(ar[i], g);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = sum_for_bf16(f[j], g[j]);
+                r[i] = pack8(f);
+                Raw8<false> back;
+                back.v[0] = r[i];
+                widen8(back, f);
+            } else {
+                r[i] = xr[i].v[0];
+            }
+            double s = 0.0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s = fma((double)f[j], (double)f[j], s);
+            sum += live[i] ? s : 0.0;
+        }
+        if (t + STEP < last) fetch(t + STEP);
+        sum = row_sum<W>(sum, slots, turn);
+        turn ^= 1;
+        const float rstd = (float)rsqrt_f64(sum * a.per_d + (double)a.eps);
+        if (a.rstd && in_row == 0) a.rstd[t] = rstd;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (a.x_out && live[i]) *reinterpret_cast<uint4*>(a.x_out + t * a.xo_stride + at[i]) = r[i];
+            if (!a.y && !a.codes) continue;
+            float f[8];
+            Raw8<false> rr;
+            rr.v[0] = r[i];
+            widen8(rr, f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * gain[i][j];
+            const uint4 y = pack8(f);
+            if (a.y && live[i]) *reinterpret_cast<uint4*>(a.y + t * a.y_stride + at[i]) = y;
+            if (a.codes) {                                     // d a multiple of 128: a block's four lanes are live together
+                uint32_t m = amax8_bf16(y);
+                m = max(m, (uint32_t)__builtin_amdgcn_update_dpp((int)m, (int)m, 0xB1, 0xF, 0xF, false));
+                m = max(m, (uint32_t)__builtin_amdgcn_update_dpp((int)m, (int)m, 0x4E, 0xF, 0xF, false));
+                const int X = e8m0_of<kMxFp8>(m);
+                const bool bad = X == 255;
+                const float sc = e8m0_f32(bad ? 127 : X);
+                const uint32_t lim = e4m3_limit(bad ? 127 : X);
+                const uint32_t q0 = fp8x4_bf16(y.x, y.y, sc, lim), q1 = fp8x4_bf16(y.z, y.w, sc, lim);
+                if (live[i]) {
+                    *reinterpret_cast<uint2*>(a.codes + (int64_t)t * a.d + at[i]) = bad ? make_uint2(0u, 0u) : make_uint2(q0, q1);
+                    if (!(lane_id() & 3)) a.scales[((int64_t)(at[i] >> 7) * a.T + t) * 4 + (at[i] >> 5 & 3)] = (uint8_t)X;
+                }
+            }
+        }
+    }
+}
+
+// F32: dy, dres and dx are float32 (else bf16).
+template <int W, int NV, bool F32>
+__global__ void __launch_bounds__(norm_threads<W>())
+norm_backward(NormBwd a) {
+    __shared__ double slots[2][W];
+    __shared__ __attribute__((aligned(16))) float part[W == 1 ? 4 : 1][W == 1 ? 512 * NV : 4];
+    const int in_row = W == 1 ? lane_id() : (int)threadIdx.x;
+    const int first = blockIdx.x * a.chunk + (W == 1 ? wave_id() : 0);
+    const int last = min(a.T, (int)(blockIdx.x + 1) * a.chunk);
+    constexpr int STEP = rows_at_once<W>();
+    using G = Raw8<F32>;
+    bool live[NV];
+    int at[NV];
+    float gain[NV][8], dg[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = 8 * (in_row + 64 * W * i);
+        live[i] = e < a.d;
+        at[i] = live[i] ? e : 0;
+        load_gain(gain[i], a.gain, a.gain_f32, at[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dg[i][j] = 0.f;
+    }
+    constexpr int64_t ES = F32 ? 4 : 2;
+    Raw8<false> xr[NV];
+    G yr[NV], rr[NV];
+    float rs = 0.f;
+    auto fetch = [&](int t) {
+        rs = a.rstd[t];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            load8(xr[i], a.x + t * a.x_stride, at[i]);
+            load8(yr[i], static_cast<const char*>(a.dy) + t * a.dy_stride * ES, at[i]);
+            if (a.dres) load8(rr[i], static_cast<const char*>(a.dres) + t * a.dres_stride * ES, at[i]);
+        }
+    };
+    if (first < last) fetch(first);
+    int turn = 0;
+    for (int t = first; t < last; t += STEP) {
+        const float rstd = rs;
+        float v[NV][8], dv[NV][8], res[NV][8];
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            widen8(xr[i], v[i]);
+            widen8(yr[i], dv[i]);
+            if (a.dres) widen8(rr[i], res[i]);
+            float s = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[i][j] *= rstd;
+                dg[i][j] = fmaf(dv[i][j], v[i][j], dg[i][j]);
+                dv[i][j] *= gain[i][j];
+                s = fmaf(dv[i][j], v[i][j], s);
+            }
+            sum += live[i] ? s : 0.f;
+        }
+        if (t + STEP < last) fetch(t + STEP);
+        if (a.dx) {
+            const float mean = (float)(row_sum<W>((double)sum, slots, turn) * a.per_d);
+            turn ^= 1;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float dr = rstd * fmaf(-v[i][j], mean, dv[i][j]);
+                    dv[i][j] = a.dres ? res[i][j] + dr : dr;
+                }
+                if (!live[i]) continue;
+                char* o = static_cast<char*>(a.dx) + (t * a.dx_stride + at[i]) * ES;
+                if constexpr (F32) {
+                    *reinterpret_cast<float4*>(o) = make_float4(dv[i][0], dv[i][1], dv[i][2], dv[i][3]);
+                    *reinterpret_cast<float4*>(o + 16) = make_float4(dv[i][4], dv[i][5], dv[i][6], dv[i][7]);
+                } else {
+                    *reinterpret_cast<uint4*>(o) = pack8(dv[i]);
+                }
+            }
+        }
+    }
+    if (!a.part) return;
+    float* out = a.part + (int64_t)blockIdx.x * a.d;
+    if constexpr (W == 1) {                                    // the four waves' rows, added in wave order
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; j += 4)
+                *reinterpret_cast<float4*>(&part[wave_id()][8 * (in_row + 64 * i) + j]) =
+                    make_float4(dg[i][j], dg[i][j + 1], dg[i][j + 2], dg[i][j + 3]);
+        __syncthreads();
+        for (int e = threadIdx.x; e < a.d; e += 256) out[e] = (part[0][e] + part[1][e]) + (part[2][e] + part[3][e]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!live[i]) continue;
+            *reinterpret_cast<float4*>(out + at[i]) = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
+            *reinterpret_cast<float4*>(out + at[i] + 4) = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
+        }
+    }
+}
+
+// dgain from the workgroups' partial sums: 16 rows of 64 threads over interleaved
+// workgroups in float64, then the rows in order.
+__global__ void __launch_bounds__(1024)
+norm_dgain(const float* __restrict__ part, int blocks, int d, float* __restrict__ dgain) {
+    __shared__ double sp[16][64];
+    const int col = threadIdx.x & 63, row = threadIdx.x >> 6, e = blockIdx.x * 64 + col;
+    double s = 0.0;
+    if (e < d) {
+#pragma unroll 8
+        for (int b = row; b < blocks; b += 16) s += (double)part[(int64_t)b * d + e];
+    }
+    sp[row][col] = s;
+    __syncthreads();
+    if (row || e >= d) return;
+    for (int r = 1; r < 16; ++r) s += sp[r][col];
+    dgain[e] = (float)s;
+}
+
+// ------------------------------------------------------------------ host side ----
+namespace {
+
+struct NormPlan { int w, nv, chunk, blocks; };
+
+// Waves a row and runs of 512 elements a wave, and rows a workgroup.
+NormPlan norm_plan(int T, int d, int most_blocks) {
+    NormPlan p{};
+    const int runs = (d + 511) / 512;
+    p.nv = runs <= 1 ? 1 : runs <= 32 ? 2 : 4;
+    p.w = 1;
+    while (p.w * p.nv < runs) p.w *= 2;
+    const int at_once = p.w == 1 ? 4 : 1;
+    const int groups = (T + at_once - 1) / at_once;
+    const int most = p.w > 4 ? most_blocks * 4 / p.w : most_blocks;
+    p.chunk = (groups + most - 1) / most * at_once;
+    if (!T) return p;
+    p.blocks = (T + p.chunk - 1) / p.chunk;
+    return p;
+}
+
+constexpr int kFwdBlocks = 2048, kBwdBlocks = 1024;
+
+template <int W, int NV>
+void launch_fwd(const NormFwd& a, const NormPlan& p, hipStream_t s) {
+    if (!a.add) norm_forward<W, NV, 0><<<p.blocks, norm_threads<W>(), 0, s>>>(a);
+    else if (!a.add_f32) norm_forward<W, NV, 1><<<p.blocks, norm_threads<W>(), 0, s>>>(a);
+    else norm_forward<W, NV, 2><<<p.blocks, norm_threads<W>(), 0, s>>>(a);
+}
+
+template <int W, int NV>
+void launch_bwd(const NormBwd& a, const NormPlan& p, hipStream_t s) {
+    if (a.f32) norm_backward<W, NV, true><<<p.blocks, norm_threads<W>(), 0, s>>>(a);
+    else norm_backward<W, NV, false><<<p.blocks, norm_threads<W>(), 0, s>>>(a);
+}
+
+template <class F>
+void by_plan(const NormPlan& p, F launch) {
+    using std::integral_constant;
+    const integral_constant<int, 2> two{};
+    if (p.nv == 1) launch(integral_constant<int, 1>{}, integral_constant<int, 1>{});
+    else if (p.nv == 4) launch(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+    else if (p.w == 1) launch(integral_constant<int, 1>{}, two);
+    else if (p.w == 2) launch(two, two);
+    else if (p.w == 4) launch(integral_constant<int, 4>{}, two);
+    else if (p.w == 8) launch(integral_constant<int, 8>{}, two);
+    else launch(integral_constant<int, 16>{}, two);
+}
+
+}  // namespace
+
+hipError_t launch_norm_forward(NormFwd a, hipStream_t s) {
+    const NormPlan p = norm_plan(a.T, a.d, kFwdBlocks);
+    a.chunk = p.chunk;
+    a.per_d = 1.0 / a.d;
+    prof_begin(s);
+    by_plan(p, [&](auto w, auto nv) { launch_fwd<decltype(w)::value, decltype(nv)::value>(a, p, s); });
+    prof_end(s, "norm_forward");
+    return hipGetLastError();
+}
+
+size_t norm_backward_ws_bytes(int T, int d) {
+    const size_t n = (size_t)norm_plan(T, d, kBwdBlocks).blocks * d * 4;
+    return n > 256 ? n : 256;
+}
+
+hipError_t launch_norm_backward(NormBwd a, void* ws, hipStream_t s) {
+    const NormPlan p = norm_plan(a.T, a.d, kBwdBlocks);
+    a.chunk = p.chunk;
+    a.per_d = 1.0 / a.d;
+    a.part = a.dgain ? static_cast<float*>(ws) : nullptr;
+    if (p.blocks) {
+        prof_begin(s);
+        by_plan(p, [&](auto w, auto nv) { launch_bwd<decltype(w)::value, decltype(nv)::value>(a, p, s); });
+        prof_end(s, "norm_backward");
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (!a.dgain) return hipSuccess;
+    prof_begin(s);
+    norm_dgain<<<(a.d + 63) / 64, 1024, 0, s>>>(a.part, p.blocks, a.d, a.dgain);
+    prof_end(s, "norm_dgain");
+    return hipGetLastError();
+}
+
+}  // namespace em

@@ -86,4 +86,70 @@ struct RouterGrad {
 size_t router_grad_ws_bytes(RouterGrad a);
 hipError_t launch_router_grad(RouterGrad a, void* ws, hipStream_t s);
 
+// ---- norm (norm.hip)
+struct NormFwd {
+    int T, d;
+    float eps;
+    const uint16_t* x; int64_t x_stride;                 // strides in elements
+    const void* add; int64_t add_stride; int add_f32;    // null: nothing to add
+    const void* gain; int gain_f32;
+    uint16_t* x_out; int64_t xo_stride;                  // each output may be null
+    uint16_t* y; int64_t y_stride;
+    uint8_t* codes; uint8_t* scales;                     // [T][d] E4M3, [d/128][T][4] E8M0
+    float* rstd;
+    int chunk; double per_d;                             // rows a workgroup, 1 / d
+};
+hipError_t launch_norm_forward(NormFwd a, hipStream_t s);
+struct NormBwd {
+    int T, d;
+    const uint16_t* x; int64_t x_stride;
+    const void* gain; int gain_f32;
+    const float* rstd;
+    const void* dy; int64_t dy_stride;
+    const void* dres; int64_t dres_stride;               // null: nothing
+    void* dx; int64_t dx_stride;                         // null: not computed
+    float* dgain;                                        // null: not computed
+    int f32;                                             // dy, dres, dx
+    int chunk; double per_d;
+    float* part;                                         // workspace: [workgroups][d]
+};
+size_t norm_backward_ws_bytes(int T, int d);
+hipError_t launch_norm_backward(NormBwd a, void* ws, hipStream_t s);
+
+// ---- products with bf16 matrices and their gradients (dense_product.hip)
+struct DenseProduct {
+    int T, R, M, N, K;
+    const uint16_t* x; int64_t x_stride;
+    const int32_t* row_src;     // [R] x row of each y row, or null (row r reads x row r)
+    const int32_t* offsets;     // [M + 1] first y row of each matrix, or null (M = 1)
+    const uint16_t* w;          // [M][N][K]
+    const uint16_t* dy; int64_t dy_stride;
+    void* out; int64_t out_stride; int out_f32;
+    int slices, row_tiles, to_part;
+    float* part;                // workspace: [slices][rows][columns] of out
+};
+struct DenseGrad {
+    DenseProduct p;
+    void* dx; int64_t dx_stride; int dx_f32;
+    const int32_t* token_rows; int per_token;            // [T][per_token] rows of each token, or null: dx by rows
+    void* dw; int dw_f32;
+};
+size_t dense_product_ws_bytes(const DenseProduct& a);
+hipError_t launch_dense_product(DenseProduct a, void* ws, hipStream_t s);
+size_t dense_backward_ws_bytes(const DenseProduct& a);
+hipError_t launch_dense_backward(const DenseGrad& g, void* ws, hipStream_t s);
+
+// ---- product with int4 matrices (int4_product.hip)
+struct Int4Product {
+    int T, R, M, N, K, gq;      // gq: elements of a scale, at most K
+    const uint16_t* x; int64_t x_stride;
+    const int32_t* row_src;     // [R] x row of each y row, or null (row r reads x row r)
+    const int32_t* offsets;     // [M + 1] first y row of each matrix, or null (M = 1)
+    const uint8_t* codes;       // [M][N][K/2]
+    const uint16_t* scales;     // [M][N][K/gq] fp16
+    void* y; int64_t y_stride; int y_f32;
+};
+size_t int4_product_ws_bytes(const Int4Product& a);
+hipError_t launch_int4_product(Int4Product a, void* ws, hipStream_t s);
+
 }  // namespace em

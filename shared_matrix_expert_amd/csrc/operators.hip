@@ -1,5 +1,5 @@
-// C-ABI entry points of the MX-matrix and router-training operators: validation
-// and launches.
+// C-ABI entry points of the operators around the expert layer (MX matrices, router
+// training, norm, dense and int4 matrices): validation and launches.
 #include <hip/hip_runtime.h>
 
 #include "edge_moe.h"
@@ -61,6 +61,53 @@ em::RouterGrad grad_args(const edge_moe_dims& d) {
     em::RouterGrad a{};
     a.T = d.T; a.E = d.n_experts; a.k = d.top_k; a.d = d.d; a.S = 1;
     return a;
+}
+
+bool type_ok(int32_t t) { return t == EDGE_MOE_BF16 || t == EDGE_MOE_FLOAT; }
+int type_bytes(int32_t t) { return t == EDGE_MOE_FLOAT ? 4 : 2; }
+
+// Rows of `cols` elements at 16 bytes each, `stride` elements apart.
+bool rows_ok(const void* p, int64_t stride, int64_t cols, int elem) {
+    return aligned(p, 16) && stride >= cols && stride <= (1ll << 32) && stride * elem % 16 == 0;
+}
+
+int norm_shape_status(int32_t T, int32_t d) {
+    if (T < 0 || d < 8 || d % 8) return EDGE_MOE_EINVAL;
+    return T > (1 << 25) || d > 32768 ? EDGE_MOE_EUNSUPPORTED : EDGE_MOE_OK;
+}
+
+// Shape checks of the products with bf16 matrices: EDGE_MOE_*.
+int dense_status(const edge_moe_dense_dims* d) {
+    if (!d || d->T < 1 || d->R < 0 || d->M < 1 || d->N < 8 || d->K < 8 || d->N % 8 || d->K % 8) return EDGE_MOE_EINVAL;
+    if (d->T > (1 << 20) || d->R > (1 << 25) || d->M > 1024 || d->N > 32768 || d->K > 32768) return EDGE_MOE_EUNSUPPORTED;
+    return EDGE_MOE_OK;
+}
+
+em::DenseProduct dense_args(const edge_moe_dense_dims& d) {
+    em::DenseProduct a{};
+    a.T = d.T; a.R = d.R; a.M = d.M; a.N = d.N; a.K = d.K;
+    return a;
+}
+
+// Shape checks of the product with int4 matrices: EDGE_MOE_*.
+int int4_status(const edge_moe_packed_dims* d) {
+    if (!d || d->T < 1 || d->R < 0 || d->M < 1 || d->N < 1 || d->K < 32 || d->K % 32) return EDGE_MOE_EINVAL;
+    const int32_t q = d->quant_group;
+    if (q < 32 || q > 4096 || (q & (q - 1)) || (q < d->K && d->K % q)) return EDGE_MOE_EINVAL;
+    if (d->T > (1 << 20) || d->R > (1 << 25) || d->M > 1024 || d->N > 32768 || d->K > 32768) return EDGE_MOE_EUNSUPPORTED;
+    return EDGE_MOE_OK;
+}
+
+em::Int4Product int4_args(const edge_moe_packed_dims& d) {
+    em::Int4Product a{};
+    a.T = d.T; a.R = d.R; a.M = d.M; a.N = d.N; a.K = d.K; a.gq = d.quant_group < d.K ? d.quant_group : d.K;
+    return a;
+}
+
+// The batch's row lists: EDGE_MOE_*.
+int lists_status(const int32_t* row_src, const int32_t* offsets, int T, int R, int M) {
+    if ((row_src && !aligned(row_src, 4)) || (offsets && !aligned(offsets, 4))) return EDGE_MOE_EINVAL;
+    return (!offsets && M != 1) || (!row_src && R > T) ? EDGE_MOE_EINVAL : EDGE_MOE_OK;
 }
 
 int hip_status(hipError_t e) { return e == hipSuccess ? EDGE_MOE_OK : EDGE_MOE_EHIP; }
@@ -171,6 +218,131 @@ int edge_moe_route_backward(const edge_moe_dims* dims, const edge_moe_route_grad
     a.x = g->x; a.w_router = g->w_router;
     a.dlogits = g->dlogits; a.dx = g->dx; a.dw_router = g->dw_router; a.dbias = g->dbias;
     return hip_status(em::launch_router_grad(a, ws, (hipStream_t)stream));
+}
+
+int edge_moe_norm(const edge_moe_norm_args* g, void* stream) {
+    if (!g) return EDGE_MOE_EINVAL;
+    const int T = g->T, d = g->d;
+    int st = norm_shape_status(T, d);
+    if (st != EDGE_MOE_OK) return st;
+    if (!(g->eps > 0.f) || !(g->eps < 3.4e38f) || !type_ok(g->gain_type) || !aligned(g->gain, 16)) return EDGE_MOE_EINVAL;
+    if (!g->x_out && !g->y && !g->codes && !g->scales && !g->rstd && T > 0) return EDGE_MOE_EINVAL;
+    if (T > 0 && !rows_ok(g->x, g->x_stride, d, 2)) return EDGE_MOE_EINVAL;
+    if (g->add && (!type_ok(g->add_type) || !rows_ok(g->add, g->add_stride, d, type_bytes(g->add_type)))) return EDGE_MOE_EINVAL;
+    if ((g->x_out && !rows_ok(g->x_out, g->x_out_stride, d, 2)) || (g->y && !rows_ok(g->y, g->y_stride, d, 2)))
+        return EDGE_MOE_EINVAL;
+    if (!g->codes != !g->scales || (g->codes && (!aligned(g->codes, 16) || !aligned(g->scales, 4)))) return EDGE_MOE_EINVAL;
+    if (g->rstd && !aligned(g->rstd, 4)) return EDGE_MOE_EINVAL;
+    if (g->codes && d % 128) return EDGE_MOE_EUNSUPPORTED;
+    st = em::device_status();
+    if (st != EDGE_MOE_OK || T == 0) return st;
+    em::NormFwd a{};
+    a.T = T; a.d = d; a.eps = g->eps;
+    a.x = g->x; a.x_stride = g->x_stride;
+    a.add = g->add; a.add_stride = g->add_stride; a.add_f32 = g->add_type == EDGE_MOE_FLOAT;
+    a.gain = g->gain; a.gain_f32 = g->gain_type == EDGE_MOE_FLOAT;
+    a.x_out = g->x_out; a.xo_stride = g->x_out_stride; a.y = g->y; a.y_stride = g->y_stride;
+    a.codes = g->codes; a.scales = g->scales; a.rstd = g->rstd;
+    return hip_status(em::launch_norm_forward(a, (hipStream_t)stream));
+}
+
+size_t edge_moe_norm_backward_ws_bytes(int32_t T, int32_t d) {
+    return norm_shape_status(T, d) == EDGE_MOE_OK ? em::norm_backward_ws_bytes(T, d) : 0;
+}
+
+int edge_moe_norm_backward(const edge_moe_norm_grad* g, void* ws, size_t ws_bytes, void* stream) {
+    if (!g) return EDGE_MOE_EINVAL;
+    const int T = g->T, d = g->d;
+    int st = norm_shape_status(T, d);
+    if (st != EDGE_MOE_OK) return st;
+    if (!type_ok(g->gain_type) || !type_ok(g->grad_type) || !aligned(g->gain, 16)) return EDGE_MOE_EINVAL;
+    const int gb = type_bytes(g->grad_type);
+    if (T > 0 && (!aligned(g->rstd, 4) || !rows_ok(g->x, g->x_stride, d, 2) || !rows_ok(g->dy, g->dy_stride, d, gb)))
+        return EDGE_MOE_EINVAL;
+    if ((g->dres && !rows_ok(g->dres, g->dres_stride, d, gb)) || (g->dx && !rows_ok(g->dx, g->dx_stride, d, gb)))
+        return EDGE_MOE_EINVAL;
+    if ((!g->dx && !g->dgain && T > 0) || (g->dgain && !aligned(g->dgain, 4))) return EDGE_MOE_EINVAL;
+    st = ws_status(ws, ws_bytes, em::norm_backward_ws_bytes(T, d));
+    if (st == EDGE_MOE_OK) st = em::device_status();
+    if (st != EDGE_MOE_OK) return st;
+    em::NormBwd a{};
+    a.T = T; a.d = d;
+    a.x = g->x; a.x_stride = g->x_stride; a.gain = g->gain; a.gain_f32 = g->gain_type == EDGE_MOE_FLOAT; a.rstd = g->rstd;
+    a.dy = g->dy; a.dy_stride = g->dy_stride; a.dres = g->dres; a.dres_stride = g->dres_stride;
+    a.dx = g->dx; a.dx_stride = g->dx_stride; a.dgain = g->dgain; a.f32 = gb == 4;
+    return hip_status(em::launch_norm_backward(a, ws, (hipStream_t)stream));
+}
+
+size_t edge_moe_dense_product_ws_bytes(const edge_moe_dense_dims* dims) {
+    return dense_status(dims) == EDGE_MOE_OK ? em::dense_product_ws_bytes(dense_args(*dims)) : 0;
+}
+
+int edge_moe_dense_product(const edge_moe_dense_dims* dims, const uint16_t* x, int64_t x_stride, const int32_t* row_src,
+                           const int32_t* offsets, const uint16_t* w, int32_t y_type, void* y, int64_t y_stride, void* ws,
+                           size_t ws_bytes, void* stream) {
+    int st = dense_status(dims);
+    if (st != EDGE_MOE_OK) return st;
+    em::DenseProduct a = dense_args(*dims);
+    if (!rows_ok(x, x_stride, a.K, 2) || !aligned(w, 16) || !type_ok(y_type)) return EDGE_MOE_EINVAL;
+    if (a.R > 0 && !rows_ok(y, y_stride, a.N, type_bytes(y_type))) return EDGE_MOE_EINVAL;
+    st = lists_status(row_src, offsets, a.T, a.R, a.M);
+    if (st == EDGE_MOE_OK) st = ws_status(ws, ws_bytes, em::dense_product_ws_bytes(a));
+    if (st == EDGE_MOE_OK) st = em::device_status();
+    if (st != EDGE_MOE_OK || a.R == 0) return st;
+    a.x = x; a.x_stride = x_stride; a.row_src = row_src; a.offsets = offsets; a.w = w;
+    a.out = y; a.out_stride = y_stride; a.out_f32 = y_type == EDGE_MOE_FLOAT;
+    return hip_status(em::launch_dense_product(a, ws, (hipStream_t)stream));
+}
+
+size_t edge_moe_dense_product_backward_ws_bytes(const edge_moe_dense_dims* dims) {
+    return dense_status(dims) == EDGE_MOE_OK ? em::dense_backward_ws_bytes(dense_args(*dims)) : 0;
+}
+
+int edge_moe_dense_product_backward(const edge_moe_dense_dims* dims, const edge_moe_dense_grad* g, void* ws, size_t ws_bytes,
+                                    void* stream) {
+    int st = dense_status(dims);
+    if (st != EDGE_MOE_OK) return st;
+    if (!g || (!g->dx && !g->dw)) return EDGE_MOE_EINVAL;
+    em::DenseGrad a{};
+    a.p = dense_args(*dims);
+    em::DenseProduct& p = a.p;
+    if (p.R > 0 && !rows_ok(g->dy, g->dy_stride, p.N, 2)) return EDGE_MOE_EINVAL;
+    if (g->dw && (!rows_ok(g->x, g->x_stride, p.K, 2) || !type_ok(g->dw_type) || !aligned(g->dw, 16))) return EDGE_MOE_EINVAL;
+    if (g->dx && (!aligned(g->w, 16) || !type_ok(g->dx_type) || !rows_ok(g->dx, g->dx_stride, p.K, type_bytes(g->dx_type))))
+        return EDGE_MOE_EINVAL;
+    if (g->dx && g->token_rows && (!aligned(g->token_rows, 4) || g->per_token < 1)) return EDGE_MOE_EINVAL;
+    if (g->dx && g->token_rows && g->per_token > 1024) return EDGE_MOE_EUNSUPPORTED;
+    st = lists_status(g->row_src, g->offsets, g->dw ? p.T : p.R, p.R, p.M);
+    if (st == EDGE_MOE_OK) st = ws_status(ws, ws_bytes, em::dense_backward_ws_bytes(p));
+    if (st == EDGE_MOE_OK) st = em::device_status();
+    if (st != EDGE_MOE_OK) return st;
+    p.x = g->x; p.x_stride = g->x_stride; p.row_src = g->row_src; p.offsets = g->offsets; p.w = g->w;
+    p.dy = g->dy; p.dy_stride = g->dy_stride;
+    a.dx = g->dx; a.dx_stride = g->dx_stride; a.dx_f32 = g->dx_type == EDGE_MOE_FLOAT;
+    a.token_rows = g->dx ? g->token_rows : nullptr; a.per_token = g->per_token;
+    a.dw = g->dw; a.dw_f32 = g->dw_type == EDGE_MOE_FLOAT;
+    return hip_status(em::launch_dense_backward(a, ws, (hipStream_t)stream));
+}
+
+size_t edge_moe_packed_product_ws_bytes(const edge_moe_packed_dims* dims) {
+    return int4_status(dims) == EDGE_MOE_OK ? em::int4_product_ws_bytes(int4_args(*dims)) : 0;
+}
+
+int edge_moe_packed_product(const edge_moe_packed_dims* dims, const uint16_t* x, int64_t x_stride, const int32_t* row_src,
+                          const int32_t* offsets, const uint8_t* codes, const uint16_t* scales, int32_t y_type, void* y,
+                          int64_t y_stride, void* ws, size_t ws_bytes, void* stream) {
+    int st = int4_status(dims);
+    if (st != EDGE_MOE_OK) return st;
+    em::Int4Product a = int4_args(*dims);
+    if (!rows_ok(x, x_stride, a.K, 2) || !aligned(codes, 16) || !aligned(scales, 4) || !type_ok(y_type)) return EDGE_MOE_EINVAL;
+    if (a.R > 0 && (!aligned(y, type_bytes(y_type)) || y_stride < a.N || y_stride > (1ll << 32))) return EDGE_MOE_EINVAL;
+    st = lists_status(row_src, offsets, a.T, a.R, a.M);
+    if (st == EDGE_MOE_OK) st = ws_status(ws, ws_bytes, em::int4_product_ws_bytes(a));
+    if (st == EDGE_MOE_OK) st = em::device_status();
+    if (st != EDGE_MOE_OK || a.R == 0) return st;
+    a.x = x; a.x_stride = x_stride; a.row_src = row_src; a.offsets = offsets; a.codes = codes; a.scales = scales;
+    a.y = y; a.y_stride = y_stride; a.y_f32 = y_type == EDGE_MOE_FLOAT;
+    return hip_status(em::launch_int4_product(a, ws, (hipStream_t)stream));
 }
 
 }  // extern "C"
