@@ -156,16 +156,23 @@ dp_stream(DenseProduct a) {
 }
 
 // ------------------------------------------------------------------ LDS tiles ----
-// A workgroup takes BT i x BN j of out in WT x WN waves.  Each step of 32 c arrives by
-// direct global -> LDS loads, three steps ahead in four stages; every wave issues the
-// same number of loads a step, so that one counted wait covers them.  Lanes without an
-// element (past the rows, columns or c of an operand, or a row that row_src does not
-// name) load zeros from dp_zero, so that nothing outside an operand meets a product.
+// A workgroup takes BT i x BN j of out in WT x WN waves, 64 of c a step.  P's and Q's
+// tiles arrive by direct global -> LDS loads two steps ahead, every wave as many loads a
+// step, counted by hand.  P's fragments of a step are read into registers during the
+// step before, so P needs two stages and Q three.
 //
-// An operand with c along its rows: 64-byte rows of 32 c, 16-byte segments XOR-swizzled
-// by the row (mx_product.hip's rule).  One with c down the rows: 32 rows of BX elements,
-// segments swizzled in pairs by the row, so that the four rows that sixteen lanes read
-// together fall on different banks.
+// An operand with c along its rows: 128-byte rows (whole cache lines), 16-byte segments
+// XOR-swizzled by the row (mx_product.hip's rule).  One with c down the rows: 64 rows of BX
+// elements, segments swizzled in pairs by the row, so that the four rows that sixteen
+// lanes read together fall on different banks.
+//
+// Rows and columns past an operand's end repeat its last ones, and what they give is not
+// stored.  Past the end of c, and for an x row of dW that row_src does not name, lanes
+// load zeros from dp_zero, so that nothing outside an operand meets a product.
+//
+// A load takes a uniform base and a 32-bit lane offset (4 to 7% faster than a 64-bit
+// address a lane at 8192^3); WIDE, for rows so far apart that the offsets do not fit,
+// and the last steps of c take whole addresses.
 namespace {
 
 template <int MODE, int BT_, int BN_>
@@ -176,37 +183,33 @@ struct DpCfg {
     static constexpr int NW = BN == 256 || (BN == 128 && BT == 256) ? 8 : 4;
     static constexpr int WN = BN == 256 ? (BT == 256 ? 2 : 4) : BN == 128 ? 2 : (BT == 256 ? 1 : 2), WT = NW / WN;
     static constexpr int NI = BN / WN / 16, NJ = BT / WT / 16;        // j and i subtiles of a wave
-    static constexpr int J_B = BN * 64, I_B = BT * 64, STAGE = J_B + I_B, STAGES = 4;
-    static constexpr int J_P = J_B / 1024, P = STAGE / 1024;          // wave loads of Q, of a stage
-    static constexpr int LOADS = (P + NW - 1) / NW;
+    static constexpr int J_B = BN * 128, I_B = BT * 128;              // bytes of a stage of Q, of P
+    static constexpr int JL = J_B / 1024 / NW, LOADS = JL + I_B / 1024 / NW;   // a wave's loads a step: Q's, then P's
     static constexpr int OUT_B = 16 * (NI * 64 + 16);                 // a wave's sixteen out rows on their way out
-    static constexpr int IDX_B = GATHER ? NW * 8 * 256 : 0;           // x rows of the next steps, eight slots a wave
-    static constexpr int LDS_B = (STAGES * STAGE > NW * OUT_B ? STAGES * STAGE : NW * OUT_B) + IDX_B;
-    static constexpr int VM = LOADS + (GATHER ? 1 : 0);               // vector-memory instructions a step
+    static constexpr int TILES_B = 3 * J_B + 2 * I_B > NW * OUT_B ? 3 * J_B + 2 * I_B : NW * OUT_B;
+    static constexpr int LDS_B = TILES_B + (GATHER ? 4 * 256 : 0);    // (GATHER) the x rows of four steps behind the tiles
+    static_assert(LDS_B <= 160 * 1024, "");
 };
 
 template <int N>
 EM_DEV void wait_loads_barrier() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" : : "n"(N) : "memory");
+}
+template <int N>
+EM_DEV void wait_lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(%0)\n\ts_barrier" : : "n"(N) : "memory");
 }
 
 template <int I> struct Set { static constexpr int value = I; };
 
-// Slot of 16-byte segment s: of row r of 64 bytes; of c row r of BX elements.
-EM_DEV int swz_row(int r, int s) { return s ^ (-(r >> 2) & 3); }
+// Slot of 16-byte segment s: of row r of 128 bytes; of c row r of BX elements.
+EM_DEV int swz_row(int r, int s) { return s ^ ((r >> 1) & 7); }
 template <int BX>
 EM_DEV int swz_col(int r, int s) { return s ^ 2 * ((r & 3) | (BX >= 128 ? (r >> 1) & 4 : 0)); }
 
-// One load of a stage: where a lane's 16 bytes come from.
-struct DpSrc {
-    const char* base;        // at step 0
-    int64_t adv;             // bytes a step
-    int lim;                 // first step without an element
-};
-
 }  // namespace
 
-template <int MODE, int BT, int BN>
+template <int MODE, int BT, int BN, bool WIDE>
 __global__ void __launch_bounds__((DpCfg<MODE, BT, BN>::NW * 64))
 dp_tile(DenseProduct a) {
     using C = DpCfg<MODE, BT, BN>;
@@ -251,72 +254,85 @@ dp_tile(DenseProduct a) {
         j0 = tn * BN;
         clen = MODE == DP_Y ? a.K : a.N;
     }
-    const int steps = (clen + 31) >> 5;
+    const int steps = (clen + 63) >> 6, whole_steps = clen >> 6;
     const int s0 = (int)((int64_t)steps * z / a.slices), s1 = (int)((int64_t)steps * (z + 1) / a.slices);
 
-    // ---- load sources
-    DpSrc src[C::LOADS];
-    int idx_at[C::LOADS];                                         // (GATHER) the load's row in a step's x rows, -1: dy
+    // ---- loads.  Load u of a wave brings piece u NW + wv: Q's first, then P's.
+    const uint16_t* wm = a.w + (int64_t)mat * a.N * a.K;          // (not with dW)
+    // Uniform base at step 0, and bytes a step.
+    const char* jbase = reinterpret_cast<const char*>(MODE == DP_Y ? wm + (int64_t)j0 * a.K : MODE == DP_DX ? wm : a.x + (int64_t)c0 * a.x_stride);
+    const char* ibase = reinterpret_cast<const char*>(MODE == DP_Y ? (a.row_src ? a.x : a.x + (int64_t)i0 * a.x_stride) : a.dy + (int64_t)(MODE == DP_DX ? i0 : c0) * a.dy_stride);
+    const int64_t jstride = MODE == DP_DX ? a.K : a.x_stride;     // of Q's rows, where c runs down them
+    const int64_t jadv = C::JT ? 128 * jstride : 128, iadv = C::IT ? 128 * a.dy_stride : 128;
+    // A lane's place in load u: its row of c and column, or its row and first c.
+    auto place = [&](int u, int& row, int& col) {
+        const bool isj = u < C::JL;
+        const int piece = (isj ? u : u - C::JL) * C::NW + wv, bx = isj ? BN : BT;
+        if (isj ? C::JT : C::IT) {
+            row = piece * (512 / bx) + lane / (bx / 8);
+            const int slot = lane % (bx / 8), at = 8 * (isj ? swz_col<BN>(row, slot) : swz_col<BT>(row, slot));
+            col = min((isj ? j0 : i0) + at, (isj ? a.K : a.N) - 8);
+        } else {
+            row = piece * 8 + lane / 8;
+            col = 8 * swz_row(row, lane % 8);
+            row = isj ? min(row, a.N - 1 - j0) : min(row, i1 - 1 - i0);
+            if (MODE == DP_Y && !isj && a.row_src) row = max(x_row(a, i0 + row), 0);   // the row of x
+        }
+    };
+    // The first c of a lane's 16 bytes of load u within a step.
+    auto c_of = [&](int u) {
+        const bool isj = u < C::JL;
+        const int piece = (isj ? u : u - C::JL) * C::NW + wv, bx = isj ? BN : BT;
+        if (isj ? C::JT : C::IT) return piece * (512 / bx) + lane / (bx / 8);
+        return 8 * swz_row(piece * 8 + lane / 8, lane % 8);
+    };
+    // Bytes of a lane from load u's base at its step.
+    auto offset = [&](int u, int row, int col) -> int64_t {
+        const bool isj = u < C::JL;
+        const int64_t stride = isj ? (MODE == DP_Y ? (int64_t)a.K : jstride) : MODE == DP_Y ? a.x_stride : a.dy_stride;
+        return 2 * (row * stride + col);
+    };
+    uint32_t off[C::LOADS];
+    int64_t woff[WIDE ? C::LOADS : 1];
 #pragma unroll
     for (int u = 0; u < C::LOADS; ++u) {
-        const int piece = (C::LOADS * wv + u) % C::P;
-        const bool isj = piece < C::J_P;
-        DpSrc o;
-        idx_at[u] = -1;
-        if (isj ? C::JT : C::IT) {                                // c down the rows
-            const int bx = isj ? BN : BT, row = (isj ? piece : piece - C::J_P) * (512 / bx) + lane / (bx / 8);
-            const int slot = lane % (bx / 8);
-            const int col = (isj ? j0 : i0) + 8 * (isj ? swz_col<BN>(row, slot) : swz_col<BT>(row, slot));
-            const int cols = isj ? a.K : a.N;                     // of x and W; of dy
-            const int64_t stride = isj ? (MODE == DP_DX ? (int64_t)a.K : a.x_stride) : a.dy_stride;
-            const uint16_t* p = isj ? (MODE == DP_DX ? a.w + (int64_t)mat * a.N * a.K : a.x) : a.dy;
-            const int64_t first = isj && C::GATHER ? 0 : (int64_t)(c0 + row) * stride;
-            o.base = reinterpret_cast<const char*>(p + first + min(col, cols - 8));
-            o.adv = 64 * stride;
-            o.lim = col < cols ? (clen - row + 31) >> 5 : 0;
-            if (isj && C::GATHER) {
-                idx_at[u] = row;
-                o.adv = 2 * stride;                               // times the x row
-            }
-        } else {                                                  // c along the rows
-            const int row = (isj ? piece : piece - C::J_P) * 16 + lane / 4, seg = swz_row(row, lane % 4);
-            const uint16_t* p;
-            bool in = true;
-            if (isj) {                                            // W of y
-                in = j0 + row < a.N;
-                p = a.w + ((int64_t)mat * a.N + min(j0 + row, a.N - 1)) * a.K;
-            } else if (MODE == DP_Y) {
-                const int s = x_row(a, min(i0 + row, i1 - 1));
-                in = s >= 0;
-                p = a.x + (int64_t)max(s, 0) * a.x_stride;
-            } else {
-                p = a.dy + (int64_t)min(i0 + row, i1 - 1) * a.dy_stride;
-            }
-            o.base = reinterpret_cast<const char*>(p + 8 * seg);
-            o.adv = 64;
-            o.lim = in ? (clen - 8 * seg + 31) >> 5 : 0;
-        }
-        src[u] = o;
+        int row, col;
+        place(u, row, col);
+        if constexpr (WIDE) woff[u] = offset(u, C::GATHER && u < C::JL ? 0 : row, col);
+        else off[u] = (uint32_t)offset(u, C::GATHER && u < C::JL ? 0 : row, col);
     }
     const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
-    const int* ring = reinterpret_cast<const int*>(lds + C::LDS_B - C::IDX_B) + wv * (8 * 64);
     const char* zero = reinterpret_cast<const char*>(&dp_zero);
-    auto fetch_rows = [&](int st) {                               // (GATHER) the x rows of step st
-        const int r = min(c0 + 32 * st + (lane & 31), c0 + clen - 1);
-        lds_load4(a.row_src, 4u * (uint32_t)r,
-                  __builtin_amdgcn_readfirstlane(base + C::LDS_B - C::IDX_B + wv * 2048 + (st & 7) * 256));
+    // (GATHER) x rows of step st to their place in the LDS (every wave brings all of them),
+    // and from there those of this wave's loads
+    int from_row[C::GATHER ? C::JL : 1];
+    auto fetch_rows = [&](int st) {
+        const int r = c0 + min(64 * st + lane, clen - 1);
+        lds_load4(a.row_src, 4u * (uint32_t)r, __builtin_amdgcn_readfirstlane(base + C::TILES_B + (st & 3) * 256));
     };
-    auto fetch = [&](int st, int u) {
-        const int piece = (C::LOADS * wv + u) % C::P;
-        const uint32_t dst = __builtin_amdgcn_readfirstlane(base + (st & 3) * C::STAGE + 1024 * piece);
-        const char* p;
-        if (C::GATHER && piece < C::J_P) {
-            const int s = ring[(st & 7) * 64 + idx_at[u]];
-            p = st < src[u].lim && (unsigned)s < (unsigned)a.T ? src[u].base + s * src[u].adv : zero;
+    auto read_rows = [&](int st) {
+        const int* rows = reinterpret_cast<const int*>(lds + C::TILES_B) + (st & 3) * 64;
+#pragma unroll
+        for (int u = 0; u < C::JL; ++u) from_row[u] = rows[c_of(u)];
+    };
+    auto jstage = [&](int st) { return (uint32_t)(st % 3) * C::J_B; };
+    auto istage = [&](int st) { return 3 * C::J_B + (uint32_t)(st & 1) * C::I_B; };
+    auto fetch = [&](int st, int u, auto fast) {                  // FAST: every c of the step exists
+        constexpr bool FAST = decltype(fast)::value;
+        const bool isj = u < C::JL;
+        const uint32_t dst = __builtin_amdgcn_readfirstlane(base + (isj ? jstage(st) + 1024 * (u * C::NW + wv)
+                                                                        : istage(st) + 1024 * ((u - C::JL) * C::NW + wv)));
+        const char* from = isj ? jbase + (C::GATHER ? -(int64_t)c0 * 2 * a.x_stride : st * jadv) : ibase + st * iadv;
+        if (C::GATHER && isj) {
+            const int s = from_row[u];
+            const bool in = (unsigned)s < (unsigned)a.T && (FAST || 64 * st + c_of(u) < clen);
+            lds_load16(in ? from + 2 * (s * a.x_stride) + (WIDE ? woff[u] : (int64_t)off[u]) : zero, dst);
+        } else if constexpr (FAST && !WIDE) {
+            lds_load16(from, off[u], dst);
         } else {
-            p = st < src[u].lim ? src[u].base + st * src[u].adv : zero;
+            const char* p = from + (WIDE ? woff[u] : (int64_t)off[u]);
+            lds_load16(64 * st + c_of(u) < clen ? p : zero, dst);
         }
-        lds_load16(p, dst);
     };
 
     const int wn = wv / C::WT, wt = wv % C::WT;
@@ -326,76 +342,99 @@ dp_tile(DenseProduct a) {
 #pragma unroll
         for (int j = 0; j < NJ; ++j) acc[p][j] = zero4();
 
-    // ---- operand reads.  Transposed: lanes 4 q .. 4 q + 3 of sixteen read 16 columns of c
-    // row q, and lane m gets column m's four c; two reads make the eight c of its slot.
-    const int row_at = m * 64 + 16 * swz_row(m, g);               // (16 rows on, the swizzle is the same)
-    auto read_t = [&](const uint8_t* tile, int sub, auto bx) {
+    // ---- operand reads: half h of a step's c.  Transposed: lanes 4 q .. 4 q + 3 of sixteen
+    // read 16 columns of c row q, and lane m gets column m's four c; two reads make the
+    // eight c of its slot.
+    const int row_at[2] = {m * 128 + 16 * swz_row(m, g), m * 128 + 16 * swz_row(m, 4 + g)};   // (16 rows on, the swizzle is the same)
+    int turn = swz_col<128>(8 * g + (m >> 2), 0);                 // what swz_col turns by, the same for all c rows of a lane
+    auto read_t = [&](uint32_t tile, int sub, int h, auto bx) {
         constexpr int BX = decltype(bx)::value;
+        const int at = (8 * g + (m >> 2)) * (2 * BX) + 16 * ((m >> 1) & 1) + 8 * (m & 1);
+        const uint8_t* p = lds + tile + (16 * ((BX >= 128 ? turn : turn & 6) ^ 2 * sub) + at);
         uint4 o;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int k = 8 * g + 4 * h + (m >> 2);
-            const uint8_t* p = tile + k * (2 * BX) + 16 * swz_col<BX>(k, 2 * sub + ((m >> 1) & 1)) + 8 * (m & 1);
-            const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)p);
+        for (int q = 0; q < 2; ++q) {
+            const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p + (32 * h + 4 * q) * (2 * BX)));
             const uint2 w = __builtin_bit_cast(uint2, v);
-            if (h == 0) { o.x = w.x; o.y = w.y; }
+            if (q == 0) { o.x = w.x; o.y = w.y; }
             else { o.z = w.x; o.w = w.y; }
         }
         return o;
     };
-    auto read_j = [&](const uint8_t* stage, int p) {
-        if constexpr (C::JT) return read_t(stage, NI * wn + p, std::integral_constant<int, BN>{});
-        else return ldg16(stage + 16 * (NI * wn + p) * 64 + row_at);
+    auto read_j = [&](int st, int p, int h) {
+        if constexpr (C::JT) return read_t(jstage(st), NI * wn + p, h, std::integral_constant<int, BN>{});
+        else return ldg16(lds + jstage(st) + 16 * (NI * wn + p) * 128 + row_at[h]);
     };
-    auto read_i = [&](const uint8_t* stage, int j) {
-        if constexpr (C::IT) return read_t(stage + C::J_B, NJ * wt + j, std::integral_constant<int, BT>{});
-        else return ldg16(stage + C::J_B + 16 * (NJ * wt + j) * 64 + row_at);
+    auto read_i = [&](int st, int j, int h) {
+        if constexpr (C::IT) return read_t(istage(st), NJ * wt + j, h, std::integral_constant<int, BT>{});
+        else return ldg16(lds + istage(st) + 16 * (NJ * wt + j) * 128 + row_at[h]);
     };
-    uint4 fi[2][NJ], fj[2];
-    auto stage_of = [&](int st) -> const uint8_t* { return lds + (st & 3) * C::STAGE; };
-    // P's fragments are read a step ahead and Q's one subtile ahead, so that the matrix
-    // cores have operands from a step's first cycle.  A step's barrier says that the next
-    // step's stage has landed and that the one before is free.
-    auto step = [&](int st, auto set) {
+    uint4 fi[2][2][NJ], fj[2][2];                                 // [set][half][subtile]; [subtile & 1][half]
+    // (GATHER: x rows are asked for four steps ahead, at a step's end: landed at the next
+    // step's MID, read at its end, used in the step after.)
+    // A step: its first barrier says that the step before is read (its stage of Q is free, and
+    // this step's of P, which is in registers), the one at MID that the next step has landed.
+    // The loads of the step after it are spread between the products; the next step's P is
+    // read from MID on, Q one subtile ahead.
+    constexpr int MID = NI / 2, SPAN = NI - MID > 1 ? NI - MID - 1 : 1;   // subtiles with reads of P
+    auto step = [&](int st, auto set, auto fast) {
         constexpr int f = decltype(set)::value;
-        const uint8_t* X = stage_of(st);
-        const uint8_t* Xn = stage_of(st + 1);
-        wait_loads_barrier<C::VM>();
-        if constexpr (C::GATHER) fetch_rows(st + 5);
+        asm volatile("" : "+v"(turn));                            // the lane addresses are made anew: kept, they take registers
+        // all of this wave's reads of P are done: those of Q behind the last of them (NI > 2: in
+        // the last subtile) may be in flight
+        wait_lds_barrier<NI == 2 ? 0 : C::JT ? 4 : 2>();
 #pragma unroll
         for (int p = 0; p < NI; ++p) {
-            fj[(p + 1) & 1] = read_j(p + 1 < NI ? X : Xn, (p + 1) % NI);
+            if (p == MID) wait_loads_barrier<MID * C::LOADS / NI>();
+            if (p >= MID) {
 #pragma unroll
-            for (int u = p * NJ / NI; u < (p + 1) * NJ / NI; ++u) fi[1 - f][u] = read_i(Xn, u);
+                for (int u = (p - MID) * 2 * NJ / SPAN; u < (p - MID + 1) * 2 * NJ / SPAN && u < 2 * NJ; ++u)
+                    fi[1 - f][u / NJ][u % NJ] = read_i(st + 1, u % NJ, u / NJ);
+            }
 #pragma unroll
-            for (int u = p * C::LOADS / NI; u < (p + 1) * C::LOADS / NI; ++u) fetch(st + 3, u);
+            for (int h = 0; h < 2; ++h) fj[(p + 1) & 1][h] = p + 1 < NI ? read_j(st, p + 1, h) : read_j(st + 1, 0, h);
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) acc[p][j] = mfma_bf16(fj[p & 1], fi[f][j], acc[p][j]);
+            for (int u = p * C::LOADS / NI; u < (p + 1) * C::LOADS / NI; ++u) fetch(st + 2, u, fast);
+            if (C::GATHER && p == NI - 1) {
+                read_rows(st + 3);
+                fetch_rows(st + 4);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) acc[p][j] = mfma_bf16(fj[p & 1][h], fi[f][h][j], acc[p][j]);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
     if (s0 < s1) {
         if constexpr (C::GATHER) {
 #pragma unroll
-            for (int st = 0; st < 5; ++st) fetch_rows(s0 + st);
+            for (int st = 0; st < 4; ++st) fetch_rows(s0 + st);
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         }
 #pragma unroll
-        for (int st = 0; st < 3; ++st) {
+        for (int st = 0; st < 2; ++st) {
+            if constexpr (C::GATHER) read_rows(s0 + st);
 #pragma unroll
-            for (int u = 0; u < C::LOADS; ++u) fetch(s0 + st, u);
+            for (int u = 0; u < C::LOADS; ++u) fetch(s0 + st, u, std::false_type{});
         }
-        wait_loads_barrier<C::GATHER ? C::LOADS : 2 * C::LOADS>();      // (a gathering step's own wait allows for its row load)
+        if constexpr (C::GATHER) read_rows(s0 + 2);
+        wait_loads_barrier<C::LOADS>();
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) fi[0][j] = read_i(stage_of(s0), j);
-        fj[0] = read_j(stage_of(s0), 0);
+        for (int u = 0; u < 2 * NJ; ++u) fi[0][u / NJ][u % NJ] = read_i(s0, u % NJ, u / NJ);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) fj[0][h] = read_j(s0, 0, h);
         int st = s0;
-        for (; st + 1 < s1; st += 2) {
-            step(st, Set<0>{});
-            step(st + 1, Set<1>{});
+        for (; st + 1 < s1 && st + 3 < whole_steps; st += 2) {
+            step(st, Set<0>{}, std::true_type{});
+            step(st + 1, Set<1>{}, std::true_type{});
         }
-        if (st < s1) step(st, Set<0>{});
-        wait_loads_barrier<0>();                                  // nothing more lands in the stages
+        for (; st + 1 < s1; st += 2) {
+            step(st, Set<0>{}, std::false_type{});
+            step(st + 1, Set<1>{}, std::false_type{});
+        }
+        if (st < s1) step(st, Set<0>{}, std::false_type{});
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");    // nothing more lands in the stages
     }
 
     // ---- out, sixteen rows of a wave at a time through the LDS, so that whole row segments
@@ -409,10 +448,13 @@ dp_tile(DenseProduct a) {
     const int left = i1 - i0 - 16 * NJ * wt, col0 = j0 + 16 * NI * wn;
     constexpr int RS = NI * 64 + 16;
     uint8_t* o = lds + wv * C::OUT_B;
+    bool named[NJ];                                               // rows of y whose x row row_src names
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) named[j] = MODE != DP_Y || x_row(a, min(i0 + 16 * (NJ * wt + j) + m, i1 - 1)) >= 0;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
 #pragma unroll
-        for (int p = 0; p < NI; ++p) *reinterpret_cast<floatx4*>(o + m * RS + 64 * p + 16 * g) = acc[p][j];
+        for (int p = 0; p < NI; ++p) *reinterpret_cast<floatx4*>(o + m * RS + 64 * p + 16 * g) = named[j] ? acc[p][j] : zero4();
         __builtin_amdgcn_wave_barrier();                          // one wave's LDS accesses complete in order
         asm volatile("" ::: "memory");
         if (f32) {
@@ -496,6 +538,13 @@ int64_t max_row_tiles(const DenseProduct& a, int BT) {
 
 struct DpPlan { int bt, bn, slices; };
 
+// Whether lane offsets within a tile pass 32 bits: 256 rows of dy or x, or a gathered row
+// anywhere in x.
+bool wide_rows(const DenseProduct& a, int mode) {
+    const int64_t rows = mode == DP_Y && a.row_src ? a.T : 256, x = mode == DP_DX || mode == DP_DWG ? 0 : a.x_stride;
+    return rows * x >= (1ll << 31) || 256 * (mode == DP_Y ? 0 : a.dy_stride) >= (1ll << 31);
+}
+
 DpPlan plan(const DenseProduct& a, int mode) {
     DpPlan p{};
     const int J = mode == DP_Y ? a.N : a.K;
@@ -515,30 +564,34 @@ DpPlan plan(const DenseProduct& a, int mode) {
     return p;
 }
 
-template <int MODE, int BT, int BN>
+template <int MODE, int BT, int BN, bool WIDE = false>
 hipError_t launch_tile(const DenseProduct& a, int64_t blocks, hipStream_t s) {
     prof_begin(s);
-    dp_tile<MODE, BT, BN><<<(unsigned)((blocks + 7) & ~7ll), DpCfg<MODE, BT, BN>::NW * 64, 0, s>>>(a);
+    dp_tile<MODE, BT, BN, WIDE><<<(unsigned)((blocks + 7) & ~7ll), DpCfg<MODE, BT, BN>::NW * 64, 0, s>>>(a);
     prof_end(s, MODE == DP_Y ? "dp_tile_y" : MODE == DP_DX ? "dp_tile_dx" : "dp_tile_dw");
     return hipGetLastError();
 }
 
 template <int MODE, int BT>
 hipError_t launch_tile(const DenseProduct& a, int bn, int64_t blocks, hipStream_t s) {
-    switch (bn) {
-        case 64: return launch_tile<MODE, BT, 64>(a, blocks, s);
-        case 128: return launch_tile<MODE, BT, 128>(a, blocks, s);
-        default: return launch_tile<MODE, BT, 256>(a, blocks, s);
+    if (bn == 64) return launch_tile<MODE, BT, 64>(a, blocks, s);
+    if constexpr (MODE != DP_DWG || BT < 256) {
+        if (bn == 256) return launch_tile<MODE, BT, 256>(a, blocks, s);
     }
+    return launch_tile<MODE, BT, 128>(a, blocks, s);
 }
 
 template <int MODE>
-hipError_t launch_tile(DenseProduct a, const DpPlan& p, hipStream_t s) {
+hipError_t launch_tile(DenseProduct a, DpPlan p, hipStream_t s) {
+    const bool wide = wide_rows(a, MODE);
+    if (wide) p.bt = p.bn = 128;
+    else if (MODE == DP_DWG && p.bt + p.bn == 512) p.bt = 128;     // the x rows have no place beside the largest tiles
     const int J = MODE == DP_Y ? a.N : a.K, nn = (J + p.bn - 1) / p.bn;
     a.slices = p.slices;
     a.row_tiles = (int)max_row_tiles(a, p.bt);
     const int64_t rows = MODE >= DP_DW ? (int64_t)a.M * ((a.N + p.bt - 1) / p.bt) : a.row_tiles;
     const int64_t blocks = rows * nn * p.slices;
+    if (wide) return launch_tile<MODE, 128, 128, true>(a, blocks, s);
     switch (p.bt) {
         case 64: return launch_tile<MODE, 64>(a, p.bn, blocks, s);
         case 128: return launch_tile<MODE, 128>(a, p.bn, blocks, s);
