@@ -207,53 +207,25 @@ EM_DEV int swz_row(int r, int s) { return s ^ ((r >> 1) & 7); }
 template <int BX>
 EM_DEV int swz_col(int r, int s) { return s ^ 2 * ((r & 3) | (BX >= 128 ? (r >> 1) & 4 : 0)); }
 
+// A tile of out: matrix mat, rows i0 .. i1 of P, from row j0 of Q; part z of the slices of c,
+// which is clen long and starts at row c0 of dy and x (dW).
+struct DpTile { int mat, i0, i1, j0, z, c0, clen; };
+
+// Tile b of `total` tiles that XCD x = block % 8 takes neighbouring ones of; -1 past them.
+EM_DEV int xcd_tile(int block, int total) {
+    const int per = (total + 7) >> 3, at = block >> 3, b = (block & 7) * per + at;
+    return at < per && b < total ? b : -1;
+}
+
 }  // namespace
 
 template <int MODE, int BT, int BN, bool WIDE>
-__global__ void __launch_bounds__((DpCfg<MODE, BT, BN>::NW * 64))
-dp_tile(DenseProduct a) {
+EM_DEV void dp_body(const DenseProduct& a, const DpTile& t, uint8_t* lds) {
     using C = DpCfg<MODE, BT, BN>;
     constexpr int NI = C::NI, NJ = C::NJ;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[C::LDS_B];
     const int lane = lane_id(), wv = wave_id(), g = lane >> 4, m = lane & 15;
-
-    // ---- the tile: i0 .. i1 of P's rows, j0 of Q's, steps s0 .. s1 of c; XCD x = blockIdx % 8
-    // takes neighbouring tiles
-    const int J = MODE == DP_Y ? a.N : a.K, nn = (J + BN - 1) / BN;
-    int mat, i0, i1, j0, z = 0, c0 = 0, clen;
-    if constexpr (MODE >= DP_DW) {
-        const int ni = (a.N + BT - 1) / BT, each = a.M * ni * nn, total = each * a.slices, per = (total + 7) >> 3;
-        const int at = blockIdx.x >> 3, b = (blockIdx.x & 7) * per + at;
-        if (at >= per || b >= total) return;
-        z = b / each;
-        const int in = b - z * each;
-        mat = in / (ni * nn);
-        const int tile = in - mat * (ni * nn);
-        i0 = tile / nn * BT;
-        i1 = min(a.N, i0 + BT);
-        j0 = tile % nn * BN;
-        c0 = a.offsets ? min(max(a.offsets[mat], 0), a.R) : 0;
-        clen = (a.offsets ? min(max(a.offsets[mat + 1], c0), a.R) : a.R) - c0;
-    } else {
-        int tn = 0;
-        const RowTile t = row_tile<BT>(a.offsets, a.M, a.R, [&](int rows) {
-            rows = min(rows, a.row_tiles);                       // more only where offsets descend
-            const int each = rows * nn, total = each * a.slices, per = (total + 7) >> 3, at = blockIdx.x >> 3;
-            int b = (blockIdx.x & 7) * per + at;
-            if (at >= per || b >= total) return -1;
-            z = b / each;
-            b -= z * each;
-            const int grp = b / (8 * nn), left = min(8, rows - 8 * grp), in = b - grp * 8 * nn;
-            tn = in / left;
-            return 8 * grp + in % left;
-        });
-        if (t.r1 == 0) return;
-        mat = t.m;
-        i0 = t.r0;
-        i1 = t.r1;
-        j0 = tn * BN;
-        clen = MODE == DP_Y ? a.K : a.N;
-    }
+    const int J = MODE == DP_Y ? a.N : a.K;
+    const int mat = t.mat, i0 = t.i0, i1 = t.i1, j0 = t.j0, z = t.z, c0 = t.c0, clen = t.clen;
     const int steps = (clen + 63) >> 6, whole_steps = clen >> 6;
     const int s0 = (int)((int64_t)steps * z / a.slices), s1 = (int)((int64_t)steps * (z + 1) / a.slices);
 
@@ -484,6 +456,70 @@ dp_tile(DenseProduct a) {
     }
 }
 
+// Tiles of the largest size come in rounds of 256, one a compute unit; what is left of the
+// last round, if it is half of one or less, is made as tiles of half the rows (5001 rows
+// in 8 groups, 4096 columns, K = 8192: 356 us whole, 317 with halves).
+template <int MODE, int BT, int BN, bool WIDE>
+__global__ void __launch_bounds__((DpCfg<MODE, BT, BN>::NW * 64))
+dp_tile(DenseProduct a) {
+    using C = DpCfg<MODE, BT, BN>;
+    constexpr bool HALVES = BT == 256 && BN == 256;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[C::LDS_B];
+    const int J = MODE == DP_Y ? a.N : a.K, nn = (J + BN - 1) / BN;
+    int half = -1;                                                // 0, 1: a tile's first or second half
+    auto pick = [&](int total) {
+        const int block = blockIdx.x;
+        const int rest = HALVES && a.slices == 1 ? total & 255 : 0, whole = rest > 128 ? total : total - rest;
+        if (whole == total || block < whole) return xcd_tile(block, whole);
+        const int h = xcd_tile(block - whole, 2 * rest);
+        if (h < 0) return -1;
+        half = h & 1;
+        return whole + (h >> 1);
+    };
+    DpTile d{};
+    if constexpr (MODE >= DP_DW) {
+        const int ni = (a.N + BT - 1) / BT, each = a.M * ni * nn;
+        const int b = pick(each * a.slices);
+        if (b < 0) return;
+        d.z = b / each;
+        const int in = b - d.z * each;
+        d.mat = in / (ni * nn);
+        const int tile = in - d.mat * (ni * nn);
+        d.i0 = tile / nn * BT;
+        d.i1 = min(a.N, d.i0 + BT);
+        d.j0 = tile % nn * BN;
+        d.c0 = a.offsets ? min(max(a.offsets[d.mat], 0), a.R) : 0;
+        d.clen = (a.offsets ? min(max(a.offsets[d.mat + 1], d.c0), a.R) : a.R) - d.c0;
+    } else {
+        const RowTile t = row_tile<BT>(a.offsets, a.M, a.R, [&](int rows) {
+            rows = min(rows, a.row_tiles);                       // more only where offsets descend
+            const int each = rows * nn;
+            int b = pick(each * a.slices);
+            if (b < 0) return -1;
+            d.z = b / each;
+            b -= d.z * each;
+            // down groups of 8 row tiles before a column tile on
+            const int grp = b / (8 * nn), left = min(8, rows - 8 * grp), in = b - grp * 8 * nn;
+            d.j0 = in / left * BN;
+            return 8 * grp + in % left;
+        });
+        if (t.r1 == 0) return;
+        d.mat = t.m;
+        d.i0 = t.r0;
+        d.i1 = t.r1;
+        d.clen = MODE == DP_Y ? a.K : a.N;
+    }
+    if constexpr (HALVES) {
+        if (half >= 0) {
+            d.i0 += half * (BT / 2);
+            d.i1 = min(d.i1, d.i0 + BT / 2);
+            if (d.i0 < d.i1) dp_body<MODE, BT / 2, BN, WIDE>(a, d, lds);
+            return;
+        }
+    }
+    dp_body<MODE, BT, BN, WIDE>(a, d, lds);
+}
+
 // ------------------------------------------------------------------ sums ---------
 // out[i] = the slices of row i, or of the rows of token i in slot order, added in
 // order.  Rows past the matrices' (which no tile has written) are left as they were, or
@@ -545,29 +581,62 @@ bool wide_rows(const DenseProduct& a, int mode) {
     return rows * x >= (1ll << 31) || 256 * (mode == DP_Y ? 0 : a.dy_stride) >= (1ll << 31);
 }
 
+// Tile sizes and slices of c: the least of an estimate in us from measured times.  A
+// launch takes 4; a tile takes `fixed` (its first loads, its way out) and a step of 64 of
+// c `alone` where it has a compute unit to itself, `full` where `fit` tiles share it (as
+// many as the LDS holds); slices are joined by a launch more and pass through memory
+// twice.  Measured with 2000 rows of 4096 x 4096 (a round of 64 steps on all of the chip)
+// and 64 rows (tiles alone).  What it chooses between (us, T x M x N x K, tiles i x j /
+// slices): y of 2000 x 1 x 4096 x 4096 256x128 61, 256x256 86, 64x64 98; 500 x 1 x 2048 x
+// 2048 64x64 12, 256x256 40; 64 x 1 x 4096 x 4096 64x64/8 15, 64x64 29; dx of 4096 tokens'
+// four of 64 x 512 x 1024 128x128 35, 256x256 40; dW of 16384 x 1 x 128 x 4096 64x256/8 34,
+// 64x256 149.
 DpPlan plan(const DenseProduct& a, int mode) {
-    DpPlan p{};
-    const int J = mode == DP_Y ? a.N : a.K;
-    const int live = a.M < a.R ? a.M : (a.R ? a.R : 1);
-    const int64_t avg = mode == DP_DW ? a.N : ((int64_t)a.R + live - 1) / live;
-    p.bt = avg <= 64 ? 64 : avg <= 128 ? 128 : 256;
-    p.bn = J <= 64 ? 64 : J <= 128 ? 128 : 256;
-    const auto tiles = [&] {
-        const int64_t nn = (J + p.bn - 1) / p.bn;
-        return mode == DP_DW ? (int64_t)a.M * ((a.N + p.bt - 1) / p.bt) * nn : max_row_tiles(a, p.bt) * nn;
-    };
-    while (tiles() < 200 && p.bt > 64) p.bt /= 2;
-    const int64_t c = mode == DP_Y ? a.K : mode == DP_DX ? a.N : ((int64_t)a.R + live - 1) / live;
-    const int steps = (int)((c + 31) / 32);
-    p.slices = 1;
-    while (tiles() * p.slices * 2 <= 512 && p.slices < 16 && steps >= 16 * p.slices) p.slices *= 2;
-    return p;
+    struct Cost { int bt, bn, fit; float fixed, alone, full, dw_full; };
+    static constexpr Cost kTiles[9] = {
+        {64, 64, 4, 2.6f, 0.37f, 0.73f, 1.05f},  {64, 128, 2, 2.8f, 0.44f, 0.69f, 0.92f},  {64, 256, 1, 3.2f, 0.54f, 0.66f, 0.69f},
+        {128, 64, 2, 2.8f, 0.42f, 0.63f, 0.69f}, {128, 128, 2, 3.6f, 0.55f, 1.20f, 1.13f}, {128, 256, 1, 4.2f, 0.65f, 0.97f, 0.99f},
+        {256, 64, 1, 3.4f, 0.55f, 0.73f, 0.74f}, {256, 128, 1, 4.2f, 0.63f, 0.97f, 0.99f}, {256, 256, 1, 6.5f, 1.05f, 1.40f, 1.52f}};
+    const int J = mode == DP_Y ? a.N : a.K, live = a.M < a.R ? a.M : (a.R ? a.R : 1);
+    const float each = (float)a.R / live;                         // rows of a matrix, on average
+    const float c = mode == DP_Y ? a.K : mode == DP_DX ? a.N : each;
+    const int steps = (int)((c + 63) / 64) > 0 ? (int)((c + 63) / 64) : 1;
+    const double out = mode == DP_DW ? (double)a.M * a.N * a.K : (double)a.R * J;
+    DpPlan best{};
+    float least = 0;
+    for (const Cost& t : kTiles) {
+        const float nn = (J + t.bn - 1) / t.bn, q = each / t.bt, up = (float)(int)(q + 0.9f);
+        // row tiles of a matrix: among few matrices the last one is half empty on average; many
+        // (routed experts) have about as many rows each
+        const float rows = a.M == 1 ? (float)((a.R + t.bt - 1) / t.bt) : (float)live * (a.M < 64 ? q + 0.5f : up > q + 0.25f ? up : q + 0.25f);
+        const float tiles = nn * (mode == DP_DW ? (float)a.M * ((a.N + t.bt - 1) / t.bt) : rows);
+        const float full = mode == DP_DW ? t.dw_full : t.full;
+        const int fit = mode == DP_DW && t.bt + t.bn == 256 && t.bt == 128 ? 1 : t.fit;   // (gathered x rows do not fit beside two)
+        for (int z = 1; z <= 16 && (z == 1 || (steps >= 2 * z && tiles * z < 4096)); z *= 2) {
+            const float n = tiles * z / 256, chain = t.fixed + (float)((steps + z - 1) / z) * full;     // a full round
+            const int rounds = (int)(n / fit);
+            const float rest = n - rounds * fit;                // tiles a compute unit in the last round
+            float us = 4 + rounds * chain;
+            if (rest > 0 && rest <= 0.5f && t.bt + t.bn == 512 && z == 1) {   // tiles of half the rows
+                us += 4.2f + steps * 0.97f;
+            } else if (rest > 0) {
+                const float share = fit == 1 ? (rounds ? 1.f : rest) : (rest < 1 ? 0.f : (rest - 1) / (fit - 1));
+                us += t.fixed + (float)((steps + z - 1) / z) * (t.alone + (full - t.alone) * (share < 1 ? share : 1.f));
+            }
+            if (z > 1) us += 4 + 0.15f * z + (float)(out * (8 * z + 2) / 5e6);
+            if (!best.bt || us < least) {
+                least = us;
+                best = DpPlan{t.bt, t.bn, z};
+            }
+        }
+    }
+    return best;
 }
 
 template <int MODE, int BT, int BN, bool WIDE = false>
 hipError_t launch_tile(const DenseProduct& a, int64_t blocks, hipStream_t s) {
     prof_begin(s);
-    dp_tile<MODE, BT, BN, WIDE><<<(unsigned)((blocks + 7) & ~7ll), DpCfg<MODE, BT, BN>::NW * 64, 0, s>>>(a);
+    dp_tile<MODE, BT, BN, WIDE><<<(unsigned)((blocks + (BT + BN == 512 ? 128 : 0) + 7) & ~7ll), DpCfg<MODE, BT, BN>::NW * 64, 0, s>>>(a);
     prof_end(s, MODE == DP_Y ? "dp_tile_y" : MODE == DP_DX ? "dp_tile_dx" : "dp_tile_dw");
     return hipGetLastError();
 }
@@ -611,9 +680,9 @@ hipError_t launch_join(const DpJoin& j, hipStream_t s) {
 // How many times 16 rows of a matrix dp_stream takes at once (0: not dp_stream).
 int stream_rows(const DenseProduct& a) {
     const int live = a.M < a.R ? a.M : a.R;
-    const int64_t avg = ((int64_t)a.R + live - 1) / live, cols = (a.N + 31) / 32;
-    for (int ns = 1; ns <= 4; ns *= 2)
-        if (max_row_tiles(a, 16 * ns) * cols <= 256 || avg <= 16 * ns) return ns;
+    const int64_t avg = ((int64_t)a.R + live - 1) / live;
+    for (int ns = 1; ns <= 2; ns *= 2)
+        if (avg <= 16 * ns) return ns;
     return 0;
 }
 
@@ -645,7 +714,6 @@ hipError_t launch_dense_product(DenseProduct a, void* ws, hipStream_t s) {
     switch (stream_rows(a)) {
         case 1: return launch_stream<1>(a, s);
         case 2: return launch_stream<2>(a, s);
-        case 4: return launch_stream<4>(a, s);
         default: break;
     }
     const DpPlan p = plan(a, DP_Y);

@@ -27,7 +27,7 @@ CASES = [
     (70, 1, 520, 264, 0), (129, 1, 136, 1000, 0), (257, 1, 264, 520, 0), (1000, 1, 2048, 1024, 0), (3000, 1, 16, 2048, 0),
     (2500, 1, 2048, 16, 0), (1, 64, 128, 512, 8), (8, 512, 128, 1024, 10), (96, 64, 128, 512, 4), (300, 8, 64, 264, 3),
     (1501, 8, 16, 1024, 3), (777, 5, 520, 776, 0), (2000, 8, 1024, 512, 0), (900, 200, 40, 72, 7), (600, 1024, 8, 64, 5),
-    (4096, 3, 768, 1544, 2),
+    (4096, 3, 768, 1544, 2), (5300, 1, 4104, 264, 0), (5000, 3, 4096, 328, 0), (300, 2, 4360, 4360, 0),
 ]
 
 
