@@ -26,6 +26,7 @@ namespace {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 
 EM_DEV uint4 ldg16(const void* p) { return *reinterpret_cast<const uint4*>(p); }
@@ -224,7 +225,6 @@ EM_DEV void dp_body(const DenseProduct& a, const DpTile& t, uint8_t* lds) {
     using C = DpCfg<MODE, BT, BN>;
     constexpr int NI = C::NI, NJ = C::NJ;
     const int lane = lane_id(), wv = wave_id(), g = lane >> 4, m = lane & 15;
-    const int J = MODE == DP_Y ? a.N : a.K;
     const int mat = t.mat, i0 = t.i0, i1 = t.i1, j0 = t.j0, z = t.z, c0 = t.c0, clen = t.clen;
     const int steps = (clen + 63) >> 6, whole_steps = clen >> 6;
     const int s0 = (int)((int64_t)steps * z / a.slices), s1 = (int)((int64_t)steps * (z + 1) / a.slices);
@@ -410,12 +410,14 @@ EM_DEV void dp_body(const DenseProduct& a, const DpTile& t, uint8_t* lds) {
     }
 
     // ---- out, sixteen rows of a wave at a time through the LDS, so that whole row segments
-    // are stored: lane (g, m) holds columns 4 g .. 4 g + 3 of each j subtile, row m
+    // are stored: lane (g, m) holds columns 4 g .. 4 g + 3 of each j subtile, row m.  out itself
+    // is stored past the caches (8192^3 814 -> 797 us, dW of 5001 rows 8 x 4096 x 8192 433 ->
+    // 395), partial sums are read again and are not.
     const int rows = MODE >= DP_DW ? a.M * a.N : a.R;
     const bool whole = a.slices == 1 && !a.to_part;
-    void* out = whole ? a.out : a.part + (int64_t)z * rows * J;
-    const int64_t stride = whole ? a.out_stride : J;
-    const int f32 = whole ? a.out_f32 : 1;
+    const int64_t stride = whole ? a.out_stride : a.cols;
+    void* out = whole ? a.out : a.part + (int64_t)z * rows * a.cols - a.col0;
+    const int f32 = whole ? a.out_f32 : 1, J = a.col0 + a.cols;
     const int64_t r0 = (MODE >= DP_DW ? (int64_t)mat * a.N : 0) + i0 + 16 * NJ * wt;
     const int left = i1 - i0 - 16 * NJ * wt, col0 = j0 + 16 * NI * wn;
     constexpr int RS = NI * 64 + 16;
@@ -435,8 +437,11 @@ EM_DEV void dp_body(const DenseProduct& a, const DpTile& t, uint8_t* lds) {
             for (int i = 0; i < 16 / RPI; ++i) {
                 const int tr = RPI * i + lane / LPR, col = col0 + 4 * (lane % LPR);
                 const floatx4 v = *reinterpret_cast<const floatx4*>(o + tr * RS + 16 * (lane % LPR));
-                if (16 * j + tr < left && col < J)
-                    *reinterpret_cast<floatx4*>(static_cast<float*>(out) + (r0 + 16 * j + tr) * stride + col) = v;
+                floatx4* to = reinterpret_cast<floatx4*>(static_cast<float*>(out) + (r0 + 16 * j + tr) * stride + col);
+                if (16 * j + tr < left && col < J) {
+                    if (whole) __builtin_nontemporal_store(v, to);
+                    else *to = v;
+                }
             }
         } else {
             constexpr int LPR = NI * 2, RPI = 64 / LPR;
@@ -446,9 +451,9 @@ EM_DEV void dp_body(const DenseProduct& a, const DpTile& t, uint8_t* lds) {
                 if (tr >= 16) continue;
                 const floatx4 u = *reinterpret_cast<const floatx4*>(o + tr * RS + 32 * (lane % LPR));
                 const floatx4 v = *reinterpret_cast<const floatx4*>(o + tr * RS + 32 * (lane % LPR) + 16);
+                const u32x4 w = {pack2(u.x, u.y), pack2(u.z, u.w), pack2(v.x, v.y), pack2(v.z, v.w)};
                 if (16 * j + tr < left && col < J)
-                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + (r0 + 16 * j + tr) * stride + col) =
-                        make_uint4(pack2(u.x, u.y), pack2(u.z, u.w), pack2(v.x, v.y), pack2(v.z, v.w));
+                    __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + (r0 + 16 * j + tr) * stride + col));
             }
         }
         __builtin_amdgcn_wave_barrier();
@@ -465,7 +470,7 @@ dp_tile(DenseProduct a) {
     using C = DpCfg<MODE, BT, BN>;
     constexpr bool HALVES = BT == 256 && BN == 256;
     __shared__ __attribute__((aligned(16))) uint8_t lds[C::LDS_B];
-    const int J = MODE == DP_Y ? a.N : a.K, nn = (J + BN - 1) / BN;
+    const int nn = (a.cols + BN - 1) / BN;
     int half = -1;                                                // 0, 1: a tile's first or second half
     auto pick = [&](int total) {
         const int block = blockIdx.x;
@@ -500,7 +505,7 @@ dp_tile(DenseProduct a) {
             b -= d.z * each;
             // down groups of 8 row tiles before a column tile on
             const int grp = b / (8 * nn), left = min(8, rows - 8 * grp), in = b - grp * 8 * nn;
-            d.j0 = in / left * BN;
+            d.j0 = a.col0 + in / left * BN;
             return 8 * grp + in % left;
         });
         if (t.r1 == 0) return;
@@ -655,7 +660,8 @@ hipError_t launch_tile(DenseProduct a, DpPlan p, hipStream_t s) {
     const bool wide = wide_rows(a, MODE);
     if (wide) p.bt = p.bn = 128;
     else if (MODE == DP_DWG && p.bt + p.bn == 512) p.bt = 128;     // the x rows have no place beside the largest tiles
-    const int J = MODE == DP_Y ? a.N : a.K, nn = (J + p.bn - 1) / p.bn;
+    if (!a.cols) a.cols = MODE == DP_Y ? a.N : a.K;
+    const int nn = (a.cols + p.bn - 1) / p.bn;
     a.slices = p.slices;
     a.row_tiles = (int)max_row_tiles(a, p.bt);
     const int64_t rows = MODE >= DP_DW ? (int64_t)a.M * ((a.N + p.bt - 1) / p.bt) : a.row_tiles;
@@ -723,13 +729,24 @@ hipError_t launch_dense_product(DenseProduct a, void* ws, hipStream_t s) {
     return launch_join(DpJoin{a.part, p.slices, a.R, a.N, a.out, a.out_stride, a.out_f32, a.R, a.offsets, a.M, nullptr, 0}, s);
 }
 
+// Columns of dx that are made for tokens at once: their rows' partial sums then stay in the
+// 256 MB memory-side cache between the two launches (16384 tokens' ten of 512 x 128 x 4096: 1565 us at once, 1419 so;
+// 48 and 96 MB at once measured more on the smaller ones).
+int token_cols(const DenseProduct& a, int slices) {
+    const int64_t fit = (192ll << 20) / ((int64_t)a.R * slices * 4 + 1);
+    const int64_t cols = fit / 256 * 256;
+    return cols < 256 ? 256 : cols < a.K ? (int)cols : a.K;
+}
+
 // dx's partial sums (or rows, for tokens) and dW's share the workspace: dW runs first.
 size_t dense_backward_ws_bytes(const DenseProduct& a) {
-    const DpPlan pw = plan(a, DP_DW);
-    const size_t w = pw.slices > 1 ? part_bytes(a, DP_DW, pw.slices) : 256;
-    if (!a.R) return w;
-    const size_t x = part_bytes(a, DP_DX, plan(a, DP_DX).slices);
-    return w > x ? w : x;
+    const DpPlan pw = plan(a, DP_DW), px = plan(a, DP_DX);
+    size_t w = pw.slices > 1 ? part_bytes(a, DP_DW, pw.slices) : 256;
+    const size_t x = px.slices > 1 ? part_bytes(a, DP_DX, px.slices) : 0;
+    const int cols = token_cols(a, px.slices);
+    const size_t t = up((size_t)px.slices * a.R * (cols < a.K ? cols : a.K) * 4);
+    if (x > w) w = x;
+    return t > w ? t : w;
 }
 
 hipError_t launch_dense_backward(const DenseGrad& gr, void* ws, hipStream_t s) {
@@ -748,14 +765,23 @@ hipError_t launch_dense_backward(const DenseGrad& gr, void* ws, hipStream_t s) {
     if (!gr.dx) return hipSuccess;
     const DpPlan p = plan(a, DP_DX);
     a.out = gr.dx; a.out_stride = gr.dx_stride; a.out_f32 = gr.dx_f32;
-    a.to_part = gr.token_rows != nullptr;
-    if (a.R) {
-        const hipError_t e = launch_tile<DP_DX>(a, p, s);
+    if (!gr.token_rows) {
+        const hipError_t e = a.R ? launch_tile<DP_DX>(a, p, s) : hipSuccess;
+        if (e != hipSuccess || p.slices == 1) return e;
+        return launch_join(DpJoin{a.part, p.slices, a.R, a.K, gr.dx, gr.dx_stride, gr.dx_f32, a.R, a.offsets, a.M, nullptr, 0}, s);
+    }
+    a.to_part = 1;
+    for (a.col0 = 0; a.col0 < a.K; a.col0 += a.cols) {
+        const int most = token_cols(a, p.slices);
+        a.cols = a.K - a.col0 < most ? a.K - a.col0 : most;
+        hipError_t e = a.R ? launch_tile<DP_DX>(a, p, s) : hipSuccess;
+        void* dx = static_cast<char*>(gr.dx) + (int64_t)a.col0 * (gr.dx_f32 ? 4 : 2);
+        if (e == hipSuccess)
+            e = launch_join(DpJoin{a.part, p.slices, a.R, a.cols, dx, gr.dx_stride, gr.dx_f32, a.T, a.offsets, a.M, gr.token_rows,
+                                   gr.per_token}, s);
         if (e != hipSuccess) return e;
     }
-    if (p.slices == 1 && !a.to_part) return hipSuccess;
-    return launch_join(DpJoin{a.part, p.slices, a.R, a.K, gr.dx, gr.dx_stride, gr.dx_f32, a.to_part ? a.T : a.R, a.offsets, a.M,
-                              gr.token_rows, gr.per_token}, s);
+    return hipSuccess;
 }
 
 }  // namespace em

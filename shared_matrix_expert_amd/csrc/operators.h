@@ -126,6 +126,7 @@ struct DenseProduct {
     const uint16_t* dy; int64_t dy_stride;
     void* out; int64_t out_stride; int out_f32;
     int slices, row_tiles, to_part;
+    int col0, cols;             // columns of out that a launch makes
     float* part;                // workspace: [slices][rows][columns] of out
 };
 struct DenseGrad {
