@@ -690,16 +690,18 @@ def mx_weights(dense: dict, stream=None) -> dict:
 # ------------------------------------------------ norm, dense and int4 matrices ----
 
 def _rows(t, count: int, cols: int, what: str):
-    """(address, stride) of a tensor of `count` rows of `cols`, at one stride; (None, 0) for None."""
+    """(address, stride) of a tensor of `count` rows of `cols`, at one stride; (0, 0) for None."""
     if t is None:
-        return None, 0
-    if t.dim() < 2 or t.shape[-1] != cols or t.numel() != count * cols:
+        return 0, 0
+    if t.numel() != count * cols or t.dim() < 2 or t.size(-1) != cols:
         raise ValueError(f"{what}: expected {count} rows of {cols}, got {tuple(t.shape)}")
-    return t.data_ptr(), _row_stride(t)
+    return t.data_ptr(), cols if t.is_contiguous() else _row_stride(t)
 
 
 def _bf16_rows(t, count: int, cols: int, what: str):
-    if t is not None and _dense_type(t) != _BF16:
+    if t is None:
+        return 0, 0
+    if _dense_types.get(t.dtype) != _BF16:
         raise ValueError(f"{what}: expected bfloat16 (or int16 bits), got {t.dtype}")
     return _rows(t, count, cols, what)
 
@@ -711,22 +713,28 @@ def _vector(t, count: int, what: str) -> int:
     return t.data_ptr()
 
 
+def _rows_of(x):
+    """(T, d) of a tensor of T rows of d values."""
+    if x.dim() < 2:
+        raise ValueError("x must be rows: a tensor of at least two dimensions")
+    d = x.size(-1)
+    T = x.numel() // (d or 1)
+    return (T, d) if T <= 0x7FFFFFFF >= d else (_i32(T), _i32(d))
+
+
 def edge_moe_norm(x, gain, eps, add=None, x_out=None, y=None, codes=None, scales=None, rstd=None, stream=None) -> None:
     """r = bf16(x + add) to x_out, y = bf16(r rstd gain) with rstd = 1 / sqrt(mean r^2
     + eps), and y's MXFP8 codes [..., T, d] and scales [..., d/128, T, 4]: those of
     the outputs that are given.  x, x_out, y bf16 rows [T][d] at one stride, add bf16
     or float32, gain [d] bf16 or float32."""
     lib = load()
-    if x.dim() < 2:
-        raise ValueError("x must be rows: a tensor of at least two dimensions")
-    d = x.shape[-1]
-    T = x.numel() // (d or 1)
+    T, d = _rows_of(x)
     dev = _same_device(x, gain, add, x_out, y, codes, scales, rstd)
-    a = CNormArgs(_i32(T), _i32(d), eps, 0 if add is None else _dense_type(add), _dense_type(gain), *_bf16_rows(x, T, d, "x"),
-                  *_rows(add, T, d, "add"), _vector(gain, d, "gain"), *_bf16_rows(x_out, T, d, "x_out"),
-                  *_bf16_rows(y, T, d, "y"), _sized(codes, "uint8", T * d, "codes"),
-                  _sized(scales, "uint8", T * (d // 32), "scales"), _sized(rstd, "float32", T, "rstd"))
-    st = lib.edge_moe_norm(a, _stream_on(dev, stream))
+    a = _pack_norm(T, d, eps, 0 if add is None else _dense_type(add), _dense_type(gain), *_bf16_rows(x, T, d, "x"),
+                   *_rows(add, T, d, "add"), _vector(gain, d, "gain"), *_bf16_rows(x_out, T, d, "x_out"),
+                   *_bf16_rows(y, T, d, "y"), _sized(codes, "uint8", T * d, "codes") or 0,
+                   _sized(scales, "uint8", T * (d // 32), "scales") or 0, _sized(rstd, "float32", T, "rstd") or 0)
+    st = lib.edge_moe_norm(CNormArgs.from_buffer_copy(a), _stream_on(dev, stream))
     if st != EDGE_MOE_OK:
         raise EdgeMoeError("edge_moe_norm", st)
 
@@ -740,21 +748,23 @@ def edge_moe_norm_backward(x, gain, rstd, dy, ws, dres=None, dx=None, dgain=None
     was added): dx = dres + the gradient through y, dgain [d] float32.  dy, dres and
     dx rows of one type, bf16 or float32."""
     lib = load()
-    if x.dim() < 2:
-        raise ValueError("x must be rows: a tensor of at least two dimensions")
-    d = x.shape[-1]
-    T = x.numel() // (d or 1)
+    T, d = _rows_of(x)
     kind = _dense_type(dy)
-    for t, what in ((dres, "dres"), (dx, "dx")):
-        if t is not None and _dense_type(t) != kind:
-            raise ValueError(f"{what} must be of dy's type, got {t.dtype} and {dy.dtype}")
+    if (dres is not None and _dense_type(dres) != kind) or (dx is not None and _dense_type(dx) != kind):
+        raise ValueError(f"dres and dx must be of dy's type, {dy.dtype}")
     dev = _same_device(x, gain, rstd, dy, ws, dres, dx, dgain)
-    g = CNormGrad(_i32(T), _i32(d), _dense_type(gain), kind, *_bf16_rows(x, T, d, "x"), _vector(gain, d, "gain"),
-                  _sized(rstd, "float32", T, "rstd"), *_rows(dy, T, d, "dy"), *_rows(dres, T, d, "dres"),
-                  *_rows(dx, T, d, "dx"), _sized(dgain, "float32", d, "dgain"))
-    st = lib.edge_moe_norm_backward(g, _ptr(ws), ws.numel() * ws.element_size(), _stream_on(dev, stream))
+    g = _pack_norm_grad(T, d, _dense_type(gain), kind, *_bf16_rows(x, T, d, "x"), _vector(gain, d, "gain"),
+                        _sized(rstd, "float32", T, "rstd"), *_rows(dy, T, d, "dy"), *_rows(dres, T, d, "dres"),
+                        *_rows(dx, T, d, "dx"), _sized(dgain, "float32", d, "dgain") or 0)
+    st = lib.edge_moe_norm_backward(CNormGrad.from_buffer_copy(g), _ptr(ws), ws.numel() * ws.element_size(), _stream_on(dev, stream))
     if st != EDGE_MOE_OK:
         raise EdgeMoeError("edge_moe_norm_backward", st)
+
+
+# the structs' layouts (native alignment), packed without a conversion per field
+_pack_norm = struct.Struct("iifii4xPqPqPPqPqPPP").pack
+_pack_norm_grad = struct.Struct("iiiiPqPPPqPqPqP").pack
+_pack_dense_grad = struct.Struct("PqPqPPPi4xPPqiiP").pack
 
 
 def _dense_dims(T, R, M, N, K) -> CDenseDims:
@@ -763,9 +773,10 @@ def _dense_dims(T, R, M, N, K) -> CDenseDims:
 
 def _matrices(w, what: str):
     """(M, N, K) and address of contiguous bf16 matrices [M][N][K] or one [N][K]."""
-    if w.dim() not in (2, 3) or _dense_type(w) != _BF16 or not w.is_contiguous():
+    n = w.dim()
+    if n not in (2, 3) or _dense_type(w) != _BF16 or not w.is_contiguous():
         raise ValueError(f"{what}: expected contiguous bfloat16 matrices [M][N][K]")
-    return (1 if w.dim() == 2 else w.shape[0]), w.shape[-2], w.shape[-1], w.data_ptr()
+    return (1 if n == 2 else w.size(0)), w.size(-2), w.size(-1), w.data_ptr()
 
 
 def edge_moe_dense_product_ws_bytes(T, R, M, N, K) -> int:
@@ -804,33 +815,29 @@ def edge_moe_dense_product_backward(dy, ws, x=None, w=None, dx=None, dw=None, of
     if (dx is not None and w is None) or (dw is not None and x is None):
         raise ValueError("dx needs w, dw needs x")
     R, N = dy.shape
-    M, K = None, None
-    for t, what in ((dw, "dw"), (w if dx is not None else None, "w")):
-        if t is None:
-            continue
-        if t.dim() not in (2, 3) or not t.is_contiguous() or (M is not None and (M, K) != ((1 if t.dim() == 2 else t.shape[0]), t.shape[-1])):
-            raise ValueError("w and dw must be contiguous matrices [M][N][K] of one shape")
-        M, K = (1 if t.dim() == 2 else t.shape[0]), t.shape[-1]
-        if t.shape[-2] != N:
-            raise ValueError(f"{what}: expected {N} rows a matrix, got {t.shape[-2]}")
+    like = dw if dx is None else w
+    M, K = (1 if like.dim() == 2 else like.size(0)), like.size(-1)
+    for t in (w if dx is not None else None, dw):
+        if t is not None and (t.dim() not in (2, 3) or not t.is_contiguous() or t.size(-2) != N or t.size(-1) != K or t.numel() != M * N * K):
+            raise ValueError(f"w and dw: expected contiguous matrices {M} x {N} x {K}, got {tuple(t.shape)}")
     if dx is not None and _dense_type(w) != _BF16:
         raise ValueError(f"w: expected bfloat16 (or int16 bits), got {w.dtype}")
     k = 0
     if token_rows is not None:
         if token_rows.dim() != 2:
             raise ValueError("token_rows must be [T][k]")
-        k = token_rows.shape[1]
-    T = x.shape[0] if dw is not None else token_rows.shape[0] if token_rows is not None else 1
+        k = token_rows.size(1)
     if dw is not None and x.dim() != 2:
         raise ValueError("x must be rows [T][K]")
+    T = x.size(0) if dw is not None else token_rows.size(0) if token_rows is not None else 1
     dev = _same_device(dy, ws, x, w, dx, dw, offsets, row_src, token_rows)
-    g = CDenseGrad(*_bf16_rows(dy, R, N, "dy"), *(_bf16_rows(x, T, K, "x") if dw is not None else (None, 0)),
-                   _sized(row_src, "int32", R, "row_src"), _sized(offsets, "int32", M + 1, "offsets"),
-                   _sized(token_rows, "int32", T * k, "token_rows"), k, None if dx is None else w.data_ptr(),
-                   *_rows(dx, T if k else R, K, "dx"), 0 if dx is None else _dense_type(dx),
-                   0 if dw is None else _dense_type(dw), None if dw is None else dw.data_ptr())
-    st = lib.edge_moe_dense_product_backward(_dense_dims(T, R, M, N, K), g, _ptr(ws), ws.numel() * ws.element_size(),
-                                             _stream_on(dev, stream))
+    g = _pack_dense_grad(*_bf16_rows(dy, R, N, "dy"), *(_bf16_rows(x, T, K, "x") if dw is not None else (0, 0)),
+                         _sized(row_src, "int32", R, "row_src") or 0, _sized(offsets, "int32", M + 1, "offsets") or 0,
+                         _sized(token_rows, "int32", T * k, "token_rows") or 0, _i32(k), 0 if dx is None else w.data_ptr(),
+                         *_rows(dx, T if k else R, K, "dx"), 0 if dx is None else _dense_type(dx),
+                         0 if dw is None else _dense_type(dw), 0 if dw is None else dw.data_ptr())
+    st = lib.edge_moe_dense_product_backward(_dense_dims(T, R, M, N, K), CDenseGrad.from_buffer_copy(g), _ptr(ws),
+                                             ws.numel() * ws.element_size(), _stream_on(dev, stream))
     if st != EDGE_MOE_OK:
         raise EdgeMoeError("edge_moe_dense_product_backward", st)
 

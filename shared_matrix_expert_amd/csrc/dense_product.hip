@@ -483,13 +483,22 @@ dp_tile(DenseProduct a) {
     };
     DpTile d{};
     if constexpr (MODE >= DP_DW) {
-        const int ni = (a.N + BT - 1) / BT, each = a.M * ni * nn;
-        const int b = pick(each * a.slices);
-        if (b < 0) return;
-        d.z = b / each;
-        const int in = b - d.z * each;
-        d.mat = in / (ni * nn);
-        const int tile = in - d.mat * (ni * nn);
+        const int ni = (a.N + BT - 1) / BT, tiles = ni * nn, each = a.M * tiles;
+        int tile;
+        if (a.M == 1 || tiles < 8) {
+            const int b = pick(each * a.slices);
+            if (b < 0) return;
+            d.z = b / each;
+            const int in = b - d.z * each;
+            d.mat = in / tiles;
+            tile = in - d.mat * tiles;
+        } else {                                                  // rows differ by matrix: every XCD takes a part of each
+            const int per = (tiles + 7) >> 3, at = blockIdx.x >> 3, q = at / per;
+            tile = (blockIdx.x & 7) * per + at - q * per;
+            d.z = q / a.M;
+            d.mat = q - d.z * a.M;
+            if (tile >= tiles || d.z >= a.slices) return;
+        }
         d.i0 = tile / nn * BT;
         d.i1 = min(a.N, d.i0 + BT);
         d.j0 = tile % nn * BN;
@@ -528,23 +537,10 @@ dp_tile(DenseProduct a) {
 // ------------------------------------------------------------------ sums ---------
 // out[i] = the slices of row i, or of the rows of token i in slot order, added in
 // order.  Rows past the matrices' (which no tile has written) are left as they were, or
-// add nothing to a token.
-struct DpJoin {
-    const float* part;
-    int slices;
-    int64_t rows;                   // of a slice
-    int cols;
-    void* out;
-    int64_t out_stride;
-    int out_f32;
-    int64_t out_rows;
-    const int32_t* offsets; int M;  // rows offsets[0] .. offsets[M] - 1 are written; null: all
-    const int32_t* token_rows; int per_token;
-};
-
+// add nothing to a token.  Bound by the partial sums' bytes.
 __global__ void __launch_bounds__(256)
-dp_join(DpJoin a) {
-    const int quads = a.cols / 4;
+dp_join(RowJoin a) {
+    const int quads = (a.cols + 3) / 4;
     const int64_t i = blockIdx.x * 256ll + threadIdx.x;
     const int64_t row = i / quads;
     const int col = (int)(i - row * quads) * 4;
@@ -559,16 +555,35 @@ dp_join(DpJoin a) {
         for (int j = 0; j < a.per_token; ++j) {
             const int64_t r = a.token_rows[row * a.per_token + j];
             if (r < lo || r >= hi) continue;
-            for (int z = 0; z < a.slices; ++z) s += *reinterpret_cast<const floatx4*>(a.part + (z * a.rows + r) * a.cols + col);
+            for (int z = 0; z < a.slices; ++z) s += *reinterpret_cast<const floatx4*>(a.part + (z * a.rows + r) * (4 * quads) + col);
         }
     } else {
         if (row < lo || row >= hi) return;
-        for (int z = 0; z < a.slices; ++z) s += *reinterpret_cast<const floatx4*>(a.part + (z * a.rows + row) * a.cols + col);
+        for (int z = 0; z < a.slices; ++z) s += *reinterpret_cast<const floatx4*>(a.part + (z * a.rows + row) * (4 * quads) + col);
     }
-    store4(a.out, a.out_f32, row * a.out_stride + col, s);
+    const int64_t at = row * a.out_stride + col;
+    if (a.whole) {
+        store4(a.out, a.out_f32, at, s);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (col + i >= a.cols) break;
+        if (a.out_f32) static_cast<float*>(a.out)[at + i] = s[i];
+        else static_cast<uint16_t*>(a.out)[at + i] = (uint16_t)pack2(s[i], s[i]);
+    }
 }
 
 // ------------------------------------------------------------------ host side ----
+hipError_t launch_join(const RowJoin& j, hipStream_t s) {
+    const int64_t n = j.out_rows * ((j.cols + 3) / 4);
+    if (!n) return hipSuccess;
+    prof_begin(s);
+    dp_join<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(j);
+    prof_end(s, "dp_join");
+    return hipGetLastError();
+}
+
 namespace {
 
 // Row tiles of BT rows that R rows in M matrices can make at most.
@@ -664,23 +679,14 @@ hipError_t launch_tile(DenseProduct a, DpPlan p, hipStream_t s) {
     const int nn = (a.cols + p.bn - 1) / p.bn;
     a.slices = p.slices;
     a.row_tiles = (int)max_row_tiles(a, p.bt);
-    const int64_t rows = MODE >= DP_DW ? (int64_t)a.M * ((a.N + p.bt - 1) / p.bt) : a.row_tiles;
-    const int64_t blocks = rows * nn * p.slices;
+    const int64_t tiles = (MODE >= DP_DW ? (int64_t)((a.N + p.bt - 1) / p.bt) : a.row_tiles) * nn;   // (dW: of a matrix)
+    const int64_t blocks = (MODE >= DP_DW ? a.M * (a.M > 1 && tiles >= 8 ? (tiles + 7) & ~7ll : tiles) : tiles) * p.slices;
     if (wide) return launch_tile<MODE, 128, 128, true>(a, blocks, s);
     switch (p.bt) {
         case 64: return launch_tile<MODE, 64>(a, p.bn, blocks, s);
         case 128: return launch_tile<MODE, 128>(a, p.bn, blocks, s);
         default: return launch_tile<MODE, 256>(a, p.bn, blocks, s);
     }
-}
-
-hipError_t launch_join(const DpJoin& j, hipStream_t s) {
-    const int64_t n = j.out_rows * (j.cols / 4);
-    if (!n) return hipSuccess;
-    prof_begin(s);
-    dp_join<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(j);
-    prof_end(s, "dp_join");
-    return hipGetLastError();
 }
 
 // How many times 16 rows of a matrix dp_stream takes at once (0: not dp_stream).
@@ -726,7 +732,7 @@ hipError_t launch_dense_product(DenseProduct a, void* ws, hipStream_t s) {
     a.part = static_cast<float*>(ws);
     const hipError_t e = launch_tile<DP_Y>(a, p, s);
     if (e != hipSuccess || p.slices == 1) return e;
-    return launch_join(DpJoin{a.part, p.slices, a.R, a.N, a.out, a.out_stride, a.out_f32, a.R, a.offsets, a.M, nullptr, 0}, s);
+    return launch_join(RowJoin{a.part, p.slices, a.R, a.N, a.out, a.out_stride, a.out_f32, 1, a.R, a.offsets, a.M, nullptr, 0}, s);
 }
 
 // Columns of dx that are made for tokens at once: their rows' partial sums then stay in the
@@ -758,7 +764,7 @@ hipError_t launch_dense_backward(const DenseGrad& gr, void* ws, hipStream_t s) {
         hipError_t e = a.row_src ? launch_tile<DP_DWG>(a, p, s) : launch_tile<DP_DW>(a, p, s);
         if (e == hipSuccess && p.slices > 1) {
             const int64_t rows = (int64_t)a.M * a.N;
-            e = launch_join(DpJoin{a.part, p.slices, rows, a.K, gr.dw, a.K, gr.dw_f32, rows, nullptr, 0, nullptr, 0}, s);
+            e = launch_join(RowJoin{a.part, p.slices, rows, a.K, gr.dw, a.K, gr.dw_f32, 1, rows, nullptr, 0, nullptr, 0}, s);
         }
         if (e != hipSuccess) return e;
     }
@@ -768,7 +774,7 @@ hipError_t launch_dense_backward(const DenseGrad& gr, void* ws, hipStream_t s) {
     if (!gr.token_rows) {
         const hipError_t e = a.R ? launch_tile<DP_DX>(a, p, s) : hipSuccess;
         if (e != hipSuccess || p.slices == 1) return e;
-        return launch_join(DpJoin{a.part, p.slices, a.R, a.K, gr.dx, gr.dx_stride, gr.dx_f32, a.R, a.offsets, a.M, nullptr, 0}, s);
+        return launch_join(RowJoin{a.part, p.slices, a.R, a.K, gr.dx, gr.dx_stride, gr.dx_f32, 1, a.R, a.offsets, a.M, nullptr, 0}, s);
     }
     a.to_part = 1;
     for (a.col0 = 0; a.col0 < a.K; a.col0 += a.cols) {
@@ -777,7 +783,7 @@ hipError_t launch_dense_backward(const DenseGrad& gr, void* ws, hipStream_t s) {
         hipError_t e = a.R ? launch_tile<DP_DX>(a, p, s) : hipSuccess;
         void* dx = static_cast<char*>(gr.dx) + (int64_t)a.col0 * (gr.dx_f32 ? 4 : 2);
         if (e == hipSuccess)
-            e = launch_join(DpJoin{a.part, p.slices, a.R, a.cols, dx, gr.dx_stride, gr.dx_f32, a.T, a.offsets, a.M, gr.token_rows,
+            e = launch_join(RowJoin{a.part, p.slices, a.R, a.cols, dx, gr.dx_stride, gr.dx_f32, 1, a.T, a.offsets, a.M, gr.token_rows,
                                    gr.per_token}, s);
         if (e != hipSuccess) return e;
     }

@@ -5,10 +5,15 @@
 // cores and the sum is scaled by a float32 fused multiply-add: every weight is exactly
 // c s, as in the layer.
 //
-//   ip_stream  four waves split K and stream the codes straight into operand registers.
+//   ip_rows    few rows a matrix: bound by the code bytes.  Four waves split K, stream the
+//              codes into operand registers and keep the x rows in the LDS.
+//   ip_stream  the same for 17 to 32 rows, and where a tile's scales or rows lie too oddly:
+//              x straight from memory.
+//   ip_tile    many rows: LDS tiles by direct global -> LDS loads, counted by hand.
 #include <type_traits>
 
 #include "common.h"
+#include "lds_load.h"
 #include "mfma_ops.h"
 #include "operators.h"
 #include "row_tile.h"
@@ -19,6 +24,12 @@ namespace {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+EM_DEV uint32_t pack2(float a, float b) {
+    const f32x2 v = {a, b};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
 
 // x row of y row r, -1 where row_src names none.
 EM_DEV int x_row(const Int4Product& a, int r) {
@@ -31,8 +42,7 @@ EM_DEV void store1(void* out, int f32, int64_t at, float v) {
     if (f32) {
         static_cast<float*>(out)[at] = v;
     } else {
-        const f32x2 p = {v, v};
-        static_cast<uint16_t*>(out)[at] = (uint16_t)__builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf16x2));
+        static_cast<uint16_t*>(out)[at] = (uint16_t)pack2(v, v);
     }
 }
 
@@ -47,11 +57,176 @@ EM_DEV uint4 by_group(uint4 v) {
     return make_uint4(c[0], c[1], d[0], d[1]);
 }
 
+// What lanes without an element read: x past K.
+__device__ const uint4 ip_zero = {0u, 0u, 0u, 0u};
+
+// The four waves' sums of 16 NS rows x 16 NC columns, added in wave order and stored: tile
+// i = (subtile s, column tile c) by wave i % 4; lane (g, m) holds rows 4 g .. 4 g + 3 of
+// column m.
+template <int NS, int NC>
+EM_DEV void join_waves(const Int4Product& a, const floatx4 (&acc)[NS][NC], float (&red)[4][NS * NC][256], int r0, int r1, int n0) {
+    const int lane = lane_id(), wv = wave_id(), g = lane >> 4, m = lane & 15;
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) *reinterpret_cast<floatx4*>(&red[wv][s * NC + c][4 * lane]) = acc[s][c];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NS * NC; ++i) {
+        if ((i & 3) != wv) continue;
+        floatx4 v = *reinterpret_cast<const floatx4*>(&red[0][i][4 * lane]);
+#pragma unroll
+        for (int q = 1; q < 4; ++q) v += *reinterpret_cast<const floatx4*>(&red[q][i][4 * lane]);
+        const int n = n0 + 16 * (i % NC) + m, r = r0 + 16 * (i / NC) + 4 * g;
+        if (n >= a.N) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (r + j < r1) store1(a.y, a.y_f32, (int64_t)(r + j) * a.y_stride + n, v[j]);
+    }
+}
+
 }  // namespace
 
-// GPC: scale groups in 128 elements of K (1: groups of 128 and more).  A workgroup takes
-// one row tile (16 NS rows of one matrix) and 16 NC columns.  The last 32, 64 or 96
-// elements of a K that is no multiple of 128 are a chunk whose missing codes are zero.
+// GPC: scale groups in 128 elements of K (1: groups of 128 and more).  The last 32, 64 or 96
+// elements of a K that is no multiple of 128 are a chunk whose missing x is zero.
+//
+// ------------------------------------------------------------------ few rows -----
+// A workgroup takes up to 16 rows of one matrix and 16 NC columns, a wave a quarter of K,
+// 1024 elements at a time: all of their codes and scales are asked for at once, then the x
+// rows into the wave's own part of the LDS, and one wait covers both.
+// VEC: a wave's scales of 1024 elements are 16 bytes (GPC 1: groups of 128, K a multiple of
+// 4096), those of a chunk 4 or 8 (GPC 2, 4: K a multiple of 128).
+template <int GPC, int NC, bool VEC>
+__global__ void __launch_bounds__(256)
+ip_rows(Int4Product a) {
+    constexpr int WD = 8, XR = 8, RS = 2 * KC * WD + 16;          // chunks and x rows at once, bytes of an x row in the LDS
+    __shared__ __attribute__((aligned(16))) uint8_t xl[4][XR * RS];
+    __shared__ __attribute__((aligned(16))) float red[4][NC][256];
+    const RowTile t = row_tile<16>(a.offsets, a.M, a.R, [](int) { return (int)blockIdx.y; });
+    if (t.r1 == 0) return;
+    const int lane = lane_id(), wv = wave_id(), g = lane >> 4, m = lane & 15;
+    const int n0 = blockIdx.x * (16 * NC);
+    const int chunks = (a.K + KC - 1) / KC;
+    const int s0 = chunks * wv / 4, s1 = chunks * (wv + 1) / 4;
+    const int ng = a.K / a.gq, rows = t.r1 - t.r0;
+
+    const uint8_t* wp[NC];
+    const uint16_t* sp[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int64_t row = (int64_t)t.m * a.N + min(n0 + 16 * c + m, a.N - 1);
+        wp[c] = a.codes + row * (a.K / 2);
+        sp[c] = a.scales + row * ng;
+    }
+    uint4 w[WD][NC];
+    constexpr bool BLOCK = VEC && GPC == 1;                       // scales by 1024 elements
+    uint4 sb[NC];
+    uint2 sc[BLOCK ? 1 : WD][NC];                                 // a chunk's scales, two a word
+    auto load_w = [&](int d, int ch) {
+        const int k = KC * ch + 32 * g;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            w[d][c] = ld16(wp[c] + min(k, a.K - 32) / 2);
+            if constexpr (BLOCK) continue;
+            if constexpr (VEC && GPC == 4) {
+                sc[d][c] = *reinterpret_cast<const uint2*>(sp[c] + 4 * ch);
+            } else if constexpr (VEC && GPC == 2) {
+                sc[d][c] = make_uint2(*reinterpret_cast<const uint32_t*>(sp[c] + 2 * ch), 0u);
+            } else {
+                uint32_t h[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int q = 0; q < GPC; ++q) {
+                    const int i = (KC * ch + KC / GPC * q) / a.gq;
+                    h[q] = i < ng ? sp[c][min(i, ng - 1)] : 0u;   // past K: nothing, whatever the last scale is
+                }
+                sc[d][c] = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+            }
+        }
+    };
+    auto scale = [&](int d, int c, int q) {
+        uint32_t v;
+        if constexpr (BLOCK) v = (d / 2 == 0 ? sb[c].x : d / 2 == 1 ? sb[c].y : d / 2 == 2 ? sb[c].z : sb[c].w) >> (16 * (d & 1));
+        else v = (q < 2 ? sc[d][c].x : sc[d][c].y) >> (16 * (q & 1));
+        return 16.0f * fp16_bits_to_f32((uint16_t)v);
+    };
+    auto load_block = [&](int ch) {
+        if constexpr (BLOCK) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) sb[c] = ld16(sp[c] + min(ch, s1 - WD));
+        }
+#pragma unroll
+        for (int d = 0; d < WD; ++d) load_w(d, min(ch + d, s1 - 1));
+    };
+    if (s0 < s1) load_block(s0);
+    const int src = x_row(a, t.r0 + min(m, rows - 1));
+    const uint16_t* xp = a.x + (int64_t)max(src, 0) * a.x_stride;  // (more than XR rows) this lane's row
+    const bool few = rows <= XR;
+    const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&xl[wv][0];
+    const uint8_t* xrow = &xl[wv][min(m, rows - 1) * RS];
+    floatx4 acc[1][NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) acc[0][c] = zero4();
+    for (int ch = s0; ch < s1; ch += WD) {
+        if (few) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");    // the rows before have been read
+            for (int r = 0; r < rows; ++r) {
+                const int from = __builtin_amdgcn_readlane(src, r);
+                const uint16_t* p = a.x + (int64_t)max(from, 0) * a.x_stride;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int k = KC * ch + 512 * h + 8 * lane;
+                    const void* at = from >= 0 && k < a.K ? static_cast<const void*>(p + k) : static_cast<const void*>(&ip_zero);
+                    lds_load16(at, __builtin_amdgcn_readfirstlane(base + r * RS + 1024 * h));
+                }
+            }
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+        uint4 sn[NC];
+        if constexpr (BLOCK) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) sn[c] = ld16(sp[c] + min(ch + WD, s1 - WD));
+        }
+#pragma unroll
+        for (int d = 0; d < WD; ++d) {
+            if (ch + d < s1) {
+                const int k0 = KC * (ch + d), left = a.K - k0;
+                uint4 x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at = GPC == 1 ? 32 * g + 8 * i : 32 * i + 8 * g;
+                    if (few) {
+                        x[i] = ld16(xrow + 2 * (KC * d + at));
+                    } else {
+                        const uint4 v = ld16(xp + k0 + (at < left ? at : 0));
+                        x[i] = at < left && src >= 0 ? v : zero_u4();
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    uint4 raw = w[d][c];
+                    if constexpr (GPC > 1) raw = by_group(raw);
+                    uint4 b[4];
+                    dequant_b(raw, b);
+#pragma unroll
+                    for (int q = 0; q < GPC; ++q) {
+                        floatx4 u = zero4();
+#pragma unroll
+                        for (int i = 4 / GPC * q; i < 4 / GPC * (q + 1); ++i) u = mfma_bf16(x[i], b[i], u);
+                        acc[0][c] = fma4(scale(d, c, q), u, acc[0][c]);
+                    }
+                }
+                load_w(d, min(ch + d + WD, s1 - 1));
+            }
+        }
+        if constexpr (BLOCK) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) sb[c] = sn[c];
+        }
+    }
+    join_waves<1, NC>(a, acc, red, t.r0, t.r1, n0);
+}
+
+// ------------------------------------------------------------------ 17 to 32 rows ----
 template <int GPC, int NS, int NC>
 __global__ void __launch_bounds__(256)
 ip_stream(Int4Product a) {
@@ -81,7 +256,10 @@ ip_stream(Int4Product a) {
         for (int c = 0; c < NC; ++c) {
             w[d][c] = ld16(wp[c] + min(k, a.K - 32) / 2);
 #pragma unroll
-            for (int q = 0; q < GPC; ++q) sc[d][c][q] = sp[c][min((KC * ch + KC / GPC * q) / a.gq, ng - 1)];
+            for (int q = 0; q < GPC; ++q) {
+                const int i = (KC * ch + KC / GPC * q) / a.gq;
+                sc[d][c][q] = i < ng ? sp[c][min(i, ng - 1)] : (uint16_t)0;     // past K: nothing, whatever the last scale is
+            }
         }
     };
     if (s0 < s1) {
@@ -135,24 +313,211 @@ ip_stream(Int4Product a) {
             }
         }
     }
+    join_waves<NS, NC>(a, acc, red, t.r0, t.r1, n0);
+}
+
+// ------------------------------------------------------------------ many rows ----
+// A workgroup takes BT rows x BN columns, each wave all rows of 32 columns, so that no code
+// is converted twice; 128 of K a step.  x, codes and scales arrive by direct global -> LDS
+// loads two steps ahead in three stages, every wave as many loads a step.  A scale comes as
+// the aligned word that holds it.  256-byte x rows, 16-byte segments XOR-swizzled by the row
+// (with groups of 128 and more the segments that lane groups 0 .. 3 read together are kept
+// side by side); 64-byte code rows as mx_product.hip's.
+namespace {
+
+template <int GPC, int BT_, int BN_>
+struct IpCfg {
+    static constexpr int BT = BT_, BN = BN_, NW = BN / 32, NJ = BT / 16;
+    static constexpr int X_B = BT * 256, W_B = BN * 64, S_B = BN * 4 * GPC, STAGE = X_B + W_B + S_B;
+    static constexpr int X_L = X_B / 1024 / NW, W_L = W_B / 1024 / NW, S_P = S_B / 256, S_L = (S_P + NW - 1) / NW;
+    static constexpr int LOADS = X_L + W_L + S_L;
+    static constexpr int RS = BN + 4;                             // floats of an out row in the LDS
+    static constexpr int LDS_B = 3 * STAGE > BT * RS * 4 ? 3 * STAGE : BT * RS * 4;
+    static_assert(LDS_B <= 160 * 1024, "");
+};
+
+// Slot of x segment s (eight elements) of row r; of code segment s (32 codes) of column r.
+template <int GPC>
+EM_DEV int x_slot(int r, int s) { return (GPC == 1 ? s >> 2 | (s & 3) << 2 : s) ^ (r & 15); }
+EM_DEV int w_slot(int r, int s) { return s ^ (-(r >> 2) & 3); }
+
+}  // namespace
+
+template <int GPC, int BT, int BN>
+__global__ void __launch_bounds__((IpCfg<GPC, BT, BN>::NW * 64))
+ip_tile(Int4Product a) {
+    using C = IpCfg<GPC, BT, BN>;
+    constexpr int NJ = C::NJ;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[C::LDS_B];
+    const int lane = lane_id(), wv = wave_id(), g = lane >> 4, m = lane & 15;
+    const int nn = (a.N + BN - 1) / BN;
+    int tn = 0, z = 0;
+    const RowTile t = row_tile<BT>(a.offsets, a.M, a.R, [&](int rows) {
+        rows = min(rows, a.row_tiles);                            // more only where offsets descend
+        const int each = rows * nn, total = each * a.slices, per = (total + 7) >> 3, at = blockIdx.x >> 3;
+        int b = (blockIdx.x & 7) * per + at;                      // XCD x takes neighbouring tiles
+        if (at >= per || b >= total) return -1;
+        z = b / each;
+        b -= z * each;
+        const int grp = b / (8 * nn), left = min(8, rows - 8 * grp), in = b - grp * 8 * nn;
+        tn = in / left;
+        return 8 * grp + in % left;
+    });
+    if (t.r1 == 0) return;
+    const int n0 = tn * BN, rows = t.r1 - t.r0, ng = a.K / a.gq;
+    const int steps = (a.K + KC - 1) / KC, whole_steps = a.K / KC;
+    const int s0 = (int)((int64_t)steps * z / a.slices), s1 = (int)((int64_t)steps * (z + 1) / a.slices);
+
+    // ---- loads: load u of a wave brings piece u NW + wv of x, of the codes, of the scales
+    const char* xbase = reinterpret_cast<const char*>(a.row_src ? a.x : a.x + (int64_t)t.r0 * a.x_stride);
+    const uint8_t* wbase = a.codes + ((int64_t)t.m * a.N + n0) * (a.K / 2);
+    uint32_t xoff[C::X_L], woff[C::W_L];
+    int xk[C::X_L], wk[C::W_L], scol[C::S_L], sgrp[C::S_L];       // the lane's first element of K within a step; scale columns and groups
 #pragma unroll
-    for (int s = 0; s < NS; ++s)
+    for (int u = 0; u < C::X_L; ++u) {
+        const int row = (u * C::NW + wv) * 4 + lane / 16, slot = (lane & 15) ^ (row & 15);
+        xk[u] = 8 * (GPC == 1 ? slot >> 2 | (slot & 3) << 2 : slot);
+        const int r = min(row, rows - 1);
+        xoff[u] = (uint32_t)(2 * ((a.row_src ? max(x_row(a, t.r0 + r), 0) : r) * a.x_stride + xk[u]));
+    }
 #pragma unroll
-        for (int c = 0; c < NC; ++c) *reinterpret_cast<floatx4*>(&red[wv][s * NC + c][4 * lane]) = acc[s][c];
-    __syncthreads();
-    // tile i = (subtile s, column tile c) is summed by wave i % 4; lane (g, m) holds rows
-    // 4 g .. 4 g + 3 of column m
+    for (int u = 0; u < C::W_L; ++u) {
+        const int row = (u * C::NW + wv) * 16 + lane / 4;
+        wk[u] = 32 * w_slot(row, lane & 3);
+        woff[u] = min(row, a.N - 1 - n0) * (a.K / 2) + wk[u] / 2;
+    }
 #pragma unroll
-    for (int i = 0; i < NS * NC; ++i) {
-        if ((i & 3) != wv) continue;
-        floatx4 v = *reinterpret_cast<const floatx4*>(&red[0][i][4 * lane]);
+    for (int u = 0; u < C::S_L; ++u) {                            // where the pieces run out before the waves, the first again
+        const int piece = (u * C::NW + wv) % C::S_P;
+        sgrp[u] = piece / (BN / 64);
+        scol[u] = min(64 * (piece % (BN / 64)) + lane, a.N - 1 - n0);
+    }
+    const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+    const int64_t srow0 = ((int64_t)t.m * a.N + n0) * ng;         // index of the first column's first scale
+    // index of scale group q of step st, the last one past K
+    auto group_of = [&](int st, int q) { return min((KC * st + KC / GPC * q) / a.gq, ng - 1); };
+    auto fetch = [&](int st, int u, auto fast) {
+        constexpr bool FAST = decltype(fast)::value;              // all of the step's K exists
+        const uint32_t stage = base + (uint32_t)(st % 3) * C::STAGE;
+        if (u < C::X_L) {
+            const uint32_t dst = __builtin_amdgcn_readfirstlane(stage + 1024 * (u * C::NW + wv));
+            const char* from = xbase + (int64_t)st * 256;
+            if constexpr (FAST) lds_load16(from, xoff[u], dst);
+            else lds_load16(KC * st + xk[u] < a.K ? from + xoff[u] : reinterpret_cast<const char*>(&ip_zero), dst);
+        } else if (u < C::X_L + C::W_L) {
+            const int v = u - C::X_L;
+            const uint32_t dst = __builtin_amdgcn_readfirstlane(stage + C::X_B + 1024 * (v * C::NW + wv));
+            if constexpr (FAST) lds_load16(wbase + (int64_t)st * 64, woff[v], dst);
+            else lds_load16(wbase + woff[v] - wk[v] / 2 + min(KC * st + wk[v], a.K - 32) / 2, dst);      // codes past K meet zeros
+        } else {
+            const int v = u - C::X_L - C::W_L, piece = (v * C::NW + wv) % C::S_P;
+            const int64_t i = srow0 + (int64_t)scol[v] * ng + group_of(st, sgrp[v]);
+            lds_load4v(a.scales + (i & ~1ll), __builtin_amdgcn_readfirstlane(stage + C::X_B + C::W_B + 256 * piece));
+        }
+    };
+
+    floatx4 acc[2][NJ];
 #pragma unroll
-        for (int q = 1; q < 4; ++q) v += *reinterpret_cast<const floatx4*>(&red[q][i][4 * lane]);
-        const int n = n0 + 16 * (i % NC) + m, r = t.r0 + 16 * (i / NC) + 4 * g;
-        if (n >= a.N) continue;
+    for (int p = 0; p < 2; ++p)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (r + j < t.r1) store1(a.y, a.y_f32, (int64_t)(r + j) * a.y_stride + n, v[j]);
+        for (int j = 0; j < NJ; ++j) acc[p][j] = zero4();
+    int odd[2];                                                   // parity of a column's first scale index
+#pragma unroll
+    for (int p = 0; p < 2; ++p) odd[p] = (int)(srow0 + (int64_t)min(32 * wv + 16 * p + m, a.N - 1 - n0) * ng) & 1;
+    auto step = [&](int st, auto fast) {
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(C::LOADS) : "memory");   // this step landed, the one before is read
+        const uint8_t* X = lds + (st % 3) * C::STAGE;
+        const uint8_t* W = X + C::X_B;
+        const uint32_t* S = reinterpret_cast<const uint32_t*>(W + C::W_B);
+        uint4 b[2][4];
+        float sc[2][GPC];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const int col = 32 * wv + 16 * p + m;
+            uint4 raw = *reinterpret_cast<const uint4*>(W + col * 64 + 16 * w_slot(m, g));
+            if constexpr (GPC > 1) raw = by_group(raw);
+            dequant_b(raw, b[p]);
+#pragma unroll
+            for (int q = 0; q < GPC; ++q) {
+                const uint32_t v = S[q * BN + col] >> (16 * ((odd[p] + group_of(st, q)) & 1));
+                const bool in = KC * st + KC / GPC * q < a.K;     // past K: nothing, whatever the last scale is
+                sc[p][q] = in ? 16.0f * fp16_bits_to_f32((uint16_t)v) : 0.f;
+            }
+        }
+        floatx4 u[2][NJ];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint4 x[NJ];
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                x[j] = *reinterpret_cast<const uint4*>(X + (16 * j + m) * 256 + 16 * x_slot<GPC>(m, GPC == 1 ? 4 * g + i : 4 * i + g));
+#pragma unroll
+            for (int v = i * C::LOADS / 4; v < (i + 1) * C::LOADS / 4; ++v) fetch(st + 2, v, fast);
+            const bool first = i % (4 / GPC) == 0, last = (i + 1) % (4 / GPC) == 0;
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) u[p][j] = mfma_bf16(x[j], b[p][i], first ? zero4() : u[p][j]);
+            if (last) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) acc[p][j] = fma4(sc[p][i * GPC / 4], u[p][j], acc[p][j]);
+            }
+        }
+    };
+    if (s0 < s1) {
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int u = 0; u < C::LOADS; ++u) fetch(s0 + st, u, std::false_type{});
+        int st = s0;
+        for (; st < s1 && st + 2 < whole_steps; ++st) step(st, std::true_type{});
+        for (; st < s1; ++st) step(st, std::false_type{});
+    }
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");        // nothing more lands in the stages
+
+    // ---- out through the LDS, whole rows: lane (g, m) holds rows 4 g .. 4 g + 3 of column m
+    float* o = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) o[(16 * j + 4 * g + v) * C::RS + 32 * wv + 16 * p + m] = acc[p][j][v];
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    const int cols = min(BN, a.N - n0);
+    if (a.slices > 1) {
+        const int Np = (a.N + 3) & ~3;
+        for (int i = threadIdx.x; i < rows * (BN / 4); i += C::NW * 64) {
+            const int r = i / (BN / 4), c = 4 * (i % (BN / 4));
+            if (c < cols) *reinterpret_cast<floatx4*>(a.part + ((int64_t)z * a.R + t.r0 + r) * Np + n0 + c) = *reinterpret_cast<const floatx4*>(o + r * C::RS + c);
+        }
+        return;
+    }
+    const int each = a.y_f32 ? 4 : 8, per = BN / each;            // columns of a store, stores of a row
+    for (int i = threadIdx.x; i < rows * per; i += C::NW * 64) {
+        const int r = i / per, c = each * (i % per);
+        if (c >= cols) continue;
+        const bool named = !a.row_src || x_row(a, t.r0 + r) >= 0;
+        const floatx4 lo = named ? *reinterpret_cast<const floatx4*>(o + r * C::RS + c) : zero4();
+        const int64_t at = (int64_t)(t.r0 + r) * a.y_stride + n0 + c;
+        if (a.y_f32) {
+            if (a.vec && c + 4 <= cols) {
+                __builtin_nontemporal_store(lo, reinterpret_cast<floatx4*>(static_cast<float*>(a.y) + at));
+            } else {
+                for (int k = 0; k < 4 && c + k < cols; ++k) static_cast<float*>(a.y)[at + k] = lo[k];
+            }
+            continue;
+        }
+        const floatx4 hi = named ? *reinterpret_cast<const floatx4*>(o + r * C::RS + c + 4) : zero4();
+        const u32x4 v = {pack2(lo.x, lo.y), pack2(lo.z, lo.w), pack2(hi.x, hi.y), pack2(hi.z, hi.w)};
+        uint16_t* y = static_cast<uint16_t*>(a.y) + at;
+        if (a.vec && c + 8 <= cols) {
+            __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(y));
+        } else {
+            for (int k = 0; k < 8 && c + k < cols; ++k) y[k] = (uint16_t)(v[k / 2] >> (16 * (k & 1)));
+        }
     }
 }
 
@@ -166,38 +531,78 @@ int64_t max_row_tiles(const Int4Product& a, int BT) {
 
 template <int GPC, int NS>
 hipError_t launch_stream(const Int4Product& a, hipStream_t s) {
-    const int64_t tiles = max_row_tiles(a, 16 * NS);
+    const dim3 grid((a.N + 31) / 32, (unsigned)max_row_tiles(a, 16 * NS));
     prof_begin(s);
-    if (tiles * ((a.N + 31) / 32) <= 128) ip_stream<GPC, NS, 1><<<dim3((a.N + 15) / 16, (unsigned)tiles), 256, 0, s>>>(a);
-    else ip_stream<GPC, NS, 2><<<dim3((a.N + 31) / 32, (unsigned)tiles), 256, 0, s>>>(a);
+    ip_stream<GPC, NS, 2><<<grid, 256, 0, s>>>(a);
     prof_end(s, "ip_stream");
     return hipGetLastError();
 }
 
-// How many times 16 rows of a matrix ip_stream takes at once.
-int stream_rows(const Int4Product& a) {
-    const int live = a.M < a.R ? a.M : a.R;
-    const int64_t avg = ((int64_t)a.R + live - 1) / live, cols = (a.N + 31) / 32;
-    for (int ns = 1; ns < 4; ns *= 2)
-        if (max_row_tiles(a, 16 * ns) * cols <= 256 || avg <= 16 * ns) return ns;
-    return 4;
+template <int GPC, int NC>
+hipError_t launch_rows(const Int4Product& a, hipStream_t s) {
+    const dim3 grid((a.N + 16 * NC - 1) / (16 * NC), (unsigned)max_row_tiles(a, 16));
+    const bool vec = GPC == 1 ? a.gq == KC && a.K % 4096 == 0 : a.K % KC == 0;
+    prof_begin(s);
+    if (vec) ip_rows<GPC, NC, true><<<grid, 256, 0, s>>>(a);
+    else ip_rows<GPC, NC, false><<<grid, 256, 0, s>>>(a);
+    prof_end(s, "ip_rows");
+    return hipGetLastError();
+}
+
+struct IpPlan { int bt, bn, slices; };                            // bt 16, 32, 64 of ip_rows and ip_stream: bn 0
+
+IpPlan plan(const Int4Product& a) {
+    const int live = a.M < a.R ? a.M : (a.R ? a.R : 1);
+    const int64_t avg = ((int64_t)a.R + live - 1) / live;
+    if (avg <= 32) return IpPlan{avg <= 16 ? 16 : 32, 0, 1};
+    if ((int64_t)a.N * (a.K / a.gq) % 2) return IpPlan{64, 0, 1};  // the last scale's word would end past the scales
+    IpPlan p{avg <= 64 ? 64 : 128, 256, 1};
+    if (a.N <= 128) p = IpPlan{64, 128, 1};
+    const int64_t tiles = max_row_tiles(a, p.bt) * ((a.N + p.bn - 1) / p.bn);
+    const int steps = (a.K + KC - 1) / KC;
+    while (tiles * p.slices * 2 <= 256 && steps >= 8 * p.slices && p.slices < 8) p.slices *= 2;
+    return p;
+}
+
+template <int GPC, int BT, int BN>
+hipError_t launch_tile(Int4Product a, const IpPlan& p, hipStream_t s) {
+    a.slices = p.slices;
+    a.row_tiles = (int)max_row_tiles(a, BT);
+    const int64_t blocks = (int64_t)a.row_tiles * ((a.N + BN - 1) / BN) * p.slices;
+    prof_begin(s);
+    ip_tile<GPC, BT, BN><<<(unsigned)((blocks + 7) & ~7ll), IpCfg<GPC, BT, BN>::NW * 64, 0, s>>>(a);
+    prof_end(s, "ip_tile");
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.slices == 1) return e;
+    return launch_join(RowJoin{a.part, p.slices, a.R, a.N, a.y, a.y_stride, a.y_f32, a.vec && a.N % 4 == 0, a.R, a.offsets, a.M,
+                               nullptr, 0}, s);
 }
 
 template <int GPC>
 hipError_t launch_product(const Int4Product& a, hipStream_t s) {
-    switch (stream_rows(a)) {
-        case 1: return launch_stream<GPC, 1>(a, s);
-        case 2: return launch_stream<GPC, 2>(a, s);
-        default: return launch_stream<GPC, 4>(a, s);
+    IpPlan p = plan(a);
+    // lane offsets of a tile's x rows have 32 bits
+    const int64_t rows = a.row_src ? a.T : 128;
+    if (p.bn && rows * a.x_stride >= (1ll << 31)) p = IpPlan{64, 0, 1};
+    if (p.bn == 0) {
+        if (p.bt == 64) return launch_stream<GPC, 4>(a, s);
+        if (p.bt == 32) return launch_stream<GPC, 2>(a, s);
+        // 32 columns a workgroup, 16 where that leaves half of the compute units idle
+        return max_row_tiles(a, 16) * ((a.N + 31) / 32) <= 128 ? launch_rows<GPC, 1>(a, s) : launch_rows<GPC, 2>(a, s);
     }
+    if (p.bn == 128) return launch_tile<GPC, 64, 128>(a, p, s);
+    return p.bt == 64 ? launch_tile<GPC, 64, 256>(a, p, s) : launch_tile<GPC, 128, 256>(a, p, s);
 }
 
 }  // namespace
 
-size_t int4_product_ws_bytes(const Int4Product&) { return 256; }
+size_t int4_product_ws_bytes(const Int4Product& a) {
+    const IpPlan p = plan(a);
+    return p.slices > 1 ? ((size_t)p.slices * a.R * ((a.N + 3) & ~3) * 4 + 255) & ~(size_t)255 : 256;
+}
 
 hipError_t launch_int4_product(Int4Product a, void* ws, hipStream_t s) {
-    (void)ws;
+    a.part = static_cast<float*>(ws);
     if (a.gq >= KC || a.gq == a.K) return launch_product<1>(a, s);    // (a narrower group is the whole of a K below 128)
     return a.gq == 64 ? launch_product<2>(a, s) : launch_product<4>(a, s);
 }

@@ -135,6 +135,20 @@ struct DenseGrad {
     const int32_t* token_rows; int per_token;            // [T][per_token] rows of each token, or null: dx by rows
     void* dw; int dw_f32;
 };
+// Sums of the slices of `rows` rows, in order: out row i from row i, or from the rows of
+// token i (dense_product.hip).
+struct RowJoin {
+    const float* part;              // [slices][rows][cols up to a multiple of 4]
+    int slices;
+    int64_t rows;
+    int cols;
+    void* out; int64_t out_stride; int out_f32;
+    int whole;                      // out rows take four columns at once
+    int64_t out_rows;
+    const int32_t* offsets; int M;  // rows offsets[0] .. offsets[M] - 1 are written; null: all
+    const int32_t* token_rows; int per_token;
+};
+hipError_t launch_join(const RowJoin& j, hipStream_t s);
 size_t dense_product_ws_bytes(const DenseProduct& a);
 hipError_t launch_dense_product(DenseProduct a, void* ws, hipStream_t s);
 size_t dense_backward_ws_bytes(const DenseProduct& a);
@@ -149,6 +163,9 @@ struct Int4Product {
     const uint8_t* codes;       // [M][N][K/2]
     const uint16_t* scales;     // [M][N][K/gq] fp16
     void* y; int64_t y_stride; int y_f32;
+    int vec;                    // y rows take 16-byte stores (8 bf16, 4 float32) at every eighth or fourth column
+    int slices, row_tiles;
+    float* part;                // workspace: [slices][R][N up to a multiple of 4]
 };
 size_t int4_product_ws_bytes(const Int4Product& a);
 hipError_t launch_int4_product(Int4Product a, void* ws, hipStream_t s);

@@ -342,6 +342,7 @@ int edge_moe_packed_product(const edge_moe_packed_dims* dims, const uint16_t* x,
     if (st != EDGE_MOE_OK || a.R == 0) return st;
     a.x = x; a.x_stride = x_stride; a.row_src = row_src; a.offsets = offsets; a.codes = codes; a.scales = scales;
     a.y = y; a.y_stride = y_stride; a.y_f32 = y_type == EDGE_MOE_FLOAT;
+    a.vec = aligned(y, 16) && y_stride % (a.y_f32 ? 4 : 8) == 0;
     return hip_status(em::launch_int4_product(a, ws, (hipStream_t)stream));
 }
 
