@@ -427,6 +427,16 @@ int edge_moe_mx_product(const edge_moe_mx_dims* dims, const uint16_t* x, int64_t
                         const int32_t* offsets, const uint8_t* codes, const uint8_t* scales, uint16_t* y,
                         int64_t y_stride, void* ws, size_t ws_bytes, void* stream);
 
+/* edge_moe_mx_product from x in MX codes already (edge_moe_norm, edge_moe_mx_quantize):
+ *   y[r] = bf16( sum_k X[src(r)][k] * W_m[k] )
+ * x_codes [T][K] (FP8) or [T][K/2] (FP4) bytes, 16-byte aligned, x_scales
+ * [K/128][T][4], 4-byte aligned: X are their values; the other arguments as there,
+ * but no workspace.  From the codes that edge_moe_mx_quantize makes of x, y has the
+ * bits of edge_moe_mx_product's. */
+int edge_moe_mx_product_coded(const edge_moe_mx_dims* dims, const uint8_t* x_codes, const uint8_t* x_scales,
+                              const int32_t* row_src, const int32_t* offsets, const uint8_t* codes, const uint8_t* scales,
+                              uint16_t* y, int64_t y_stride, void* stream);
+
 /* ------------------------------------------ norm, dense and int4 matrices --
  * Root-mean-square norm with the residual's addition, between two layers:
  *   r = bf16(x + add)                    (the exact sum rounded once, as

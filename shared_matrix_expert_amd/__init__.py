@@ -37,6 +37,7 @@ EXPORTED = ("edge_moe_workspace_bytes", "edge_moe_route", "edge_moe_forward",
             "edge_moe_prefetch", "edge_moe_cache_create", "edge_moe_cache_destroy", "edge_moe_cache_map",
             "edge_moe_cache_prefetch", "edge_moe_cache_totals", "edge_moe_cache_slot_of",
             "edge_moe_mx_quantize", "edge_moe_mx_dequantize", "edge_moe_mx_product_ws_bytes", "edge_moe_mx_product",
+            "edge_moe_mx_product_coded",
             "edge_moe_balance_ws_bytes", "edge_moe_balance", "edge_moe_route_backward_ws_bytes",
             "edge_moe_route_backward", "edge_moe_norm", "edge_moe_norm_backward_ws_bytes", "edge_moe_norm_backward",
             "edge_moe_dense_product_ws_bytes", "edge_moe_dense_product", "edge_moe_dense_product_backward_ws_bytes",
@@ -232,6 +233,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.edge_moe_mx_product_ws_bytes.restype = sz
     lib.edge_moe_mx_product.argtypes = [ctypes.POINTER(CMxDims), vp, i64, vp, vp, vp, vp, vp, i64, vp, sz, vp]
     lib.edge_moe_mx_product.restype = i32
+    lib.edge_moe_mx_product_coded.argtypes = [ctypes.POINTER(CMxDims), vp, vp, vp, vp, vp, vp, vp, i64, vp]
+    lib.edge_moe_mx_product_coded.restype = i32
     lib.edge_moe_balance_ws_bytes.argtypes = [ctypes.POINTER(CDims), i32]
     lib.edge_moe_balance_ws_bytes.restype = sz
     lib.edge_moe_balance.argtypes = [ctypes.POINTER(CDims), vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]
@@ -665,6 +668,28 @@ def edge_moe_mx_product(x_format, x, codes, scales, y, ws, offsets=None, row_src
                                     _stream_on(dev, stream))
     if st != EDGE_MOE_OK:
         raise EdgeMoeError("edge_moe_mx_product", st)
+
+
+def edge_moe_mx_product_coded(x_format, x_codes, x_scales, codes, scales, y, offsets=None, row_src=None, stream=None) -> None:
+    """edge_moe_mx_product from x in MX codes: x_codes uint8 [T][K] (MX_FP8) or
+    [T][K/2] (MX_FP4), x_scales uint8 [K/128][T][4], as edge_moe_norm and
+    edge_moe_mx_quantize write them."""
+    lib = load()
+    if x_format not in (MX_FP4, MX_FP8):
+        raise ValueError("x_format must be MX_FP4 or MX_FP8")
+    if x_codes.dim() != 2 or y.dim() != 2 or _dense_type(y) != _BF16:
+        raise ValueError("x_codes must be [T][K] bytes, y bfloat16 (or int16 bits) [R][N]")
+    (T, K), (R, N) = x_codes.shape, y.shape
+    K *= 2 if x_format == MX_FP4 else 1
+    M = 1 if codes.dim() == 2 else codes.shape[0]
+    dev = _same_device(x_codes, x_scales, codes, scales, y, offsets, row_src)
+    st = lib.edge_moe_mx_product_coded(
+        _int32s(CMxDims, _pack_mx_dims, T, R, M, N, K, x_format), _sized(x_codes, "uint8", x_codes.numel(), "x_codes"),
+        _sized(x_scales, "uint8", T * (K // 32), "x_scales"), _sized(row_src, "int32", R, "row_src"),
+        _sized(offsets, "int32", M + 1, "offsets"), _sized(codes, "uint8", M * N * (K // 2), "codes"),
+        _sized(scales, "uint8", M * N * (K // 32), "scales"), *_rows(y, R, N, "y"), _stream_on(dev, stream))
+    if st != EDGE_MOE_OK:
+        raise EdgeMoeError("edge_moe_mx_product_coded", st)
 
 
 def mx_weights(dense: dict, stream=None) -> dict:

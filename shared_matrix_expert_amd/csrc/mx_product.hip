@@ -629,16 +629,8 @@ size_t mx_product_ws_bytes(const MxProduct& a) {
     return ((size_t)x_rows(a) * row + 511) & ~(size_t)255;
 }
 
-hipError_t launch_mx_product(MxProduct a, void* ws, hipStream_t s) {
-    const int ns = stream_rows(a);
-    if (ns == 1 && rounds_in_stream(a)) return launch_stream<1, true>(a, s);
-    a.xrows = x_rows(a);
-    a.gathered = a.row_src && a.xrows < a.T;
-    a.xq = static_cast<uint8_t*>(ws);
-    a.xs = a.xq + (((size_t)a.xrows * a.K / (a.fmt == kMxFp4 ? 2 : 1) + 255) & ~(size_t)255);
-    const MxRows rows{a.xrows, a.xrows, a.K, a.x_stride, a.fmt, 0, a.gathered ? a.row_src : nullptr, a.T};
-    const hipError_t e = launch_mx_quantize(rows, a.x, const_cast<uint8_t*>(a.xq), const_cast<uint8_t*>(a.xs), s);
-    if (e != hipSuccess) return e;
+// The product from x in the workspace, or from codes that the caller has.
+static hipError_t launch_coded(const MxProduct& a, int ns, hipStream_t s) {
     switch (ns) {
         case 1: return launch_stream<1, false>(a, s);
         case 2: return launch_stream<2, false>(a, s);
@@ -659,6 +651,25 @@ hipError_t launch_mx_product(MxProduct a, void* ws, hipStream_t s) {
         case 192: return launch_gemm<192, 256>(a, s);
         default: return launch_gemm<256, 256>(a, s);
     }
+}
+
+hipError_t launch_mx_product(MxProduct a, void* ws, hipStream_t s) {
+    const int ns = stream_rows(a);
+    if (ns == 1 && rounds_in_stream(a)) return launch_stream<1, true>(a, s);
+    a.xrows = x_rows(a);
+    a.gathered = a.row_src && a.xrows < a.T;
+    a.xq = static_cast<uint8_t*>(ws);
+    a.xs = a.xq + (((size_t)a.xrows * a.K / (a.fmt == kMxFp4 ? 2 : 1) + 255) & ~(size_t)255);
+    const MxRows rows{a.xrows, a.xrows, a.K, a.x_stride, a.fmt, 0, a.gathered ? a.row_src : nullptr, a.T};
+    const hipError_t e = launch_mx_quantize(rows, a.x, const_cast<uint8_t*>(a.xq), const_cast<uint8_t*>(a.xs), s);
+    if (e != hipSuccess) return e;
+    return launch_coded(a, ns, s);
+}
+
+hipError_t launch_mx_product_coded(MxProduct a, hipStream_t s) {
+    a.xrows = a.T;
+    a.gathered = 0;
+    return launch_coded(a, stream_rows(a), s);
 }
 
 }  // namespace em

@@ -41,11 +41,12 @@ struct MxProduct {
     int64_t y_stride;
     int vec;                    // y rows take 4-, 8- or 16-byte stores (1, 2, 3) at every second, fourth or eighth column
     int xrows, gathered;        // rows of x in the workspace; gathered: row r is y row r's, else x row r
-    uint8_t* xq;                // workspace: x's codes [xrows][K] or [xrows][K/2] ...
-    uint8_t* xs;                // ... and scales [K/128][xrows][4]
+    const uint8_t* xq;          // workspace: x's codes [xrows][K] or [xrows][K/2] ...
+    const uint8_t* xs;          // ... and scales [K/128][xrows][4]
 };
 size_t mx_product_ws_bytes(const MxProduct& a);
 hipError_t launch_mx_product(MxProduct a, void* ws, hipStream_t s);
+hipError_t launch_mx_product_coded(MxProduct a, hipStream_t s);   // xq, xs: the caller's, [T] rows
 
 // ---- router load and losses (router_train.hip)
 struct RouterLoad {

@@ -159,6 +159,24 @@ int edge_moe_mx_product(const edge_moe_mx_dims* dims, const uint16_t* x, int64_t
     return hip_status(em::launch_mx_product(a, ws, (hipStream_t)stream));
 }
 
+int edge_moe_mx_product_coded(const edge_moe_mx_dims* dims, const uint8_t* x_codes, const uint8_t* x_scales, const int32_t* row_src,
+                              const int32_t* offsets, const uint8_t* codes, const uint8_t* scales, uint16_t* y,
+                              int64_t y_stride, void* stream) {
+    int st = mx_product_status(dims);
+    if (st != EDGE_MOE_OK) return st;
+    em::MxProduct a = mx_product_args(*dims);
+    if (!aligned(x_codes, 16) || !aligned(x_scales, 4) || !aligned(codes, 16) || !aligned(scales, 4) || (a.R > 0 && !aligned(y, 2)))
+        return EDGE_MOE_EINVAL;
+    if (y_stride < a.N || y_stride > (1ll << 32)) return EDGE_MOE_EINVAL;
+    st = lists_status(row_src, offsets, a.T, a.R, a.M);
+    if (st == EDGE_MOE_OK) st = em::device_status();
+    if (st != EDGE_MOE_OK || a.R == 0) return st;
+    a.xq = x_codes; a.xs = x_scales; a.row_src = row_src; a.offsets = offsets; a.codes = codes; a.scales = scales;
+    a.y = y; a.y_stride = y_stride;
+    a.vec = y_stride % 8 == 0 && aligned(y, 16) ? 3 : y_stride % 4 == 0 && aligned(y, 8) ? 2 : y_stride % 2 == 0 && aligned(y, 4) ? 1 : 0;
+    return hip_status(em::launch_mx_product_coded(a, (hipStream_t)stream));
+}
+
 size_t edge_moe_balance_ws_bytes(const edge_moe_dims* dims, int32_t n_seq) {
     if (em::layer_dims_status(dims) != EDGE_MOE_OK || n_seq < 1 || n_seq > 4095) return 0;
     em::RouterLoad a{};

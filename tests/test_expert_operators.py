@@ -121,6 +121,22 @@ def test_packed_validation_before_any_device_call():
         assert em.edge_moe_packed_product_ws_bytes(*bad) == 0
 
 
+def test_coded_product_validation_before_any_device_call():
+    ok = dict(T=8, R=8, M=1, N=64, K=256, fmt=em.MX_FP8, x=BASE, xs=BASE, src=None, off=None, q=BASE, e=BASE, y=BASE, ys=64)
+
+    def call(**kw):
+        a = {**ok, **kw}
+        d = em.CMxDims(*(a[n] for n in ("T", "R", "M", "N", "K", "fmt")))
+        return em.load().edge_moe_mx_product_coded(ctypes.byref(d), *(a[n] for n in ("x", "xs", "src", "off", "q", "e", "y", "ys")), None)
+    refused(call, [
+        (INVALID, [dict(T=0), dict(R=-1), dict(M=0), dict(N=0), dict(K=0), dict(fmt=2), dict(x=None), dict(x=BASE + 8), dict(xs=None),
+                   dict(xs=BASE + 2), dict(src=BASE + 2), dict(off=BASE + 1), dict(q=None), dict(q=BASE + 8), dict(e=BASE + 2), dict(y=None),
+                   dict(y=BASE + 1), dict(ys=63), dict(ys=(1 << 32) + 1), dict(M=2), dict(R=9)]),
+        (UNSUPPORTED, [dict(K=192), dict(T=(1 << 20) + 1), dict(R=(1 << 25) + 1, src=BASE), dict(M=1025, off=BASE),
+                       dict(N=32769, ys=32769), dict(K=32896)])])
+    assert em.load().edge_moe_mx_product_coded(None, BASE, BASE, None, None, BASE, BASE, BASE, 64, None) == INVALID
+
+
 # ------------------------------------------------------------------ the binding ---
 
 T, D, M, N, K, R, PER, Q = 5, 256, 2, 64, 256, 6, 3, 64
@@ -132,10 +148,12 @@ CALLS = {
     "dense_product": dict(x=((T, K), BF16), w=((M, N, K), BF16), y=((R, N), F32), offsets=((M + 1,), I32), row_src=((R,), I32)),
     "dense_product_backward": dict(dy=((R, N), BF16), x=((T, K), BF16), w=((M, N, K), BF16), dx=((T, K), F32), dw=((M, N, K), F32),
                                    offsets=((M + 1,), I32), row_src=((R,), I32), token_rows=((T, PER), I32)),
+    "mx_product_coded": dict(x_codes=((T, K), U8), x_scales=((K // 128, T, 4), U8), codes=((M, N, K // 2), U8),
+                             scales=((M, K // 128, N, 4), U8), y=((R, N), BF16), offsets=((M + 1,), I32), row_src=((R,), I32)),
     "packed_product": dict(x=((T, K), BF16), codes=((M, N, K // 2), U8), scales=((M, N, K // Q), F16), y=((R, N), F32),
                            offsets=((M + 1,), I32), row_src=((R,), I32)),
 }
-WITH_WS = [n for n in CALLS if n != "norm"]
+WITH_WS = [n for n in CALLS if n not in ("norm", "mx_product_coded")]
 ARGS = [(c, a) for c in CALLS for a in CALLS[c]]
 args = pytest.mark.parametrize("name,arg", ARGS, ids=[f"{c}-{a}" for c, a in ARGS])
 
@@ -158,12 +176,13 @@ def tensors(name):
 def call(name, a):
     a = dict(a)
     first = {"norm": ("x", "gain"), "norm_backward": ("x", "gain", "rstd", "dy", "ws"), "dense_product": ("x", "w", "y", "ws"),
-             "dense_product_backward": ("dy", "ws"), "packed_product": ("x", "codes", "scales", "y", "ws")}[name]
+             "dense_product_backward": ("dy", "ws"), "packed_product": ("x", "codes", "scales", "y", "ws"),
+             "mx_product_coded": ("x_codes", "x_scales", "codes", "scales", "y")}[name]
     lead = [a.pop(n) for n in first]
     if name == "norm":
         lead.append(1e-5)
-    if name == "packed_product":
-        lead.insert(0, Q)
+    if name in ("packed_product", "mx_product_coded"):
+        lead.insert(0, Q if name == "packed_product" else em.MX_FP8)
     return getattr(em, "edge_moe_" + name)(*lead, **a)
 
 
@@ -197,6 +216,9 @@ def test_valid_calls_reach_the_library(lib):
         elif name == "dense_product":
             assert list(values(got[0]).values()) == [T, R, M, N, K]
             assert list(got[1:]) == [p["x"], K, p["row_src"], p["offsets"], p["w"], 1, p["y"], N, p["ws"], 999, 0x99]
+        elif name == "mx_product_coded":
+            assert list(values(got[0]).values()) == [T, R, M, N, K, em.MX_FP8]
+            assert list(got[1:]) == [p["x_codes"], p["x_scales"], p["row_src"], p["offsets"], p["codes"], p["scales"], p["y"], N, 0x99]
         else:
             assert list(values(got[0]).values()) == [T, R, M, N, K, Q]
             assert list(got[1:]) == [p["x"], K, p["row_src"], p["offsets"], p["codes"], p["scales"], 1, p["y"], N, p["ws"], 999, 0x99]
