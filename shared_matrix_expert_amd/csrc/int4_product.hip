@@ -371,29 +371,28 @@ ip_tile(Int4Product a) {
     // ---- loads: load u of a wave brings piece u NW + wv of x, of the codes, of the scales
     const char* xbase = reinterpret_cast<const char*>(a.row_src ? a.x : a.x + (int64_t)t.r0 * a.x_stride);
     const uint8_t* wbase = a.codes + ((int64_t)t.m * a.N + n0) * (a.K / 2);
-    uint32_t xoff[C::X_L], woff[C::W_L];
-    int xk[C::X_L], wk[C::W_L], scol[C::S_L], sgrp[C::S_L];       // the lane's first element of K within a step; scale columns and groups
+    uint32_t xoff[C::X_L], woff[C::W_L], soff[C::S_L];
+    // The lane's first element of K within a step: of an x load, of a code load.
+    auto x_k = [&](int u) {
+        const int row = (u * C::NW + wv) * 4 + lane / 16, slot = (lane & 15) ^ (row & 15);
+        return 8 * (GPC == 1 ? slot >> 2 | (slot & 3) << 2 : slot);
+    };
+    auto w_k = [&](int u) { return 32 * w_slot((u * C::NW + wv) * 16 + lane / 4, lane & 3); };
 #pragma unroll
     for (int u = 0; u < C::X_L; ++u) {
-        const int row = (u * C::NW + wv) * 4 + lane / 16, slot = (lane & 15) ^ (row & 15);
-        xk[u] = 8 * (GPC == 1 ? slot >> 2 | (slot & 3) << 2 : slot);
-        const int r = min(row, rows - 1);
-        xoff[u] = (uint32_t)(2 * ((a.row_src ? max(x_row(a, t.r0 + r), 0) : r) * a.x_stride + xk[u]));
+        const int r = min((u * C::NW + wv) * 4 + lane / 16, rows - 1);
+        xoff[u] = (uint32_t)(2 * ((a.row_src ? max(x_row(a, t.r0 + r), 0) : r) * a.x_stride + x_k(u)));
     }
 #pragma unroll
-    for (int u = 0; u < C::W_L; ++u) {
-        const int row = (u * C::NW + wv) * 16 + lane / 4;
-        wk[u] = 32 * w_slot(row, lane & 3);
-        woff[u] = min(row, a.N - 1 - n0) * (a.K / 2) + wk[u] / 2;
-    }
+    for (int u = 0; u < C::W_L; ++u) woff[u] = min((u * C::NW + wv) * 16 + lane / 4, a.N - 1 - n0) * (a.K / 2) + w_k(u) / 2;
+    // where the scales' pieces run out before the waves, the first again
+    auto s_piece = [&](int u) { return (u * C::NW + wv) % C::S_P; };
 #pragma unroll
-    for (int u = 0; u < C::S_L; ++u) {                            // where the pieces run out before the waves, the first again
-        const int piece = (u * C::NW + wv) % C::S_P;
-        sgrp[u] = piece / (BN / 64);
-        scol[u] = min(64 * (piece % (BN / 64)) + lane, a.N - 1 - n0);
-    }
+    for (int u = 0; u < C::S_L; ++u) soff[u] = min(64 * (s_piece(u) % (BN / 64)) + lane, a.N - 1 - n0) * ng;
     const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
     const int64_t srow0 = ((int64_t)t.m * a.N + n0) * ng;         // index of the first column's first scale
+    const uint16_t* sbase = a.scales + (srow0 & ~1ll);
+    const int sodd = (int)srow0 & 1;
     // index of scale group q of step st, the last one past K
     auto group_of = [&](int st, int q) { return min((KC * st + KC / GPC * q) / a.gq, ng - 1); };
     auto fetch = [&](int st, int u, auto fast) {
@@ -403,16 +402,16 @@ ip_tile(Int4Product a) {
             const uint32_t dst = __builtin_amdgcn_readfirstlane(stage + 1024 * (u * C::NW + wv));
             const char* from = xbase + (int64_t)st * 256;
             if constexpr (FAST) lds_load16(from, xoff[u], dst);
-            else lds_load16(KC * st + xk[u] < a.K ? from + xoff[u] : reinterpret_cast<const char*>(&ip_zero), dst);
+            else lds_load16(KC * st + x_k(u) < a.K ? from + xoff[u] : reinterpret_cast<const char*>(&ip_zero), dst);
         } else if (u < C::X_L + C::W_L) {
             const int v = u - C::X_L;
             const uint32_t dst = __builtin_amdgcn_readfirstlane(stage + C::X_B + 1024 * (v * C::NW + wv));
             if constexpr (FAST) lds_load16(wbase + (int64_t)st * 64, woff[v], dst);
-            else lds_load16(wbase + woff[v] - wk[v] / 2 + min(KC * st + wk[v], a.K - 32) / 2, dst);      // codes past K meet zeros
+            else lds_load16(wbase, woff[v] - w_k(v) / 2 + min(KC * st + w_k(v), a.K - 32) / 2, dst);      // codes past K meet zeros
         } else {
-            const int v = u - C::X_L - C::W_L, piece = (v * C::NW + wv) % C::S_P;
-            const int64_t i = srow0 + (int64_t)scol[v] * ng + group_of(st, sgrp[v]);
-            lds_load4v(a.scales + (i & ~1ll), __builtin_amdgcn_readfirstlane(stage + C::X_B + C::W_B + 256 * piece));
+            const int v = u - C::X_L - C::W_L, piece = s_piece(v);
+            const uint32_t i = (uint32_t)sodd + soff[v] + group_of(st, piece / (BN / 64));
+            lds_load4(sbase, 2u * (i & ~1u), __builtin_amdgcn_readfirstlane(stage + C::X_B + C::W_B + 256 * piece));
         }
     };
 
@@ -423,20 +422,19 @@ ip_tile(Int4Product a) {
         for (int j = 0; j < NJ; ++j) acc[p][j] = zero4();
     int odd[2];                                                   // parity of a column's first scale index
 #pragma unroll
-    for (int p = 0; p < 2; ++p) odd[p] = (int)(srow0 + (int64_t)min(32 * wv + 16 * p + m, a.N - 1 - n0) * ng) & 1;
+    for (int p = 0; p < 2; ++p) odd[p] = (sodd + min(32 * wv + 16 * p + m, a.N - 1 - n0) * ng) & 1;
     auto step = [&](int st, auto fast) {
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(C::LOADS) : "memory");   // this step landed, the one before is read
         const uint8_t* X = lds + (st % 3) * C::STAGE;
         const uint8_t* W = X + C::X_B;
         const uint32_t* S = reinterpret_cast<const uint32_t*>(W + C::W_B);
-        uint4 b[2][4];
+        uint4 raw[2];
         float sc[2][GPC];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             const int col = 32 * wv + 16 * p + m;
-            uint4 raw = *reinterpret_cast<const uint4*>(W + col * 64 + 16 * w_slot(m, g));
-            if constexpr (GPC > 1) raw = by_group(raw);
-            dequant_b(raw, b[p]);
+            raw[p] = *reinterpret_cast<const uint4*>(W + col * 64 + 16 * w_slot(m, g));
+            if constexpr (GPC > 1) raw[p] = by_group(raw[p]);
 #pragma unroll
             for (int q = 0; q < GPC; ++q) {
                 const uint32_t v = S[q * BN + col] >> (16 * ((odd[p] + group_of(st, q)) & 1));
@@ -447,17 +445,23 @@ ip_tile(Int4Product a) {
         floatx4 u[2][NJ];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint4 x[NJ];
+            uint4 x[NJ], b[2];                                    // converted 32 of K at a time, under the other wave's products
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
                 x[j] = *reinterpret_cast<const uint4*>(X + (16 * j + m) * 256 + 16 * x_slot<GPC>(m, GPC == 1 ? 4 * g + i : 4 * i + g));
 #pragma unroll
             for (int v = i * C::LOADS / 4; v < (i + 1) * C::LOADS / 4; ++v) fetch(st + 2, v, fast);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                uint32_t q[4];
+                dequant8(i == 0 ? raw[p].x : i == 1 ? raw[p].y : i == 2 ? raw[p].z : raw[p].w, q);
+                b[p] = make_uint4(q[0], q[1], q[2], q[3]);
+            }
             const bool first = i % (4 / GPC) == 0, last = (i + 1) % (4 / GPC) == 0;
 #pragma unroll
             for (int p = 0; p < 2; ++p)
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) u[p][j] = mfma_bf16(x[j], b[p][i], first ? zero4() : u[p][j]);
+                for (int j = 0; j < NJ; ++j) u[p][j] = mfma_bf16(x[j], b[p], first ? zero4() : u[p][j]);
             if (last) {
 #pragma unroll
                 for (int p = 0; p < 2; ++p)
@@ -549,19 +553,62 @@ hipError_t launch_rows(const Int4Product& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-struct IpPlan { int bt, bn, slices; };                            // bt 16, 32, 64 of ip_rows and ip_stream: bn 0
+struct IpPlan { int bt, bn, slices; };                            // bn 0: ip_rows (bt 16) or ip_stream (32, 64)
 
+// The least of an estimate in us from measured times.  Few rows: K / 4096 times a part of
+// its own and one a workgroup.  Tiles: a step of 128 of K alone on a compute unit or with it
+// full, 1.25 and 1.6 times that with two and four scale groups a step; slices of K are
+// joined by a launch more.  Measured (us, rows through M x N x K; 16, 32: rows a workgroup,
+// tiles rows x columns / slices): 20 through 4096 x 4096 16 13.0, 32 14.5, 64x128/8 13.9; 64
+// through 1024 x 4096 16 10.6, 32 15.9; 32 through 8192 x 4096 16 20, 32 17; 256 through 4096
+// x 4096 64x128/2 25.6, 128x256/8 29.6, 64x128 34; 4096 through 4096 x 4096 128x256 134, 64x128
+// 175; 4096 routed over 64 of 128 x 4096 64x128/4 24, 128x256/4 29.
 IpPlan plan(const Int4Product& a) {
+    struct Cost { int bt, bn, fit; float fixed, alone, full; };
+    static constexpr Cost kTiles[3] = {{64, 128, 2, 3.0f, 0.98f, 1.33f}, {64, 256, 1, 3.0f, 1.25f, 1.30f}, {128, 256, 1, 4.0f, 1.70f, 2.00f}};
     const int live = a.M < a.R ? a.M : (a.R ? a.R : 1);
-    const int64_t avg = ((int64_t)a.R + live - 1) / live;
-    if (avg <= 32) return IpPlan{avg <= 16 ? 16 : 32, 0, 1};
-    if ((int64_t)a.N * (a.K / a.gq) % 2) return IpPlan{64, 0, 1};  // the last scale's word would end past the scales
-    IpPlan p{avg <= 64 ? 64 : 128, 256, 1};
-    if (a.N <= 128) p = IpPlan{64, 128, 1};
-    const int64_t tiles = max_row_tiles(a, p.bt) * ((a.N + p.bn - 1) / p.bn);
+    const float each = (float)a.R / live, k = a.K / 4096.0f;
+    // row tiles of a matrix: among few matrices the last one is half empty on average; many
+    // (routed experts) have about as many rows each
+    const auto row_tiles = [&](int bt) {
+        const float q = each / bt, up = (float)(int)(q + 0.9f);
+        return a.M == 1 ? (float)((a.R + bt - 1) / bt) : (float)live * (a.M < 64 && q > 0.5f ? q + 0.5f : up > q + 0.25f ? up : q + 0.25f);
+    };
+    const auto few = [&](int bt, float own, float one, int fit) {  // workgroups past `fit` cost 0.055 each
+        const float n = row_tiles(bt) * ((a.N + 31) / 32);
+        return 4 + k * (own + one * (n < fit ? n : fit) + 0.055f * (n > fit ? n - fit : 0));
+    };
+    IpPlan best{16, 0, 1};
+    float least = few(16, 3.4f, 0.0234f, 512);
+    const auto take = [&](float us, IpPlan p) {
+        if (us < least) {
+            least = us;
+            best = p;
+        }
+    };
+    take(few(32, 9.8f, 0.0115f, 256), IpPlan{32, 0, 1});
+    if ((int64_t)a.N * (a.K / a.gq) % 2) {                        // the last scale's word would end past the scales
+        take(each > 64 ? 0.f : least, IpPlan{64, 0, 1});
+        return best;
+    }
     const int steps = (a.K + KC - 1) / KC;
-    while (tiles * p.slices * 2 <= 256 && steps >= 8 * p.slices && p.slices < 8) p.slices *= 2;
-    return p;
+    const float groups = a.gq >= KC || a.gq == a.K ? 1.f : a.gq == 64 ? 1.25f : 1.6f;
+    for (const Cost& t : kTiles) {
+        const float tiles = row_tiles(t.bt) * ((a.N + t.bn - 1) / t.bn);
+        for (int z = 1; z <= 8 && (z == 1 || (steps >= 2 * z && tiles * z < 2048)); z *= 2) {
+            const float n = tiles * z / 256, part = (float)((steps + z - 1) / z) * groups;
+            const int rounds = (int)(n / t.fit);
+            const float rest = n - rounds * t.fit;                // tiles a compute unit in the last round
+            float us = 4 + rounds * (t.fixed + part * t.full);
+            if (rest > 0) {
+                const float share = t.fit == 1 ? (rounds ? 1.f : rest) : (rest < 1 ? 0.f : rest - 1);
+                us += t.fixed + part * (t.alone + (t.full - t.alone) * (share < 1 ? share : 1.f));
+            }
+            if (z > 1) us += 4 + 0.15f * z + (float)((double)a.R * a.N * (8 * z + 2) / 5e6);
+            take(us, IpPlan{t.bt, t.bn, z});
+        }
+    }
+    return best;
 }
 
 template <int GPC, int BT, int BN>

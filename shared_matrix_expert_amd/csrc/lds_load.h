@@ -34,10 +34,4 @@ EM_DEV void lds_load4(const void* base, uint32_t off, uint32_t dst) {
                  : "=&s"(m0) : "v"(off), "s"(base), "s"(dst) : "memory");
 }
 
-EM_DEV void lds_load4v(const void* src, uint32_t dst) {       // from each lane's own address
-    uint32_t m0;
-    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %1, off\n\ts_mov_b32 m0, %0"
-                 : "=&s"(m0) : "v"(src), "s"(dst) : "memory");
-}
-
 }  // namespace em

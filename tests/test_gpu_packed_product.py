@@ -27,7 +27,8 @@ CASES = [
     (1, 64, 128, 512, 8, 128), (8, 512, 128, 1024, 10, 128), (96, 64, 128, 512, 4, 32), (300, 8, 65, 256, 3, 64),
     (777, 5, 520, 768, 0, 256), (1001, 8, 512, 1024, 0, 128), (900, 200, 40, 96, 7, 32), (600, 1024, 9, 64, 5, 64),
     (9, 1, 300, 4096, 0, 128), (13, 1, 96, 8192, 0, 128), (40, 1, 256, 4096, 0, 32), (500, 2, 300, 4096, 0, 64), (1200, 1, 130, 416, 0, 32),
-    (90, 3, 1000, 2080, 0, 32),
+    (90, 3, 1000, 2080, 0, 32), (700, 1, 1024, 4096, 0, 128), (5000, 2, 2048, 512, 0, 32), (4000, 1, 1000, 288, 0, 32),
+    (300, 64, 128, 1024, 8, 64), (77, 1, 130, 1152, 0, 128), (41, 1, 128, 96, 0, 128),
 ]
 
 
