@@ -5,8 +5,8 @@
 // cores and the sum is scaled by a float32 fused multiply-add: every weight is exactly
 // c s, as in the layer.
 //
-//   ip_rows    few rows a matrix: bound by the code bytes.  Four waves split K, stream the
-//              codes into operand registers and keep the x rows in the LDS.
+//   ip_rows    few rows a matrix: bound by the code bytes.  Four or eight waves split K, ask
+//              for their codes all at once in operand registers and keep the x rows in the LDS.
 //   ip_stream  the same for 17 to 32 rows, and where a tile's scales or rows lie too oddly:
 //              x straight from memory.
 //   ip_tile    many rows: LDS tiles by direct global -> LDS loads, counted by hand.
@@ -60,11 +60,11 @@ EM_DEV uint4 by_group(uint4 v) {
 // What lanes without an element read: x past K.
 __device__ const uint4 ip_zero = {0u, 0u, 0u, 0u};
 
-// The four waves' sums of 16 NS rows x 16 NC columns, added in wave order and stored: tile
-// i = (subtile s, column tile c) by wave i % 4; lane (g, m) holds rows 4 g .. 4 g + 3 of
+// The W waves' sums of 16 NS rows x 16 NC columns, added in wave order and stored: tile
+// i = (subtile s, column tile c) by wave i % W; lane (g, m) holds rows 4 g .. 4 g + 3 of
 // column m.
-template <int NS, int NC>
-EM_DEV void join_waves(const Int4Product& a, const floatx4 (&acc)[NS][NC], float (&red)[4][NS * NC][256], int r0, int r1, int n0) {
+template <int W, int NS, int NC>
+EM_DEV void join_waves(const Int4Product& a, const floatx4 (&acc)[NS][NC], float (&red)[W][NS * NC][256], int r0, int r1, int n0) {
     const int lane = lane_id(), wv = wave_id(), g = lane >> 4, m = lane & 15;
 #pragma unroll
     for (int s = 0; s < NS; ++s)
@@ -73,10 +73,10 @@ EM_DEV void join_waves(const Int4Product& a, const floatx4 (&acc)[NS][NC], float
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < NS * NC; ++i) {
-        if ((i & 3) != wv) continue;
+        if (i % W != wv) continue;
         floatx4 v = *reinterpret_cast<const floatx4*>(&red[0][i][4 * lane]);
 #pragma unroll
-        for (int q = 1; q < 4; ++q) v += *reinterpret_cast<const floatx4*>(&red[q][i][4 * lane]);
+        for (int q = 1; q < W; ++q) v += *reinterpret_cast<const floatx4*>(&red[q][i][4 * lane]);
         const int n = n0 + 16 * (i % NC) + m, r = r0 + 16 * (i / NC) + 4 * g;
         if (n >= a.N) continue;
 #pragma unroll
@@ -91,23 +91,23 @@ EM_DEV void join_waves(const Int4Product& a, const floatx4 (&acc)[NS][NC], float
 // elements of a K that is no multiple of 128 are a chunk whose missing x is zero.
 //
 // ------------------------------------------------------------------ few rows -----
-// A workgroup takes up to 16 rows of one matrix and 16 NC columns, a wave a quarter of K,
-// 1024 elements at a time: all of their codes and scales are asked for at once, then the x
-// rows into the wave's own part of the LDS, and one wait covers both.
-// VEC: a wave's scales of 1024 elements are 16 bytes (GPC 1: groups of 128, K a multiple of
-// 4096), those of a chunk 4 or 8 (GPC 2, 4: K a multiple of 128).
-template <int GPC, int NC, bool VEC>
-__global__ void __launch_bounds__(256)
+// A workgroup takes up to 16 rows of one matrix and 16 NC columns, each of its W waves a part
+// of K, 4096 / W elements at a time: all of their codes and scales are asked for at once, then
+// the x rows into the wave's own part of the LDS, and one wait covers both.
+// VEC: a wave's scales of such a block are 8 or 16 bytes (GPC 1: groups of 128, K a multiple
+// of 4096), those of a chunk 4 or 8 (GPC 2, 4: K a multiple of 128).
+template <int W, int GPC, int NC, bool VEC>
+__global__ void __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2)))
 ip_rows(Int4Product a) {
-    constexpr int WD = 8, XR = 8, RS = 2 * KC * WD + 16;          // chunks and x rows at once, bytes of an x row in the LDS
-    __shared__ __attribute__((aligned(16))) uint8_t xl[4][XR * RS];
-    __shared__ __attribute__((aligned(16))) float red[4][NC][256];
+    constexpr int WD = 32 / W, XR = 8, RS = 2 * KC * WD + 16;     // chunks and x rows at once, bytes of an x row in the LDS
+    static_assert(XR * RS >= NC * 1024, "");
+    __shared__ __attribute__((aligned(16))) uint8_t xl[W][XR * RS];
     const RowTile t = row_tile<16>(a.offsets, a.M, a.R, [](int) { return (int)blockIdx.y; });
     if (t.r1 == 0) return;
     const int lane = lane_id(), wv = wave_id(), g = lane >> 4, m = lane & 15;
     const int n0 = blockIdx.x * (16 * NC);
     const int chunks = (a.K + KC - 1) / KC;
-    const int s0 = chunks * wv / 4, s1 = chunks * (wv + 1) / 4;
+    const int s0 = chunks * wv / W, s1 = chunks * (wv + 1) / W;
     const int ng = a.K / a.gq, rows = t.r1 - t.r0;
 
     const uint8_t* wp[NC];
@@ -119,7 +119,7 @@ ip_rows(Int4Product a) {
         sp[c] = a.scales + row * ng;
     }
     uint4 w[WD][NC];
-    constexpr bool BLOCK = VEC && GPC == 1;                       // scales by 1024 elements
+    constexpr bool BLOCK = VEC && GPC == 1;                       // scales by blocks
     uint4 sb[NC];
     uint2 sc[BLOCK ? 1 : WD][NC];                                 // a chunk's scales, two a word
     auto load_w = [&](int d, int ch) {
@@ -149,10 +149,15 @@ ip_rows(Int4Product a) {
         else v = (q < 2 ? sc[d][c].x : sc[d][c].y) >> (16 * (q & 1));
         return 16.0f * fp16_bits_to_f32((uint16_t)v);
     };
+    auto load_scales_of = [&](int c, int ch) {                    // (BLOCK)
+        if constexpr (WD == 8) return ld16(sp[c] + ch);
+        const uint2 v = *reinterpret_cast<const uint2*>(sp[c] + ch);
+        return make_uint4(v.x, v.y, 0u, 0u);
+    };
     auto load_block = [&](int ch) {
         if constexpr (BLOCK) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c) sb[c] = ld16(sp[c] + min(ch, s1 - WD));
+            for (int c = 0; c < NC; ++c) sb[c] = load_scales_of(c, ch);
         }
 #pragma unroll
         for (int d = 0; d < WD; ++d) load_w(d, min(ch + d, s1 - 1));
@@ -166,64 +171,84 @@ ip_rows(Int4Product a) {
     floatx4 acc[1][NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) acc[0][c] = zero4();
-    for (int ch = s0; ch < s1; ch += WD) {
-        if (few) {
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");    // the rows before have been read
-            for (int r = 0; r < rows; ++r) {
-                const int from = __builtin_amdgcn_readlane(src, r);
-                const uint16_t* p = a.x + (int64_t)max(from, 0) * a.x_stride;
+    // One chunk of a block, and two at once: their conversions and products then interleave.
+    // (More at once cost registers, and with them waves: whole blocks without a branch took
+    // 7.6 us on one token through 8192 x 4096 with four waves, pairs 7.9, single chunks 9.0; 80
+    // rows over 512 of 128 x 4096 15.6, 12.4, 13.4.)
+    auto chunk = [&](int ch, int d, auto in_lds) {
+        constexpr bool LDS = decltype(in_lds)::value;
+        const int k0 = KC * (ch + d), left = a.K - k0;
+        uint4 x[4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int k = KC * ch + 512 * h + 8 * lane;
-                    const void* at = from >= 0 && k < a.K ? static_cast<const void*>(p + k) : static_cast<const void*>(&ip_zero);
-                    lds_load16(at, __builtin_amdgcn_readfirstlane(base + r * RS + 1024 * h));
-                }
-            }
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        }
-        uint4 sn[NC];
-        if constexpr (BLOCK) {
-#pragma unroll
-            for (int c = 0; c < NC; ++c) sn[c] = ld16(sp[c] + min(ch + WD, s1 - WD));
-        }
-#pragma unroll
-        for (int d = 0; d < WD; ++d) {
-            if (ch + d < s1) {
-                const int k0 = KC * (ch + d), left = a.K - k0;
-                uint4 x[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int at = GPC == 1 ? 32 * g + 8 * i : 32 * i + 8 * g;
-                    if (few) {
-                        x[i] = ld16(xrow + 2 * (KC * d + at));
-                    } else {
-                        const uint4 v = ld16(xp + k0 + (at < left ? at : 0));
-                        x[i] = at < left && src >= 0 ? v : zero_u4();
-                    }
-                }
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    uint4 raw = w[d][c];
-                    if constexpr (GPC > 1) raw = by_group(raw);
-                    uint4 b[4];
-                    dequant_b(raw, b);
-#pragma unroll
-                    for (int q = 0; q < GPC; ++q) {
-                        floatx4 u = zero4();
-#pragma unroll
-                        for (int i = 4 / GPC * q; i < 4 / GPC * (q + 1); ++i) u = mfma_bf16(x[i], b[i], u);
-                        acc[0][c] = fma4(scale(d, c, q), u, acc[0][c]);
-                    }
-                }
-                load_w(d, min(ch + d + WD, s1 - 1));
+        for (int i = 0; i < 4; ++i) {
+            const int at = GPC == 1 ? 32 * g + 8 * i : 32 * i + 8 * g;
+            if constexpr (LDS) {
+                x[i] = ld16(xrow + 2 * (KC * d + at));
+            } else {
+                const uint4 v = ld16(xp + k0 + (at < left ? at : 0));
+                x[i] = at < left && src >= 0 ? v : zero_u4();
             }
         }
-        if constexpr (BLOCK) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c) sb[c] = sn[c];
+        for (int c = 0; c < NC; ++c) {
+            uint4 raw = w[d][c];
+            if constexpr (GPC > 1) raw = by_group(raw);
+            uint4 b[4];
+            dequant_b(raw, b);
+#pragma unroll
+            for (int q = 0; q < GPC; ++q) {
+                floatx4 u = zero4();
+#pragma unroll
+                for (int i = 4 / GPC * q; i < 4 / GPC * (q + 1); ++i) u = mfma_bf16(x[i], b[i], u);
+                acc[0][c] = fma4(scale(d, c, q), u, acc[0][c]);
+            }
         }
-    }
-    join_waves<1, NC>(a, acc, red, t.r0, t.r1, n0);
+    };
+    auto run = [&](auto in_lds) {
+        for (int ch = s0; ch < s1; ch += WD) {
+            if constexpr (decltype(in_lds)::value) {
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");    // the rows before have been read
+                for (int r = 0; r < rows; ++r) {
+                    const int from = __builtin_amdgcn_readlane(src, r);
+                    const uint16_t* p = a.x + (int64_t)max(from, 0) * a.x_stride;
+#pragma unroll
+                    for (int h = 0; h < WD / 4; ++h) {
+                        const int k = KC * ch + 512 * h + 8 * lane;
+                        const void* at = from >= 0 && k < a.K ? static_cast<const void*>(p + k) : static_cast<const void*>(&ip_zero);
+                        lds_load16(at, __builtin_amdgcn_readfirstlane(base + r * RS + 1024 * h));
+                    }
+                }
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            }
+            const bool more = ch + WD < s1;
+            uint4 sn[NC];
+            if constexpr (BLOCK) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) sn[c] = load_scales_of(c, min(ch + WD, s1 - WD));
+            }
+#pragma unroll
+            for (int d = 0; d < WD; d += 2) {
+                if (ch + d + 1 < s1) {
+                    chunk(ch, d, in_lds);
+                    chunk(ch, d + 1, in_lds);
+                } else if (ch + d < s1) {
+                    chunk(ch, d, in_lds);
+                }
+                if (more) {
+                    load_w(d, min(ch + d + WD, s1 - 1));
+                    load_w(d + 1, min(ch + d + 1 + WD, s1 - 1));
+                }
+            }
+            if constexpr (BLOCK) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) sb[c] = sn[c];
+            }
+        }
+    };
+    if (few) run(std::true_type{});
+    else run(std::false_type{});
+    __syncthreads();                                              // the x rows have been read: their place takes the sums
+    join_waves<W, 1, NC>(a, acc, *reinterpret_cast<float(*)[W][NC][256]>(&xl[0][0]), t.r0, t.r1, n0);
 }
 
 // ------------------------------------------------------------------ 17 to 32 rows ----
@@ -313,7 +338,7 @@ ip_stream(Int4Product a) {
             }
         }
     }
-    join_waves<NS, NC>(a, acc, red, t.r0, t.r1, n0);
+    join_waves<4, NS, NC>(a, acc, red, t.r0, t.r1, n0);
 }
 
 // ------------------------------------------------------------------ many rows ----
@@ -542,13 +567,13 @@ hipError_t launch_stream(const Int4Product& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <int GPC, int NC>
+template <int W, int GPC, int NC>
 hipError_t launch_rows(const Int4Product& a, hipStream_t s) {
     const dim3 grid((a.N + 16 * NC - 1) / (16 * NC), (unsigned)max_row_tiles(a, 16));
     const bool vec = GPC == 1 ? a.gq == KC && a.K % 4096 == 0 : a.K % KC == 0;
     prof_begin(s);
-    if (vec) ip_rows<GPC, NC, true><<<grid, 256, 0, s>>>(a);
-    else ip_rows<GPC, NC, false><<<grid, 256, 0, s>>>(a);
+    if (vec) ip_rows<W, GPC, NC, true><<<grid, 64 * W, 0, s>>>(a);
+    else ip_rows<W, GPC, NC, false><<<grid, 64 * W, 0, s>>>(a);
     prof_end(s, "ip_rows");
     return hipGetLastError();
 }
@@ -634,8 +659,12 @@ hipError_t launch_product(const Int4Product& a, hipStream_t s) {
     if (p.bn == 0) {
         if (p.bt == 64) return launch_stream<GPC, 4>(a, s);
         if (p.bt == 32) return launch_stream<GPC, 2>(a, s);
-        // 32 columns a workgroup, 16 where that leaves half of the compute units idle
-        return max_row_tiles(a, 16) * ((a.N + 31) / 32) <= 128 ? launch_rows<GPC, 1>(a, s) : launch_rows<GPC, 2>(a, s);
+        // 32 columns a workgroup, 16 where that leaves half of the compute units idle; eight
+        // waves a workgroup while each has a compute unit to itself, four where two share one
+        // (one token through 8192 x 4096 with four 7.9 us, with eight 7.7, 12 tokens 10.5 and
+        // 8.9; 80 rows over 512 of 128 x 4096, 340 workgroups, 12.4 and 14.8)
+        const int64_t wgs = max_row_tiles(a, 16) * ((a.N + 31) / 32);
+        return wgs <= 128 ? launch_rows<8, GPC, 1>(a, s) : wgs <= 256 ? launch_rows<8, GPC, 2>(a, s) : launch_rows<4, GPC, 2>(a, s);
     }
     if (p.bn == 128) return launch_tile<GPC, 64, 128>(a, p, s);
     return p.bt == 64 ? launch_tile<GPC, 64, 256>(a, p, s) : launch_tile<GPC, 128, 256>(a, p, s);
