@@ -2,6 +2,7 @@
 // their gradients:
 //   DP_Y    y[r][n]     = sum_k x[src(r)][k] W_m[n][k]       (m the matrix of row r)
 //   DP_DX   dx[r][k]    = sum_n dy[r][n] W_m[n][k]           (or summed over a token's rows)
+//   DP_DXT  dx[t][k]    = sum over token t's rows r of the same, in one sum over all matrices
 //   DP_DW   dW_m[n][k]  = sum over m's rows r of dy[r][n] x[src(r)][k]
 // All three are out[i][j] = sum_c P[i][c] Q[j][c].  An operand whose c lies along its
 // rows comes from the LDS as it is; one whose c runs down the rows (W in dx, both in dW)
@@ -36,7 +37,7 @@ EM_DEV uint32_t pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
-enum DpMode { DP_Y = 0, DP_DX = 1, DP_DW = 2, DP_DWG = 3 };       // DWG: dW with gathered x rows
+enum DpMode { DP_Y = 0, DP_DX = 1, DP_DW = 2, DP_DWG = 3, DP_DXT = 4 };   // DWG: dW with gathered x rows
 
 // What lanes without an element read: rows and columns past an operand's end.
 __device__ const uint4 dp_zero = {0u, 0u, 0u, 0u};
@@ -178,7 +179,8 @@ namespace {
 
 template <int MODE, int BT_, int BN_>
 struct DpCfg {
-    static constexpr bool JT = MODE != DP_Y, IT = MODE >= DP_DW;      // c runs down the rows of Q, of P
+    static constexpr bool DW = MODE == DP_DW || MODE == DP_DWG;
+    static constexpr bool JT = MODE != DP_Y, IT = DW;                 // c runs down the rows of Q, of P
     static constexpr bool GATHER = MODE == DP_DWG;
     static constexpr int BT = BT_, BN = BN_;
     static constexpr int NW = BN == 256 || (BN == 128 && BT == 256) ? 8 : 4;
@@ -227,14 +229,15 @@ EM_DEV void dp_body(const DenseProduct& a, const DpTile& t, uint8_t* lds) {
     const int lane = lane_id(), wv = wave_id(), g = lane >> 4, m = lane & 15;
     const int mat = t.mat, i0 = t.i0, i1 = t.i1, j0 = t.j0, z = t.z, c0 = t.c0, clen = t.clen;
     const int steps = (clen + 63) >> 6, whole_steps = clen >> 6;
-    const int s0 = (int)((int64_t)steps * z / a.slices), s1 = (int)((int64_t)steps * (z + 1) / a.slices);
+    const int s0 = MODE == DP_DXT ? 0 : (int)((int64_t)steps * z / a.slices);
+    const int s1 = MODE == DP_DXT ? z * a.pass_steps : (int)((int64_t)steps * (z + 1) / a.slices);   // (z: the tile's passes)
 
     // ---- loads.  Load u of a wave brings piece u NW + wv: Q's first, then P's.
     const uint16_t* wm = a.w + (int64_t)mat * a.N * a.K;          // (not with dW)
     // Uniform base at step 0, and bytes a step.
-    const char* jbase = reinterpret_cast<const char*>(MODE == DP_Y ? wm + (int64_t)j0 * a.K : MODE == DP_DX ? wm : a.x + (int64_t)c0 * a.x_stride);
+    const char* jbase = reinterpret_cast<const char*>(MODE == DP_Y ? wm + (int64_t)j0 * a.K : !C::DW ? wm : a.x + (int64_t)c0 * a.x_stride);
     const char* ibase = reinterpret_cast<const char*>(MODE == DP_Y ? (a.row_src ? a.x : a.x + (int64_t)i0 * a.x_stride) : a.dy + (int64_t)(MODE == DP_DX ? i0 : c0) * a.dy_stride);
-    const int64_t jstride = MODE == DP_DX ? a.K : a.x_stride;     // of Q's rows, where c runs down them
+    const int64_t jstride = !C::DW ? a.K : a.x_stride;            // of Q's rows, where c runs down them
     const int64_t jadv = C::JT ? 128 * jstride : 128, iadv = C::IT ? 128 * a.dy_stride : 128;
     // A lane's place in load u: its row of c and column, or its row and first c.
     auto place = [&](int u, int& row, int& col) {
@@ -268,6 +271,7 @@ EM_DEV void dp_body(const DenseProduct& a, const DpTile& t, uint8_t* lds) {
     int64_t woff[WIDE ? C::LOADS : 1];
 #pragma unroll
     for (int u = 0; u < C::LOADS; ++u) {
+        if constexpr (MODE == DP_DXT) continue;                   // (made at each load)
         int row, col;
         place(u, row, col);
         if constexpr (WIDE) woff[u] = offset(u, C::GATHER && u < C::JL ? 0 : row, col);
@@ -294,6 +298,21 @@ EM_DEV void dp_body(const DenseProduct& a, const DpTile& t, uint8_t* lds) {
         const bool isj = u < C::JL;
         const uint32_t dst = __builtin_amdgcn_readfirstlane(base + (isj ? jstage(st) + 1024 * (u * C::NW + wv)
                                                                         : istage(st) + 1024 * ((u - C::JL) * C::NW + wv)));
+        if constexpr (MODE == DP_DXT) {                           // st: step of a pass over all matrices' rows
+            const int pass = st / a.pass_steps, c = 64 * (st - pass * a.pass_steps) + c_of(u), all = a.M * a.N;
+            const char* p = zero;
+            if (isj) {
+                int row, col;
+                place(u, row, col);
+                if (c < all) p = jbase + 2 * ((int64_t)c * a.K + col);
+            } else if (c < all && pass < t.z) {
+                const int tok = min(i0 + ((u - C::JL) * C::NW + wv) * 8 + lane / 8, i1 - 1), mt = c / a.N;
+                const int r = pass == 0 || pass < a.passes[tok] ? a.map[((int64_t)pass * a.T + tok) * a.M + mt] : -1;
+                if (r >= 0) p = reinterpret_cast<const char*>(a.dy + r * a.dy_stride + (c - mt * a.N));
+            }
+            lds_load16(p, dst);
+            return;
+        }
         const char* from = isj ? jbase + (C::GATHER ? -(int64_t)c0 * 2 * a.x_stride : st * jadv) : ibase + st * iadv;
         if (C::GATHER && isj) {
             const int s = from_row[u];
@@ -397,7 +416,7 @@ EM_DEV void dp_body(const DenseProduct& a, const DpTile& t, uint8_t* lds) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) fj[0][h] = read_j(s0, 0, h);
         int st = s0;
-        for (; st + 1 < s1 && st + 3 < whole_steps; st += 2) {
+        for (; MODE != DP_DXT && st + 1 < s1 && st + 3 < whole_steps; st += 2) {
             step(st, Set<0>{}, std::true_type{});
             step(st + 1, Set<1>{}, std::true_type{});
         }
@@ -413,12 +432,12 @@ EM_DEV void dp_body(const DenseProduct& a, const DpTile& t, uint8_t* lds) {
     // are stored: lane (g, m) holds columns 4 g .. 4 g + 3 of each j subtile, row m.  out itself
     // is stored past the caches (8192^3 814 -> 797 us, dW of 5001 rows 8 x 4096 x 8192 433 ->
     // 395), partial sums are read again and are not.
-    const int rows = MODE >= DP_DW ? a.M * a.N : a.R;
+    const int rows = C::DW ? a.M * a.N : a.R;
     const bool whole = a.slices == 1 && !a.to_part;
     const int64_t stride = whole ? a.out_stride : a.cols;
-    void* out = whole ? a.out : a.part + (int64_t)z * rows * a.cols - a.col0;
+    void* out = whole ? a.out : a.part + (int64_t)z * rows * a.cols - a.col0;            // (DP_DXT: whole)
     const int f32 = whole ? a.out_f32 : 1, J = a.col0 + a.cols;
-    const int64_t r0 = (MODE >= DP_DW ? (int64_t)mat * a.N : 0) + i0 + 16 * NJ * wt;
+    const int64_t r0 = (C::DW ? (int64_t)mat * a.N : 0) + i0 + 16 * NJ * wt;
     const int left = i1 - i0 - 16 * NJ * wt, col0 = j0 + 16 * NI * wn;
     constexpr int RS = NI * 64 + 16;
     uint8_t* o = lds + wv * C::OUT_B;
@@ -431,6 +450,32 @@ EM_DEV void dp_body(const DenseProduct& a, const DpTile& t, uint8_t* lds) {
         for (int p = 0; p < NI; ++p) *reinterpret_cast<floatx4*>(o + m * RS + 64 * p + 16 * g) = named[j] ? acc[p][j] : zero4();
         __builtin_amdgcn_wave_barrier();                          // one wave's LDS accesses complete in order
         asm volatile("" ::: "memory");
+        if constexpr (MODE == DP_DXT) {
+            // the one sum multiplies every matrix's rows, by zeros where the token has no row of
+            // it: what is not finite is summed anew from the token's own rows alone
+            bool bad = false;
+#pragma unroll
+            for (int p = 0; p < NI; ++p)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) bad |= !(fabsf(acc[p][j][v]) < __builtin_inff());
+            if (__ballot(bad)) {
+                for (int e = lane; e < 16 * 16 * NI; e += 64) {
+                    float* at = reinterpret_cast<float*>(o + e / (16 * NI) * RS) + e % (16 * NI);
+                    const int tok = i0 + 16 * (NJ * wt + j) + e / (16 * NI), col = col0 + e % (16 * NI);
+                    if (fabsf(*at) < __builtin_inff() || tok >= i1 || col >= a.K) continue;
+                    float sum = 0.f;
+                    for (int pass = 0; pass < a.passes[tok]; ++pass)
+                        for (int mt = 0; mt < a.M; ++mt) {
+                            const int r = a.map[((int64_t)pass * a.T + tok) * a.M + mt];
+                            for (int n = 0; r >= 0 && n < a.N; ++n)
+                                sum = fmaf(bf16_to_f32(a.dy[r * a.dy_stride + n]), bf16_to_f32(a.w[((int64_t)mt * a.N + n) * a.K + col]), sum);
+                        }
+                    *at = sum;
+                }
+                __builtin_amdgcn_wave_barrier();
+                asm volatile("" ::: "memory");
+            }
+        }
         if (f32) {
             constexpr int LPR = NI * 4, RPI = 64 / LPR;
 #pragma unroll
@@ -463,7 +508,7 @@ EM_DEV void dp_body(const DenseProduct& a, const DpTile& t, uint8_t* lds) {
 
 // Tiles of the largest size come in rounds of 256, one a compute unit; what is left of the
 // last round, if it is half of one or less, is made as tiles of half the rows (5001 rows
-// in 8 groups, 4096 columns, K = 8192: 356 us whole, 317 with halves).
+// in 8 groups, 4096 columns, K = 8192: 364 us whole, 338 with halves).
 template <int MODE, int BT, int BN, bool WIDE>
 __global__ void __launch_bounds__((DpCfg<MODE, BT, BN>::NW * 64))
 dp_tile(DenseProduct a) {
@@ -482,7 +527,7 @@ dp_tile(DenseProduct a) {
         return whole + (h >> 1);
     };
     DpTile d{};
-    if constexpr (MODE >= DP_DW) {
+    if constexpr (C::DW) {
         const int ni = (a.N + BT - 1) / BT, tiles = ni * nn, each = a.M * tiles;
         int tile;
         if (a.M == 1 || tiles < 8) {
@@ -504,6 +549,16 @@ dp_tile(DenseProduct a) {
         d.j0 = tile % nn * BN;
         d.c0 = a.offsets ? min(max(a.offsets[d.mat], 0), a.R) : 0;
         d.clen = (a.offsets ? min(max(a.offsets[d.mat + 1], d.c0), a.R) : a.R) - d.c0;
+    } else if constexpr (MODE == DP_DXT) {                        // tokens; z: the most passes that one of them needs
+        const int b = pick(a.row_tiles * nn);
+        if (b < 0) return;
+        d.i0 = b / nn * BT;
+        d.i1 = min(a.T, d.i0 + BT);
+        d.j0 = b % nn * BN;
+        for (int t0 = d.i0; t0 < d.i1; t0 += 64) {
+            const int n = a.passes[min(t0 + lane_id(), d.i1 - 1)];
+            for (int p = d.z + 1; __ballot(n >= p); ++p) d.z = p;
+        }
     } else {
         const RowTile t = row_tile<BT>(a.offsets, a.M, a.R, [&](int rows) {
             rows = min(rows, a.row_tiles);                       // more only where offsets descend
@@ -532,6 +587,45 @@ dp_tile(DenseProduct a) {
         }
     }
     dp_body<MODE, BT, BN, WIDE>(a, d, lds);
+}
+
+// map[p][t][m]: the p-th row of token t that belongs to matrix m, -1 for none (passes past
+// the first: only where some matrix has that many); passes[t]: the most rows that token t
+// has of one matrix.  A thread a token, offsets and counts in the LDS.
+constexpr int kMapMatrices = 128, kMapRows = 32;                  // most matrices, and rows of a token
+__global__ void __launch_bounds__(64)
+dp_token_map(const int32_t* __restrict__ offsets, const int32_t* __restrict__ token_rows, int per_token, int T, int M, int R,
+             int32_t* __restrict__ map, int32_t* __restrict__ passes) {
+    __shared__ int32_t off[kMapMatrices + 1];
+    __shared__ uint8_t count[64][kMapMatrices];
+    for (int i = threadIdx.x; i <= M; i += 64) off[i] = offsets ? min(max(offsets[i], 0), R) : i ? R : 0;
+    __syncthreads();
+    const int t = blockIdx.x * 64 + threadIdx.x;
+    if (t >= T) return;
+    uint8_t* n = count[threadIdx.x];
+    for (int m = 0; m < M; ++m) {
+        n[m] = 0;
+        map[(int64_t)t * M + m] = -1;
+    }
+    int most = 0;
+    for (int j = 0; j < per_token; ++j) {
+        const int r = token_rows[(int64_t)t * per_token + j];
+        if (r < off[0] || r >= off[M]) continue;
+        int lo = 0, hi = M;                                       // off[lo] <= r < off[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (off[mid] <= r) lo = mid;
+            else hi = mid;
+        }
+        const int p = n[lo]++;
+        int32_t* to = map + ((int64_t)p * T + t) * M;
+        if (p == most) {
+            most = p + 1;
+            for (int m = 0; p > 0 && m < M; ++m) to[m] = -1;
+        }
+        to[lo] = r;
+    }
+    passes[t] = most;
 }
 
 // ------------------------------------------------------------------ sums ---------
@@ -611,7 +705,7 @@ bool wide_rows(const DenseProduct& a, int mode) {
 // 2048 64x64 12, 256x256 40; 64 x 1 x 4096 x 4096 64x64/8 15, 64x64 29; dx of 4096 tokens'
 // four of 64 x 512 x 1024 128x128 35, 256x256 40; dW of 16384 x 1 x 128 x 4096 64x256/8 34,
 // 64x256 149.
-DpPlan plan(const DenseProduct& a, int mode) {
+DpPlan plan(const DenseProduct& a, int mode, int most_slices = 16, float* us_out = nullptr) {
     struct Cost { int bt, bn, fit; float fixed, alone, full, dw_full; };
     static constexpr Cost kTiles[9] = {
         {64, 64, 4, 2.6f, 0.37f, 0.73f, 1.05f},  {64, 128, 2, 2.8f, 0.44f, 0.69f, 0.92f},  {64, 256, 1, 3.2f, 0.54f, 0.66f, 0.69f},
@@ -632,7 +726,7 @@ DpPlan plan(const DenseProduct& a, int mode) {
         const float tiles = nn * (mode == DP_DW ? (float)a.M * ((a.N + t.bt - 1) / t.bt) : rows);
         const float full = mode == DP_DW ? t.dw_full : t.full;
         const int fit = mode == DP_DW && t.bt + t.bn == 256 && t.bt == 128 ? 1 : t.fit;   // (gathered x rows do not fit beside two)
-        for (int z = 1; z <= 16 && (z == 1 || (steps >= 2 * z && tiles * z < 4096)); z *= 2) {
+        for (int z = 1; z <= most_slices && (z == 1 || (steps >= 2 * z && tiles * z < 4096)); z *= 2) {
             const float n = tiles * z / 256, chain = t.fixed + (float)((steps + z - 1) / z) * full;     // a full round
             const int rounds = (int)(n / fit);
             const float rest = n - rounds * fit;                // tiles a compute unit in the last round
@@ -650,6 +744,7 @@ DpPlan plan(const DenseProduct& a, int mode) {
             }
         }
     }
+    if (us_out) *us_out = least;
     return best;
 }
 
@@ -657,7 +752,7 @@ template <int MODE, int BT, int BN, bool WIDE = false>
 hipError_t launch_tile(const DenseProduct& a, int64_t blocks, hipStream_t s) {
     prof_begin(s);
     dp_tile<MODE, BT, BN, WIDE><<<(unsigned)((blocks + (BT + BN == 512 ? 128 : 0) + 7) & ~7ll), DpCfg<MODE, BT, BN>::NW * 64, 0, s>>>(a);
-    prof_end(s, MODE == DP_Y ? "dp_tile_y" : MODE == DP_DX ? "dp_tile_dx" : "dp_tile_dw");
+    prof_end(s, MODE == DP_Y ? "dp_tile_y" : MODE == DP_DX || MODE == DP_DXT ? "dp_tile_dx" : "dp_tile_dw");
     return hipGetLastError();
 }
 
@@ -679,8 +774,9 @@ hipError_t launch_tile(DenseProduct a, DpPlan p, hipStream_t s) {
     const int nn = (a.cols + p.bn - 1) / p.bn;
     a.slices = p.slices;
     a.row_tiles = (int)max_row_tiles(a, p.bt);
-    const int64_t tiles = (MODE >= DP_DW ? (int64_t)((a.N + p.bt - 1) / p.bt) : a.row_tiles) * nn;   // (dW: of a matrix)
-    const int64_t blocks = (MODE >= DP_DW ? a.M * (a.M > 1 && tiles >= 8 ? (tiles + 7) & ~7ll : tiles) : tiles) * p.slices;
+    constexpr bool DW = MODE == DP_DW || MODE == DP_DWG;
+    const int64_t tiles = (DW ? (int64_t)((a.N + p.bt - 1) / p.bt) : a.row_tiles) * nn;              // (dW: of a matrix)
+    const int64_t blocks = (DW ? a.M * (a.M > 1 && tiles >= 8 ? (tiles + 7) & ~7ll : tiles) : tiles) * p.slices;
     if (wide) return launch_tile<MODE, 128, 128, true>(a, blocks, s);
     switch (p.bt) {
         case 64: return launch_tile<MODE, 64>(a, p.bn, blocks, s);
@@ -744,6 +840,31 @@ int token_cols(const DenseProduct& a, int slices) {
     return cols < 256 ? 256 : cols < a.K ? (int)cols : a.K;
 }
 
+// dx of tokens in one sum over all matrices (DP_DXT), where that is estimated to take less
+// than the rows' products and their way through memory: few matrices of few rows, LoRA's
+// inputs among them.  A step waits for its rows' places in the map, so it counts for two of
+// plan()'s; the rows' half counts what the caches leave of 8 bytes written and read again.
+// us, rows and then added -> one sum, fp32 out, T tokens' k of M matrices: T 512 k 3 of
+// 8 x 16 x 4096 18.6 -> 16.0, T 1501 36.1 -> 18.3, T 16384 352 -> 87; T 1501 k 8 of
+// 64 x 16 x 4096 78 -> 55; and left as rows: T 16 of 8 x 16 x 4096 15.8 -> 16.0, T 1501 k 3 of
+// 8 x 128 x 4096 39 -> 48, k 2 of 4 x 256 x 1024 17.4 -> 24.4, T 4096 k 2 of 128 x 8 x 1024 30 -> 44.
+struct TokenPlan { bool one_sum; DpPlan p; size_t bytes; };
+TokenPlan token_plan(const DenseProduct& a) {
+    TokenPlan t{};
+    const int64_t c = (int64_t)a.M * a.N, bytes = ((int64_t)kMapRows * a.M + 1) * a.T * 4;
+    if (c > 1024 || a.M > kMapMatrices || bytes > (256ll << 20)) return t;
+    DenseProduct one{};
+    one.T = one.R = a.T; one.M = 1; one.N = (int)c; one.K = a.K;
+    float sum = 0, rows = 0;
+    t.p = plan(one, DP_DX, 1, &sum);
+    if (t.p.bt > 128) t.p.bt = 128;
+    if (t.p.bn < 128 || t.p.bt < 128) t.p.bn = 128;
+    plan(a, DP_DX, 16, &rows);
+    t.one_sum = 2 * sum + a.M / 16.f < rows + 5 + (float)((double)a.R * a.K * 4 / 4.5e6);
+    t.bytes = (size_t)bytes;
+    return t;
+}
+
 // dx's partial sums (or rows, for tokens) and dW's share the workspace: dW runs first.
 size_t dense_backward_ws_bytes(const DenseProduct& a) {
     const DpPlan pw = plan(a, DP_DW), px = plan(a, DP_DX);
@@ -751,8 +872,10 @@ size_t dense_backward_ws_bytes(const DenseProduct& a) {
     const size_t x = px.slices > 1 ? part_bytes(a, DP_DX, px.slices) : 0;
     const int cols = token_cols(a, px.slices);
     const size_t t = up((size_t)px.slices * a.R * (cols < a.K ? cols : a.K) * 4);
+    const TokenPlan tp = token_plan(a);
     if (x > w) w = x;
-    return t > w ? t : w;
+    if (t > w) w = t;
+    return tp.one_sum && tp.bytes > w ? tp.bytes : w;
 }
 
 hipError_t launch_dense_backward(const DenseGrad& gr, void* ws, hipStream_t s) {
@@ -775,6 +898,25 @@ hipError_t launch_dense_backward(const DenseGrad& gr, void* ws, hipStream_t s) {
         const hipError_t e = a.R ? launch_tile<DP_DX>(a, p, s) : hipSuccess;
         if (e != hipSuccess || p.slices == 1) return e;
         return launch_join(RowJoin{a.part, p.slices, a.R, a.K, gr.dx, gr.dx_stride, gr.dx_f32, 1, a.R, a.offsets, a.M, nullptr, 0}, s);
+    }
+    const TokenPlan tp = token_plan(a);
+    if (tp.one_sum && gr.per_token <= kMapRows) {
+        int32_t* passes = static_cast<int32_t*>(ws);
+        int32_t* map = passes + a.T;
+        prof_begin(s);
+        dp_token_map<<<(a.T + 63) / 64, 64, 0, s>>>(a.offsets, gr.token_rows, gr.per_token, a.T, a.M, a.R, map, passes);
+        prof_end(s, "dp_token_map");
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        a.map = map;
+        a.passes = passes;
+        a.pass_steps = (a.M * a.N + 63) / 64;
+        a.slices = 1;
+        a.cols = a.K;
+        a.row_tiles = (a.T + tp.p.bt - 1) / tp.p.bt;
+        const int64_t blocks = (int64_t)a.row_tiles * ((a.K + tp.p.bn - 1) / tp.p.bn);
+        if (tp.p.bt == 64) return launch_tile<DP_DXT, 64, 128>(a, blocks, s);
+        return tp.p.bn == 128 ? launch_tile<DP_DXT, 128, 128>(a, blocks, s) : launch_tile<DP_DXT, 128, 256>(a, blocks, s);
     }
     a.to_part = 1;
     for (a.col0 = 0; a.col0 < a.K; a.col0 += a.cols) {

@@ -128,6 +128,7 @@ struct DenseProduct {
     void* out; int64_t out_stride; int out_f32;
     int slices, row_tiles, to_part;
     int col0, cols;             // columns of out that a launch makes
+    const int32_t* map; const int32_t* passes; int pass_steps;   // dx of tokens in one sum: rows by token and matrix
     float* part;                // workspace: [slices][rows][columns] of out
 };
 struct DenseGrad {

@@ -27,7 +27,7 @@ CASES = [
     (70, 1, 520, 264, 0), (129, 1, 136, 1000, 0), (257, 1, 264, 520, 0), (1000, 1, 2048, 1024, 0), (3000, 1, 16, 2048, 0),
     (2500, 1, 2048, 16, 0), (1, 64, 128, 512, 8), (8, 512, 128, 1024, 10), (96, 64, 128, 512, 4), (300, 8, 64, 264, 3),
     (1501, 8, 16, 1024, 3), (777, 5, 520, 776, 0), (2000, 8, 1024, 512, 0), (900, 200, 40, 72, 7), (600, 1024, 8, 64, 5),
-    (4096, 3, 768, 1544, 2), (5300, 1, 4104, 264, 0), (5000, 3, 4096, 328, 0), (300, 2, 4360, 4360, 0),
+    (1000, 16, 8, 2056, 6), (3000, 12, 80, 1000, 4), (20000, 40, 16, 520, 5), (4096, 3, 768, 1544, 2), (5300, 1, 4104, 264, 0), (5000, 3, 4096, 328, 0), (300, 2, 4360, 4360, 0),
 ]
 
 
@@ -250,6 +250,30 @@ def test_what_is_not_finite_reaches_only_its_own_sums():
     y = run(x, w, R, torch.float32, offsets, None)
     bad = ~y[4:41].isfinite()
     assert not bool(bad[:, :5].any()) and not bool(bad[:, 6:].any())
+
+
+@pytest.mark.parametrize("T,M,N,K,k", [(150, 8, 16, 264, 3), (600, 8, 16, 2056, 4), (2500, 8, 24, 1160, 3), (250, 16, 64, 8200, 6), (5000, 40, 16, 520, 5)])
+def test_tokens_see_only_their_own_matrices(T, M, N, K, k):
+    """dx by tokens where one matrix is NaN and one infinite: the tokens that have no row
+    of them have their exact sums; tokens with several rows of one matrix."""
+    g = torch.Generator(device=DEV).manual_seed(16)
+    R, off, offsets, src, token_rows = plan(T, M, k, 9)
+    token_rows[1] = token_rows[0]                                 # rows of two tokens
+    token_rows[2] = token_rows[2, 0]                              # one row k times
+    token_rows[3, 0] = -1
+    w, dy = whole(g, M, N, K), whole(g, R, N)
+    want = gradients(torch.zeros(T, K, device=DEV), w, dy, off, None if src is None else src, token_rows)[0]
+    w[1], w[3, :, ::2] = float("nan"), float("inf")
+    dx = torch.full((T, K), 7.0, device=DEV)
+    ws = workspace(em.edge_moe_dense_product_backward_ws_bytes(T, R, M, N, K))
+    em.edge_moe_dense_product_backward(dy, ws[:-GUARD], w=w, dx=dx, offsets=offsets, token_rows=token_rows)
+    assert bool((ws[-GUARD:] == 0xA5).all())
+    tr = token_rows.cpu().numpy()
+    mats = [set(np.searchsorted(off, r, side="right") - 1 for r in row if r >= 0) for row in tr]
+    clean = torch.tensor([not ms & {1, 3} for ms in mats], device=DEV)
+    assert torch.equal(dx[clean].double(), want[clean]) and bool(clean.any())
+    nans = torch.tensor([1 in ms for ms in mats], device=DEV)
+    assert bool(dx[nans].isnan().all()) and bool(nans.any())
 
 
 def test_offsets_that_are_no_offsets_stay_inside():
