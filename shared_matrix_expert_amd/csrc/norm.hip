@@ -6,11 +6,20 @@
 //             dx = dres + dr,  dgain = sum_t dy v
 //
 // Each row is read once, kept in registers over the reduction and written once, so
-// both directions are bound by HBM.  W waves share a row, each lane NV runs of eight
-// neighbours; an MX block is then four neighbouring lanes.  A workgroup takes a run
-// of neighbouring rows and asks for the next row before it reduces the present one;
-// the gain stays in registers.  The squares are summed in float64: no bf16 row
-// overflows there, and the sum's order does not show.
+// both directions are bound by HBM (measured: a large copy passes 5.1 TB/s).  W waves
+// share a row, each lane NV runs of eight neighbours; an MX block is then four
+// neighbouring lanes.  The squares are summed in float64: no bf16 row overflows there,
+// and the sum's order does not show.
+//
+// Forward: a workgroup a row, or four rows of 1024 and less.  16384 rows of 4096, float32
+// added, codes out, 606 MB: 103 us, 5.9 TB/s; runs of rows a workgroup, the next row asked
+// for ahead, 116 us (4096 workgroups) and 126 us (2048).  bf16 added, bf16 out, 537 MB: 80,
+// 82 and 110 us.
+//
+// Backward: a workgroup takes a run of neighbouring rows and asks for the next one before it
+// reduces the present one; the gain and its gradient stay in registers, so that dgain passes
+// through memory once a workgroup.  16384 rows of 4096, bf16, 537 MB: 109 us with dgain's
+// launch, 5 us of it; 1024 workgroups 122, 256 117.
 #include <type_traits>
 
 #include "mx_format.h"
@@ -111,8 +120,8 @@ EM_DEV double wave_sum_f64(double v) {
 }
 
 // Sum over the row's W waves; `turn` alternates, so that one barrier a row is enough.
-template <int W>
-EM_DEV double row_sum(double v, double (&slots)[2][W], int turn) {
+template <int W, int N>
+EM_DEV double row_sum(double v, double (&slots)[N][W], int turn) {
     v = wave_sum_f64(v);
     if constexpr (W == 1) return v;
     const int wv = wave_id();
@@ -131,6 +140,16 @@ EM_DEV double rsqrt_f64(double m) {
     return r * fma(-0.5 * m * r, r, 1.5);
 }
 
+// Stored past the caches, where the rows read next would take their place.
+EM_DEV void past_caches(void* to, const uint4& v) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, static_cast<u32x4*>(to));
+}
+EM_DEV void past_caches(void* to, const uint2& v) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    __builtin_nontemporal_store(u32x2{v.x, v.y}, static_cast<u32x2*>(to));
+}
+
 // Rows of a workgroup: W > 1 one at a time, W = 1 one a wave.
 template <int W> constexpr int rows_at_once() { return W == 1 ? 4 : 1; }
 template <int W> constexpr int norm_threads() { return W == 1 ? 256 : 64 * W; }
@@ -141,12 +160,10 @@ template <int W> constexpr int norm_threads() { return W == 1 ? 256 : 64 * W; }
 template <int W, int NV, int ADD>
 __global__ void __launch_bounds__(norm_threads<W>())
 norm_forward(NormFwd a) {
-    __shared__ double slots[2][W];
+    __shared__ double slots[1][W];
     const int in_row = W == 1 ? lane_id() : (int)threadIdx.x;
-    const int first = blockIdx.x * a.chunk + (W == 1 ? wave_id() : 0);
-    const int last = min(a.T, (int)(blockIdx.x + 1) * a.chunk);
-    constexpr int STEP = rows_at_once<W>();
-    if (first >= last) return;                                 // W = 1 only: a wave without rows (no barrier there)
+    const int t = W == 1 ? 4 * blockIdx.x + wave_id() : blockIdx.x;
+    if (t >= a.T) return;                                      // W = 1 only: a wave without a row (no barrier there)
     bool live[NV];
     int at[NV];                                                // lanes past the row read its first elements again
     float gain[NV][8];
@@ -159,70 +176,62 @@ norm_forward(NormFwd a) {
     }
     Raw8<false> xr[NV];
     Raw8<ADD == 2> ar[NV];
-    auto fetch = [&](int t) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            load8(xr[i], a.x + t * a.x_stride, at[i]);
-            if constexpr (ADD == 2) load8(ar[i], static_cast<const float*>(a.add) + t * a.add_stride, at[i]);
-            if constexpr (ADD == 1) load8(ar[i], static_cast<const uint16_t*>(a.add) + t * a.add_stride, at[i]);
+    for (int i = 0; i < NV; ++i) {
+        load8(xr[i], a.x + t * a.x_stride, at[i]);
+        if constexpr (ADD == 2) load8(ar[i], static_cast<const float*>(a.add) + t * a.add_stride, at[i]);
+        if constexpr (ADD == 1) load8(ar[i], static_cast<const uint16_t*>(a.add) + t * a.add_stride, at[i]);
+    }
+    uint4 r[NV];                                           // the row in bf16
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float f[8];
+        widen8(xr[i], f);
+        if constexpr (ADD != 0) {
+            float g[8];
+            widen8(ar[i], g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = sum_for_bf16(f[j], g[j]);
+            r[i] = pack8(f);
+            Raw8<false> back;
+            back.v[0] = r[i];
+            widen8(back, f);
+        } else {
+            r[i] = xr[i].v[0];
         }
-    };
-    fetch(first);
-    int turn = 0;
-    for (int t = first; t < last; t += STEP) {
-        uint4 r[NV];                                           // the row in bf16
-        double sum = 0.0;
+        double s = 0.0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float f[8];
-            widen8(xr[i], f);
-            if constexpr (ADD != 0) {
-                float g[8];
-                widen8(ar[i], g);
+        for (int j = 0; j < 8; ++j) s = fma((double)f[j], (double)f[j], s);
+        sum += live[i] ? s : 0.0;
+    }
+    sum = row_sum<W>(sum, slots, 0);
+    const float rstd = (float)rsqrt_f64(sum * a.per_d + (double)a.eps);
+    if (a.rstd && in_row == 0) a.rstd[t] = rstd;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = sum_for_bf16(f[j], g[j]);
-                r[i] = pack8(f);
-                Raw8<false> back;
-                back.v[0] = r[i];
-                widen8(back, f);
-            } else {
-                r[i] = xr[i].v[0];
-            }
-            double s = 0.0;
+    for (int i = 0; i < NV; ++i) {
+        if (a.x_out && live[i]) past_caches(a.x_out + t * a.xo_stride + at[i], r[i]);
+        if (!a.y && !a.codes) continue;
+        float f[8];
+        Raw8<false> rr;
+        rr.v[0] = r[i];
+        widen8(rr, f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s = fma((double)f[j], (double)f[j], s);
-            sum += live[i] ? s : 0.0;
-        }
-        if (t + STEP < last) fetch(t + STEP);
-        sum = row_sum<W>(sum, slots, turn);
-        turn ^= 1;
-        const float rstd = (float)rsqrt_f64(sum * a.per_d + (double)a.eps);
-        if (a.rstd && in_row == 0) a.rstd[t] = rstd;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (a.x_out && live[i]) *reinterpret_cast<uint4*>(a.x_out + t * a.xo_stride + at[i]) = r[i];
-            if (!a.y && !a.codes) continue;
-            float f[8];
-            Raw8<false> rr;
-            rr.v[0] = r[i];
-            widen8(rr, f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * gain[i][j];
-            const uint4 y = pack8(f);
-            if (a.y && live[i]) *reinterpret_cast<uint4*>(a.y + t * a.y_stride + at[i]) = y;
-            if (a.codes) {                                     // d a multiple of 128: a block's four lanes are live together
-                uint32_t m = amax8_bf16(y);
-                m = max(m, (uint32_t)__builtin_amdgcn_update_dpp((int)m, (int)m, 0xB1, 0xF, 0xF, false));
-                m = max(m, (uint32_t)__builtin_amdgcn_update_dpp((int)m, (int)m, 0x4E, 0xF, 0xF, false));
-                const int X = e8m0_of<kMxFp8>(m);
-                const bool bad = X == 255;
-                const float sc = e8m0_f32(bad ? 127 : X);
-                const uint32_t lim = e4m3_limit(bad ? 127 : X);
-                const uint32_t q0 = fp8x4_bf16(y.x, y.y, sc, lim), q1 = fp8x4_bf16(y.z, y.w, sc, lim);
-                if (live[i]) {
-                    *reinterpret_cast<uint2*>(a.codes + (int64_t)t * a.d + at[i]) = bad ? make_uint2(0u, 0u) : make_uint2(q0, q1);
-                    if (!(lane_id() & 3)) a.scales[((int64_t)(at[i] >> 7) * a.T + t) * 4 + (at[i] >> 5 & 3)] = (uint8_t)X;
-                }
+        for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * gain[i][j];
+        const uint4 y = pack8(f);
+        if (a.y && live[i]) past_caches(a.y + t * a.y_stride + at[i], y);
+        if (a.codes) {                                     // d a multiple of 128: a block's four lanes are live together
+            uint32_t m = amax8_bf16(y);
+            m = max(m, (uint32_t)__builtin_amdgcn_update_dpp((int)m, (int)m, 0xB1, 0xF, 0xF, false));
+            m = max(m, (uint32_t)__builtin_amdgcn_update_dpp((int)m, (int)m, 0x4E, 0xF, 0xF, false));
+            const int X = e8m0_of<kMxFp8>(m);
+            const bool bad = X == 255;
+            const float sc = e8m0_f32(bad ? 127 : X);
+            const uint32_t lim = e4m3_limit(bad ? 127 : X);
+            const uint32_t q0 = fp8x4_bf16(y.x, y.y, sc, lim), q1 = fp8x4_bf16(y.z, y.w, sc, lim);
+            if (live[i]) {
+                past_caches(a.codes + (int64_t)t * a.d + at[i], bad ? make_uint2(0u, 0u) : make_uint2(q0, q1));
+                if (!(lane_id() & 3)) a.scales[((int64_t)(at[i] >> 7) * a.T + t) * 4 + (at[i] >> 5 & 3)] = (uint8_t)X;
             }
         }
     }
@@ -302,7 +311,7 @@ norm_backward(NormBwd a) {
                     *reinterpret_cast<float4*>(o) = make_float4(dv[i][0], dv[i][1], dv[i][2], dv[i][3]);
                     *reinterpret_cast<float4*>(o + 16) = make_float4(dv[i][4], dv[i][5], dv[i][6], dv[i][7]);
                 } else {
-                    *reinterpret_cast<uint4*>(o) = pack8(dv[i]);
+                    past_caches(o, pack8(dv[i]));         // (pairs of float4 half a line apart: 16384 x 512 22.6 us, past the caches 24.6)
                 }
             }
         }
@@ -351,7 +360,9 @@ namespace {
 
 struct NormPlan { int w, nv, chunk, blocks; };
 
-// Waves a row and runs of 512 elements a wave, and rows a workgroup.
+// Waves a row, runs of 512 elements a wave, rows a workgroup and workgroups: at most
+// `most_blocks` of four waves, or half or a quarter as many larger ones (0: as few rows a
+// workgroup as can be).  Backward, 4096 rows of 8192: 256 of eight waves 45.9 us, 512 52.
 NormPlan norm_plan(int T, int d, int most_blocks) {
     NormPlan p{};
     const int runs = (d + 511) / 512;
@@ -360,14 +371,14 @@ NormPlan norm_plan(int T, int d, int most_blocks) {
     while (p.w * p.nv < runs) p.w *= 2;
     const int at_once = p.w == 1 ? 4 : 1;
     const int groups = (T + at_once - 1) / at_once;
-    const int most = p.w > 4 ? most_blocks * 4 / p.w : most_blocks;
-    p.chunk = (groups + most - 1) / most * at_once;
     if (!T) return p;
+    const int most = !most_blocks ? groups : p.w > 4 ? most_blocks * 4 / p.w : most_blocks;
+    p.chunk = (groups + most - 1) / most * at_once;
     p.blocks = (T + p.chunk - 1) / p.chunk;
     return p;
 }
 
-constexpr int kFwdBlocks = 2048, kBwdBlocks = 1024;
+constexpr int kBwdBlocks = 512;
 
 template <int W, int NV>
 void launch_fwd(const NormFwd& a, const NormPlan& p, hipStream_t s) {
@@ -398,8 +409,7 @@ void by_plan(const NormPlan& p, F launch) {
 }  // namespace
 
 hipError_t launch_norm_forward(NormFwd a, hipStream_t s) {
-    const NormPlan p = norm_plan(a.T, a.d, kFwdBlocks);
-    a.chunk = p.chunk;
+    const NormPlan p = norm_plan(a.T, a.d, 0);
     a.per_d = 1.0 / a.d;
     prof_begin(s);
     by_plan(p, [&](auto w, auto nv) { launch_fwd<decltype(w)::value, decltype(nv)::value>(a, p, s); });

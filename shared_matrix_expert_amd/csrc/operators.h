@@ -98,7 +98,7 @@ struct NormFwd {
     uint16_t* y; int64_t y_stride;
     uint8_t* codes; uint8_t* scales;                     // [T][d] E4M3, [d/128][T][4] E8M0
     float* rstd;
-    int chunk; double per_d;                             // rows a workgroup, 1 / d
+    double per_d;                                        // 1 / d
 };
 hipError_t launch_norm_forward(NormFwd a, hipStream_t s);
 struct NormBwd {
@@ -111,7 +111,7 @@ struct NormBwd {
     void* dx; int64_t dx_stride;                         // null: not computed
     float* dgain;                                        // null: not computed
     int f32;                                             // dy, dres, dx
-    int chunk; double per_d;
+    int chunk; double per_d;                             // rows a workgroup, 1 / d
     float* part;                                         // workspace: [workgroups][d]
 };
 size_t norm_backward_ws_bytes(int T, int d);
