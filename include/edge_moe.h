@@ -555,8 +555,8 @@ size_t edge_moe_dense_product_backward_ws_bytes(const edge_moe_dense_dims* dims)
 /* Without token_rows, dx rows outside offsets[0] .. offsets[M] - 1 are left as they
  * were; with them every dx row is written.  A row whose row_src entry is outside
  * 0..T-1 adds nothing to dW; the dW of a matrix without rows is zero.  Types, sums
- * and rounding as edge_moe_dense_product's (a token's rows are added in float32, in
- * slot order).  Bitwise reproducible. */
+ * and rounding as edge_moe_dense_product's (a token's rows are added in float32, in a
+ * fixed order).  Bitwise reproducible. */
 int edge_moe_dense_product_backward(const edge_moe_dense_dims* dims, const edge_moe_dense_grad* grad, void* ws,
                                     size_t ws_bytes, void* stream);
 

@@ -849,8 +849,8 @@ def edge_moe_dense_product_backward(dy, ws, x=None, w=None, dx=None, dw=None, of
         raise ValueError(f"w: expected bfloat16 (or int16 bits), got {w.dtype}")
     k = 0
     if token_rows is not None:
-        if token_rows.dim() != 2:
-            raise ValueError("token_rows must be [T][k]")
+        if token_rows.dim() != 2 or token_rows.size(1) < 1:
+            raise ValueError("token_rows must be [T][k], k at least 1")
         k = token_rows.size(1)
     if dw is not None and x.dim() != 2:
         raise ValueError("x must be rows [T][K]")

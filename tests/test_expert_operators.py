@@ -242,6 +242,13 @@ def test_outputs_that_are_not_asked_for(lib):
             call("dense_product_backward", bad)
 
 
+@pytest.mark.parametrize("rows", [T, R])
+def test_token_rows_without_a_row_are_not_dx_by_rows(lib, rows):
+    """[T][0] names no rows of any token: refused, whatever rows dx has."""
+    for extra in ({}, dict(x=None, dw=None)):
+        refuses(lib, "dense_product_backward", token_rows=fake(rows, 0, dtype=I32), dx=fake(R, K, dtype=F32), **extra)
+
+
 def refuses(lib, name, **changed):
     with pytest.raises((ValueError, em.EdgeMoeError)):
         call(name, {**tensors(name), **changed})
