@@ -58,15 +58,17 @@ EM_DEV void store4(void* out, int f32, int64_t at, const floatx4& v) {
 }  // namespace
 
 // ------------------------------------------------------------------ few rows -----
-// A workgroup takes one row tile (16 NS rows of one matrix) and 16 NC columns; its four
-// waves split K into contiguous quarters, WD steps of 32 ahead, and their partial sums
-// are added through LDS in wave order.
-template <int NS, int NC>
+// A workgroup takes one row tile (16 rows of one matrix) and 16 NC columns; its four
+// waves split K into contiguous quarters, D steps of 32 ahead, and their partial sums
+// are added through LDS in wave order.  Bound by W's bytes and by the latencies in front of
+// them (offsets, the row list, x): 80 rows over 512 of 128 x 4096, 80 MB, 21.4 us; 8 rows
+// through 8192 x 4096, 67 MB from the memory-side cache, 13.6 us, 4.9 TB/s.
+template <int NC>
 __global__ void __launch_bounds__(256)
 dp_stream(DenseProduct a) {
-    constexpr int WD = NS == 4 ? 4 : 8, XD = NS == 4 ? 1 : 2;
-    __shared__ __attribute__((aligned(16))) float red[4][NS * NC][256];
-    const RowTile t = row_tile<16 * NS>(a.offsets, a.M, a.R, [](int) { return (int)blockIdx.y; });
+    constexpr int D = 8;
+    __shared__ __attribute__((aligned(16))) float red[4][NC][256];
+    const RowTile t = row_tile<16>(a.offsets, a.M, a.R, [](int) { return (int)blockIdx.y; });
     if (t.r1 == 0) return;
     const int lane = lane_id(), wv = wave_id(), g = lane >> 4, m = lane & 15;
     const int n0 = blockIdx.x * (16 * NC);
@@ -76,85 +78,59 @@ dp_stream(DenseProduct a) {
     const uint16_t* wp[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) wp[c] = a.w + ((int64_t)t.m * a.N + min(n0 + 16 * c + m, a.N - 1)) * a.K + 8 * g;
-    uint4 w[WD][NC], x[XD][NS];
+    uint4 w[D][NC], x[D];
     auto load_w = [&](int d, int st) {
 #pragma unroll
         for (int c = 0; c < NC; ++c) w[d][c] = ldg16(wp[c] + 32 * st);
     };
     if (s0 < s1) {
 #pragma unroll
-        for (int d = 0; d < WD; ++d) load_w(d, min(s0 + d, s1 - 1));
+        for (int d = 0; d < D; ++d) load_w(d, min(s0 + d, s1 - 1));
     }
-    bool live[NS];
-    const uint16_t* xp[NS];
+    const int src = x_row(a, min(t.r0 + m, t.r1 - 1));
+    const uint16_t* xp = a.x + (int64_t)max(src, 0) * a.x_stride + 8 * g;
+    floatx4 acc[NC];
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-        const int r = t.r0 + 16 * s + m, src = x_row(a, min(r, t.r1 - 1));
-        live[s] = src >= 0;
-        xp[s] = a.x + (int64_t)max(src, 0) * a.x_stride + 8 * g;
-    }
-    auto load_x = [&](int d, int st) {
-#pragma unroll
-        for (int s = 0; s < NS; ++s) x[d][s] = ldg16(xp[s] + 32 * st);
-    };
-    floatx4 acc[NS][NC];
-#pragma unroll
-    for (int s = 0; s < NS; ++s)
-#pragma unroll
-        for (int c = 0; c < NC; ++c) acc[s][c] = zero4();
+    for (int c = 0; c < NC; ++c) acc[c] = zero4();
     if (s0 < s1) {
 #pragma unroll
-        for (int d = 0; d < XD; ++d) load_x(d, min(s0 + d, s1 - 1));
+        for (int d = 0; d < D; ++d) x[d] = ldg16(xp + 32 * min(s0 + d, s1 - 1));
     }
-    auto run = [&](int st, auto more) {                       // WD steps, without a branch but for the last ones
+    auto run = [&](int st, auto more) {                       // D steps, without a branch but for the last ones
         constexpr bool MORE = decltype(more)::value;
 #pragma unroll
-        for (int d = 0; d < WD; ++d) {
+        for (int d = 0; d < D; ++d) {
             if (MORE || st + d < s1) {
 #pragma unroll
-                for (int s = 0; s < NS; ++s)
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) acc[s][c] = mfma_bf16(w[d][c], x[d % XD][s], acc[s][c]);
-                load_x(d % XD, min(st + d + XD, s1 - 1));
-                if constexpr (MORE) load_w(d, min(st + d + WD, s1 - 1));
+                for (int c = 0; c < NC; ++c) acc[c] = mfma_bf16(w[d][c], x[d], acc[c]);
+                if constexpr (MORE) x[d] = ldg16(xp + 32 * min(st + d + D, s1 - 1));
+                if constexpr (MORE) load_w(d, min(st + d + D, s1 - 1));
+                __builtin_amdgcn_sched_barrier(0);            // loads complete in order: x asked for later would wait for W's
             }
         }
     };
     int st = s0;
-    for (; st + WD < s1; st += WD) run(st, std::true_type{});
+    for (; st + D < s1; st += D) run(st, std::true_type{});
     if (st < s1) run(st, std::false_type{});
     if (rest && wv == 3) {                                    // the last 8, 16 or 24 of K: zeros past them on both sides
         const bool in = 8 * g < rest;
         const int off = in ? 32 * steps : -8 * g;             // else the row's first elements, not used
-        uint4 xr[NS];
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            const uint4 v = ldg16(xp[s] + off);
-            xr[s] = in ? v : make_uint4(0u, 0u, 0u, 0u);
-        }
+        const uint4 v = ldg16(xp + off), xr = in ? v : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const uint4 v = ldg16(wp[c] + off);
-            const uint4 wr = in ? v : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int s = 0; s < NS; ++s) acc[s][c] = mfma_bf16(wr, xr[s], acc[s][c]);
+            const uint4 u = ldg16(wp[c] + off), wr = in ? u : make_uint4(0u, 0u, 0u, 0u);
+            acc[c] = mfma_bf16(wr, xr, acc[c]);
         }
     }
 #pragma unroll
-    for (int s = 0; s < NS; ++s)
-#pragma unroll
-        for (int c = 0; c < NC; ++c) *reinterpret_cast<floatx4*>(&red[wv][s * NC + c][4 * lane]) = acc[s][c];
+    for (int c = 0; c < NC; ++c) *reinterpret_cast<floatx4*>(&red[wv][c][4 * lane]) = acc[c];
     __syncthreads();
-    // tile i = (subtile s, column tile c) is summed by wave i % 4
+    if (wv >= NC) return;                                     // column tile c is summed by wave c
+    floatx4 v = *reinterpret_cast<const floatx4*>(&red[0][wv][4 * lane]);
 #pragma unroll
-    for (int i = 0; i < NS * NC; ++i) {
-        if ((i & 3) != wv) continue;
-        floatx4 v = *reinterpret_cast<const floatx4*>(&red[0][i][4 * lane]);
-#pragma unroll
-        for (int q = 1; q < 4; ++q) v += *reinterpret_cast<const floatx4*>(&red[q][i][4 * lane]);
-        const int s = i / NC, r = t.r0 + 16 * s + m, n = n0 + 16 * (i % NC) + 4 * g;
-        if (r < t.r1 && n < a.N) store4(a.out, a.out_f32, (int64_t)r * a.out_stride + n, live[s] ? v : zero4());
-    }
+    for (int q = 1; q < 4; ++q) v += *reinterpret_cast<const floatx4*>(&red[q][wv][4 * lane]);
+    const int r = t.r0 + m, n = n0 + 16 * wv + 4 * g;
+    if (r < t.r1 && n < a.N) store4(a.out, a.out_f32, (int64_t)r * a.out_stride + n, src >= 0 ? v : zero4());
 }
 
 // ------------------------------------------------------------------ LDS tiles ----
@@ -785,21 +761,26 @@ hipError_t launch_tile(DenseProduct a, DpPlan p, hipStream_t s) {
     }
 }
 
-// How many times 16 rows of a matrix dp_stream takes at once (0: not dp_stream).
-int stream_rows(const DenseProduct& a) {
+// Whether dp_stream makes y: sixteen rows a matrix on average, twelve of many (routed
+// experts, some of which have more than sixteen), and not very many workgroups of a short K.
+// us, streamed and by dp_tile: 16 rows through 4096 x 4096 10.1 and 16.1, 16 through 8192 x 8192
+// 25.1 and 28.3, 24 through 4096 x 4096 15.9 and 14.0 (two row tiles a workgroup 15.9 as well);
+// 80 rows over 512 of 128 x 4096 21.7 and 32; over 64 of 128 x 4096 512 rows 15.9 and 24.5, 768
+// 25.2 and 24.4, 1024 27 and 22; 4096 over 512 of 128 x 512 33 and 24, 512 over 64 of 1024 x
+// 1024 25 and 28.
+bool streams(const DenseProduct& a) {
     const int live = a.M < a.R ? a.M : a.R;
-    const int64_t avg = ((int64_t)a.R + live - 1) / live;
-    for (int ns = 1; ns <= 2; ns *= 2)
-        if (avg <= 16 * ns) return ns;
-    return 0;
+    if (a.R > (int64_t)live * (a.M < 64 ? 16 : 12)) return false;
+    return a.K >= 1024 || (int64_t)live * ((a.N + 31) / 32) <= 1024;
 }
 
-template <int NS>
 hipError_t launch_stream(const DenseProduct& a, hipStream_t s) {
-    const int64_t tiles = max_row_tiles(a, 16 * NS);
+    const int64_t tiles = max_row_tiles(a, 16);
     prof_begin(s);
-    if (NS == 1 && tiles * ((a.N + 31) / 32) <= 128) dp_stream<NS, 1><<<dim3((a.N + 15) / 16, (unsigned)tiles), 256, 0, s>>>(a);
-    else dp_stream<NS, 2><<<dim3((a.N + 31) / 32, (unsigned)tiles), 256, 0, s>>>(a);
+    // 32 columns a workgroup; 16 where that leaves half of the compute units idle (16 rows through
+    // 4096 x 4096 10.2 us, 10.8 with 32; through 8192 x 8192, 256 workgroups, 31.8 and 25.1)
+    if (tiles * ((a.N + 31) / 32) <= 128) dp_stream<1><<<dim3((a.N + 15) / 16, (unsigned)tiles), 256, 0, s>>>(a);
+    else dp_stream<2><<<dim3((a.N + 31) / 32, (unsigned)tiles), 256, 0, s>>>(a);
     prof_end(s, "dp_stream");
     return hipGetLastError();
 }
@@ -813,17 +794,13 @@ size_t part_bytes(const DenseProduct& a, int mode, int slices) {
 }  // namespace
 
 size_t dense_product_ws_bytes(const DenseProduct& a) {
-    if (!a.R || stream_rows(a)) return 256;
+    if (!a.R || streams(a)) return 256;
     const DpPlan p = plan(a, DP_Y);
     return p.slices > 1 ? part_bytes(a, DP_Y, p.slices) : 256;
 }
 
 hipError_t launch_dense_product(DenseProduct a, void* ws, hipStream_t s) {
-    switch (stream_rows(a)) {
-        case 1: return launch_stream<1>(a, s);
-        case 2: return launch_stream<2>(a, s);
-        default: break;
-    }
+    if (streams(a)) return launch_stream(a, s);
     const DpPlan p = plan(a, DP_Y);
     a.part = static_cast<float*>(ws);
     const hipError_t e = launch_tile<DP_Y>(a, p, s);
