@@ -775,11 +775,14 @@ bool streams(const DenseProduct& a) {
 }
 
 hipError_t launch_stream(const DenseProduct& a, hipStream_t s) {
-    const int64_t tiles = max_row_tiles(a, 16);
+    const int64_t tiles = max_row_tiles(a, 16), live = a.M == 1 ? tiles : a.M < a.R ? a.M : a.R;
+    const int64_t wgs = live * ((a.N + 31) / 32), last = (wgs - 1) % 256 + 1;
     prof_begin(s);
-    // 32 columns a workgroup; 16 where that leaves half of the compute units idle (16 rows through
-    // 4096 x 4096 10.2 us, 10.8 with 32; through 8192 x 8192, 256 workgroups, 31.8 and 25.1)
-    if (tiles * ((a.N + 31) / 32) <= 128) dp_stream<1><<<dim3((a.N + 15) / 16, (unsigned)tiles), 256, 0, s>>>(a);
+    // 32 columns a workgroup; 16 where 32 leave half of the compute units idle, throughout or in the
+    // last of two or three rounds (us with 16 and 32: 16 rows through 4096 x 4096 10.2 and 10.8, through
+    // 8192 x 8192, 256 workgroups, 31.8 and 25.1; 80 rows over 512 of 128 x 4096 19.6 and 22.2, 120 25.1
+    // and 22.1, 160 31.0 and 33.4; 512 over 64 of 512 x 1024, 1024 workgroups, 17.9 and 16.1)
+    if (wgs <= 128 || (wgs > 256 && wgs < 768 && last <= 128)) dp_stream<1><<<dim3((a.N + 15) / 16, (unsigned)tiles), 256, 0, s>>>(a);
     else dp_stream<2><<<dim3((a.N + 31) / 32, (unsigned)tiles), 256, 0, s>>>(a);
     prof_end(s, "dp_stream");
     return hipGetLastError();
