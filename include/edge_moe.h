@@ -319,8 +319,8 @@ int edge_moe_balance(const edge_moe_dims* dims, const float* logits, const int32
  * (S' sequences with tokens, n tokens in them; the counts are constants, as the
  * selection is), and from it
  *   dx = dz W_r,   dW_r = dz^T x,   dbias = sum_t dz_t
- * dx is the router's share of the gradient at the layer's input: the library has no
- * backward pass through the experts, whose share the caller adds.  An entry of
+ * dx is the router's share of the gradient at the layer's input; the experts' share
+ * (of dense experts: edge_moe_dense_product_backward's) is the caller's to add.  An entry of
  * topk_idx outside 0..E-1 has no term of its own; its weight and gradient stay in
  * the sum over i.  The first term is every token's: a padded batch gives the tokens
  * of no sequence d_topk_w = 0, and finite x (their dz = 0 meets it in dW_r).
