@@ -430,7 +430,8 @@ EM_DEV void dp_body(const DenseProduct& a, const DpTile& t, uint8_t* lds) {
         asm volatile("" ::: "memory");
         if constexpr (MODE == DP_DXT) {
             // the one sum multiplies every matrix's rows, by zeros where the token has no row of
-            // it: what is not finite is summed anew from the token's own rows alone
+            // it: what is not finite is summed anew from the token's own rows alone (all of it:
+            // 1501 tokens' three of 8 x 16 x 4096 0.4 ms, 16384 tokens' eight of 64 x 16 x 4096 22)
             bool bad = false;
 #pragma unroll
             for (int p = 0; p < NI; ++p)
