@@ -526,7 +526,10 @@ ip_tile(Int4Product a) {
         const int Np = (a.N + 3) & ~3;
         for (int i = threadIdx.x; i < rows * (BN / 4); i += C::NW * 64) {
             const int r = i / (BN / 4), c = 4 * (i % (BN / 4));
-            if (c < cols) *reinterpret_cast<floatx4*>(a.part + ((int64_t)z * a.R + t.r0 + r) * Np + n0 + c) = *reinterpret_cast<const floatx4*>(o + r * C::RS + c);
+            if (c >= cols) continue;
+            const bool named = !a.row_src || x_row(a, t.r0 + r) >= 0;     // (the join knows no row_src)
+            *reinterpret_cast<floatx4*>(a.part + ((int64_t)z * a.R + t.r0 + r) * Np + n0 + c) =
+                named ? *reinterpret_cast<const floatx4*>(o + r * C::RS + c) : zero4();
         }
         return;
     }
