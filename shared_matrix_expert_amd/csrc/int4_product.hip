@@ -62,9 +62,11 @@ __device__ const uint4 ip_zero = {0u, 0u, 0u, 0u};
 
 // The W waves' sums of 16 NS rows x 16 NC columns, added in wave order and stored: tile
 // i = (subtile s, column tile c) by wave i % W; lane (g, m) holds rows 4 g .. 4 g + 3 of
-// column m.
+// column m.  Bit r of named[s]: row_src names an x row for row 16 s + r; without one the row is
+// zeros, whatever the scales that met its zeros of x.
 template <int W, int NS, int NC>
-EM_DEV void join_waves(const Int4Product& a, const floatx4 (&acc)[NS][NC], float (&red)[W][NS * NC][256], int r0, int r1, int n0) {
+EM_DEV void join_waves(const Int4Product& a, const floatx4 (&acc)[NS][NC], const uint32_t (&named)[NS], float (&red)[W][NS * NC][256],
+                       int r0, int r1, int n0) {
     const int lane = lane_id(), wv = wave_id(), g = lane >> 4, m = lane & 15;
 #pragma unroll
     for (int s = 0; s < NS; ++s)
@@ -81,7 +83,7 @@ EM_DEV void join_waves(const Int4Product& a, const floatx4 (&acc)[NS][NC], float
         if (n >= a.N) continue;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (r + j < r1) store1(a.y, a.y_f32, (int64_t)(r + j) * a.y_stride + n, v[j]);
+            if (r + j < r1) store1(a.y, a.y_f32, (int64_t)(r + j) * a.y_stride + n, named[i / NC] >> (4 * g + j) & 1 ? v[j] : 0.f);
     }
 }
 
@@ -250,7 +252,8 @@ ip_rows(Int4Product a) {
     if (few) run(std::true_type{});
     else run(std::false_type{});
     __syncthreads();                                              // the x rows have been read: their place takes the sums
-    join_waves<W, 1, NC>(a, acc, *reinterpret_cast<float(*)[W][NC][256]>(&xl[0][0]), t.r0, t.r1, n0);
+    const uint32_t named[1] = {(uint32_t)__ballot(src >= 0)};     // (lanes 0 .. 15: rows 0 .. 15)
+    join_waves<W, 1, NC>(a, acc, named, *reinterpret_cast<float(*)[W][NC][256]>(&xl[0][0]), t.r0, t.r1, n0);
 }
 
 // ------------------------------------------------------------------ 17 to 32 rows ----
@@ -340,7 +343,10 @@ ip_stream(Int4Product a) {
             }
         }
     }
-    join_waves<4, NS, NC>(a, acc, red, t.r0, t.r1, n0);
+    uint32_t named[NS];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) named[s] = (uint32_t)__ballot(live[s]);      // (lanes 0 .. 15: rows 16 s .. 16 s + 15)
+    join_waves<4, NS, NC>(a, acc, named, red, t.r0, t.r1, n0);
 }
 
 // ------------------------------------------------------------------ many rows ----

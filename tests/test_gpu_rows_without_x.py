@@ -63,3 +63,25 @@ def test_int4_rows_without_x_are_zeros(R, M, N, K, q, out):
     codes, scales, w = matrices(g, M, N, K, q)
     y = run_packed(q, x, codes, scales, R, N, TYPES[out], offsets, src)
     same(y, product(x, w, off, src, R), (int(off[0]), int(off[-1])))
+
+
+@pytest.mark.parametrize("R,M,N,K,q", PACKED)
+def test_int4_rows_without_x_are_zeros_beside_scales_that_are_not_finite(R, M, N, K, q):
+    """Infinite and NaN scales, and a row 0 of x that is NaN: the rows without x stay zeros,
+    the other rows of the other columns exact."""
+    say(f"case: int4 rows without x, scales not finite, {R} through {M} x {N} x {K}, groups of {q}")
+    g = torch.Generator(device=DEV).manual_seed(R + K)
+    src, off, offsets, none = rows(R, M, R)
+    src[src == 0] = 1
+    x = whole(g, T, K)
+    codes, scales, w = matrices(g, M, N, K, q)
+    want = product(x, w, off, src, R)
+    x[0] = float("nan")
+    scales[:, 3, 0], scales[:, 5, -1] = float("inf"), float("nan")
+    y = run_packed(q, x, codes, scales, R, N, torch.float32, offsets, src)
+    live = torch.zeros(R, dtype=torch.bool, device=DEV)
+    live[int(off[0]):int(off[-1])] = True
+    assert bool((y[live & none] == 0).all())
+    keep = [n for n in range(N) if n not in (3, 5)]
+    assert torch.equal(y[live][:, keep].double(), want[live][:, keep])
+    assert bool((y[~live] == 7).all())
