@@ -148,7 +148,8 @@ dp_stream(DenseProduct a) {
 //
 // Rows and columns past an operand's end repeat its last ones, and what they give is not
 // stored.  Past the end of c, and for an x row of dW that row_src does not name, lanes
-// load zeros from dp_zero, so that nothing outside an operand meets a product.
+// load zeros from dp_zero, so that nothing outside an operand meets a product; dy of such a
+// row becomes zeros in the registers.
 //
 // A load takes a uniform base and a 32-bit lane offset (4 to 7% faster than a 64-bit
 // address a lane at 8192^3); WIDE, for rows so far apart that the offsets do not fit,
@@ -260,14 +261,18 @@ EM_DEV void dp_body(const DenseProduct& a, const DpTile& t, uint8_t* lds) {
     // (GATHER) x rows of step st to their place in the LDS (every wave brings all of them),
     // and from there those of this wave's loads
     int from_row[C::GATHER ? C::JL : 1];
+    // (GATHER) c of the step whose P comes next that have no x row; the rows of the one behind it
+    uint64_t unnamed = 0;
+    int seen = 0;
+    auto rows_of = [&](int st) { return reinterpret_cast<const int*>(lds + C::TILES_B) + (st & 3) * 64; };
+    auto without_x = [&](int row) { return __ballot((unsigned)row >= (unsigned)a.T); };
     auto fetch_rows = [&](int st) {
         const int r = c0 + min(64 * st + lane, clen - 1);
         lds_load4(a.row_src, 4u * (uint32_t)r, __builtin_amdgcn_readfirstlane(base + C::TILES_B + (st & 3) * 256));
     };
     auto read_rows = [&](int st) {
-        const int* rows = reinterpret_cast<const int*>(lds + C::TILES_B) + (st & 3) * 64;
 #pragma unroll
-        for (int u = 0; u < C::JL; ++u) from_row[u] = rows[c_of(u)];
+        for (int u = 0; u < C::JL; ++u) from_row[u] = rows_of(st)[c_of(u)];
     };
     auto jstage = [&](int st) { return (uint32_t)(st % 3) * C::J_B; };
     auto istage = [&](int st) { return 3 * C::J_B + (uint32_t)(st & 1) * C::I_B; };
@@ -341,6 +346,23 @@ EM_DEV void dp_body(const DenseProduct& a, const DpTile& t, uint8_t* lds) {
     uint4 fi[2][2][NJ], fj[2][2];                                 // [set][half][subtile]; [subtile & 1][half]
     // (GATHER: x rows are asked for four steps ahead, at a step's end: landed at the next
     // step's MID, read at its end, used in the step after.)
+    // A row without x adds nothing, whatever its dy is: its x is loaded as zeros, and its dy, which
+    // need not be finite, becomes zeros in the registers (a branch a step; looked at in every
+    // load of dy it cost up to 15%).
+    auto drop_rows = [&](uint4 (&p)[2][NJ], uint64_t rows) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t b = (uint32_t)(rows >> (32 * h)) >> (8 * g);           // a lane's eight c, two a word
+            auto keep = [&](int i) { return (b >> (2 * i) & 1 ? 0u : 0xFFFFu) | (b >> (2 * i + 1) & 1 ? 0u : 0xFFFF0000u); };
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                p[h][j].x &= keep(0);
+                p[h][j].y &= keep(1);
+                p[h][j].z &= keep(2);
+                p[h][j].w &= keep(3);
+            }
+        }
+    };
     // A step: its first barrier says that the step before is read (its stage of Q is free, and
     // this step's of P, which is in registers), the one at MID that the next step has landed.
     // The loads of the step after it are spread between the products; the next step's P is
@@ -374,6 +396,11 @@ EM_DEV void dp_body(const DenseProduct& a, const DpTile& t, uint8_t* lds) {
                 for (int j = 0; j < NJ; ++j) acc[p][j] = mfma_bf16(fj[p & 1][h], fi[f][h][j], acc[p][j]);
             __builtin_amdgcn_sched_barrier(0);
         }
+        if constexpr (C::GATHER) {
+            if (unnamed) drop_rows(fi[1 - f], unnamed);           // (step st + 1's)
+            unnamed = without_x(seen);
+            seen = rows_of(st + 3)[lane];
+        }
     };
     if (s0 < s1) {
         if constexpr (C::GATHER) {
@@ -391,6 +418,12 @@ EM_DEV void dp_body(const DenseProduct& a, const DpTile& t, uint8_t* lds) {
         wait_loads_barrier<C::LOADS>();
 #pragma unroll
         for (int u = 0; u < 2 * NJ; ++u) fi[0][u / NJ][u % NJ] = read_i(s0, u % NJ, u / NJ);
+        if constexpr (C::GATHER) {
+            const uint64_t first = without_x(rows_of(s0)[lane]);
+            if (first) drop_rows(fi[0], first);
+            unnamed = without_x(rows_of(s0 + 1)[lane]);
+            seen = rows_of(s0 + 2)[lane];
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) fj[0][h] = read_j(s0, 0, h);
         int st = s0;

@@ -1,5 +1,6 @@
-"""Rows of the products with int4 matrices whose row_src entry is no row of x: rows of
-zeros, whatever kernel, tile and number of slices the sizes choose.
+"""Rows of the products with int4 and bf16 matrices whose row_src entry is no row of x:
+rows of zeros, whatever kernel, tile and number of slices the sizes choose, that add
+nothing to dW.
 
 Whole-number x and scales that are powers of two make every sum exact in float32: the
 result must be the formula's, rounded once, bit for bit."""
@@ -9,7 +10,7 @@ import torch
 
 import shared_matrix_expert_amd as em
 from gpu_helpers import DEV, say
-from test_gpu_dense_product import TYPES, product, same, whole
+from test_gpu_dense_product import TYPES, gradients, product, run, run_backward, same, whole
 from test_gpu_packed_product import matrices
 from test_gpu_packed_product import run as run_packed
 
@@ -85,3 +86,38 @@ def test_int4_rows_without_x_are_zeros_beside_scales_that_are_not_finite(R, M, N
     keep = [n for n in range(N) if n not in (3, 5)]
     assert torch.equal(y[live][:, keep].double(), want[live][:, keep])
     assert bool((y[~live] == 7).all())
+
+
+# R, M, N, K
+DENSE = [(4, 1, 8, 8), (7, 64, 128, 512), (300, 64, 128, 512), (4503, 8, 16, 1024), (6300, 200, 40, 72), (700, 1, 264, 520),
+         (5000, 3, 768, 1544), (6000, 16, 8, 2056), (3000, 2, 72, 104), (2000, 1, 4096, 264), (9000, 12, 80, 1000)]
+
+
+@pytest.mark.parametrize("far", [False, True], ids=["", "rows far apart"])
+@pytest.mark.parametrize("out", list(TYPES))
+@pytest.mark.parametrize("R,M,N,K", DENSE)
+def test_dense_rows_without_x_add_nothing(R, M, N, K, out, far):
+    """Such a row is zeros in y and adds nothing to dW, whatever its dy and the first row
+    of x hold."""
+    say(f"case: dense rows without x, {R} through {M} x {N} x {K}, {out}{', far apart' if far else ''}")
+    g = torch.Generator(device=DEV).manual_seed(R + K)
+    R = min(R, 300) if far else R
+    src, off, offsets, none = rows(R, M, R)
+    src[src == 0] = 1
+    x, w, dy = whole(g, T, K), whole(g, M, N, K), whole(g, R, N)
+    live = (int(off[0]), int(off[-1]))
+    want_y = product(x, w, off, src, R)
+    want_dx, want_dw = gradients(x, w, dy, off, src, None)
+    x[0] = float("nan")
+    bad = dy.clone()
+    bad[none], bad[none, ::3] = float("nan"), float("inf")
+    bad[:live[0]], bad[live[1]:] = float("nan"), float("nan")
+    if far:                                                      # lane offsets within a tile pass 32 bits
+        wide = torch.empty(R << 23, dtype=torch.bfloat16, device=DEV).as_strided((R, N), (1 << 23, 1), 0)
+        bad = wide.copy_(bad)
+    same(run(x, w, R, TYPES[out], offsets, src), want_y, live)
+    dx, dw = run_backward(x, w, bad, offsets, src, None, TYPES[out])
+    same(dw, want_dw)
+    named = ~none
+    named[:live[0]], named[live[1]:] = False, False
+    same(dx[named], want_dx[named])
