@@ -464,8 +464,9 @@ typedef struct edge_moe_norm_args {
     float*          rstd;          /* [T] or NULL                                */
 } edge_moe_norm_args;
 
-/* The mean is summed in float64: no row of finite bf16 overflows it.  A NaN or
- * an infinity in r makes its own row NaN or zero.  codes and scales are the x
+/* The mean is summed in float64: no row of finite bf16 overflows it.  A NaN in r
+ * makes its own row NaN; an infinity makes rstd zero, and with it the row: zeros, and
+ * NaN in the infinity's place.  codes and scales are the x
  * that edge_moe_mx_product_coded takes, and the rounding that edge_moe_mx_product
  * would make of y.  Bitwise reproducible. */
 int edge_moe_norm(const edge_moe_norm_args* args, void* stream);

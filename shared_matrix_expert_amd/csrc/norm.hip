@@ -133,11 +133,13 @@ EM_DEV double row_sum(double v, double (&slots)[N][W], int turn) {
     return s;
 }
 
-// 1 / sqrt(m) in float64: the hardware's estimate and two steps towards the root.
+// 1 / sqrt(m) in float64: the hardware's estimate and two steps towards the root (of an
+// infinity, zero, as it is: a step would multiply the two).
 EM_DEV double rsqrt_f64(double m) {
-    double r = __builtin_amdgcn_rsq(m);
+    const double e = __builtin_amdgcn_rsq(m);
+    double r = e * fma(-0.5 * m * e, e, 1.5);
     r = r * fma(-0.5 * m * r, r, 1.5);
-    return r * fma(-0.5 * m * r, r, 1.5);
+    return m == __builtin_inf() ? 0.0 : r;
 }
 
 // Stored past the caches, where the rows read next would take their place.
