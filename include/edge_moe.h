@@ -493,8 +493,8 @@ typedef struct edge_moe_norm_grad {
  * is taken: dgain is then zero). */
 size_t edge_moe_norm_backward_ws_bytes(int32_t T, int32_t d);
 
-/* Sums over a row and over rows are float32 in a fixed order, the workgroups'
- * sums float64: bitwise reproducible.  ws 256-byte aligned. */
+/* Sums over a row are float32 in a fixed order, those over rows float64 (rounded to
+ * float32 once a workgroup): bitwise reproducible.  ws 256-byte aligned. */
 int edge_moe_norm_backward(const edge_moe_norm_grad* grad, void* ws, size_t ws_bytes, void* stream);
 
 /* Product of bf16 rows with bf16 matrices, dense or grouped over a routed

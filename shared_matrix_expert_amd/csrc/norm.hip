@@ -18,8 +18,10 @@
 //
 // Backward: a workgroup takes a run of neighbouring rows and asks for the next one before it
 // reduces the present one; the gain and its gradient stay in registers, so that dgain passes
-// through memory once a workgroup.  16384 rows of 4096, bf16, 537 MB: 109 us with dgain's
-// launch, 5 us of it; 1024 workgroups 122, 256 117.
+// through memory once a workgroup.  dgain is summed in float64, exact products included: its
+// error does not grow with the rows, and no time shows (a float32 sum lost up to half a unit a
+// row).  16384 rows of 4096, bf16, 537 MB: 109 us with dgain's launch, 5 us of it; 1024
+// workgroups 122, 256 117.
 #include <type_traits>
 
 #include "mx_format.h"
@@ -239,11 +241,18 @@ norm_forward(NormFwd a) {
     }
 }
 
+// Rows of sixteen waves (more than 8192) leave a lane 128 registers: dgain's sums are then made
+// in a pass of their own (norm_gain_sums), and rows of more than 16384 are not asked for ahead.
+// 4096 rows of 16384, bf16 130 us (the sums beside the rows 311), float32 261 (595); 2048 of
+// 32768 248 (771) and 395 (1049).
+template <int W> constexpr bool sums_beside_rows() { return W < 16; }
+
 // F32: dy, dres and dx are float32 (else bf16).
 template <int W, int NV, bool F32>
 __global__ void __launch_bounds__(norm_threads<W>())
 norm_backward(NormBwd a) {
     __shared__ double slots[2][W];
+    constexpr bool SUMS = sums_beside_rows<W>(), AHEAD = NV < 4;
     __shared__ __attribute__((aligned(16))) float part[W == 1 ? 4 : 1][W == 1 ? 512 * NV : 4];
     const int in_row = W == 1 ? lane_id() : (int)threadIdx.x;
     const int first = blockIdx.x * a.chunk + (W == 1 ? wave_id() : 0);
@@ -252,7 +261,8 @@ norm_backward(NormBwd a) {
     using G = Raw8<F32>;
     bool live[NV];
     int at[NV];
-    float gain[NV][8], dg[NV][8];
+    float gain[NV][8];
+    double dg[SUMS ? NV : 1][8];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int e = 8 * (in_row + 64 * W * i);
@@ -260,7 +270,7 @@ norm_backward(NormBwd a) {
         at[i] = live[i] ? e : 0;
         load_gain(gain[i], a.gain, a.gain_f32, at[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dg[i][j] = 0.f;
+        for (int j = 0; SUMS && j < 8; ++j) dg[i][j] = 0.0;
     }
     constexpr int64_t ES = F32 ? 4 : 2;
     Raw8<false> xr[NV];
@@ -275,9 +285,10 @@ norm_backward(NormBwd a) {
             if (a.dres) load8(rr[i], static_cast<const char*>(a.dres) + t * a.dres_stride * ES, at[i]);
         }
     };
-    if (first < last) fetch(first);
+    if (AHEAD && first < last) fetch(first);
     int turn = 0;
     for (int t = first; t < last; t += STEP) {
+        if (!AHEAD) fetch(t);
         const float rstd = rs;
         float v[NV][8], dv[NV][8], res[NV][8];
         float sum = 0.f;
@@ -290,13 +301,13 @@ norm_backward(NormBwd a) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 v[i][j] *= rstd;
-                dg[i][j] = fmaf(dv[i][j], v[i][j], dg[i][j]);
+                if constexpr (SUMS) dg[i][j] = fma((double)dv[i][j], (double)v[i][j], dg[i][j]);
                 dv[i][j] *= gain[i][j];
                 s = fmaf(dv[i][j], v[i][j], s);
             }
             sum += live[i] ? s : 0.f;
         }
-        if (t + STEP < last) fetch(t + STEP);
+        if (AHEAD && t + STEP < last) fetch(t + STEP);
         if (a.dx) {
             const float mean = (float)(row_sum<W>((double)sum, slots, turn) * a.per_d);
             turn ^= 1;
@@ -318,7 +329,7 @@ norm_backward(NormBwd a) {
             }
         }
     }
-    if (!a.part) return;
+    if (!SUMS || !a.part) return;
     float* out = a.part + (int64_t)blockIdx.x * a.d;
     if constexpr (W == 1) {                                    // the four waves' rows, added in wave order
 #pragma unroll
@@ -326,17 +337,63 @@ norm_backward(NormBwd a) {
 #pragma unroll
             for (int j = 0; j < 8; j += 4)
                 *reinterpret_cast<float4*>(&part[wave_id()][8 * (in_row + 64 * i) + j]) =
-                    make_float4(dg[i][j], dg[i][j + 1], dg[i][j + 2], dg[i][j + 3]);
+                    make_float4((float)dg[i][j], (float)dg[i][j + 1], (float)dg[i][j + 2], (float)dg[i][j + 3]);
         __syncthreads();
         for (int e = threadIdx.x; e < a.d; e += 256) out[e] = (part[0][e] + part[1][e]) + (part[2][e] + part[3][e]);
     } else {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (!live[i]) continue;
-            *reinterpret_cast<float4*>(out + at[i]) = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
-            *reinterpret_cast<float4*>(out + at[i] + 4) = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
+            *reinterpret_cast<float4*>(out + at[i]) = make_float4((float)dg[i][0], (float)dg[i][1], (float)dg[i][2], (float)dg[i][3]);
+            *reinterpret_cast<float4*>(out + at[i] + 4) = make_float4((float)dg[i][4], (float)dg[i][5], (float)dg[i][6], (float)dg[i][7]);
         }
     }
+}
+
+// Sums of dgain's terms over a run of rows, where they have no place beside the rows: a
+// workgroup takes 512 columns, its sixteen waves four rows each at once, added in wave order.
+// The only run's sums are dgain.
+template <bool F32>
+__global__ void __launch_bounds__(1024)
+norm_gain_sums(NormBwd a, int run) {
+    __shared__ double sp[16][512];
+    constexpr int64_t ES = F32 ? 4 : 2;
+    constexpr int ROWS = 4;
+    const int wv = wave_id(), col = 8 * lane_id(), e = min(512 * (int)blockIdx.x + col, a.d - 8);
+    const int first = blockIdx.y * run, last = min(a.T, first + run);
+    double dg[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dg[j] = 0.0;
+    for (int t = first + ROWS * wv; t < last; t += 16 * ROWS) {
+        Raw8<false> x[ROWS];
+        Raw8<F32> dy[ROWS];
+        float rstd[ROWS];
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const int at = min(t + i, last - 1);
+            rstd[i] = a.rstd[at];
+            load8(x[i], a.x + at * a.x_stride, e);
+            load8(dy[i], static_cast<const char*>(a.dy) + at * a.dy_stride * ES, e);
+        }
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            if (t + i >= last) break;
+            float v[8], g[8];
+            widen8(x[i], v);
+            widen8(dy[i], g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dg[j] = fma((double)g[j], (double)(v[j] * rstd[i]), dg[j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sp[wv][col + j] = dg[j];
+    __syncthreads();
+    const int out = 512 * blockIdx.x + threadIdx.x;
+    if (threadIdx.x >= 512 || out >= a.d) return;
+    double s = sp[0][threadIdx.x];
+    for (int r = 1; r < 16; ++r) s += sp[r][threadIdx.x];
+    if (gridDim.y == 1) a.dgain[out] = (float)s;
+    else a.part[(int64_t)blockIdx.y * a.d + out] = (float)s;
 }
 
 // dgain from the workgroups' partial sums: 16 rows of 64 threads over interleaved
@@ -363,8 +420,9 @@ namespace {
 struct NormPlan { int w, nv, chunk, blocks; };
 
 // Waves a row, runs of 512 elements a wave, rows a workgroup and workgroups: at most
-// `most_blocks` of four waves, or half or a quarter as many larger ones (0: as few rows a
-// workgroup as can be).  Backward, 4096 rows of 8192: 256 of eight waves 45.9 us, 512 52.
+// `most_blocks`, or half as many of more than four waves (0: as few rows a workgroup as can
+// be).  Backward, 4096 rows of 8192: 256 of eight waves 45.9 us, 512 52; dx of 4096 rows of
+// 16384, float32, 256 of sixteen waves 189 us, 512 196, 4096 212.
 NormPlan norm_plan(int T, int d, int most_blocks) {
     NormPlan p{};
     const int runs = (d + 511) / 512;
@@ -374,13 +432,24 @@ NormPlan norm_plan(int T, int d, int most_blocks) {
     const int at_once = p.w == 1 ? 4 : 1;
     const int groups = (T + at_once - 1) / at_once;
     if (!T) return p;
-    const int most = !most_blocks ? groups : p.w > 4 ? most_blocks * 4 / p.w : most_blocks;
+    const int most = !most_blocks ? groups : p.w > 4 ? most_blocks / 2 : most_blocks;
     p.chunk = (groups + most - 1) / most * at_once;
     p.blocks = (T + p.chunk - 1) / p.chunk;
     return p;
 }
 
-constexpr int kBwdBlocks = 512;
+constexpr int kBwdBlocks = 512, kSumBlocks = 512;
+
+// Rows of dgain's partial sums: a workgroup of norm_backward each, or a run of `run` rows
+// each (norm_gain_sums, two workgroups a compute unit; 256 rows and fewer in one run spare
+// norm_dgain's launch).
+struct GainPlan { int run, parts; };
+GainPlan gain_plan(const NormPlan& p, int T, int d) {
+    if (p.w < 16 || !T) return GainPlan{0, p.blocks};
+    const int most = kSumBlocks / ((d + 511) / 512), even = ((T + most - 1) / most + 3) / 4 * 4;
+    const int run = even < 256 ? 256 : even;
+    return GainPlan{run, (T + run - 1) / run};
+}
 
 template <int W, int NV>
 void launch_fwd(const NormFwd& a, const NormPlan& p, hipStream_t s) {
@@ -420,25 +489,35 @@ hipError_t launch_norm_forward(NormFwd a, hipStream_t s) {
 }
 
 size_t norm_backward_ws_bytes(int T, int d) {
-    const size_t n = (size_t)norm_plan(T, d, kBwdBlocks).blocks * d * 4;
+    const size_t n = (size_t)gain_plan(norm_plan(T, d, kBwdBlocks), T, d).parts * d * 4;
     return n > 256 ? n : 256;
 }
 
 hipError_t launch_norm_backward(NormBwd a, void* ws, hipStream_t s) {
     const NormPlan p = norm_plan(a.T, a.d, kBwdBlocks);
+    const GainPlan sums = gain_plan(p, a.T, a.d);
     a.chunk = p.chunk;
     a.per_d = 1.0 / a.d;
     a.part = a.dgain ? static_cast<float*>(ws) : nullptr;
-    if (p.blocks) {
+    if (sums.run && a.dgain) {                                    // first: dx may lie on dy
+        const dim3 grid((a.d + 511) / 512, sums.parts);
+        prof_begin(s);
+        if (a.f32) norm_gain_sums<true><<<grid, 1024, 0, s>>>(a, sums.run);
+        else norm_gain_sums<false><<<grid, 1024, 0, s>>>(a, sums.run);
+        prof_end(s, "norm_gain_sums");
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (p.blocks && (a.dx || !sums.run)) {
         prof_begin(s);
         by_plan(p, [&](auto w, auto nv) { launch_bwd<decltype(w)::value, decltype(nv)::value>(a, p, s); });
         prof_end(s, "norm_backward");
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (!a.dgain) return hipSuccess;
+    if (!a.dgain || (sums.run && sums.parts == 1)) return hipSuccess;
     prof_begin(s);
-    norm_dgain<<<(a.d + 63) / 64, 1024, 0, s>>>(a.part, p.blocks, a.d, a.dgain);
+    norm_dgain<<<(a.d + 63) / 64, 1024, 0, s>>>(a.part, sums.parts, a.d, a.dgain);
     prof_end(s, "norm_dgain");
     return hipGetLastError();
 }

@@ -112,7 +112,7 @@ struct NormBwd {
     float* dgain;                                        // null: not computed
     int f32;                                             // dy, dres, dx
     int chunk; double per_d;                             // rows a workgroup, 1 / d
-    float* part;                                         // workspace: [workgroups][d]
+    float* part;                                         // workspace: [workgroups or runs of rows][d]
 };
 size_t norm_backward_ws_bytes(int T, int d);
 hipError_t launch_norm_backward(NormBwd a, void* ws, hipStream_t s);
