@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(norm_threads<W>())
 norm_forward(NormFwd a) {
     __shared__ double slots[1][W];
     const int in_row = W == 1 ? lane_id() : (int)threadIdx.x;
-    const int t = W == 1 ? 4 * blockIdx.x + wave_id() : blockIdx.x;
+    const int t = a.t0 + (W == 1 ? 4 * (int)blockIdx.x + wave_id() : (int)blockIdx.x);
     if (t >= a.T) return;                                      // W = 1 only: a wave without a row (no barrier there)
     bool live[NV];
     int at[NV];                                                // lanes past the row read its first elements again
@@ -419,11 +419,13 @@ namespace {
 
 struct NormPlan { int w, nv, chunk, blocks; };
 
-// Waves a row, runs of 512 elements a wave, rows a workgroup and workgroups: at most
-// `most_blocks`, or half as many of more than four waves (0: as few rows a workgroup as can
-// be).  Backward, 4096 rows of 8192: 256 of eight waves 45.9 us, 512 52; dx of 4096 rows of
-// 16384, float32, 256 of sixteen waves 189 us, 512 196, 4096 212.
-NormPlan norm_plan(int T, int d, int most_blocks) {
+constexpr int kBwdBlocks = 512, kSumBlocks = 512;
+
+// Waves a row, runs of 512 elements a wave; backward, rows a workgroup and workgroups: at most
+// kBwdBlocks, or half as many of more than four waves.  4096 rows of 8192: 256 of eight waves
+// 45.9 us, 512 52; dx of 4096 rows of 16384, float32, 256 of sixteen waves 189 us, 512 196,
+// 4096 212.
+NormPlan norm_plan(int T, int d) {
     NormPlan p{};
     const int runs = (d + 511) / 512;
     p.nv = runs <= 1 ? 1 : runs <= 32 ? 2 : 4;
@@ -432,13 +434,11 @@ NormPlan norm_plan(int T, int d, int most_blocks) {
     const int at_once = p.w == 1 ? 4 : 1;
     const int groups = (T + at_once - 1) / at_once;
     if (!T) return p;
-    const int most = !most_blocks ? groups : p.w > 4 ? most_blocks / 2 : most_blocks;
+    const int most = p.w > 4 ? kBwdBlocks / 2 : kBwdBlocks;
     p.chunk = (groups + most - 1) / most * at_once;
     p.blocks = (T + p.chunk - 1) / p.chunk;
     return p;
 }
-
-constexpr int kBwdBlocks = 512, kSumBlocks = 512;
 
 // Rows of dgain's partial sums: a workgroup of norm_backward each, or a run of `run` rows
 // each (norm_gain_sums, two workgroups a compute unit; 256 rows and fewer in one run spare
@@ -451,11 +451,16 @@ GainPlan gain_plan(const NormPlan& p, int T, int d) {
     return GainPlan{run, (T + run - 1) / run};
 }
 
+// A launch holds fewer than 2^32 threads: rows of more than 2^31 of them take several.
 template <int W, int NV>
-void launch_fwd(const NormFwd& a, const NormPlan& p, hipStream_t s) {
-    if (!a.add) norm_forward<W, NV, 0><<<p.blocks, norm_threads<W>(), 0, s>>>(a);
-    else if (!a.add_f32) norm_forward<W, NV, 1><<<p.blocks, norm_threads<W>(), 0, s>>>(a);
-    else norm_forward<W, NV, 2><<<p.blocks, norm_threads<W>(), 0, s>>>(a);
+void launch_fwd(NormFwd a, hipStream_t s) {
+    constexpr int kRows = (int)((1ll << 31) / norm_threads<W>()) * rows_at_once<W>();
+    for (a.t0 = 0; a.t0 < a.T; a.t0 += kRows) {
+        const int rows = a.T - a.t0 < kRows ? a.T - a.t0 : kRows, blocks = (rows + rows_at_once<W>() - 1) / rows_at_once<W>();
+        if (!a.add) norm_forward<W, NV, 0><<<blocks, norm_threads<W>(), 0, s>>>(a);
+        else if (!a.add_f32) norm_forward<W, NV, 1><<<blocks, norm_threads<W>(), 0, s>>>(a);
+        else norm_forward<W, NV, 2><<<blocks, norm_threads<W>(), 0, s>>>(a);
+    }
 }
 
 template <int W, int NV>
@@ -480,21 +485,21 @@ void by_plan(const NormPlan& p, F launch) {
 }  // namespace
 
 hipError_t launch_norm_forward(NormFwd a, hipStream_t s) {
-    const NormPlan p = norm_plan(a.T, a.d, 0);
+    const NormPlan p = norm_plan(a.T, a.d);
     a.per_d = 1.0 / a.d;
     prof_begin(s);
-    by_plan(p, [&](auto w, auto nv) { launch_fwd<decltype(w)::value, decltype(nv)::value>(a, p, s); });
+    by_plan(p, [&](auto w, auto nv) { launch_fwd<decltype(w)::value, decltype(nv)::value>(a, s); });
     prof_end(s, "norm_forward");
     return hipGetLastError();
 }
 
 size_t norm_backward_ws_bytes(int T, int d) {
-    const size_t n = (size_t)gain_plan(norm_plan(T, d, kBwdBlocks), T, d).parts * d * 4;
+    const size_t n = (size_t)gain_plan(norm_plan(T, d), T, d).parts * d * 4;
     return n > 256 ? n : 256;
 }
 
 hipError_t launch_norm_backward(NormBwd a, void* ws, hipStream_t s) {
-    const NormPlan p = norm_plan(a.T, a.d, kBwdBlocks);
+    const NormPlan p = norm_plan(a.T, a.d);
     const GainPlan sums = gain_plan(p, a.T, a.d);
     a.chunk = p.chunk;
     a.per_d = 1.0 / a.d;

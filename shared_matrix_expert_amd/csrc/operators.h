@@ -99,6 +99,7 @@ struct NormFwd {
     uint8_t* codes; uint8_t* scales;                     // [T][d] E4M3, [d/128][T][4] E8M0
     float* rstd;
     double per_d;                                        // 1 / d
+    int t0;                                              // a launch's first row
 };
 hipError_t launch_norm_forward(NormFwd a, hipStream_t s);
 struct NormBwd {
