@@ -849,10 +849,11 @@ hipError_t launch_dense_product(DenseProduct a, void* ws, hipStream_t s) {
 
 // Columns of dx that are made for tokens at once: their rows' partial sums then stay in the
 // 256 MB memory-side cache between the two launches (16384 tokens' ten of 512 x 128 x 4096: 1565 us at once, 1419 so;
-// 48 and 96 MB at once measured more on the smaller ones).
+// 48 and 96 MB at once measured more on the smaller ones).  Few rows of very many tokens: no
+// more than 2^31 threads add them (2^20 tokens by 8192 columns).
 int token_cols(const DenseProduct& a, int slices) {
-    const int64_t fit = (192ll << 20) / ((int64_t)a.R * slices * 4 + 1);
-    const int64_t cols = fit / 256 * 256;
+    const int64_t fit = (192ll << 20) / ((int64_t)a.R * slices * 4 + 1), threads = (1ll << 33) / a.T;
+    const int64_t cols = (fit < threads ? fit : threads) / 256 * 256;
     return cols < 256 ? 256 : cols < a.K ? (int)cols : a.K;
 }
 

@@ -4,6 +4,7 @@ import torch
 
 import shared_matrix_expert_amd as em
 from gpu_helpers import DEV, say
+from test_gpu_dense_product import GUARD, same, whole, workspace
 from test_gpu_norm import U, half
 
 pytestmark = pytest.mark.gpu
@@ -34,3 +35,27 @@ def test_norm_of_more_rows_than_a_launch_holds(T, d):
     for got in seen:
         assert bool(((got.double() - ys).abs() <= (half(torch.bfloat16) + 4 * U) * ys.abs() + 2.0 ** -134).all())
     assert torch.equal(y[n * 61:], y[:T - n * 61])
+
+
+def test_few_rows_of_more_tokens_than_a_launch_holds():
+    """2^20 tokens' dx of 16384 columns, 2^32 threads in one launch, from 2000 rows."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    T, R, M, N, K = 1 << 20, 2000, 3, 408, 16384
+    off = [0, 700, 1300, R]
+    w, dy = whole(g, M, N, K), whole(g, R, N)
+    token_rows = torch.full((T, 2), -1, dtype=torch.int32, device=DEV)
+    tokens = torch.randperm(T, generator=g, device=DEV)[:R]
+    tokens[0], tokens[1] = T - 1, tokens[2]                      # the last token; one with two rows
+    token_rows[tokens, torch.arange(R, device=DEV) % 2] = torch.arange(R, dtype=torch.int32, device=DEV)
+    rows = torch.cat([dy[a:b].double() @ w[m].double() for m, (a, b) in enumerate(zip(off, off[1:]))])
+    dx = torch.full((T, K), 7.0, dtype=torch.bfloat16, device=DEV)
+    ws = workspace(em.edge_moe_dense_product_backward_ws_bytes(T, R, M, N, K))
+    em.edge_moe_dense_product_backward(dy, ws[:-GUARD], w=w, dx=dx, offsets=torch.tensor(off, dtype=torch.int32, device=DEV),
+                                       token_rows=token_rows)
+    assert bool((ws[-GUARD:] == 0xA5).all())
+    live = (token_rows >= 0).any(1)
+    named = token_rows[live].long()
+    want = (rows[named.clamp(min=0)] * (named >= 0).unsqueeze(-1)).sum(1)
+    same(dx[live], want)
+    for i in range(0, T, 1 << 16):
+        assert not bool(dx[i:i + (1 << 16)][~live[i:i + (1 << 16)]].any())

@@ -56,6 +56,31 @@ def norms():
             yield "norm_backward", dict(T=min(T, FITS // ((6 if dx else 4) * d)), d=d, dx=dx)
 
 
+def products():
+    """(name, arguments) of the products': many rows, tokens, columns and matrices of them."""
+    dims = []
+    for M in (1, 8, 200, 1024):
+        for N in (8, 72, 1032, 4096, 32768):
+            for K in (32, 512, 4096, 16384, 32768):
+                for R in (2000, 1 << 18, 1 << 25):
+                    for T in (1 << 10, 1 << 20):
+                        dims.append((T, R, M, N, K))
+    for T, R, M, N, K in dims:
+        if 2 * (T * K + R * N + M * N * K) <= FITS:
+            yield "dense_product", dict(T=T, R=R, M=M, N=N, K=K)
+        if 2 * (T * K + R * N + M * N * K) <= FITS:
+            yield "dense_backward", dict(T=T, R=R, M=M, N=N, K=K, tokens=True)
+        if 2 * (R * K + R * N + M * N * K) <= FITS:
+            yield "dense_backward", dict(T=T, R=R, M=M, N=N, K=K, tokens=False)
+        if 2 * (T * K + R * N + 2 * M * N * K) <= FITS:
+            yield "dense_backward_dw", dict(T=T, R=R, M=M, N=N, K=K)
+        if 2 * (T * K + R * N) + M * N * K // 2 <= FITS:
+            yield "packed_product", dict(T=T, R=R, M=M, N=N, K=K)
+            yield "packed_product", dict(T=T, R=R, M=M, N=N - 1, K=K)
+        if K % 128 == 0 and T * K + 2 * R * N + M * N * K // 2 <= FITS:
+            yield "mx_product_coded", dict(T=T, R=R, M=M, N=N, K=K)
+
+
 def launch(lib, name, a):
     """Status of the call."""
     if name == "norm":
@@ -65,15 +90,36 @@ def launch(lib, name, a):
         g = em.CNormGrad(T=a["T"], d=a["d"], x=BASE, x_stride=a["d"], gain=BASE, rstd=BASE, dy=BASE, dy_stride=a["d"],
                          dx=BASE if a["dx"] else None, dx_stride=a["d"], dgain=BASE)
         return lib.edge_moe_norm_backward(ctypes.byref(g), BASE, 1 << 62, None)
+    T, R, M, N, K = (a[n] for n in ("T", "R", "M", "N", "K"))
+    if name == "packed_product":
+        return lib.edge_moe_packed_product(ctypes.byref(em.CPackedDims(T, R, M, N, K, 32)), BASE, K, BASE, BASE, BASE, BASE, 0, BASE, N, BASE,
+                                           1 << 62, None)
+    if name == "mx_product_coded":
+        return lib.edge_moe_mx_product_coded(ctypes.byref(em.CMxDims(T, R, M, N, K, em.MX_FP8)), BASE, BASE, BASE, BASE, BASE, BASE, BASE, N, None)
+    dims = ctypes.byref(em.CDenseDims(T, R, M, N, K))
+    if name == "dense_product":
+        return lib.edge_moe_dense_product(dims, BASE, K, BASE, BASE, BASE, 0, BASE, N, BASE, 1 << 62, None)
+    g = em.CDenseGrad(dy=BASE, dy_stride=N, row_src=BASE, offsets=BASE)
+    if name == "dense_backward":
+        g.w, g.dx, g.dx_stride = BASE, BASE, K
+        if a["tokens"]:
+            g.token_rows, g.per_token = BASE, 8
+    else:
+        g.x, g.x_stride, g.dw = BASE, K, BASE
+    return lib.edge_moe_dense_product_backward(dims, ctypes.byref(g), BASE, 1 << 62, None)
 
 
 def run(runtime, cases):
     """Every case's status and launches (grid and block sizes)."""
     ctypes.CDLL(runtime, ctypes.RTLD_GLOBAL)                      # found before the library's own runtime
     lib, rt = ctypes.CDLL(em.LIB_PATH), ctypes.CDLL(runtime)
-    vp, sz = ctypes.c_void_p, ctypes.c_size_t
+    vp, i64, sz, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
     lib.edge_moe_norm.argtypes = [vp, vp]
     lib.edge_moe_norm_backward.argtypes = [vp, vp, sz, vp]
+    lib.edge_moe_dense_product.argtypes = [vp, vp, i64, vp, vp, vp, i32, vp, i64, vp, sz, vp]
+    lib.edge_moe_dense_product_backward.argtypes = [vp, vp, vp, sz, vp]
+    lib.edge_moe_packed_product.argtypes = [vp, vp, i64, vp, vp, vp, vp, i32, vp, i64, vp, sz, vp]
+    lib.edge_moe_mx_product_coded.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, vp]
     rt.launches.restype, rt.launches.argtypes = sz, [vp, sz]
     out, buf = [], (ctypes.c_ulonglong * 6000)()
     for name, a in cases:
@@ -94,7 +140,7 @@ def runtime(tmp_path_factory):
     return str(so)
 
 
-@pytest.mark.parametrize("which", ["norms"])
+@pytest.mark.parametrize("which", ["norms", "products"])
 def test_fewer_than_2_to_the_32_threads(runtime, which):
     cases = list(globals()[which]())
     r = subprocess.run([sys.executable, os.path.abspath(__file__), runtime], input=json.dumps(cases), capture_output=True, text=True,
