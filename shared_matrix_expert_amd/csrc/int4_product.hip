@@ -402,6 +402,10 @@ ip_tile(Int4Product a) {
     });
     if (t.r1 == 0) return;
     const int n0 = tn * BN, rows = t.r1 - t.r0, ng = a.K / a.gq;
+    uint64_t named[BT / 64];                                      // rows whose x row row_src names
+#pragma unroll
+    for (int h = 0; h < BT / 64; ++h) named[h] = __ballot(x_row(a, t.r0 + min(64 * h + lane, rows - 1)) >= 0);
+    auto has_x = [&](int r) { return (BT == 64 || r < 64 ? named[0] : named[BT / 64 - 1]) >> (r & 63) & 1; };
     const int steps = (a.K + KC - 1) / KC, whole_steps = a.K / KC;
     const int s0 = (int)((int64_t)steps * z / a.slices), s1 = (int)((int64_t)steps * (z + 1) / a.slices);
 
@@ -532,10 +536,9 @@ ip_tile(Int4Product a) {
         const int Np = (a.N + 3) & ~3;
         for (int i = threadIdx.x; i < rows * (BN / 4); i += C::NW * 64) {
             const int r = i / (BN / 4), c = 4 * (i % (BN / 4));
-            if (c >= cols) continue;
-            const bool named = !a.row_src || x_row(a, t.r0 + r) >= 0;     // (the join knows no row_src)
-            *reinterpret_cast<floatx4*>(a.part + ((int64_t)z * a.R + t.r0 + r) * Np + n0 + c) =
-                named ? *reinterpret_cast<const floatx4*>(o + r * C::RS + c) : zero4();
+            if (c < cols)                                         // (the join knows no row_src)
+                *reinterpret_cast<floatx4*>(a.part + ((int64_t)z * a.R + t.r0 + r) * Np + n0 + c) =
+                    has_x(r) ? *reinterpret_cast<const floatx4*>(o + r * C::RS + c) : zero4();
         }
         return;
     }
@@ -543,8 +546,8 @@ ip_tile(Int4Product a) {
     for (int i = threadIdx.x; i < rows * per; i += C::NW * 64) {
         const int r = i / per, c = each * (i % per);
         if (c >= cols) continue;
-        const bool named = !a.row_src || x_row(a, t.r0 + r) >= 0;
-        const floatx4 lo = named ? *reinterpret_cast<const floatx4*>(o + r * C::RS + c) : zero4();
+        const bool live = has_x(r);
+        const floatx4 lo = live ? *reinterpret_cast<const floatx4*>(o + r * C::RS + c) : zero4();
         const int64_t at = (int64_t)(t.r0 + r) * a.y_stride + n0 + c;
         if (a.y_f32) {
             if (a.vec && c + 4 <= cols) {
@@ -554,7 +557,7 @@ ip_tile(Int4Product a) {
             }
             continue;
         }
-        const floatx4 hi = named ? *reinterpret_cast<const floatx4*>(o + r * C::RS + c + 4) : zero4();
+        const floatx4 hi = live ? *reinterpret_cast<const floatx4*>(o + r * C::RS + c + 4) : zero4();
         const u32x4 v = {pack2(lo.x, lo.y), pack2(lo.z, lo.w), pack2(hi.x, hi.y), pack2(hi.z, hi.w)};
         uint16_t* y = static_cast<uint16_t*>(a.y) + at;
         if (a.vec && c + 8 <= cols) {
