@@ -5,7 +5,7 @@ import torch
 
 import shared_matrix_expert_amd as em
 from gpu_helpers import DEV, say
-from test_gpu_norm import TYPES, run_backward
+from test_gpu_norm import TYPES, check_backward, run_backward
 
 pytestmark = pytest.mark.gpu
 
@@ -71,3 +71,20 @@ def test_dgain_of_many_rows(T, d, grad):
     for i in range(0, T, 8192):
         want += (dy[i:i + 8192].double() * x[i:i + 8192].double() * rstd[i:i + 8192, None].double()).sum(0)
     assert bool(((dgain.double() - want).abs() <= TERM * want).all())
+
+
+@pytest.mark.parametrize("grad", list(TYPES))
+@pytest.mark.parametrize("T,d", [(41, 1000), (300, 4096), (700, 8200), (257, 16384), (300, 32768)])
+def test_gradients_over_the_ones_they_come_from(T, d, grad):
+    """dx over dy, and over dres, with dgain: the bits of a call with rows of its own."""
+    g = torch.Generator(device=DEV).manual_seed(T)
+    x, rstd = torch.randn(T, d, generator=g, device=DEV).to(torch.bfloat16), torch.rand(T, generator=g, device=DEV) + 0.5
+    dy, dres = (torch.randn(T, d, generator=g, device=DEV).to(TYPES[grad]) for _ in range(2))
+    gain = torch.randn(d, generator=g, device=DEV)
+    dx, dgain, again = torch.empty_like(dy), torch.empty(d, device=DEV), torch.empty(d, device=DEV)
+    run_backward(x, gain, rstd, dy, dres, dx, dgain)
+    check_backward(x, gain, rstd, dy, dres, dx, dgain)
+    for over in ("dy", "dres"):
+        a = dict(dy=dy.clone(), dres=dres.clone())
+        run_backward(x, gain, rstd, a["dy"], a["dres"], a[over], again)
+        assert torch.equal(a[over], dx) and torch.equal(again, dgain)
