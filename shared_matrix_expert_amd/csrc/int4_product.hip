@@ -106,7 +106,7 @@ ip_rows(Int4Product a) {
     constexpr int WD = 32 / W, XR = 8, RS = 2 * KC * WD + 16;     // chunks and x rows at once, bytes of an x row in the LDS
     static_assert(XR * RS >= NC * 1024, "");
     __shared__ __attribute__((aligned(16))) uint8_t xl[W][XR * RS];
-    const RowTile t = row_tile<16>(a.offsets, a.M, a.R, [](int) { return (int)blockIdx.y; });
+    const RowTile t = row_tile<16>(a.offsets, a.M, a.R, [&](int) { return a.tile0 + (int)blockIdx.y; });
     if (t.r1 == 0) return;
     const int lane = lane_id(), wv = wave_id(), g = lane >> 4, m = lane & 15;
     const int n0 = blockIdx.x * (16 * NC);
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(256)
 ip_stream(Int4Product a) {
     constexpr int WD = NS == 4 ? 2 : 4;
     __shared__ __attribute__((aligned(16))) float red[4][NS * NC][256];
-    const RowTile t = row_tile<16 * NS>(a.offsets, a.M, a.R, [](int) { return (int)blockIdx.y; });
+    const RowTile t = row_tile<16 * NS>(a.offsets, a.M, a.R, [&](int) { return a.tile0 + (int)blockIdx.y; });
     if (t.r1 == 0) return;
     const int lane = lane_id(), wv = wave_id(), g = lane >> 4, m = lane & 15;
     const int n0 = blockIdx.x * (16 * NC);
@@ -576,24 +576,30 @@ int64_t max_row_tiles(const Int4Product& a, int BT) {
     return a.M > 1 ? a.R / BT + live : (a.R + BT - 1) / BT;
 }
 
+// Launches of `tiles` row tiles: a grid takes up to 65536 of them in its second dimension.
+template <class F>
+hipError_t launch_row_tiles(Int4Product a, int64_t tiles, const char* name, hipStream_t s, F launch) {
+    prof_begin(s);
+    for (; a.tile0 < tiles; a.tile0 += 65536) launch(a, (unsigned)(tiles - a.tile0 < 65536 ? tiles - a.tile0 : 65536));
+    prof_end(s, name);
+    return hipGetLastError();
+}
+
 template <int GPC, int NS>
 hipError_t launch_stream(const Int4Product& a, hipStream_t s) {
-    const dim3 grid((a.N + 31) / 32, (unsigned)max_row_tiles(a, 16 * NS));
-    prof_begin(s);
-    ip_stream<GPC, NS, 2><<<grid, 256, 0, s>>>(a);
-    prof_end(s, "ip_stream");
-    return hipGetLastError();
+    return launch_row_tiles(a, max_row_tiles(a, 16 * NS), "ip_stream", s, [&](const Int4Product& b, unsigned tiles) {
+        ip_stream<GPC, NS, 2><<<dim3((a.N + 31) / 32, tiles), 256, 0, s>>>(b);
+    });
 }
 
 template <int W, int GPC, int NC>
 hipError_t launch_rows(const Int4Product& a, hipStream_t s) {
-    const dim3 grid((a.N + 16 * NC - 1) / (16 * NC), (unsigned)max_row_tiles(a, 16));
     const bool vec = GPC == 1 ? a.gq == KC && a.K % 4096 == 0 : a.K % KC == 0;
-    prof_begin(s);
-    if (vec) ip_rows<W, GPC, NC, true><<<grid, 64 * W, 0, s>>>(a);
-    else ip_rows<W, GPC, NC, false><<<grid, 64 * W, 0, s>>>(a);
-    prof_end(s, "ip_rows");
-    return hipGetLastError();
+    return launch_row_tiles(a, max_row_tiles(a, 16), "ip_rows", s, [&](const Int4Product& b, unsigned tiles) {
+        const dim3 grid((a.N + 16 * NC - 1) / (16 * NC), tiles);
+        if (vec) ip_rows<W, GPC, NC, true><<<grid, 64 * W, 0, s>>>(b);
+        else ip_rows<W, GPC, NC, false><<<grid, 64 * W, 0, s>>>(b);
+    });
 }
 
 struct IpPlan { int bt, bn, slices; };                            // bn 0: ip_rows (bt 16) or ip_stream (32, 64)

@@ -168,6 +168,7 @@ struct Int4Product {
     void* y; int64_t y_stride; int y_f32;
     int vec;                    // y rows take 16-byte stores (8 bf16, 4 float32) at every eighth or fourth column
     int slices, row_tiles;
+    int tile0;                  // a launch's first row tile
     float* part;                // workspace: [slices][R][N up to a multiple of 4]
 };
 size_t int4_product_ws_bytes(const Int4Product& a);

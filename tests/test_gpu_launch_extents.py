@@ -1,11 +1,13 @@
-"""Calls of more work than one launch holds (2^32 threads in a dimension)."""
+"""Calls of more work than one launch holds (2^32 threads in a dimension, 65536 workgroups
+in the second one)."""
 import pytest
 import torch
 
 import shared_matrix_expert_amd as em
 from gpu_helpers import DEV, say
-from test_gpu_dense_product import GUARD, same, whole, workspace
+from test_gpu_dense_product import GUARD, product, same, whole, workspace
 from test_gpu_norm import U, half
+from test_gpu_packed_product import matrices
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +61,21 @@ def test_few_rows_of_more_tokens_than_a_launch_holds():
     same(dx[live], want)
     for i in range(0, T, 1 << 16):
         assert not bool(dx[i:i + (1 << 16)][~live[i:i + (1 << 16)]].any())
+
+
+def test_int4_rows_past_a_grids_second_dimension():
+    """More than 65536 tiles of 16 and of 64 rows, in a matrix and in three of them."""
+    g = torch.Generator(device=DEV).manual_seed(4)
+    T, K = 4096, 64
+    x = whole(g, T, K)
+    for R, N, q in (((1 << 22) + 77, 8, 32), ((1 << 22) + 77, 3, 64)):
+        src = torch.randint(-1, T, (R,), generator=g, device=DEV, dtype=torch.int32)
+        for off in ([0, R], [5, 17, R // 2 + 3, R - 2]):
+            M = len(off) - 1
+            codes, scales, w = matrices(g, M, N, K, q)
+            y = torch.full((R, N), 7.0, device=DEV)
+            ws = workspace(em.edge_moe_packed_product_ws_bytes(T, R, M, N, K, q))
+            em.edge_moe_packed_product(q, x, codes, scales, y, ws[:-GUARD], offsets=torch.tensor(off, dtype=torch.int32, device=DEV),
+                                       row_src=src)
+            assert bool((ws[-GUARD:] == 0xA5).all())
+            same(y, product(x, w, off, src, R), (off[0], off[-1]))
