@@ -370,13 +370,20 @@ EM_DEV void dp_body(const DenseProduct& a, const DpTile& t, uint8_t* lds) {
     constexpr int MID = NI / 2, SPAN = NI - MID > 1 ? NI - MID - 1 : 1;   // subtiles with reads of P
     auto step = [&](int st, auto set, auto fast) {
         constexpr int f = decltype(set)::value;
+        uint64_t behind = 0;                                      // (GATHER) unnamed of step st + 2
         asm volatile("" : "+v"(turn));                            // the lane addresses are made anew: kept, they take registers
         // all of this wave's reads of P are done: those of Q behind the last of them (NI > 2: in
         // the last subtile) may be in flight
         wait_lds_barrier<NI == 2 ? 0 : C::JT ? 4 : 2>();
 #pragma unroll
         for (int p = 0; p < NI; ++p) {
-            if (p == MID) wait_loads_barrier<MID * C::LOADS / NI>();
+            if (p == MID) {
+                wait_loads_barrier<MID * C::LOADS / NI>();
+                if constexpr (C::GATHER) {
+                    behind = without_x(seen);
+                    seen = rows_of(st + 3)[lane];
+                }
+            }
             if (p >= MID) {
 #pragma unroll
                 for (int u = (p - MID) * 2 * NJ / SPAN; u < (p - MID + 1) * 2 * NJ / SPAN && u < 2 * NJ; ++u)
@@ -398,8 +405,7 @@ EM_DEV void dp_body(const DenseProduct& a, const DpTile& t, uint8_t* lds) {
         }
         if constexpr (C::GATHER) {
             if (unnamed) drop_rows(fi[1 - f], unnamed);           // (step st + 1's)
-            unnamed = without_x(seen);
-            seen = rows_of(st + 3)[lane];
+            unnamed = behind;
         }
     };
     if (s0 < s1) {
@@ -414,16 +420,17 @@ EM_DEV void dp_body(const DenseProduct& a, const DpTile& t, uint8_t* lds) {
 #pragma unroll
             for (int u = 0; u < C::LOADS; ++u) fetch(s0 + st, u, std::false_type{});
         }
-        if constexpr (C::GATHER) read_rows(s0 + 2);
-        wait_loads_barrier<C::LOADS>();
-#pragma unroll
-        for (int u = 0; u < 2 * NJ; ++u) fi[0][u / NJ][u % NJ] = read_i(s0, u % NJ, u / NJ);
+        uint64_t first = 0;                                       // (GATHER) unnamed of step s0
         if constexpr (C::GATHER) {
-            const uint64_t first = without_x(rows_of(s0)[lane]);
-            if (first) drop_rows(fi[0], first);
+            read_rows(s0 + 2);
+            first = without_x(rows_of(s0)[lane]);
             unnamed = without_x(rows_of(s0 + 1)[lane]);
             seen = rows_of(s0 + 2)[lane];
         }
+        wait_loads_barrier<C::LOADS>();
+#pragma unroll
+        for (int u = 0; u < 2 * NJ; ++u) fi[0][u / NJ][u % NJ] = read_i(s0, u % NJ, u / NJ);
+        if (C::GATHER && first) drop_rows(fi[0], first);
 #pragma unroll
         for (int h = 0; h < 2; ++h) fj[0][h] = read_j(s0, 0, h);
         int st = s0;
