@@ -138,8 +138,8 @@ dp_stream(DenseProduct a) {
 // tiles arrive by direct global -> LDS loads two steps ahead, every wave as many loads a
 // step, counted by hand.  P's fragments of a step are read into registers during the
 // step before, so P needs two stages and Q three.  Bound by the matrix cores: y of 8192^3
-// 730 to 790 us, 1.39 to 1.50 PFLOP/s, dx 750, dW 805 (large library products of the three
-// layouts 749, 854, 965); 5001 rows in 8 groups, 4096 x 8192, y 330, dx 317, dW 375.
+// 737 us, 1.49 PFLOP/s, dx 754, dW 816 (large library products of the three layouts 749, 854,
+// 965); 5001 rows in 8 groups, 4096 x 8192, y 324, dx 310, dW 397.
 //
 // An operand with c along its rows: 128-byte rows (whole cache lines), 16-byte segments
 // XOR-swizzled by the row (mx_product.hip's rule).  One with c down the rows: 64 rows of BX
@@ -720,10 +720,10 @@ bool wide_rows(const DenseProduct& a, int mode) {
 // many as the LDS holds); slices are joined by a launch more and pass through memory
 // twice.  Measured with 2000 rows of 4096 x 4096 (a round of 64 steps on all of the chip)
 // and 64 rows (tiles alone).  What it chooses between (us, T x M x N x K, tiles i x j /
-// slices): y of 2000 x 1 x 4096 x 4096 256x128 61, 256x256 86, 64x64 98; 500 x 1 x 2048 x
-// 2048 64x64 12, 256x256 40; 64 x 1 x 4096 x 4096 64x64/8 15, 64x64 29; dx of 4096 tokens'
-// four of 64 x 512 x 1024 128x128 35, 256x256 40; dW of 16384 x 1 x 128 x 4096 64x256/8 34,
-// 64x256 149.
+// slices, inputs in the memory-side cache): y of 2000 x 1 x 4096 x 4096 128x256 58, 256x256 58,
+// 64x64 97; 500 x 1 x 2048 x 2048 64x64 11, 256x256 25; 64 x 1 x 4096 x 4096 64x64/8 14, 64x64
+// 28; dx of 4096 tokens' four of 64 x 512 x 1024 128x128 32, 256x256 31, 64x64 42; dW of 16384 x
+// 1 x 128 x 4096 128x64/8 38, 64x256/8 35, 64x256 155.
 DpPlan plan(const DenseProduct& a, int mode, int most_slices = 16, float* us_out = nullptr) {
     struct Cost { int bt, bn, fit; float fixed, alone, full, dw_full; };
     static constexpr Cost kTiles[9] = {
@@ -806,11 +806,11 @@ hipError_t launch_tile(DenseProduct a, DpPlan p, hipStream_t s) {
 
 // Whether dp_stream makes y: sixteen rows a matrix on average, twelve of many (routed
 // experts, some of which have more than sixteen), and not very many workgroups of a short K.
-// us, streamed and by dp_tile: 16 rows through 4096 x 4096 10.1 and 16.1, 16 through 8192 x 8192
-// 25.1 and 28.3, 24 through 4096 x 4096 15.9 and 14.0 (two row tiles a workgroup 15.9 as well);
-// 80 rows over 512 of 128 x 4096 21.7 and 32; over 64 of 128 x 4096 512 rows 15.9 and 24.5, 768
-// 25.2 and 24.4, 1024 27 and 22; 4096 over 512 of 128 x 512 33 and 24, 512 over 64 of 1024 x
-// 1024 25 and 28.
+// us, streamed and by dp_tile (the better of its tiles): 16 rows through 4096 x 4096 9.3 and 12.6,
+// 16 through 8192 x 8192 24.2 and 26.3, 24 through 4096 x 4096 12.7 and 12.7; 80 rows over 512 of
+// 128 x 4096 18.3 and 22.4; over 64 of 128 x 4096 with as many rows each 512 rows 15.0 and 17.8,
+// 768 15.8 and 18.4, routed at random 21.9 and 18.3, 24.1 and 18.5, 1024 rows 25.6 and 18.7; 4096
+// over 512 of 128 x 512 32.7 and 16.0, 512 over 64 of 1024 x 1024 26.1 and 22.5.
 bool streams(const DenseProduct& a) {
     const int live = a.M < a.R ? a.M : a.R;
     if (a.R > (int64_t)live * (a.M < 64 ? 16 : 12)) return false;

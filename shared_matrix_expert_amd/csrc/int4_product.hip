@@ -99,7 +99,10 @@ EM_DEV void join_waves(const Int4Product& a, const floatx4 (&acc)[NS][NC], const
 // one trip to memory and what follows it: one token through 8192 x 4096, 18 MB, 7.6 us; 80
 // rows over 512 of 128 x 4096, 22 MB, 12.4.
 // VEC: a wave's scales of such a block are 8 or 16 bytes (GPC 1: groups of 128, K a multiple
-// of 4096), those of a chunk 4 or 8 (GPC 2, 4: K a multiple of 128).
+// of 4096), those of a chunk 4 or 8 (GPC 2, 4: K a multiple of 128).  One row through 8192 x 5120,
+// whose scales are loaded one by one, takes 10.0 us, 4096 of K 7.8, 3968 7.0.
+// Four waves with four groups in 128 of K spill 22 registers: the 80 rows take 17 us with
+// groups of 32, 16 with groups of 64, 12.9 with groups of 128.
 template <int W, int GPC, int NC, bool VEC>
 __global__ void __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2)))
 ip_rows(Int4Product a) {
@@ -357,7 +360,7 @@ ip_stream(Int4Product a) {
 // (with groups of 128 and more the segments that lane groups 0 .. 3 read together are kept
 // side by side); 64-byte code rows as mx_product.hip's.  Bound by the matrix cores and, of
 // the same order, the conversion of the codes: 4096 rows in 8 groups through 8192 x 4096
-// 308 us, 0.89 PFLOP/s, 1001 through 4096 x 8192 114 (groups of 32 173); waves of 64 rows x
+// 308 us, 0.89 PFLOP/s, 1001 through 4096 x 8192 114 (groups of 32 179); waves of 64 rows x
 // 64 columns, which read half as much of x from the LDS and convert each code twice, 364 and
 // 141.
 namespace {
@@ -607,11 +610,12 @@ struct IpPlan { int bt, bn, slices; };                            // bn 0: ip_ro
 // The least of an estimate in us from measured times.  Few rows: K / 4096 times a part of
 // its own and one a workgroup.  Tiles: a step of 128 of K alone on a compute unit or with it
 // full, 1.25 and 1.6 times that with two and four scale groups a step; slices of K are
-// joined by a launch more.  Measured (us, rows through M x N x K; 16, 32: rows a workgroup,
-// tiles rows x columns / slices): 20 through 4096 x 4096 16 13.0, 32 14.5, 64x128/8 13.9; 64
-// through 1024 x 4096 16 10.6, 32 15.9; 32 through 8192 x 4096 16 20, 32 17; 256 through 4096
-// x 4096 64x128/2 25.6, 128x256/8 29.6, 64x128 34; 4096 through 4096 x 4096 128x256 134, 64x128
-// 175; 4096 routed over 64 of 128 x 4096 64x128/4 24, 128x256/4 29.
+// joined by a launch more.  Measured (us, inputs in the memory-side cache, rows through M x N x
+// K; 16, 32: rows a workgroup, tiles rows x columns / slices): 20 through 4096 x 4096 16 8.9, 32
+// 13.0, 64x128/8 12.5; 64 through 1024 x 4096 16 8.1, 32 14.8; 32 through 8192 x 4096 16 14.9, 32
+// 15.6, 64x128/4 16.3; 256 through 4096 x 4096 64x256/4 26.5, 64x128/2 24.2, 128x256/8 27.6, 64x128
+// 33.6; 4096 through 4096 x 4096 128x256 128, 64x128 181; 4096 routed over 64 of 128 x 4096 64x128/4
+// 22.3, 128x256/4 27.4.
 IpPlan plan(const Int4Product& a) {
     struct Cost { int bt, bn, fit; float fixed, alone, full; };
     static constexpr Cost kTiles[3] = {{64, 128, 2, 3.0f, 0.98f, 1.33f}, {64, 256, 1, 3.0f, 1.25f, 1.30f}, {128, 256, 1, 4.0f, 1.70f, 2.00f}};
@@ -636,7 +640,9 @@ IpPlan plan(const Int4Product& a) {
         }
     };
     take(few(32, 9.8f, 0.0115f, 256), IpPlan{32, 0, 1});
-    if ((int64_t)a.N * (a.K / a.gq) % 2) {                        // the last scale's word would end past the scales
+    // a tile takes scales by words, and the last word would end past them where a matrix has an odd
+    // number (1001 rows through 1025 x 4224, 33 groups a column, 52 us; through 1024 columns 25)
+    if ((int64_t)a.N * (a.K / a.gq) % 2) {
         take(each > 64 ? 0.f : least, IpPlan{64, 0, 1});
         return best;
     }
@@ -677,7 +683,8 @@ hipError_t launch_tile(Int4Product a, const IpPlan& p, hipStream_t s) {
 template <int GPC>
 hipError_t launch_product(const Int4Product& a, hipStream_t s) {
     IpPlan p = plan(a);
-    // lane offsets of a tile's x rows have 32 bits
+    // lane offsets of a tile's x rows have 32 bits (600 gathered rows through 4096 x 4096, x rows 2^22
+    // elements apart: 105 us, close together in tiles 49)
     const int64_t rows = a.row_src ? a.T : 128;
     if (p.bn && rows * a.x_stride >= (1ll << 31)) p = IpPlan{64, 0, 1};
     if (p.bn == 0) {
