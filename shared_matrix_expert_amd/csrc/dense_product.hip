@@ -856,11 +856,10 @@ hipError_t launch_dense_product(DenseProduct a, void* ws, hipStream_t s) {
 
 // Columns of dx that are made for tokens at once: their rows' partial sums then stay in the
 // 256 MB memory-side cache between the two launches (16384 tokens' ten of 512 x 128 x 4096: 1565 us at once, 1419 so;
-// 48 and 96 MB at once measured more on the smaller ones).  Few rows of very many tokens: no
-// more than 2^31 threads add them (2^20 tokens by 8192 columns).
+// 48 and 96 MB at once measured more on the smaller ones).
 int token_cols(const DenseProduct& a, int slices) {
-    const int64_t fit = (192ll << 20) / ((int64_t)a.R * slices * 4 + 1), threads = (1ll << 33) / a.T;
-    const int64_t cols = (fit < threads ? fit : threads) / 256 * 256;
+    const int64_t fit = (192ll << 20) / ((int64_t)a.R * slices * 4 + 1);
+    const int64_t cols = fit / 256 * 256;
     return cols < 256 ? 256 : cols < a.K ? (int)cols : a.K;
 }
 
@@ -943,8 +942,10 @@ hipError_t launch_dense_backward(const DenseGrad& gr, void* ws, hipStream_t s) {
         return tp.p.bn == 128 ? launch_tile<DP_DXT, 128, 128>(a, blocks, s) : launch_tile<DP_DXT, 128, 256>(a, blocks, s);
     }
     a.to_part = 1;
+    // few rows of very many tokens: no more than 2^31 threads add them (2^20 tokens by 8192 columns)
+    const int64_t threads = (1ll << 33) / a.T / 256 * 256;
+    const int fit = token_cols(a, p.slices), most = fit < threads ? fit : (int)threads;
     for (a.col0 = 0; a.col0 < a.K; a.col0 += a.cols) {
-        const int most = token_cols(a, p.slices);
         a.cols = a.K - a.col0 < most ? a.K - a.col0 : most;
         hipError_t e = a.R ? launch_tile<DP_DX>(a, p, s) : hipSuccess;
         void* dx = static_cast<char*>(gr.dx) + (int64_t)a.col0 * (gr.dx_f32 ? 4 : 2);
