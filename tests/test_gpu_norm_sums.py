@@ -88,3 +88,36 @@ def test_gradients_over_the_ones_they_come_from(T, d, grad):
         a = dict(dy=dy.clone(), dres=dres.clone())
         run_backward(x, gain, rstd, a["dy"], a["dres"], a[over], again)
         assert torch.equal(a[over], dx) and torch.equal(again, dgain)
+
+
+def test_wide_rows_on_two_streams_and_replayed():
+    """Rows whose dgain is a pass of its own: two calls at once with a workspace each, and a
+    captured one replayed over new gradients between eager calls."""
+    g = torch.Generator(device=DEV).manual_seed(12)
+    T, d = 700, 16384
+    x, rstd = torch.randn(T, d, generator=g, device=DEV).to(torch.bfloat16), torch.rand(T, generator=g, device=DEV) + 0.5
+    gain, dres = torch.randn(d, generator=g, device=DEV), torch.randn(T, d, generator=g, device=DEV)
+    dys = [torch.randn(T, d, generator=g, device=DEV) for _ in range(2)]
+    out = [(torch.empty(T, d, device=DEV), torch.empty(d, device=DEV),
+            torch.empty(em.edge_moe_norm_backward_ws_bytes(T, d), dtype=torch.uint8, device=DEV)) for _ in range(2)]
+
+    def call(i):
+        em.edge_moe_norm_backward(x, gain, rstd, dys[i], out[i][2], dres=dres, dx=out[i][0], dgain=out[i][1])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        call(0)
+    call(1)
+    torch.cuda.synchronize()
+    for i in range(2):
+        check_backward(x, gain, rstd, dys[i], dres, out[i][0], out[i][1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(0)
+    for _ in range(3):
+        dys[0].copy_(torch.randn(T, d, generator=g, device=DEV))
+        call(1)
+        graph.replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            check_backward(x, gain, rstd, dys[i], dres, out[i][0], out[i][1])

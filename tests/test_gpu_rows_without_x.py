@@ -121,3 +121,36 @@ def test_dense_rows_without_x_add_nothing(R, M, N, K, out, far):
     named = ~none
     named[:live[0]], named[live[1]:] = False, False
     same(dx[named], want_dx[named])
+
+
+def test_rows_that_lose_their_x_between_replays():
+    """A captured step of products with int4 and bf16 matrices and dW; other rows are without
+    x, beside a dy that is not finite, in each replay."""
+    g = torch.Generator(device=DEV).manual_seed(2)
+    R, M, N, K = 4100, 8, 128, 1024
+    x, w, dy = whole(g, T, K), whole(g, M, N, K), whole(g, R, N)
+    codes, scales, w4 = matrices(g, M, N, K, 128)
+    src, off, offsets, _ = rows(R, M, 0)
+    live = (int(off[0]), int(off[-1]))
+    y, y4, dw = (torch.full(s, 7.0, device=DEV) for s in ((R, N), (R, N), (M, N, K)))
+    ws = torch.empty(max(em.edge_moe_dense_product_ws_bytes(T, R, M, N, K), em.edge_moe_packed_product_ws_bytes(T, R, M, N, K, 128),
+                         em.edge_moe_dense_product_backward_ws_bytes(T, R, M, N, K)), dtype=torch.uint8, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        em.edge_moe_dense_product(x, w, y, ws, offsets=offsets, row_src=src)
+        em.edge_moe_packed_product(128, x, codes, scales, y4, ws, offsets=offsets, row_src=src)
+        em.edge_moe_dense_product_backward(dy, ws, x=x, dw=dw, offsets=offsets, row_src=src)
+    for seed in range(1, 4):
+        other, off, o, none = rows(R, M, seed)
+        src.copy_(other)
+        offsets.copy_(o)
+        dy.copy_(whole(g, R, N))
+        want = gradients(x, w, dy, off, src, None)[1]
+        dy[none] = float("nan")
+        y.fill_(7.0)
+        y4.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        same(y, product(x, w, off, src, R), live)
+        same(y4, product(x, w4, off, src, R), live)
+        same(dw, want)
