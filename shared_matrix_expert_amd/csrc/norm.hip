@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(norm_threads<W>())
 norm_backward(NormBwd a) {
     __shared__ double slots[2][W];
     constexpr bool SUMS = sums_beside_rows<W>(), AHEAD = NV < 4;
-    __shared__ __attribute__((aligned(16))) float part[W == 1 ? 4 : 1][W == 1 ? 512 * NV : 4];
+    __shared__ __attribute__((aligned(16))) double part[W == 1 ? 4 : 1][W == 1 ? 512 * NV : 2];
     const int in_row = W == 1 ? lane_id() : (int)threadIdx.x;
     const int first = blockIdx.x * a.chunk + (W == 1 ? wave_id() : 0);
     const int last = min(a.T, (int)(blockIdx.x + 1) * a.chunk);
@@ -335,11 +335,9 @@ norm_backward(NormBwd a) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; j += 4)
-                *reinterpret_cast<float4*>(&part[wave_id()][8 * (in_row + 64 * i) + j]) =
-                    make_float4((float)dg[i][j], (float)dg[i][j + 1], (float)dg[i][j + 2], (float)dg[i][j + 3]);
+            for (int j = 0; j < 8; ++j) part[wave_id()][8 * (in_row + 64 * i) + j] = dg[i][j];
         __syncthreads();
-        for (int e = threadIdx.x; e < a.d; e += 256) out[e] = (part[0][e] + part[1][e]) + (part[2][e] + part[3][e]);
+        for (int e = threadIdx.x; e < a.d; e += 256) out[e] = (float)((part[0][e] + part[1][e]) + (part[2][e] + part[3][e]));
     } else {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {

@@ -38,9 +38,8 @@ def test_rows_with_an_infinity(d):
 
 
 U = 2.0 ** -24
-# Roundings of a term of dgain: v's, that of a wave's sum over its rows, two where four waves
-# are added, and dgain's own.
-TERM = 6 * U
+# Roundings of a term of dgain: v's, that of a workgroup's sum over its rows, and dgain's own.
+TERM = 3.01 * U
 
 
 @pytest.mark.parametrize("T,d", [(1 << 20, 8), (1 << 18, 512), (1 << 17, 1024), (1 << 17, 2048), (1 << 16, 4096), (1 << 15, 8192),
